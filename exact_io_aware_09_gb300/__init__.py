@@ -14,6 +14,9 @@ import os
 __all__ = [
     "AttnError", "attn_fwd", "attn_fwd_window", "attn_fwd_block_sparse", "attn_fwd_fp8",
     "attn_fwd_fp8_workspace_bytes", "attn_fwd_fp8_workspace_offsets",
+    "attn_fwd_window_sinks", "attn_bwd_window_sinks", "attn_bwd_window_sinks_workspace_bytes",
+    "attn_fwd_paged", "attn_fwd_paged_workspace_bytes",
+    "attn_cache_write_fp8", "attn_cache_read_fp8", "attn_decode_paged_fp8",
     "attn_bwd", "attn_bwd_workspace_bytes",
     "attn_decode_splitkv", "attn_decode_workspace_bytes", "attn_decode_paged",
     "attn_decode_splitkv_static", "attn_decode_static_scratch_bytes",
@@ -52,6 +55,24 @@ lib.attn_fwd_fp8.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
 lib.attn_fwd_fp8.restype = _I
 lib.attn_fwd_window.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _I]
 lib.attn_fwd_window.restype = _I
+lib.attn_fwd_window_sinks.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
+                                      _I]
+lib.attn_fwd_window_sinks.restype = _I
+lib.attn_bwd_window_sinks_workspace_bytes.argtypes = [_I] * 8
+lib.attn_bwd_window_sinks_workspace_bytes.restype = _SZ
+lib.attn_bwd_window_sinks.argtypes = [_P] * 9 + [_I] * 8 + [_F, _I, _P, _SZ, _P]
+lib.attn_bwd_window_sinks.restype = _I
+lib.attn_fwd_paged_workspace_bytes.argtypes = [_I] * 9
+lib.attn_fwd_paged_workspace_bytes.restype = _SZ
+lib.attn_fwd_paged.argtypes = [_P] * 6 + [_I] * 6 + [_P, _P] + [_I] * 6 + [_F, _I, _P, _SZ, _P]
+lib.attn_fwd_paged.restype = _I
+lib.attn_cache_write_fp8.argtypes = [_P] * 9 + [_I] * 8 + [_P]
+lib.attn_cache_write_fp8.restype = _I
+lib.attn_cache_read_fp8.argtypes = [_P] * 6 + [_I] * 3 + [_P, _P] + [_I] * 5 + [_P]
+lib.attn_cache_read_fp8.restype = _I
+lib.attn_decode_paged_fp8.argtypes = [_P] * 7 + [_I] * 4 + [_P, _P] + [_I] * 5 + [_F, _I, _P, _SZ,
+                                                                              _P]
+lib.attn_decode_paged_fp8.restype = _I
 lib.attn_fwd_block_sparse.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _F, _P,
                                       _I]
 lib.attn_fwd_block_sparse.restype = _I
@@ -181,6 +202,12 @@ def attn_fwd(q, k, v, o=None, lse=None, causal: bool = False, scale: float | Non
     return o, lse
 
 
+def _expect(where, t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise AttnError(-1, f"{where}: {name} must be {dtype} {tuple(shape)}, "
+                            f"got {t.dtype} {tuple(t.shape)}")
+
+
 def _fwd_prep(q, k, v, o, lse, scale):
     torch = _torch()
     B, Hq, N_q, d = q.shape
@@ -284,6 +311,65 @@ def attn_fwd_window(q, k, v, window: int, o=None, lse=None, scale: float | None 
     return o, lse
 
 
+def attn_fwd_window_sinks(q, k, v, window: int, sinks: int, o=None, lse=None,
+                          scale: float | None = None, stream=None):
+    """Sliding-window prefill whose first ``sinks`` keys stay visible: key j visible to row i,
+    p = i + N_kv - N_q, iff j <= p and (p - j <= window or j < sinks).
+
+    Shapes and return value as attn_fwd.
+    """
+    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
+    with _on_device("attn_fwd_window_sinks", q, k, v, o, lse):
+        st = lib.attn_fwd_window_sinks(_dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+                                       _dev_ptr(o, "o"), _dev_ptr(lse, "lse"), B, Hq, Hkv, N_q,
+                                       N_kv, d, int(window), int(sinks), scale,
+                                       _stream_handle(stream, q.device), _dtype_code(q))
+    _check(st, "attn_fwd_window_sinks")
+    return o, lse
+
+
+def attn_bwd_window_sinks_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window, sinks) -> int:
+    return int(lib.attn_bwd_window_sinks_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, int(window),
+                                                         int(sinks)))
+
+
+def attn_bwd_window_sinks(q, k, v, o, dout, lse, window: int, sinks: int,
+                          scale: float | None = None, dq=None, dk=None, dv=None, workspace=None,
+                          stream=None):
+    """Gradients (dq, dk, dv) of attn_fwd_window_sinks (sinks = 0: of attn_fwd_window) for the
+    incoming gradient ``dout``.  Arguments as attn_bwd with the mask of the forward call; the
+    workspace takes attn_bwd_window_sinks_workspace_bytes(...) bytes.  Deterministic.
+    """
+    torch = _torch()
+    where = "attn_bwd_window_sinks"
+    B, Hq, N_q, d = q.shape
+    _, Hkv, N_kv, _ = k.shape
+    for t, nm, like in ((o, "o", q), (dout, "dout", q), (v, "v", k), (dq, "dq", q), (dk, "dk", k),
+                        (dv, "dv", k)):
+        if t is not None and (t.shape != like.shape or t.dtype != q.dtype):
+            raise AttnError(-1, f"{where}: {nm} must be {tuple(like.shape)} {q.dtype}")
+    if k.shape[0] != B or k.shape[3] != d or k.dtype != q.dtype:
+        raise AttnError(-1, f"{where}: q/k/v shapes or dtypes disagree")
+    _expect(where, lse, "lse", torch.float32, (B, Hq, N_q))
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        need = attn_bwd_window_sinks_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window, sinks)
+        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    with _on_device(where, q, k, v, o, dout, lse, dq, dk, dv, workspace):
+        st = lib.attn_bwd_window_sinks(
+            _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(o, "o"),
+            _dev_ptr(dout, "dout"), _dev_ptr(lse, "lse"), _dev_ptr(dq, "dq"), _dev_ptr(dk, "dk"),
+            _dev_ptr(dv, "dv"), B, Hq, Hkv, N_q, N_kv, d, int(window), int(sinks), float(scale),
+            _dtype_code(q), _dev_ptr(workspace, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream, q.device))
+    _check(st, where)
+    return dq, dk, dv
+
+
 def attn_fwd_block_sparse(q, k, v, block_mask, causal: bool = False, o=None, lse=None,
                           scale: float | None = None, stream=None):
     """Block-sparse prefill.  block_mask: uint8 CUDA tensor [ceil(N_q/128), ceil(N_kv/128)],
@@ -351,6 +437,187 @@ def attn_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k:
                                    float(scale), _dtype_code(q), _dev_ptr(workspace, "workspace"),
                                    workspace.numel(), _stream_handle(stream, q.device))
     _check(st, "attn_decode_paged")
+    return o, lse
+
+
+def attn_fwd_paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, window=-1,
+                                   sinks=0) -> int:
+    return int(lib.attn_fwd_paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k,
+                                                  window, sinks, d))
+
+
+def attn_fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int,
+                   max_seqlen_k: int, window: int = -1, sinks: int = 0, o=None, lse=None,
+                   scale: float | None = None, workspace=None, stream=None):
+    """A chunk of new tokens of each sequence over its paged cache, causal; the new tokens' keys
+    and values are the cache's last rows already.
+
+    q [total_q,Hq,d] packed new tokens; cu_seqlens_q int32 CUDA [B+1]; k_pages/v_pages
+    [num_pages, page_size, Hkv, d]; block_table int32 CUDA [B, max_pages_per_seq]; seqlens_k int32
+    CUDA [B], the new tokens included.  window (-1: none) and sinks as attn_fwd_window_sinks, by
+    cache position.  Returns (o [total_q,Hq,d], lse [total_q,Hq] fp32).
+    """
+    torch = _torch()
+    where = "attn_fwd_paged"
+    total_q, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = k_pages.shape
+    if (v_pages.shape != k_pages.shape or dk != d or k_pages.dtype != q.dtype
+            or v_pages.dtype != q.dtype):
+        raise AttnError(-1, f"{where}: page pools disagree with q")
+    B = seqlens_k.shape[0]
+    _expect(where, seqlens_k, "seqlens_k", torch.int32, (B,))
+    _expect(where, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise AttnError(-1, f"{where}: block_table must be int32 [B, max_pages]")
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _expect(where, o, "o", q.dtype, q.shape)
+    if lse is None:
+        lse = torch.empty((total_q, Hq), device=q.device, dtype=torch.float32)
+    else:
+        _expect(where, lse, "lse", torch.float32, (total_q, Hq))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        need = attn_fwd_paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d,
+                                              window, sinks)
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+    with _on_device(where, q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, o, lse,
+                    workspace):
+        st = lib.attn_fwd_paged(
+            _dev_ptr(q, "q"), _dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"),
+            _dev_ptr(block_table, "block_table"), _dev_ptr(cu_seqlens_q, "cu_seqlens_q"),
+            _dev_ptr(seqlens_k, "seqlens_k"), num_pages, page_size, block_table.shape[1], total_q,
+            int(max_seqlen_q), int(max_seqlen_k), _dev_ptr(o, "o"), _dev_ptr(lse, "lse"), B, Hq,
+            Hkv, d, int(window), int(sinks), float(scale), _dtype_code(q),
+            _dev_ptr(workspace, "workspace"),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0,
+            _stream_handle(stream, q.device))
+    _check(st, where)
+    return o, lse
+
+
+def _check_cache_fp8(where, k_pages, v_pages, k_scales, v_scales, block_table, B):
+    """The (num_pages, page_size, Hkv, d) of a quantised cache, its tensors checked."""
+    torch = _torch()
+    num_pages, page_size, Hkv, d = k_pages.shape
+    _expect(where, k_pages, "k_pages", torch.float8_e4m3fn, k_pages.shape)
+    _expect(where, v_pages, "v_pages", torch.float8_e4m3fn, k_pages.shape)
+    _expect(where, k_scales, "k_scales", torch.float32, (num_pages, Hkv, page_size))
+    _expect(where, v_scales, "v_scales", torch.float32, (num_pages, Hkv, page_size))
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise AttnError(-1, f"{where}: block_table must be int32 [B, max_pages]")
+    return num_pages, page_size, Hkv, d
+
+
+def attn_cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_q,
+                         seqlens_k, stream=None) -> None:
+    """New tokens into a paged cache held in 8 bits.
+
+    k/v [total,Hkv,d] packed new tokens (fp16/bf16), sequence b's rows cu_seqlens_q[b] ..
+    cu_seqlens_q[b+1]-1 going to its last cache positions; k_pages/v_pages float8_e4m3fn
+    [num_pages, page_size, Hkv, d] and k_scales/v_scales fp32 [num_pages, Hkv, page_size], written
+    in place; block_table int32 CUDA [B, max_pages_per_seq]; seqlens_k int32 CUDA [B], the new
+    tokens included.  Each (token, head) row gets the scale 2^e, the smallest that brings its
+    largest magnitude to at most 448.
+    """
+    torch = _torch()
+    where = "attn_cache_write_fp8"
+    B = seqlens_k.shape[0]
+    num_pages, page_size, Hkv, d = _check_cache_fp8(where, k_pages, v_pages, k_scales, v_scales,
+                                                    block_table, B)
+    total = k.shape[0]
+    _expect(where, k, "k", k.dtype, (total, Hkv, d))
+    _expect(where, v, "v", k.dtype, (total, Hkv, d))
+    _expect(where, seqlens_k, "seqlens_k", torch.int32, (B,))
+    _expect(where, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    with _on_device(where, k, v, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_q,
+                    seqlens_k):
+        st = lib.attn_cache_write_fp8(
+            _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(k_pages, "k_pages"),
+            _dev_ptr(v_pages, "v_pages"), _dev_ptr(k_scales, "k_scales"),
+            _dev_ptr(v_scales, "v_scales"), _dev_ptr(block_table, "block_table"),
+            _dev_ptr(cu_seqlens_q, "cu_seqlens_q"), _dev_ptr(seqlens_k, "seqlens_k"), num_pages,
+            page_size, block_table.shape[1], total, B, Hkv, d, _dtype_code(k),
+            _stream_handle(stream, k.device))
+    _check(st, where)
+
+
+def attn_cache_read_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_k, total: int,
+                        dtype=None, k=None, v=None, stream=None):
+    """The first tokens of each sequence of a quantised cache as a packed 16-bit cache.
+
+    Sequence b's tokens 0 .. cu_seqlens_k[b+1]-cu_seqlens_k[b]-1 go to rows cu_seqlens_k[b] ..
+    of (k, v) [total,Hkv,d], allocated here in ``dtype`` (bfloat16 when omitted) unless given.
+    The cache as attn_cache_write_fp8 takes it.  Returns (k, v).
+    """
+    torch = _torch()
+    where = "attn_cache_read_fp8"
+    B = cu_seqlens_k.shape[0] - 1
+    num_pages, page_size, Hkv, d = _check_cache_fp8(where, k_pages, v_pages, k_scales, v_scales,
+                                                    block_table, B)
+    _expect(where, cu_seqlens_k, "cu_seqlens_k", torch.int32, (B + 1,))
+    if dtype is None:
+        dtype = k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16
+    total = int(total)
+    if k is None:
+        k = torch.empty((total, Hkv, d), device=k_pages.device, dtype=dtype)
+    if v is None:
+        v = torch.empty((total, Hkv, d), device=k_pages.device, dtype=dtype)
+    _expect(where, k, "k", dtype, (total, Hkv, d))
+    _expect(where, v, "v", dtype, (total, Hkv, d))
+    with _on_device(where, k, v, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_k):
+        st = lib.attn_cache_read_fp8(
+            _dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"),
+            _dev_ptr(k_scales, "k_scales"), _dev_ptr(v_scales, "v_scales"),
+            _dev_ptr(block_table, "block_table"), _dev_ptr(cu_seqlens_k, "cu_seqlens_k"),
+            num_pages, page_size, block_table.shape[1], _dev_ptr(k, "k"), _dev_ptr(v, "v"), total,
+            B, Hkv, d, _dtype_code(k), _stream_handle(stream, k.device))
+    _check(st, where)
+    return k, v
+
+
+def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k,
+                          max_seqlen_k: int, o=None, lse=None, split_size: int = 512,
+                          scale: float | None = None, workspace=None, stream=None):
+    """One split-KV decode step over a quantised paged cache (written by attn_cache_write_fp8).
+
+    Arguments and return value as attn_decode_paged, with float8_e4m3fn pools and their fp32
+    power-of-two scales [num_pages, Hkv, page_size].
+    """
+    torch = _torch()
+    where = "attn_decode_paged_fp8"
+    B, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = _check_cache_fp8(where, k_pages, v_pages, k_scales, v_scales,
+                                                     block_table, B)
+    if dk != d:
+        raise AttnError(-1, f"{where}: page pools disagree with q")
+    _expect(where, seqlens_k, "seqlens_k", torch.int32, (B,))
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _expect(where, o, "o", q.dtype, q.shape)
+    if lse is None:
+        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+    else:
+        _expect(where, lse, "lse", torch.float32, (B, Hq))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        need = attn_decode_workspace_bytes(B, Hq, max_seqlen_k, split_size, d)
+        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    with _on_device(where, q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, o, lse,
+                    workspace):
+        st = lib.attn_decode_paged_fp8(
+            _dev_ptr(q, "q"), _dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"),
+            _dev_ptr(k_scales, "k_scales"), _dev_ptr(v_scales, "v_scales"),
+            _dev_ptr(block_table, "block_table"), _dev_ptr(seqlens_k, "seqlens_k"), num_pages,
+            page_size, block_table.shape[1], int(max_seqlen_k), _dev_ptr(o, "o"),
+            _dev_ptr(lse, "lse"), B, Hq, Hkv, d, int(split_size), float(scale), _dtype_code(q),
+            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _stream_handle(stream, q.device))
+    _check(st, where)
     return o, lse
 
 

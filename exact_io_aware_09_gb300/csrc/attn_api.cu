@@ -113,8 +113,8 @@ bool make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        box0 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -143,8 +143,8 @@ __global__ void selftest_timeout_kernel(int* status, uint64_t limit_ns) {
 
 // Dispatch order of the dK/dV kernel's blocks (attn_bwd.cu): job of every block in job[0 .. n),
 // n returned; 0 = the default order.
-int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, int off, int n_sm,
-                 uint16_t* job, int cap);
+int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, int off, int window,
+                 int sinks, int n_sm, uint16_t* job, int cap);
 
 }  // namespace attn
 
@@ -152,11 +152,11 @@ using namespace attn;
 
 extern "C" {
 
-// The three prefill entry points share their checks and the kernel.
+// The prefill entry points share their checks and the kernel.
 static int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                       int Hq, int Hkv, int N_q, int N_kv, int d, int causal, int window,
                       const uint8_t* block_mask, float scale, attn_stream_t stream,
-                      attn_dtype_t dtype) {
+                      attn_dtype_t dtype, int sinks = 0) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || N_q < 0 || N_kv < 0 || Hq % Hkv != 0)
     return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
@@ -171,6 +171,7 @@ static int fwd_common(const void* q, const void* k, const void* v, void* o, floa
   if (dev_ok != ATTN_OK) return dev_ok;
   FwdArgs a{q, k, v, o, lse, B, Hq, Hkv, N_q, N_kv, d, causal ? 1 : 0, scale,
             dtype == ATTN_BF16, window, block_mask};
+  a.sinks = sinks;
   return launch_attn_fwd(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -187,6 +188,14 @@ int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float*
   if (window < 0) return ATTN_ERR_INVALID_ARG;
   return fwd_common(q, k, v, o, lse, B, Hq, Hkv, N_q, N_kv, d, 1, window, nullptr, scale,
                     stream, dtype);
+}
+
+int attn_fwd_window_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                          int Hq, int Hkv, int N_q, int N_kv, int d, int window, int sinks,
+                          float scale, attn_stream_t stream, attn_dtype_t dtype) {
+  if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return fwd_common(q, k, v, o, lse, B, Hq, Hkv, N_q, N_kv, d, 1, window, nullptr, scale,
+                    stream, dtype, sinks);
 }
 
 int attn_fwd_block_sparse(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -247,10 +256,12 @@ int attn_fwd_kv_span(int q_tile, int block_m, int block_n, int N_q, int N_kv, in
 
 size_t attn_bwd_workspace_bytes(int B, int Hq, int N_q) { return bwd_workspace_bytes(B, Hq, N_q); }
 
-int attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
-             const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N_q,
-             int N_kv, int d, int causal, float scale, attn_dtype_t dtype, void* workspace,
-             size_t workspace_bytes, attn_stream_t stream) {
+// The two backward entry points share their checks and the kernels; window < 0: attn_bwd.
+static int bwd_common(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                      const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                      int N_q, int N_kv, int d, int causal, int window, int sinks, float scale,
+                      attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                      attn_stream_t stream) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || N_q < 0 || N_kv < 0 || Hq % Hkv != 0)
     return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
@@ -276,10 +287,39 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const v
       return ATTN_ERR_LAUNCH;
     return ATTN_OK;
   }
-  if (!workspace || workspace_bytes < bwd_workspace_bytes(B, Hq, N_q)) return ATTN_ERR_WORKSPACE;
+  const size_t need = window < 0 ? bwd_workspace_bytes(B, Hq, N_q)
+                                 : attn_bwd_window_sinks_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d,
+                                                                         window, sinks);
+  if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
   BwdArgs a{q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, N_q, N_kv, d, causal ? 1 : 0, scale,
             dtype == ATTN_BF16, workspace};
+  a.window = window;
+  a.sinks = sinks;
   return launch_attn_bwd(a, st);
+}
+
+int attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
+             const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N_q,
+             int N_kv, int d, int causal, float scale, attn_dtype_t dtype, void* workspace,
+             size_t workspace_bytes, attn_stream_t stream) {
+  return bwd_common(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, N_q, N_kv, d, causal, -1, 0,
+                    scale, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t attn_bwd_window_sinks_workspace_bytes(int B, int Hq, int Hkv, int N_q, int N_kv, int d,
+                                             int window, int sinks) {
+  if (Hkv <= 0 || Hq % Hkv || N_kv < 0 || (d != 64 && d != 128) || window < 0 || sinks < 0) return 0;
+  return bwd_workspace_bytes(B, Hq, N_q);
+}
+
+int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const void* o,
+                          const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
+                          int Hq, int Hkv, int N_q, int N_kv, int d, int window, int sinks,
+                          float scale, attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                          attn_stream_t stream) {
+  if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return bwd_common(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, N_q, N_kv, d, 1, window, sinks,
+                    scale, dtype, workspace, workspace_bytes, stream);
 }
 
 size_t attn_decode_workspace_bytes(int B, int Hq, int max_seqlen_k, int split_size, int d) {
@@ -392,6 +432,151 @@ int attn_decode_splitkv_static(const void* q, const void* k_cache, const void* v
   return launch_attn_decode(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t attn_fwd_paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_seqlen_q,
+                                      int max_seqlen_k, int window, int sinks, int d) {
+  return paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, window, sinks, d);
+}
+
+// Checks of a page pool and its block table, for tables that reach max_tokens tokens a sequence.
+static int check_pages(int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens) {
+  if (num_pages < 0 || max_pages_per_seq < 0) return ATTN_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > (1 << 16) || (page_size & (page_size - 1)) != 0)
+    return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_pages_per_seq) * page_size < max_tokens) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                   const int32_t* block_table, const int32_t* cu_seqlens_q,
+                   const int32_t* seqlens_k, int num_pages, int page_size, int max_pages_per_seq,
+                   int total_q, int max_seqlen_q, int max_seqlen_k, void* o, float* lse, int B,
+                   int Hq, int Hkv, int d, int window, int sinks, float scale, attn_dtype_t dtype,
+                   void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || total_q < 0 || max_seqlen_q < 0 ||
+      max_seqlen_k < max_seqlen_q || window < -1 || sinks < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  const int pages_ok = check_pages(num_pages, page_size, max_pages_per_seq, max_seqlen_k);
+  if (pages_ok != ATTN_OK) return pages_ok;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 128) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || total_q == 0 || max_seqlen_q == 0) return ATTN_OK;
+  if (!q || !o || !lse || !block_table || !cu_seqlens_q || !seqlens_k || num_pages == 0 ||
+      !k_pages || !v_pages)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned16(workspace) || !aligned4(lse) || !aligned4(block_table) ||
+      !aligned4(cu_seqlens_q) || !aligned4(seqlens_k))
+    return ATTN_ERR_MISALIGNED;
+  const size_t need = paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, window,
+                                            sinks, d);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+  const int dev_ok = check_device(q);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  const PagedArgs a{q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, num_pages, page_size,
+                    max_pages_per_seq, total_q, max_seqlen_q, max_seqlen_k, o, lse, B, Hq, Hkv, d,
+                    window, sinks, scale, dtype == ATTN_BF16, workspace};
+  return launch_attn_fwd_paged(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Checks shared by the entry points of the quantised cache.
+static int check_cache_fp8(const CacheFp8& c, const int32_t* lengths, int total, int B, int Hkv,
+                           int d, attn_dtype_t dtype) {
+  if (B < 0 || Hkv <= 0 || total < 0) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  const int pages_ok = check_pages(c.num_pages, c.page_size, c.max_pages, 0);
+  if (pages_ok != ATTN_OK) return pages_ok;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || total == 0) return ATTN_OK;
+  if (!c.k_pages || !c.v_pages || !c.k_scales || !c.v_scales || !c.block_table || !lengths ||
+      c.num_pages == 0 || c.max_pages == 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(c.k_pages) || !aligned16(c.v_pages) || !aligned16(c.k_scales) ||
+      !aligned16(c.v_scales) || !aligned4(c.block_table) || !aligned4(lengths))
+    return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+int attn_cache_write_fp8(const void* k, const void* v, void* k_pages, void* v_pages,
+                         float* k_scales, float* v_scales, const int32_t* block_table,
+                         const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int num_pages,
+                         int page_size, int max_pages_per_seq, int total, int B, int Hkv, int d,
+                         attn_dtype_t dtype, attn_stream_t stream) {
+  const CacheFp8 c{static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages), k_scales,
+                   v_scales, block_table, num_pages, page_size, max_pages_per_seq};
+  const int ok = check_cache_fp8(c, cu_seqlens_q, total, B, Hkv, d, dtype);
+  if (ok != ATTN_OK) return ok;
+  if (B == 0 || total == 0) return ATTN_OK;
+  if (!k || !v || !seqlens_k) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(seqlens_k)) return ATTN_ERR_MISALIGNED;
+  const int dev_ok = check_device(k);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  return launch_cache_write_fp8(c, k, v, cu_seqlens_q, seqlens_k, total, B, Hkv, d,
+                                dtype == ATTN_BF16, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_read_fp8(const void* k_pages, const void* v_pages, const float* k_scales,
+                        const float* v_scales, const int32_t* block_table,
+                        const int32_t* cu_seqlens_k, int num_pages, int page_size,
+                        int max_pages_per_seq, void* k, void* v, int total, int B, int Hkv, int d,
+                        attn_dtype_t dtype, attn_stream_t stream) {
+  const CacheFp8 c{static_cast<uint8_t*>(const_cast<void*>(k_pages)),
+                   static_cast<uint8_t*>(const_cast<void*>(v_pages)),
+                   const_cast<float*>(k_scales), const_cast<float*>(v_scales), block_table,
+                   num_pages, page_size, max_pages_per_seq};
+  const int ok = check_cache_fp8(c, cu_seqlens_k, total, B, Hkv, d, dtype);
+  if (ok != ATTN_OK) return ok;
+  if (B == 0 || total == 0) return ATTN_OK;
+  if (!k || !v) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_MISALIGNED;
+  const int dev_ok = check_device(k);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  return launch_cache_read_fp8(c, k, v, cu_seqlens_k, total, B, Hkv, d, dtype == ATTN_BF16,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                          const float* k_scales, const float* v_scales,
+                          const int32_t* block_table, const int32_t* seqlens_k, int num_pages,
+                          int page_size, int max_pages_per_seq, int max_seqlen_k, void* o,
+                          float* lse, int B, int Hq, int Hkv, int d, int split_size, float scale,
+                          attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                          attn_stream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_seqlen_k < 0) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  const int pages_ok = check_pages(num_pages, page_size, max_pages_per_seq, max_seqlen_k);
+  if (pages_ok != ATTN_OK) return pages_ok;
+  if (split_size < 64 || split_size > 8192 || split_size % 64 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
+  if (B > kMaxDecodeBatch || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0) return ATTN_OK;
+  if (!q || !o || !lse || !block_table || !seqlens_k) return ATTN_ERR_INVALID_ARG;
+  if (max_seqlen_k > 0 && (num_pages == 0 || !k_pages || !v_pages || !k_scales || !v_scales))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned16(k_scales) || !aligned16(v_scales) || !aligned16(workspace) || !aligned4(lse) ||
+      !aligned4(block_table) || !aligned4(seqlens_k))
+    return ATTN_ERR_MISALIGNED;
+  const size_t need = decode_workspace_bytes(B, Hq, max_seqlen_k, split_size, d);
+  if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+  const int dev_ok = check_device(q);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  DecodeArgs a{q, nullptr, nullptr, nullptr, num_pages * page_size, max_seqlen_k, o, lse, B,
+               Hq, Hkv, d, split_size, scale, dtype == ATTN_BF16, workspace};
+  a.seqlens = seqlens_k;
+  const CacheFp8 c{static_cast<uint8_t*>(const_cast<void*>(k_pages)),
+                   static_cast<uint8_t*>(const_cast<void*>(v_pages)),
+                   const_cast<float*>(k_scales), const_cast<float*>(v_scales), block_table,
+                   num_pages, page_size, max_pages_per_seq};
+  return launch_attn_decode_fp8(a, c, reinterpret_cast<cudaStream_t>(stream));
+}
+
 size_t attn_decode_static_scratch_bytes(void) { return size_t(32) << 20; }
 
 int attn_poll_status(attn_stream_t stream) {
@@ -448,8 +633,8 @@ int attn_bwd_kv_order(int B, int Hq, int Hkv, int N_q, int N_kv, int causal, int
       cap < 0 || (cap > 0 && !job))
     return ATTN_ERR_INVALID_ARG;
   const int n_qtiles = (N_q + 127) / 128, n_kvtiles = (N_kv + 127) / 128;
-  *n = bwd_kv_order(B * Hkv, n_kvtiles, n_qtiles, Hq / Hkv, causal ? 1 : 0, N_kv - N_q, n_sm, job,
-                    cap);
+  *n = bwd_kv_order(B * Hkv, n_kvtiles, n_qtiles, Hq / Hkv, causal ? 1 : 0, N_kv - N_q, -1, 0, n_sm,
+                    job, cap);
   return ATTN_OK;
 }
 

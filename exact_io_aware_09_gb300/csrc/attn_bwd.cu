@@ -73,7 +73,21 @@ struct BwdParams {
   int Hq, Hkv, G, N_q, N_kv, n_qtiles, n_kvtiles, nqp, causal;
   float sl2;    // scale * log2(e)
   float scale;
+  int window, sinks;  // window variant: keys behind the diagonal, first keys always visible
 };
+
+// Window variant: the query tiles [qt_lo, qt_hi) that see key tile kt.  A tile with a sink is seen
+// from its diagonal to the last row, any other until the window has passed its last key.
+__host__ __device__ inline void window_q_tiles(int kt, int n_qtiles, int off, int window, int sinks,
+                                               int& qt_lo, int& qt_hi) {
+  const long long first = static_cast<long long>(kt) * 128 - off;
+  const long long last = first + 127 + window;
+  qt_lo = first > 0 ? static_cast<int>(first / 128) : 0;
+  if (qt_lo > n_qtiles) qt_lo = n_qtiles;
+  long long hi = last >= 0 ? last / 128 + 1 : 0;
+  if (static_cast<long long>(kt) * 128 < sinks || hi > n_qtiles) hi = n_qtiles;
+  qt_hi = hi > qt_lo ? static_cast<int>(hi) : qt_lo;
+}
 
 template <bool BF16>
 __device__ __forceinline__ float half_to_f32(uint32_t h) {
@@ -227,7 +241,7 @@ __device__ __forceinline__ void mma_tmem_rows_d(uint32_t d_tmem, uint32_t a_tmem
            (accumulate || kk > 0) ? 1u : 0u);
 }
 
-template <int D, bool BF16, int QS>
+template <int D, bool BF16, int QS, bool WINDOW>
 __global__ void __launch_bounds__(kKvThreads, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -275,7 +289,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     const int first_row = kt * kBT - off;  // first query row that sees key kt * 128
     qt_lo = first_row > 0 ? first_row / kBT : 0;
   }
-  const int nq_per = p.n_qtiles - qt_lo;  // query tiles per query head
+  int qt_hi = p.n_qtiles;
+  if constexpr (WINDOW) window_q_tiles(kt, p.n_qtiles, off, p.window, p.sinks, qt_lo, qt_hi);
+  const int nq_per = qt_hi - qt_lo;  // query tiles per query head
   const int n = nq_per > 0 ? p.G * nq_per : 0;
   const int n_steps = 2 * n;              // two 64-query steps per query tile
 
@@ -414,6 +430,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     const uint32_t row_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sl2 = p.sl2, scale = p.scale;
     const int q_first_visible = kr - off;  // the smallest query row that sees this key
+    // window variant: the largest
+    [[maybe_unused]] int q_last_visible = 0x7fffffff;
+    if constexpr (WINDOW) {
+      const long long last = static_cast<long long>(kr) - off + p.window;
+      if (kr >= p.sinks && last < q_last_visible) q_last_visible = static_cast<int>(last);
+    }
     const uint32_t s_col = L::kColS + wg * kStepQ, dp_col = L::kColDP + wg * kStepQ;
     bool ok = true;
     for (int i = wg; i < n_steps; i += 2) {
@@ -438,7 +460,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         tmem_ld32(row_tmem + s_col, sv[0]);
         tmem_ld32(row_tmem + s_col + 32, sv[1]);
         tmem_wait_ld();
-        const bool full = !p.causal || q0 >= q_first_visible;
+        const bool full =
+            WINDOW ? q0 >= q_first_visible && q0 + (kStepQ - 1) <= q_last_visible
+                   : !p.causal || q0 >= q_first_visible;
         const bool all_full = __all_sync(0xffffffffu, full);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -452,10 +476,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                  l4.w);
             if (!all_full) {
               const int rel = q_first_visible - (q0 + col);  // columns below rel precede the key
-              a0 = (0 >= rel) ? a0 : -INFINITY;
-              a1 = (1 >= rel) ? a1 : -INFINITY;
-              a2 = (2 >= rel) ? a2 : -INFINITY;
-              a3 = (3 >= rel) ? a3 : -INFINITY;
+              // ... and columns past rel_hi are past the window
+              const int rel_hi = WINDOW ? q_last_visible - (q0 + col) : 3;
+              a0 = (0 >= rel && 0 <= rel_hi) ? a0 : -INFINITY;
+              a1 = (1 >= rel && 1 <= rel_hi) ? a1 : -INFINITY;
+              a2 = (2 >= rel && 2 <= rel_hi) ? a2 : -INFINITY;
+              a3 = (3 >= rel && 3 <= rel_hi) ? a3 : -INFINITY;
             }
             pv[col] = ex2(a0);
             pv[col + 1] = ex2(a1);
@@ -609,7 +635,7 @@ __device__ __forceinline__ void row_to_tmem(uint32_t taddr, const uint4 (&w)[D /
   }
 }
 
-template <int D, bool BF16, int KR, int VR>
+template <int D, bool BF16, int KR, int VR, bool WINDOW>
 __global__ void __launch_bounds__(kQThreads, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
@@ -647,7 +673,20 @@ __global__ void __launch_bounds__(kQThreads, 1)
   const int bh = static_cast<int>(blockIdx.x) % n_bh;
   const int kv_plane = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / p.G;
   int n, first_masked;
-  kv_tile_range(qt, kBT, kBT, p.N_q, p.N_kv, p.causal, n, first_masked);
+  // window variant: the key tiles that hold sinks, then those of the window
+  [[maybe_unused]] int j_begin = 0, lo_masked = 0, sink_tiles = 0;
+  if constexpr (WINDOW) {
+    int j_end;
+    kv_tile_span(qt, kBT, kBT, p.N_q, p.N_kv, 1, p.window, j_begin, j_end, lo_masked, first_masked);
+    sink_tiles = min((p.sinks + kBT - 1) / kBT, j_begin);
+    n = sink_tiles + j_end - j_begin;
+  } else {
+    kv_tile_range(qt, kBT, kBT, p.N_q, p.N_kv, p.causal, n, first_masked);
+  }
+  auto key_tile = [&](int t) {  // key tile of step t
+    if constexpr (WINDOW) return t < sink_tiles ? t : j_begin + t - sink_tiles;
+    return t;
+  };
   // warpgroup 0 (thread = query row) starts loading the tile's Q rows now
   uint4 q_row[D / 8];
   if (n > 0 && threadIdx.x < kEwThreads) {
@@ -706,14 +745,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
 #pragma unroll
         for (int sub = 0; sub < D / 64; ++sub)
           tma_load_3d(base + L::kK + sk * L::kTile + sub * kSub, &tm_k, K_FULL(sk), sub * 64,
-                      t * kBT, kv_plane);
+                      key_tile(t) * kBT, kv_plane);
         issued_k = t + 1;
         if (t >= VR && !wait_bounded(V_EMPTY(sv), ((t / VR) - 1) & 1, abort_flag, p.status)) break;
         mbar_arrive_expect_tx(V_FULL(sv), L::kTile);
 #pragma unroll
         for (int sub = 0; sub < D / 64; ++sub)
           tma_load_3d(base + L::kV + sv * L::kTile + sub * kSub, &tm_v, V_FULL(sv), sub * 64,
-                      t * kBT, kv_plane);
+                      key_tile(t) * kBT, kv_plane);
         issued_v = t + 1;
       }
       wait_bounded(bar_do, 0, nullptr, p.status, kBwdDrainNs);
@@ -813,8 +852,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     const uint32_t s_col = L::kColS + c0, dp_col = L::kColDP + c0, ds_col = L::kColDS + wg * 32;
     for (int t = 0; t < n; ++t) {
-      const bool masked = t >= first_masked;
-      const int rel = lim - (t * kBT + c0);  // last visible key, relative to this half tile
+      const int j = key_tile(t);
+      const bool masked = WINDOW ? j >= first_masked || j < lo_masked : j >= first_masked;
+      const int rel = lim - (j * kBT + c0);  // last visible key, relative to this half tile
+      // window variant: the first key of the window and the last sink, likewise
+      [[maybe_unused]] int rel_lo = 0, rel_sink = 0;
+      if constexpr (WINDOW) {
+        const long long lo = static_cast<long long>(row) + (p.N_kv - p.N_q) - p.window;
+        rel_lo = static_cast<int>(lo > 0 ? lo : 0) - (j * kBT + c0);
+        rel_sink = min(p.sinks - 1 - (j * kBT + c0), rel);
+      }
       if (!ew_wait(bar_sfull, t & 1, abort_flag, p.status)) {
         ok = false;
         break;
@@ -837,8 +884,13 @@ __global__ void __launch_bounds__(kQThreads, 1)
           float a0, a1;
           fma2(a0, a1, __uint_as_float(sv[h][e]), __uint_as_float(sv[h][e + 1]), sl2, sl2, nl2, nl2);
           if (masked) {
-            a0 = (col <= rel) ? a0 : -INFINITY;
-            a1 = (col + 1 <= rel) ? a1 : -INFINITY;
+            if constexpr (WINDOW) {
+              a0 = ((col <= rel && col >= rel_lo) || col <= rel_sink) ? a0 : -INFINITY;
+              a1 = ((col + 1 <= rel && col + 1 >= rel_lo) || col + 1 <= rel_sink) ? a1 : -INFINITY;
+            } else {
+              a0 = (col <= rel) ? a0 : -INFINITY;
+              a1 = (col + 1 <= rel) ? a1 : -INFINITY;
+            }
           }
           pv[col] = ex2(a0);
           pv[col + 1] = ex2(a1);
@@ -919,8 +971,13 @@ size_t bwd_workspace_bytes(int B, int Hq, int N_q) {
 }
 
 // 64-query steps of the dK/dV job for key tile kt (as the kernel counts them).
-static int kv_job_steps(int kt, int n_qtiles, int G, int causal, int off) {
+static int kv_job_steps(int kt, int n_qtiles, int G, int causal, int off, int window, int sinks) {
   int qt_lo = 0;
+  if (window >= 0) {
+    int qt_hi;
+    window_q_tiles(kt, n_qtiles, off, window, sinks, qt_lo, qt_hi);
+    return 2 * G * (qt_hi - qt_lo);
+  }
   if (causal) {
     const int first_row = kt * kBT - off;
     qt_lo = first_row > 0 ? first_row / kBT : 0;
@@ -932,8 +989,8 @@ static int kv_job_steps(int kt, int n_qtiles, int G, int causal, int off) {
 // The packed dispatch order for a grid of n_planes x n_kvtiles jobs on n_sm SMs: writes the job
 // of every block to job[0 .. n) and returns n, or 0 when the default order stands (no causal
 // mask: equal jobs; no more jobs than SMs; more than `cap` jobs).
-int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, int off, int n_sm,
-                 uint16_t* job, int cap) {
+int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, int off, int window,
+                 int sinks, int n_sm, uint16_t* job, int cap) {
   const long long n_jobs_ll = static_cast<long long>(n_planes) * n_kvtiles;
   if (!causal || n_sm <= 0 || n_jobs_ll <= n_sm || n_jobs_ll > cap || n_jobs_ll > 65536) return 0;
   const int n_jobs = static_cast<int>(n_jobs_ll);
@@ -942,7 +999,7 @@ int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, i
   std::vector<long long> w(n_jobs);
   long long total = 0;
   for (int j = 0; j < n_jobs; ++j) {
-    w[j] = kv_job_steps(j / n_planes, n_qtiles, G, causal, off) + 4;
+    w[j] = kv_job_steps(j / n_planes, n_qtiles, G, causal, off, window, sinks) + 4;
     total += w[j];
   }
   std::vector<int> by_size(n_jobs);
@@ -995,28 +1052,28 @@ int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, i
 // The packed dispatch order (KvOrder) for one shape on the current device, computed once and
 // kept.
 static const KvOrder* kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal,
-                               int off) {
+                               int off, int window, int sinks) {
   static const KvOrder kDefault = {0, {}};
   int dev = 0, n_sm = 0;
   if (!causal || cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return &kDefault;
-  using Key = std::tuple<int, int, int, int, int, int>;
+  using Key = std::tuple<int, int, int, int, int, int, int, int>;
   static std::map<Key, std::unique_ptr<KvOrder>> cache;
   static std::mutex mu;
-  const Key key{n_planes, n_kvtiles, n_qtiles, G, off, n_sm};
+  const Key key{n_planes, n_kvtiles, n_qtiles, G, off, window, sinks, n_sm};
   std::lock_guard<std::mutex> lock(mu);
   auto it = cache.find(key);
   if (it != cache.end()) return it->second.get();
   auto order = std::make_unique<KvOrder>();
-  order->n = bwd_kv_order(n_planes, n_kvtiles, n_qtiles, G, causal, off, n_sm, order->job,
-                          kMaxKvOrder);
+  order->n = bwd_kv_order(n_planes, n_kvtiles, n_qtiles, G, causal, off, window, sinks, n_sm,
+                          order->job, kMaxKvOrder);
   const KvOrder* out = order.get();
   cache.emplace(key, std::move(order));
   return out;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WINDOW>
 static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   constexpr int QS = (D == 128) ? 4 : 6;  // 64-query stages of the dK/dV kernel
   constexpr int KR = (D == 128) ? 3 : 6;  // K slots of the dQ kernel
@@ -1060,13 +1117,15 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   p.causal = a.causal;
   p.scale = a.scale;
   p.sl2 = a.scale * 1.4426950408889634f;
+  p.window = a.window;
+  p.sinks = a.sinks;
   const long long rows = static_cast<long long>(bhq) * nqp;
   attn_bwd_pre_kernel<D, BF16><<<static_cast<unsigned>((rows * (D / 8) + 255) / 256), 256, 0, stream>>>(
       static_cast<const uint16_t*>(a.o), static_cast<const uint16_t*>(a.dout), a.lse,
       const_cast<float*>(p.lse2), const_cast<float*>(p.dvec), a.N_q, nqp, rows, a.scale);
   if (cudaGetLastError() != cudaSuccess) return -5;
-  auto kkv = attn_bwd_dkdv_kernel<D, BF16, QS>;
-  auto kq = attn_bwd_dq_kernel<D, BF16, KR, VR>;
+  auto kkv = attn_bwd_dkdv_kernel<D, BF16, QS, WINDOW>;
+  auto kq = attn_bwd_dq_kernel<D, BF16, KR, VR, WINDOW>;
   if (cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::kBytes) != cudaSuccess ||
       cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, LQ::kBytes) != cudaSuccess)
     return -5;
@@ -1074,7 +1133,7 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   const uint64_t q_blocks = bhq * n_qtiles;
   if (kv_blocks > 0x7fffffffull || q_blocks > 0x7fffffffull) return -2;
   const KvOrder* order = kv_order(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.causal,
-                                  a.N_kv - a.N_q);
+                                  a.N_kv - a.N_q, a.window, a.sinks);
   kkv<<<static_cast<unsigned>(kv_blocks), kKvThreads, LK::kBytes, stream>>>(tq64, tk, tv, tdo64, p,
                                                                             *order);
   if (cudaGetLastError() != cudaSuccess) return -5;
@@ -1094,10 +1153,21 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
 }
 
 int launch_attn_bwd(const BwdArgs& a, cudaStream_t stream) {
-  if (a.d == 64)
-    return a.bf16 ? launch_bwd_variant<64, true>(a, stream) : launch_bwd_variant<64, false>(a, stream);
-  if (a.d == 128)
-    return a.bf16 ? launch_bwd_variant<128, true>(a, stream) : launch_bwd_variant<128, false>(a, stream);
+  const bool w = a.window >= 0;
+  if (a.d == 64) {
+    if (a.bf16)
+      return w ? launch_bwd_variant<64, true, true>(a, stream)
+               : launch_bwd_variant<64, true, false>(a, stream);
+    return w ? launch_bwd_variant<64, false, true>(a, stream)
+             : launch_bwd_variant<64, false, false>(a, stream);
+  }
+  if (a.d == 128) {
+    if (a.bf16)
+      return w ? launch_bwd_variant<128, true, true>(a, stream)
+               : launch_bwd_variant<128, true, false>(a, stream);
+    return w ? launch_bwd_variant<128, false, true>(a, stream)
+             : launch_bwd_variant<128, false, false>(a, stream);
+  }
   return -2;
 }
 

@@ -28,30 +28,9 @@
 // two.
 #include <mutex>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "attn_decode.cuh"
 
 namespace attn {
-
-constexpr int kDecTok = 64;      // tokens per ring stage
-constexpr int kDecWarps = 4;     // compute warps, 16 tokens of each stage apiece
-constexpr int kDecThreads = 160;  // + one producer warp
-constexpr int kDecStages = 3;
-constexpr int kMaxGroup = 16;    // query heads per key/value head (rows of the m16 tile)
-
-struct DecParams {
-  const uint16_t* q;   // [B, Hq, D]
-  const int32_t* cu;   // [B + 1] (packed cache)
-  const int32_t* block_table;  // [B, max_pages] (paged cache) or null
-  const int32_t* seqlens;      // [B] (paged cache)
-  int page_size, page_log2, max_pages, num_pages;
-  int box_log2;        // log2 of the rows of one TMA box: min(page_size, 64); 64 when packed
-  float* ws_o;         // [B * Hq * max_splits, D]  normalised partial outputs
-  float* ws_ml;        // [B * Hq * max_splits, 2]  (m in log2 units, l)
-  int* status;
-  int Hq, Hkv, G, capacity, max_seqlen, split, max_splits;
-  float sl2;
-};
 
 template <int D>
 struct DecLayout {
@@ -68,31 +47,6 @@ struct DecLayout {
   static constexpr int kMaxSplitPages = 8192 / 16;
   static constexpr uint32_t kBytes = kPages + kMaxSplitPages * 4 + 1024;
 };
-
-__device__ __forceinline__ bool dec_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                              int* status) {
-  const bool ok = wait_bounded(bar, parity, abort, status);
-  return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ bool lengths_ok(const DecParams& p, int t_start, int t_stop) {
-  const int len = t_stop - t_start;
-  return t_start >= 0 && len >= 0 && len <= p.max_seqlen && t_stop <= p.capacity;
-}
-
-// Sequence b's tokens: rows [t_start, t_stop) of the packed cache, or logical positions
-// [0, seqlens[b]) of a paged one.  False for lengths the caller's bounds do not allow.
-__device__ __forceinline__ bool seq_bounds(const DecParams& p, int b, int& t_start, int& t_stop) {
-  if (p.block_table) {
-    t_start = 0;
-    t_stop = p.seqlens[b];
-    return t_stop >= 0 && t_stop <= p.max_seqlen &&
-           ((t_stop + p.page_size - 1) >> p.page_log2) <= p.max_pages;
-  }
-  t_start = p.cu[b];
-  t_stop = p.cu[b + 1];
-  return lengths_ok(p, t_start, t_stop);
-}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kDecThreads)
@@ -502,6 +456,37 @@ size_t decode_workspace_bytes(int B, int Hq, int max_seqlen, int split, int d) {
 }
 
 template <int D, bool BF16>
+static int launch_merge_variant(const DecParams& p, int B, void* o, float* lse,
+                                cudaStream_t stream) {
+  // The merge goes out as a programmatic dependent of the kernel before it (the split kernel,
+  // or whatever the stream ran last): its blocks are scheduled early and wait at their start
+  // (griddepcontrol.wait) until that grid has completed, which hides the launch gap.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.Hq, B);
+  cfg.blockDim = dim3(D);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_decode_merge_kernel<D, BF16>, p, static_cast<uint16_t*>(o),
+                         lse) != cudaSuccess)
+    return -5;
+  return cudaGetLastError() == cudaSuccess ? 0 : -5;
+}
+
+int launch_decode_merge(const DecParams& p, int d, bool bf16, int B, void* o, float* lse,
+                        cudaStream_t stream) {
+  if (d == 64)
+    return bf16 ? launch_merge_variant<64, true>(p, B, o, lse, stream)
+                : launch_merge_variant<64, false>(p, B, o, lse, stream);
+  return bf16 ? launch_merge_variant<128, true>(p, B, o, lse, stream)
+              : launch_merge_variant<128, false>(p, B, o, lse, stream);
+}
+
+template <int D, bool BF16>
 static int launch_decode_variant(const DecodeArgs& a, cudaStream_t stream) {
   using L = DecLayout<D>;
   const int max_splits = (a.max_seqlen + a.split - 1) / a.split;
@@ -555,23 +540,7 @@ static int launch_decode_variant(const DecodeArgs& a, cudaStream_t stream) {
     kern<<<grid, kDecThreads, L::kBytes, stream>>>(tk, tv, p);
     if (cudaGetLastError() != cudaSuccess) return -5;
   }
-  // The merge goes out as a programmatic dependent of the kernel before it (the split kernel,
-  // or whatever the stream ran last): its blocks are scheduled early and wait at their start
-  // (griddepcontrol.wait) until that grid has completed, which hides the launch gap.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.Hq, a.B);
-  cfg.blockDim = dim3(D);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_decode_merge_kernel<D, BF16>, p, static_cast<uint16_t*>(a.o),
-                         a.lse) != cudaSuccess)
-    return -5;
-  return cudaGetLastError() == cudaSuccess ? 0 : -5;
+  return launch_decode_merge(p, D, BF16, a.B, a.o, a.lse, stream);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -1,0 +1,211 @@
+// A chunk of new tokens of each sequence over a paged KV cache: causal attention of the last
+// positions of every sequence, with or without a sliding window and sinks.
+//
+// The prefill kernel (attn_fwd_kernel.cuh) runs it with three changes.  (1) A query tile's 128
+// rows are (token, query head) pairs of one key/value head, 128 / G tokens of the G heads that
+// share it, so that a tile reads each cache row once for all its heads and a chunk of a few
+// tokens still fills the tile: the number of products is that of one head per tile, the diagonal
+// takes G times fewer masked tiles.  (2) A 128-key tile comes in page by page, each page's TMA
+// copy issued by its own lane of the producer warp, with the block-table entries read one tile
+// ahead.  (3) When the chunks give fewer tiles than keep the SMs evenly busy, an item's key tiles
+// are split and the parts' normalised rows merged with the (m, l) rule by a second kernel.
+//
+// Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.
+#include "attn_fwd_kernel.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kSms = 152;       // SMs of a GB300, the split rule's unit
+constexpr int kUnitsPerSm = 4;  // work items per SM below which items are split
+constexpr int kMinSplitTiles = 4;
+
+struct PagedSplit {
+  int tile_tokens, n_qtiles, n_splits, split_tiles;
+};
+
+// How a call's work is cut.  An item is one query tile of one key/value head of a sequence; its
+// key tiles are cut so that about kUnitsPerSm items exist per SM.
+PagedSplit paged_split(int B, int Hq, int Hkv, int max_q, int max_k, int window, int sinks) {
+  PagedSplit s;
+  s.tile_tokens = kBlockM / (Hq / Hkv);
+  s.n_qtiles = (max_q + s.tile_tokens - 1) / s.tile_tokens;
+  long long tiles = (static_cast<long long>(max_k) + kBlockN - 1) / kBlockN;
+  if (window >= 0) {
+    const long long near = (static_cast<long long>(window) + s.tile_tokens) / kBlockN + 2 +
+                           (static_cast<long long>(sinks) + kBlockN - 1) / kBlockN;
+    if (near < tiles) tiles = near;
+  }
+  const long long items = static_cast<long long>(B) * Hkv * s.n_qtiles;
+  s.n_splits = 1;
+  s.split_tiles = static_cast<int>(tiles);
+  if (items > 0 && items < kSms * kUnitsPerSm && tiles > kMinSplitTiles) {
+    const long long want = (kSms * kUnitsPerSm + items - 1) / items;
+    long long per = (tiles + want - 1) / want;
+    if (per < kMinSplitTiles) per = kMinSplitTiles;
+    s.split_tiles = static_cast<int>(per);
+    s.n_splits = static_cast<int>((tiles + per - 1) / per);
+  }
+  return s;
+}
+
+size_t parts_o_bytes(size_t parts, int d) {
+  return (parts * d * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
+                             int sinks, int d) {
+  if (total_q <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > kBlockM ||
+      max_q <= 0 || max_k <= 0 || d <= 0)
+    return 0;
+  const PagedSplit s = paged_split(B, Hq, Hkv, max_q, max_k, window, sinks);
+  if (s.n_splits == 1) return 0;
+  const size_t parts = static_cast<size_t>(total_q) * Hq * s.n_splits;
+  return parts_o_bytes(parts, d) + parts * 8;
+}
+
+// One warp per row: the merge of its splits' (m, l, o).  A split without a visible key has
+// (m, l) = (-inf, 0) and no row of its own.  Rows outside the packed sequences are left alone.
+constexpr int kMergeWarps = 4;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    attn_paged_merge_kernel(const float* ws_o, const float* ws_ml, const int32_t* cu_q, int B,
+                            int Hq, size_t rows, int n_splits, uint16_t* out, float* lse) {
+  constexpr int kC = D / 32;  // channels per lane
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const size_t row = static_cast<size_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const size_t tok = row / Hq;
+  if (static_cast<long long>(tok) < cu_q[0] || static_cast<long long>(tok) >= cu_q[B]) return;
+  const float2* ml = reinterpret_cast<const float2*>(ws_ml) + row * n_splits;
+  float m = -INFINITY;
+  for (int s = lane; s < n_splits; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[kC] = {}, l = 0.0f;
+  for (int s0 = 0; s0 < n_splits; s0 += 32) {
+    float w_lane = 0.0f;
+    if (s0 + lane < n_splits) {
+      const float2 v = ml[s0 + lane];
+      w_lane = v.x == -INFINITY ? v.y : ex2(v.x - m) * v.y;
+    }
+    const int n = min(32, n_splits - s0);
+    for (int s = 0; s < n; ++s) {
+      const float w = __shfl_sync(0xffffffffu, w_lane, s);
+      if (w == 0.0f) continue;
+      l += w;
+      const float* src = ws_o + (row * n_splits + s0 + s) * D + lane * kC;
+      float v[kC];
+      if constexpr (kC == 4)
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+      else
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+      for (int c = 0; c < kC; ++c) acc[c] = fmaf(w, v[c], acc[c]);
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(out + row * D + lane * kC);
+#pragma unroll
+  for (int c = 0; c < kC; c += 2) dst[c / 2] = pack2<BF16>(acc[c] * inv, acc[c + 1] * inv);
+  if (lane == 0) lse[row] = l == 0.0f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+}
+
+template <int D, bool BF16, int KS, int VS>
+static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
+  using L = FwdLayout<D, KS, VS>;
+  const PagedSplit sp = paged_split(a.B, a.Hq, a.Hkv, a.max_q, a.max_k, a.window, a.sinks);
+  const int G = a.Hq / a.Hkv;
+  const uint64_t row = static_cast<uint64_t>(D) * 2;
+  const uint64_t tokens = static_cast<uint64_t>(a.num_pages) * a.page_size;
+  const uint32_t box = static_cast<uint32_t>(a.page_size < kBlockN ? a.page_size : kBlockN);
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_3d(&tq, a.q, BF16, D, a.Hq, a.total_q, row, row * a.Hq, 64, G, sp.tile_tokens) ||
+      !make_tmap_3d(&tk, a.k_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box) ||
+      !make_tmap_3d(&tv, a.v_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box))
+    return -5;
+  FwdParamsPaged p = {};
+  p.o = a.o;
+  p.lse = a.lse;
+  p.status = device_status_ptr();
+  if (!p.status) return -5;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.n_qtiles = sp.n_qtiles;
+  p.group = G;
+  p.causal = 1;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  const uint64_t planes = static_cast<uint64_t>(a.B) * a.Hkv;
+  if (planes > 0x7fffffffull) return -2;
+  p.BH = static_cast<int>(planes);
+  {
+    // planes whose cache fills about half of L2 walk their query tiles together
+    uint64_t group = (64ull << 20) / (2ull * a.max_k * D * 2);
+    if (group < 1) group = 1;
+    if (group > planes) group = planes;
+    p.head_group = static_cast<int>(group);
+  }
+  p.sl2 = a.scale * 1.4426950408889634f;
+  p.block_table = a.block_table;
+  p.cu_q = a.cu_q;
+  p.seqlens = a.seqlens;
+  while ((1 << p.page_log2) < a.page_size) ++p.page_log2;
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.total_q = a.total_q;
+  p.max_q = a.max_q;
+  p.max_k = a.max_k;
+  p.tile_tokens = sp.tile_tokens;
+  p.n_splits = sp.n_splits;
+  p.split_tiles = sp.split_tiles;
+  const size_t rows = static_cast<size_t>(a.total_q) * a.Hq;
+  if (sp.n_splits > 1) {
+    const size_t parts = rows * sp.n_splits;
+    p.ws_o = static_cast<float*>(a.workspace);
+    p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + parts_o_bytes(parts, D));
+  }
+  auto kern = attn_fwd_kernel<D, BF16, KS, VS, false, true, true>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
+      cudaSuccess)
+    return -5;
+  const uint64_t blocks = planes * sp.n_qtiles * sp.n_splits;
+  if (blocks > 0x7fffffffull) return -2;
+  kern<<<static_cast<unsigned>(blocks), kFwdThreads, L::kBytes, stream>>>(tq, tk, tv, tq, p);
+  if (cudaGetLastError() != cudaSuccess) return -5;
+  if (sp.n_splits == 1) return 0;
+  const uint64_t merge_blocks = (rows + kMergeWarps - 1) / kMergeWarps;
+  if (merge_blocks > 0x7fffffffull) return -2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(merge_blocks));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<D, BF16>,
+                         static_cast<const float*>(p.ws_o), static_cast<const float*>(p.ws_ml),
+                         a.cu_q, a.B, a.Hq, rows, sp.n_splits, static_cast<uint16_t*>(a.o),
+                         a.lse) != cudaSuccess)
+    return -5;
+  return cudaGetLastError() == cudaSuccess ? 0 : -5;
+}
+
+int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
+  if (a.d == 64)
+    return a.bf16 ? launch_paged_variant<64, true, 4, 4>(a, stream)
+                  : launch_paged_variant<64, false, 4, 4>(a, stream);
+  if (a.d == 128)
+    return a.bf16 ? launch_paged_variant<128, true, 3, 2>(a, stream)
+                  : launch_paged_variant<128, false, 3, 2>(a, stream);
+  return -2;
+}
+
+}  // namespace attn

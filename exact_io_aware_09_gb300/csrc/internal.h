@@ -20,7 +20,7 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t dim0, 
 bool make_tmap_4d(CUtensorMap* map, const void* base, bool bf16, const uint64_t dims[4],
                   const uint64_t strides[3], const uint32_t box[4]);
 
-// The same over a contiguous 8-bit tensor (E4M3 codes).
+// The same over an 8-bit tensor (E4M3 codes); rows of a 64-byte box take the 64-byte swizzle.
 bool make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t dim1,
                      uint64_t dim2, uint64_t stride1, uint64_t stride2, uint32_t box0,
                      uint32_t box1, uint32_t box2);
@@ -111,6 +111,24 @@ struct FwdArgs {
   const float* k_scale = nullptr;
   const float* v_scale = nullptr;
   int nkvp = 0;
+  int sinks = 0;  // with a window: the first keys that stay visible outside it
+};
+
+// A chunk of new tokens of each sequence over a paged 16-bit cache.
+struct PagedArgs {
+  const void* q;        // [total_q, Hq, d]
+  const void* k_pages;  // [num_pages, page_size, Hkv, d]
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* cu_q;
+  const int32_t* seqlens;
+  int num_pages, page_size, max_pages, total_q, max_q, max_k;
+  void* o;
+  float* lse;
+  int B, Hq, Hkv, d, window, sinks;
+  float scale;
+  bool bf16;
+  void* workspace;
 };
 
 struct DecodeArgs {
@@ -147,6 +165,8 @@ struct BwdArgs {
   float scale;
   bool bf16;
   void* workspace;
+  int window = -1;  // sliding window (keys behind the diagonal); -1 = none
+  int sinks = 0;    // with a window: the first keys that stay visible outside it
 };
 
 // Launchers (return an attn_status_t value).
@@ -162,6 +182,26 @@ int launch_attn_fwd_fp8(const FwdArgs& a, const int8_t* signs, void* workspace,
                         cudaStream_t stream);
 size_t fp8_workspace_layout(int B, int Hq, int Hkv, int N_q, int N_kv, int d, size_t off[7]);
 int launch_attn_decode(const DecodeArgs& a, cudaStream_t stream);
+// A quantised paged cache: E4M3 codes [num_pages, page_size, Hkv, d] and power-of-two scales
+// [num_pages, Hkv, page_size].
+struct CacheFp8 {
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* block_table;
+  int num_pages, page_size, max_pages;
+};
+// New tokens k, v [total, Hkv, d] into the cache / cached tokens back out of it.
+int launch_cache_write_fp8(const CacheFp8& c, const void* k, const void* v, const int32_t* cu_q,
+                           const int32_t* seqlens, int total, int B, int Hkv, int d, bool bf16,
+                           cudaStream_t stream);
+int launch_cache_read_fp8(const CacheFp8& c, void* k, void* v, const int32_t* cu_k, int total,
+                          int B, int Hkv, int d, bool bf16, cudaStream_t stream);
+int launch_attn_decode_fp8(const DecodeArgs& a, const CacheFp8& c, cudaStream_t stream);
+int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream);
+size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
+                             int sinks, int d);
 int launch_attn_bwd(const BwdArgs& a, cudaStream_t stream);
 size_t bwd_workspace_bytes(int B, int Hq, int N_q);
 size_t decode_workspace_bytes(int B, int Hq, int max_seqlen, int split, int d);

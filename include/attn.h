@@ -172,6 +172,41 @@ int attn_fwd_window(const void *q, const void *k, const void *v, void *o, float 
                     attn_stream_t stream, attn_dtype_t dtype);
 
 /*
+ * attn_fwd_window_sinks -- the sliding window with a few first keys that stay visible to every
+ * later row (attention sinks; no counterpart on the pages).
+ *
+ * Arguments as attn_fwd_window, plus
+ *   sinks    s >= 0: key j is visible to query row i, p = i + N_kv - N_q, iff j <= p and
+ *            (p - j <= W or j < s); s = 0 is attn_fwd_window
+ * Key tiles between the sinks and the window are neither loaded nor computed.  A NaN or infinite
+ * score of a masked key does not reach a row (its value row does where it shares a 128-key tile
+ * with a visible key, as 0 times a NaN does in the definition).  A row with no visible key gets
+ * O = 0, L = -inf.  Returns ATTN_OK, ATTN_ERR_INVALID_ARG (W < 0, s < 0) or another attn_status_t.
+ */
+int attn_fwd_window_sinks(const void *q, const void *k, const void *v, void *o, float *lse, int B,
+                          int Hq, int Hkv, int N_q, int N_kv, int d, int window, int sinks,
+                          float scale, attn_stream_t stream, attn_dtype_t dtype);
+
+/*
+ * attn_bwd_window_sinks_workspace_bytes -- bytes of the workspace attn_bwd_window_sinks needs
+ * (0 for invalid arguments).
+ */
+size_t attn_bwd_window_sinks_workspace_bytes(int B, int Hq, int Hkv, int N_q, int N_kv, int d,
+                                             int window, int sinks);
+
+/*
+ * attn_bwd_window_sinks -- gradients of attn_fwd_window_sinks (and, with sinks = 0, of
+ * attn_fwd_window): attn_bwd's formulas under that mask.  Arguments as attn_bwd with `causal`
+ * replaced by window and sinks, and the workspace of attn_bwd_window_sinks_workspace_bytes.
+ * Tiles no row sees are neither loaded nor computed.  Deterministic: no atomics.
+ */
+int attn_bwd_window_sinks(const void *q, const void *k, const void *v, const void *o,
+                          const void *dout, const float *lse, void *dq, void *dk, void *dv, int B,
+                          int Hq, int Hkv, int N_q, int N_kv, int d, int window, int sinks,
+                          float scale, attn_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                          attn_stream_t stream);
+
+/*
  * attn_fwd_block_sparse -- prefill attention restricted to a pattern of (query tile, key
  * tile) blocks ("FlashAttention, annotated", section 3.3, block-sparse FlashAttention: a fixed
  * pattern of tiles to compute and skip; the BlockMask of "FlashAttention Explained", one
@@ -301,6 +336,102 @@ int attn_decode_paged(const void *q, const void *k_pages, const void *v_pages,
                       int B, int Hq, int Hkv, int d, int split_size, float scale,
                       attn_dtype_t dtype, void *workspace, size_t workspace_bytes,
                       attn_stream_t stream);
+
+/*
+ * attn_fwd_paged_workspace_bytes -- bytes of the workspace attn_fwd_paged needs: partial states of
+ * the key splits a call with few query tiles is cut into; 0 when the call is not split (the
+ * workspace may then be null) and for invalid arguments.
+ */
+size_t attn_fwd_paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_seqlen_q,
+                                      int max_seqlen_k, int window, int sinks, int d);
+
+/*
+ * attn_fwd_paged -- a chunk of new tokens of each sequence over its paged KV cache (chunked
+ * prefill, draft verification, or one token each), causal, optionally under a sliding window with
+ * sinks.  The new tokens' keys and values are in the cache already: they are its last rows.
+ *
+ *   q             [total_q, Hq, d] device, contiguous: the new tokens, packed; sequence b's are rows
+ *                 cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 and stand at the cache positions
+ *                 seqlens_k[b] - n_b .. seqlens_k[b] - 1, n_b = cu_seqlens_q[b+1] - cu_seqlens_q[b]
+ *   k_pages, v_pages, block_table, num_pages, page_size, max_pages_per_seq
+ *                 as attn_decode_paged; rows of a page past the sequence's end are not used
+ *   cu_seqlens_q  [B + 1] int32 device, non-decreasing
+ *   seqlens_k     [B] int32 device: cached tokens, the new ones included
+ *   max_seqlen_q, max_seqlen_k   upper bounds of n_b and seqlens_k (max_seqlen_k >= max_seqlen_q,
+ *                 <= max_pages_per_seq * page_size); they size the grid and the workspace
+ *   o             [total_q, Hq, d] out;  lse [total_q, Hq] out, fp32 (natural log)
+ *   window, sinks the token at position p sees key j iff j <= p and (window == -1 or
+ *                 p - j <= window or j < sinks); sinks without a window change nothing
+ *   Query head h reads key/value head h / (Hq / Hkv); Hq / Hkv <= 128.
+ *   workspace     device scratch of attn_fwd_paged_workspace_bytes(...) bytes, caller-owned, its
+ *                 contents need no initialisation; calls that share it must not overlap
+ * A sequence may have no new tokens.  Rows of o and lse outside cu_seqlens_q[0] .. cu_seqlens_q[B]-1
+ * are left as they were.  Lengths past their bounds (n_b > seqlens_k[b] among them) and block-table
+ * entries outside [0, num_pages) are reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status (that
+ * sequence's output is then undefined).  Returns ATTN_OK or a negative attn_status_t.
+ */
+int attn_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
+                   const int32_t *block_table, const int32_t *cu_seqlens_q,
+                   const int32_t *seqlens_k, int num_pages, int page_size, int max_pages_per_seq,
+                   int total_q, int max_seqlen_q, int max_seqlen_k, void *o, float *lse, int B,
+                   int Hq, int Hkv, int d, int window, int sinks, float scale, attn_dtype_t dtype,
+                   void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * attn_cache_write_fp8 -- new tokens into a paged KV cache held in 8 bits.
+ *
+ *   k, v          [total, Hkv, d] device, contiguous, `dtype`: the new tokens, packed; sequence b's
+ *                 are rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 and go to the cache positions
+ *                 seqlens_k[b] - n_b .. seqlens_k[b] - 1
+ *   k_pages, v_pages    [num_pages, page_size, Hkv, d] device: E4M3 codes
+ *   k_scales, v_scales  [num_pages, Hkv, page_size] device, fp32: each row's scale
+ *   block_table, num_pages, page_size, max_pages_per_seq   as attn_decode_paged
+ *   seqlens_k     [B] int32 device: cached tokens, the new ones included
+ * A row (one token of one head) is stored with the scale 2^e, e the smallest integer >= -126 with
+ * max |x| <= 448 * 2^e over the row's finite values (e = 0 for a zero row), as the codes
+ * E4M3(x 2^-e), nearest even; a value that is not finite becomes the NaN code.  Only the new
+ * tokens' rows and scales are written.  A position outside the table or a block-table entry outside
+ * the pool is reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status and not written.  Two tokens
+ * must not share a slot.  d in {64, 128}.  Returns ATTN_OK or a negative attn_status_t.
+ */
+int attn_cache_write_fp8(const void *k, const void *v, void *k_pages, void *v_pages,
+                         float *k_scales, float *v_scales, const int32_t *block_table,
+                         const int32_t *cu_seqlens_q, const int32_t *seqlens_k, int num_pages,
+                         int page_size, int max_pages_per_seq, int total, int B, int Hkv, int d,
+                         attn_dtype_t dtype, attn_stream_t stream);
+
+/*
+ * attn_cache_read_fp8 -- the first tokens of each sequence of a quantised cache as the packed
+ * 16-bit cache attn_decode_splitkv takes.
+ *
+ *   cu_seqlens_k  [B + 1] int32 device: sequence b's tokens 0 .. cu[b+1]-cu[b]-1 go to the rows
+ *                 cu[b] .. cu[b+1]-1 of k and v
+ *   k, v          [total, Hkv, d] out, `dtype`: code times scale, rounded to the type (exact unless
+ *                 it falls into the type's subnormals) and saturated at its largest finite value
+ *   the cache     as attn_cache_write_fp8
+ * Rows outside cu_seqlens_k[0] .. cu_seqlens_k[B]-1 are left as they were.  Bad positions and
+ * block-table entries are reported as there, and their rows not written.
+ */
+int attn_cache_read_fp8(const void *k_pages, const void *v_pages, const float *k_scales,
+                        const float *v_scales, const int32_t *block_table,
+                        const int32_t *cu_seqlens_k, int num_pages, int page_size,
+                        int max_pages_per_seq, void *k, void *v, int total, int B, int Hkv, int d,
+                        attn_dtype_t dtype, attn_stream_t stream);
+
+/*
+ * attn_decode_paged_fp8 -- attn_decode_paged over a quantised cache: keys and values are code times
+ * scale, read as attn_cache_write_fp8 stores them (the scales powers of two; V's from 2^-126 to
+ * 2^94).  Arguments as attn_decode_paged with the two scale arrays added; q, o in `dtype`.  Both
+ * products take the codes as they are (exact in fp16); a bf16 query is scaled by a power of two
+ * per row and rounded to fp16, the weights are rounded to fp16, sums are fp32.
+ */
+int attn_decode_paged_fp8(const void *q, const void *k_pages, const void *v_pages,
+                          const float *k_scales, const float *v_scales,
+                          const int32_t *block_table, const int32_t *seqlens_k, int num_pages,
+                          int page_size, int max_pages_per_seq, int max_seqlen_k, void *o,
+                          float *lse, int B, int Hq, int Hkv, int d, int split_size, float scale,
+                          attn_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                          attn_stream_t stream);
 
 /* attn_decode_static_scratch_bytes -- size of the scratch attn_decode_splitkv_static uses. */
 size_t attn_decode_static_scratch_bytes(void);

@@ -38,7 +38,7 @@ two D's."""
 
 
 def _head_backward(q, k, v, do, causal, scale, window=None, stored_dtype=None, unit=None,
-                   tiny=0.0):
+                   tiny=0.0, sinks=0):
     """One head, fp64 arrays q [Nq, d], k/v [Nkv, d], do [Nq, d] -> (dq, dk, dv, o, lse).
     stored_dtype: round O to this storage type before forming D (None: exact O).
     unit: if given, also return the rounding scales described below for this unit roundoff
@@ -51,7 +51,7 @@ def _head_backward(q, k, v, do, causal, scale, window=None, stored_dtype=None, u
     if causal or window is not None:
         vis = j <= i
         if window is not None:
-            vis &= (i - j) <= window
+            vis &= ((i - j) <= window) | (j < sinks)
         s = np.where(vis, s, -np.inf)
     m = s.max(axis=1, keepdims=True) if Nkv else np.full((Nq, 1), -np.inf)
     live = np.isfinite(m[:, 0])
@@ -121,10 +121,11 @@ def _head_backward(q, k, v, do, causal, scale, window=None, stored_dtype=None, u
 
 
 def attention_backward(q, k, v, do, dtype, B, Hq, Hkv, Nq, Nkv, d, causal, scale,
-                       window=None, heads=None, exact_o=False, error_scales=False):
+                       window=None, heads=None, exact_o=False, error_scales=False, sinks=0):
     """Gradients of every (or the listed) query head.
 
     q, do: uint16 storage bits [B, Hq, Nq, d]; k, v: [B, Hkv, Nkv, d].
+    window, sinks: sliding window and the first keys that stay visible outside it.
     heads: optional list of flat query heads b * Hq + h to compute (their key/value head's dK
     and dV then hold only those query heads' contributions).
     exact_o: form D from the exact fp64 O (the exact gradient) instead of O rounded to the
@@ -157,7 +158,7 @@ def attention_backward(q, k, v, do, dtype, B, Hq, Hkv, Nq, Nkv, d, causal, scale
         b, h = divmod(int(bh), Hq)
         hk = h // G
         res = _head_backward(qd[b, h], kd[b, hk], vd[b, hk], dod[b, h], causal, scale, window,
-                             None if exact_o else dtype, unit, tiny)
+                             None if exact_o else dtype, unit, tiny, sinks)
         gq, gk, gv, go, gl = res[:5]
         dq[b, h], o[b, h], lse[b, h] = gq, go, gl
         dk[b, hk] += gk

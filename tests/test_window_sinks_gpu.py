@@ -1,0 +1,263 @@
+"""GPU parity of the sliding window with sinks, forward and backward, against fp64 definitions.
+
+attn_fwd_window_sinks: key j visible to row i, p = i + N_kv - N_q, iff j <= p and (p - j <= W or
+j < s).  The forward tolerance is derived in oracle/chunk.py (row_tolerance), the gradients' in
+oracle/backward.py (error_scales); the gradients are also tested against differences of the
+forward definition.  Shapes cover sinks inside one key tile, across tiles, reaching into the window
+and past the sequence, rows without keys, one row, ragged ends, grouped heads and more work items
+than SMs.
+"""
+import numpy as np
+import pytest
+
+import synthetic as syn
+from oracle import bits_to_double, chunk
+from oracle.backward import attention_backward
+from parity import check_grad
+
+pytestmark = pytest.mark.gpu
+
+EPS = {"bf16": 2.0 ** -7, "f16": 2.0 ** -10}
+TINY = {"bf16": 2.0 ** -133, "f16": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def attn():
+    import exact_io_aware_09_gb300 as m
+
+    return m
+
+
+CASES = [
+    # (B, Hq, Hkv, N_q, N_kv, d, dtype), W, sinks
+    ((1, 2, 1, 1, 1, 64, "f16"), 0, 1),
+    ((1, 2, 2, 300, 300, 64, "bf16"), 0, 4),
+    ((1, 2, 1, 700, 700, 128, "f16"), 100, 1),
+    ((2, 4, 2, 200, 933, 64, "bf16"), 100, 128),    # a whole sink tile, N_kv > N_q
+    ((1, 2, 2, 900, 900, 128, "bf16"), 128, 130),   # sinks across two tiles
+    ((1, 3, 1, 1017, 1017, 128, "f16"), 300, 500),  # sinks reach into the window of early rows
+    ((1, 2, 2, 400, 100, 64, "f16"), 50, 7),        # N_kv < N_q: top rows see no key
+    ((1, 2, 1, 1, 777, 128, "bf16"), 200, 4),       # one row
+    ((1, 2, 2, 600, 600, 128, "bf16"), 5000, 9),    # wider than the sequence: causal
+    ((1, 2, 2, 500, 500, 64, "bf16"), 30, 9999),    # every key a sink: causal
+    ((2, 96, 8, 520, 520, 128, "bf16"), 127, 4),    # more items than SMs
+    ((2, 30, 6, 777, 777, 64, "f16"), 200, 64),
+]
+ids = lambda x: str(x)
+
+
+def _inputs(shape, seed):
+    B, Hq, Hkv, Nq, Nkv, d, dt = shape
+    cfg = syn.PrefillConfig("sinks", B, Hq, Hkv, Nq, Nkv, d, dt, True, seed)
+    return cfg, cfg.host_inputs()
+
+
+def _oracle(cfg, q, k, v, W, s):
+    q, k, v = (bits_to_double(x, cfg.dtype) for x in (q, k, v))
+    pos = np.arange(cfg.N_q) + cfg.N_kv - cfg.N_q
+    G = cfg.Hq // cfg.Hkv
+    heads = [chunk.attend(q[b, h], k[b, h // G], v[b, h // G], pos, cfg.scale, W, s)
+             for b in range(cfg.B) for h in range(cfg.Hq)]
+    return chunk.Rows(*(np.stack(x) for x in zip(*heads)))
+
+
+def _check(cfg, o, lse, rows, what):
+    e = EPS[cfg.dtype]
+    tol = chunk.row_tolerance(rows, e, e, TINY[cfg.dtype])
+    chunk.check(o.float().cpu().numpy().reshape(rows.o.shape),
+                lse.cpu().numpy().reshape(rows.lse.shape), rows, tol, what)
+
+
+@pytest.mark.parametrize("shape,W,s", CASES, ids=ids)
+def test_forward(attn, shape, W, s):
+    import torch
+
+    cfg, (q, k, v) = _inputs(shape, 900 + W + s + sum(shape[:6]))
+    qt, kt, vt = (syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v))
+    o = torch.full_like(qt, float("nan"))
+    lse = torch.full(qt.shape[:3], float("nan"), device="cuda")
+    attn.attn_fwd_window_sinks(qt, kt, vt, W, s, o=o, lse=lse, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    _check(cfg, o, lse, _oracle(cfg, q, k, v, W, s), f"{shape} W={W} sinks={s}")
+
+
+@pytest.mark.parametrize("shape,W,s", CASES, ids=ids)
+def test_backward(attn, shape, W, s):
+    import torch
+
+    cfg, (q, k, v) = _inputs(shape, 1300 + W + s + sum(shape[:6]))
+    do = syn.host_normal_bits(q.shape, 77 + s, cfg.dtype)
+    qt, kt, vt, dot = (syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v, do))
+    o, lse = attn.attn_fwd_window_sinks(qt, kt, vt, W, s, scale=cfg.scale)
+    nan = lambda t: torch.full_like(t, float("nan"))
+    got = attn.attn_bwd_window_sinks(qt, kt, vt, o, dot, lse, W, s, scale=cfg.scale, dq=nan(qt),
+                                     dk=nan(kt), dv=nan(vt))
+    assert attn.attn_poll_status() == 0
+    r = attention_backward(q, k, v, do, cfg.dtype, cfg.B, cfg.Hq, cfg.Hkv, cfg.N_q, cfg.N_kv, cfg.d,
+                           True, cfg.scale, window=W, sinks=s, error_scales=True)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        check_grad(name, got[i].float().cpu().numpy(), r[i], r[5].row[i], r[5].elem[i], cfg.dtype,
+                   f"{shape} W={W} sinks={s}")
+    again = attn.attn_bwd_window_sinks(qt, kt, vt, o, dot, lse, W, s, scale=cfg.scale)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+def test_gradient_against_differences(attn):
+    """The directional derivative of sum(do * o) along random directions, by central differences of
+    the fp64 definition, against the GPU gradients: each gradient g lies within the row scales'
+    norms of the exact one, so <g, u> lies within their product with |u|."""
+    W, s = 40, 3
+    cfg, (q, k, v) = _inputs((1, 2, 1, 150, 150, 64, "f16"), 5)
+    do = syn.host_normal_bits(q.shape, 6, cfg.dtype)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v, do)]
+    o, lse = attn.attn_fwd_window_sinks(*t[:3], W, s, scale=cfg.scale)
+    grads = attn.attn_bwd_window_sinks(*t[:3], o, t[3], lse, W, s, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    r = attention_backward(q, k, v, do, cfg.dtype, 1, 2, 1, 150, 150, 64, True, cfg.scale, window=W,
+                           sinks=s, error_scales=True)
+    x = [bits_to_double(b, cfg.dtype) for b in (q, k, v)]
+    dod = bits_to_double(do, cfg.dtype)
+    pos = np.arange(150)
+
+    def loss(q_, k_, v_):
+        return sum(float((dod[0, h] * chunk.attend(q_[0, h], k_[0, 0], v_[0, 0], pos, cfg.scale, W,
+                                                   s).o).sum()) for h in range(2))
+
+    rng = np.random.default_rng(3)
+    for i in range(3):
+        u = rng.standard_normal(x[i].shape)
+        step = 2.0 ** -14
+        args = lambda sign: [x[n] + sign * step * u if n == i else x[n] for n in range(3)]
+        slope = (loss(*args(1.0)) - loss(*args(-1.0))) / (2.0 * step)
+        g = grads[i].double().cpu().numpy()
+        err = 2.0 * r[5].row[i] + 1e-2 * np.linalg.norm(r[i], axis=-1) + 1e-6
+        # the differences' own error: step^2 times the third derivative, below 1e-3 here
+        assert abs(float((g * u).sum()) - slope) <= float((err * np.linalg.norm(u, axis=-1)).sum()) + 1e-3
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_no_sinks_is_the_window(attn, d):
+    import torch
+
+    cfg, (q, k, v) = _inputs((1, 4, 2, 600, 600, d, "bf16"), 21)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v)]
+    a = attn.attn_fwd_window(*t, 200, scale=cfg.scale)
+    b = attn.attn_fwd_window_sinks(*t, 200, 0, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_wide_window_backward_is_the_causal_one(attn, d):
+    import torch
+
+    cfg, (q, k, v) = _inputs((1, 4, 2, 600, 600, d, "bf16"), 22)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v)]
+    do = torch.randn_like(t[0])
+    o, lse = attn.attn_fwd(*t, causal=True, scale=cfg.scale)
+    a = attn.attn_bwd(*t, o, do, lse, causal=True, scale=cfg.scale)
+    b = attn.attn_bwd_window_sinks(*t, o, do, lse, 2 ** 31 - 1, 0, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("nq,nkv", [(0, 300), (300, 0)], ids=["no_queries", "no_keys"])
+def test_empty_side(attn, nq, nkv):
+    import torch
+
+    q = torch.randn((2, 4, nq, 64), device="cuda").half()
+    k = torch.randn((2, 2, nkv, 64), device="cuda").half()
+    o, lse = attn.attn_fwd_window_sinks(q, k, k, 10, 4)
+    grads = attn.attn_bwd_window_sinks(q, k, k, o, q, lse, 10, 4)
+    assert attn.attn_poll_status() == 0
+    assert not o.any() and torch.isneginf(lse).all() and not any(g.any() for g in grads)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_masked_scores_that_are_not_finite(attn, d):
+    """Keys outside every row's mask share tiles with visible ones and give infinite and NaN scores:
+    the rows are those of finite keys in their place.  Their values stay finite."""
+    import torch
+
+    W, s = 70, 5
+    cfg, (q, k, v) = _inputs((1, 2, 1, 100, 900, d, "bf16"), 31)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v)]
+    a = attn.attn_fwd_window_sinks(*t, W, s, scale=cfg.scale)
+    pos0 = 800  # row 0 sees keys 0-4 and 730-800
+    t[1][:, :, s:pos0 - W] = float("nan")
+    t[1][:, :, s + 1:pos0 - W:3] = float("inf")
+    b = attn.attn_fwd_window_sinks(*t, W, s, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("shape,W,s", [((1, 64, 8, 8192, 8192, 128, "bf16"), 1024, 4)], ids=ids)
+def test_full_size(attn, shape, W, s):
+    """The long grouped-query prefill under the 1024-key window, and its gradients: the eight query
+    heads of one key/value head."""
+    cfg, (q, k, v) = _inputs(shape, 4001)
+    do = syn.host_normal_bits(q.shape, 4002, cfg.dtype)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v, do)]
+    o, lse = attn.attn_fwd_window_sinks(*t[:3], W, s, scale=cfg.scale)
+    got = attn.attn_bwd_window_sinks(*t[:3], o, t[3], lse, W, s, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    hk = 5
+    qs = slice(hk * 8, hk * 8 + 8)
+    part = [np.ascontiguousarray(x) for x in (q[:, qs], k[:, hk:hk + 1], v[:, hk:hk + 1], do[:, qs])]
+    r = attention_backward(*part, cfg.dtype, 1, 8, 1, 8192, 8192, 128, True, cfg.scale, window=W,
+                           sinks=s, error_scales=True)
+    for i, (name, g) in enumerate(zip(("dq", "dk", "dv"), got)):
+        g = g[:, qs] if i == 0 else g[:, hk:hk + 1]
+        check_grad(name, g.float().cpu().numpy(), r[i], r[5].row[i], r[5].elem[i], cfg.dtype, "8192")
+    sub = syn.PrefillConfig("one", 1, 2, 1, 8192, 8192, 128, "bf16", True, 0)
+    rows = _oracle(sub, part[0][:, :2], part[1], part[2], W, s)
+    _check(cfg, o[:, qs][:, :2], lse[:, qs][:, :2], rows, "8192")
+
+
+def test_two_streams_and_a_graph(attn):
+    """Calls on a side stream, captured and replayed on new inputs: the same bits as eager calls."""
+    import torch
+
+    cfg, (q, k, v) = _inputs((1, 4, 2, 500, 500, 128, "bf16"), 41)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v)]
+    do = torch.randn_like(t[0])
+
+    def step():
+        o, lse = attn.attn_fwd_window_sinks(*t, 100, 4)
+        return (o, lse, *attn.attn_bwd_window_sinks(*t, o, do, lse, 100, 4))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        first = step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(first, out))
+    t[0].copy_(torch.randn_like(t[0]))
+    graph.replay()
+    want = step()
+    assert attn.attn_poll_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(want, out))
+
+
+def test_refusals(attn):
+    import torch
+
+    q = torch.zeros((1, 2, 128, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((1, 2, 128), device="cuda")
+    for W, s in ((-1, 4), (10, -1)):
+        with pytest.raises(attn.AttnError):
+            attn.attn_fwd_window_sinks(q, q, q, W, s)
+        with pytest.raises(attn.AttnError):
+            attn.attn_bwd_window_sinks(q, q, q, q, q, lse, W, s)
+    with pytest.raises(attn.AttnError):
+        attn.attn_bwd_window_sinks(q, q, q, q, q.half(), lse, 10, 4)
+    with pytest.raises(attn.AttnError):
+        attn.attn_bwd_window_sinks(q, q, q, q, q, lse[:, :, :5], 10, 4)
+    with pytest.raises(attn.AttnError):
+        attn.attn_bwd_window_sinks(q, q, q, q, q, lse, 10, 4,
+                                   workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
