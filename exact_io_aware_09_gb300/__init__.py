@@ -7,6 +7,7 @@ library is missing the import fails, and an unsupported request raises ``AttnErr
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -16,7 +17,8 @@ __all__ = [
     "attn_fwd_fp8_workspace_bytes", "attn_fwd_fp8_workspace_offsets",
     "attn_fwd_window_sinks", "attn_bwd_window_sinks", "attn_bwd_window_sinks_workspace_bytes",
     "attn_fwd_paged", "attn_fwd_paged_workspace_bytes",
-    "attn_cache_write_fp8", "attn_cache_read_fp8", "attn_decode_paged_fp8",
+    "attn_cache_write_fp8", "attn_cache_read_fp8",
+    "attn_decode_paged_fp8", "attn_decode_paged_fp8_workspace_bytes",
     "attn_bwd", "attn_bwd_workspace_bytes",
     "attn_decode_splitkv", "attn_decode_workspace_bytes", "attn_decode_paged",
     "attn_decode_splitkv_static", "attn_decode_static_scratch_bytes",
@@ -73,6 +75,8 @@ lib.attn_cache_read_fp8.restype = _I
 lib.attn_decode_paged_fp8.argtypes = [_P] * 7 + [_I] * 4 + [_P, _P] + [_I] * 5 + [_F, _I, _P, _SZ,
                                                                               _P]
 lib.attn_decode_paged_fp8.restype = _I
+lib.attn_decode_paged_fp8_workspace_bytes.argtypes = [_I] * 6
+lib.attn_decode_paged_fp8_workspace_bytes.restype = _SZ
 lib.attn_fwd_block_sparse.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _F, _P,
                                       _I]
 lib.attn_fwd_block_sparse.restype = _I
@@ -129,16 +133,20 @@ def _torch():
     return torch
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
 def _stream_handle(stream, device=None):
     """The raw handle of ``stream`` (a torch stream or an integer handle); None = torch's
     current stream of ``device`` (of the current device when that is None too).  A torch
     stream must belong to ``device``."""
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif device is not None and getattr(stream, "device", device) != device:
+        cuda = _torch()._C
+        return cuda._cuda_getCurrentRawStream(cuda._cuda_getDevice() if device is None
+                                              else device.index)
+    if device is not None and getattr(stream, "device", device) != device:
         raise AttnError(-1, f"stream on {stream.device}, tensors on {device}")
-    return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _on_device(where, first, *others):
@@ -148,9 +156,12 @@ def _on_device(where, first, *others):
     torch = _torch()
     if not first.is_cuda:
         raise AttnError(-1, f"{where}: tensors must be CUDA tensors")
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise AttnError(-1, f"{where}: tensors on {first.device} and {t.device}")
+    if torch._C._cuda_getDevice() == index:
+        return _NO_SWITCH  # entering a device context costs a microsecond
     return torch.cuda.device(first.device)
 
 
@@ -173,7 +184,7 @@ def _dev_ptr(t, name):
         return None
     if not t.is_cuda or not t.is_contiguous():
         raise AttnError(-1, f"{name} must be a contiguous CUDA tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def attn_fwd(q, k, v, o=None, lse=None, causal: bool = False, scale: float | None = None,
@@ -203,7 +214,7 @@ def attn_fwd(q, k, v, o=None, lse=None, causal: bool = False, scale: float | Non
 
 
 def _expect(where, t, name, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise AttnError(-1, f"{where}: {name} must be {dtype} {tuple(shape)}, "
                             f"got {t.dtype} {tuple(t.shape)}")
 
@@ -578,13 +589,18 @@ def attn_cache_read_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_se
     return k, v
 
 
+def attn_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d, split_size: int = 0) -> int:
+    return int(lib.attn_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, max_seqlen_k, split_size, d))
+
+
 def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k,
-                          max_seqlen_k: int, o=None, lse=None, split_size: int = 512,
+                          max_seqlen_k: int, o=None, lse=None, split_size: int = 0,
                           scale: float | None = None, workspace=None, stream=None):
     """One split-KV decode step over a quantised paged cache (written by attn_cache_write_fp8).
 
     Arguments and return value as attn_decode_paged, with float8_e4m3fn pools and their fp32
-    power-of-two scales [num_pages, Hkv, page_size].
+    power-of-two scales [num_pages, Hkv, page_size].  split_size 0: the library's choice; the
+    workspace takes attn_decode_paged_fp8_workspace_bytes(...) bytes (none for few splits).
     """
     torch = _torch()
     where = "attn_decode_paged_fp8"
@@ -605,8 +621,8 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        need = attn_decode_workspace_bytes(B, Hq, max_seqlen_k, split_size, d)
-        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+        need = attn_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d, split_size)
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
     with _on_device(where, q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, o, lse,
                     workspace):
         st = lib.attn_decode_paged_fp8(
@@ -615,7 +631,8 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
             _dev_ptr(block_table, "block_table"), _dev_ptr(seqlens_k, "seqlens_k"), num_pages,
             page_size, block_table.shape[1], int(max_seqlen_k), _dev_ptr(o, "o"),
             _dev_ptr(lse, "lse"), B, Hq, Hkv, d, int(split_size), float(scale), _dtype_code(q),
-            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _dev_ptr(workspace, "workspace"),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0,
             _stream_handle(stream, q.device))
     _check(st, where)
     return o, lse

@@ -539,6 +539,13 @@ int attn_cache_read_fp8(const void* k_pages, const void* v_pages, const float* k
                                reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t attn_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int max_seqlen_k,
+                                             int split_size, int d) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || max_seqlen_k < 0 || split_size < 0) return 0;
+  if (split_size == 0) split_size = decode_fp8_split(B, Hkv, max_seqlen_k);
+  return decode_fp8_workspace_bytes(B, Hq, max_seqlen_k, split_size, d);
+}
+
 int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
                           const float* k_scales, const float* v_scales,
                           const int32_t* block_table, const int32_t* seqlens_k, int num_pages,
@@ -551,6 +558,7 @@ int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_page
   if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
   const int pages_ok = check_pages(num_pages, page_size, max_pages_per_seq, max_seqlen_k);
   if (pages_ok != ATTN_OK) return pages_ok;
+  if (split_size == 0) split_size = decode_fp8_split(B, Hkv, max_seqlen_k);
   if (split_size < 64 || split_size > 8192 || split_size % 64 != 0) return ATTN_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
@@ -563,8 +571,8 @@ int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_page
       !aligned16(k_scales) || !aligned16(v_scales) || !aligned16(workspace) || !aligned4(lse) ||
       !aligned4(block_table) || !aligned4(seqlens_k))
     return ATTN_ERR_MISALIGNED;
-  const size_t need = decode_workspace_bytes(B, Hq, max_seqlen_k, split_size, d);
-  if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+  const size_t need = decode_fp8_workspace_bytes(B, Hq, max_seqlen_k, split_size, d);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   const int dev_ok = check_device(q);
   if (dev_ok != ATTN_OK) return dev_ok;
   DecodeArgs a{q, nullptr, nullptr, nullptr, num_pages * page_size, max_seqlen_k, o, lse, B,

@@ -199,6 +199,8 @@ int launch_cache_write_fp8(const CacheFp8& c, const void* k, const void* v, cons
 int launch_cache_read_fp8(const CacheFp8& c, void* k, void* v, const int32_t* cu_k, int total,
                           int B, int Hkv, int d, bool bf16, cudaStream_t stream);
 int launch_attn_decode_fp8(const DecodeArgs& a, const CacheFp8& c, cudaStream_t stream);
+size_t decode_fp8_workspace_bytes(int B, int Hq, int max_seqlen, int split, int d);
+int decode_fp8_split(int B, int Hkv, int max_seqlen);
 int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream);
 size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
                              int sinks, int d);

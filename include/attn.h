@@ -419,9 +419,19 @@ int attn_cache_read_fp8(const void *k_pages, const void *v_pages, const float *k
                         attn_dtype_t dtype, attn_stream_t stream);
 
 /*
+ * attn_decode_paged_fp8_workspace_bytes -- bytes of the workspace attn_decode_paged_fp8 needs: 0 for
+ * calls whose sequences have at most eight splits (the workspace may then be null) and for invalid
+ * arguments.
+ */
+size_t attn_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int max_seqlen_k,
+                                             int split_size, int d);
+
+/*
  * attn_decode_paged_fp8 -- attn_decode_paged over a quantised cache: keys and values are code times
  * scale, read as attn_cache_write_fp8 stores them (the scales powers of two; V's from 2^-126 to
- * 2^94).  Arguments as attn_decode_paged with the two scale arrays added; q, o in `dtype`.  Both
+ * 2^94).  Arguments as attn_decode_paged with the two scale arrays added; q, o in `dtype`;
+ * split_size 0 leaves the choice to the library; the workspace is that of
+ * attn_decode_paged_fp8_workspace_bytes.  Both
  * products take the codes as they are (exact in fp16); a bf16 query is scaled by a power of two
  * per row and rounded to fp16, the weights are rounded to fp16, sums are fp32.
  */

@@ -176,10 +176,12 @@ def decode_oracle(qd, seqs, scale, Hq, Hkv):
     return rows, extra.reshape(-1, d), qk.reshape(-1)
 
 
+@pytest.mark.parametrize("split", [0, 64, 512])   # clusters of 1 to 8 blocks, and the workspace
 @pytest.mark.parametrize("page", [16, 32, 64, 256])
 @pytest.mark.parametrize("d,dtype,Hq,Hkv", [(128, "bf16", 16, 2), (64, "f16", 16, 4),
-                                            (64, "bf16", 3, 3), (128, "f16", 16, 1)])
-def test_decode(attn, page, d, dtype, Hq, Hkv):
+                                            (64, "bf16", 3, 3), (128, "f16", 16, 1),
+                                            (64, "bf16", 11, 1), (128, "bf16", 5, 1)])
+def test_decode(attn, page, d, dtype, Hq, Hkv, split):
     import torch
 
     B = len(DEC_LENGTHS)
@@ -191,7 +193,8 @@ def test_decode(attn, page, d, dtype, Hq, Hkv):
     seq = torch.tensor(DEC_LENGTHS, dtype=torch.int32, device="cuda")
     o = torch.full_like(qt, float("nan"))
     lse = torch.full((B, Hq), float("nan"), device="cuda")
-    attn.attn_decode_paged_fp8(qt, *cache, table, seq, max(DEC_LENGTHS), o=o, lse=lse, scale=scale)
+    attn.attn_decode_paged_fp8(qt, *cache, table, seq, max(DEC_LENGTHS), o=o, lse=lse, scale=scale,
+                               split_size=split)
     assert attn.attn_poll_status() == 0
     rows, extra, qk = decode_oracle(qd, seqs, scale, Hq, Hkv)
     # weights and codes in fp16, o in the type of q; a bf16 query's conversion to fp16 is off by at
@@ -210,7 +213,7 @@ def test_decode_with_scales_far_apart(attn):
 
     lengths, Hq, Hkv, d = [700, 65], 8, 2, 128
     cache, table, seqs = make_cache(lengths, Hkv, d, 64, 3)
-    rng = np.random.default_rng(4)
+    rng = np.random.default_rng(4)  # several splits, of scales that differ by head
     f = np.exp2(rng.integers(-60, 41, size=(2, Hkv))).astype(np.float64)  # per sequence and head
     pages = [table[b][: -(-lengths[b] // 64)].long() for b in range(2)]
     for b in range(2):
@@ -359,5 +362,5 @@ def test_refusals(attn):
     with pytest.raises(E):
         attn.attn_decode_paged_fp8(q, *cache, tab, seq, 8, split_size=100)
     with pytest.raises(E):
-        attn.attn_decode_paged_fp8(q, *cache, tab, seq, 8,
+        attn.attn_decode_paged_fp8(q, *cache, i32([[0] * 40]), seq, 640, split_size=64,
                                    workspace=torch.empty(4, dtype=torch.uint8, device="cuda"))

@@ -114,7 +114,11 @@ def test_cache_refusals(attn):
 
     assert dec(hq=9) == -1 and dec(mk=65) == -1 and dec(d=96) == -2 and dec(split=100) == -2
     assert dec(hq=34) == -2 and dec(B=65536) == -2 and dec(page=48) == -2
-    assert dec(ws=NUL) == -4 and dec(n=8) == -4 and dec(codes=NUL) == -1 and dec(codes=ODD) == -3
+    # nine splits go through the workspace, eight do not
+    assert dec(ws=NUL, mk=513, split=64, width=64) == -4 and dec(n=8, mk=513, split=64, width=64) == -4
+    assert attn.attn_decode_paged_fp8_workspace_bytes(2, 8, 2, 512, 64, 64) == 0
+    assert attn.attn_decode_paged_fp8_workspace_bytes(2, 8, 2, 513, 64, 64) > 0
+    assert dec(codes=NUL) == -1 and dec(codes=ODD) == -3
     assert dec(B=0) == 0
     if _no_cuda():
         assert dec() == -7
