@@ -309,7 +309,7 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const v
 size_t attn_bwd_window_sinks_workspace_bytes(int B, int Hq, int Hkv, int N_q, int N_kv, int d,
                                              int window, int sinks) {
   if (Hkv <= 0 || Hq % Hkv || N_kv < 0 || (d != 64 && d != 128) || window < 0 || sinks < 0) return 0;
-  return bwd_workspace_bytes(B, Hq, N_q);
+  return bwd_window_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window, sinks);
 }
 
 int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const void* o,

@@ -74,6 +74,8 @@ struct BwdParams {
   float sl2;    // scale * log2(e)
   float scale;
   int window, sinks;  // window variant: keys behind the diagonal, first keys always visible
+  int sink_tiles, sink_parts;  // ... its key tiles with sinks, each cut into that many blocks
+  float* part;        // [B*Hkv, sink_tiles, sink_parts][dV, dK][128, d] their partial sums
 };
 
 // Window variant: the query tiles [qt_lo, qt_hi) that see key tile kt.  A tile with a sink is seen
@@ -123,6 +125,25 @@ __device__ __forceinline__ void store_acc_row(uint32_t row_tmem_col, uint16_t* d
                              pack2<BF16>(__uint_as_float(a[8 * q4 + 4]), __uint_as_float(a[8 * q4 + 5])),
                              pack2<BF16>(__uint_as_float(a[8 * q4 + 6]), __uint_as_float(a[8 * q4 + 7])));
     }
+  }
+}
+
+// The same as fp32 values (zeros for an accumulator nothing was added to).
+template <int D>
+__device__ __forceinline__ void store_part_row(uint32_t row_tmem_col, float* dst, bool any) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t a[32];
+    if (any) {
+      tmem_ld32(row_tmem_col + c * 32, a);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) a[e] = 0;
+    }
+    uint4* out = reinterpret_cast<uint4*>(dst + c * 32);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = make_uint4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]);
   }
 }
 
@@ -277,8 +298,22 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 
   // job: key tile kt of (batch, key/value head) bkv, numbered key tile major; the launch order
   // is the packed one of KvOrder when the launcher gives one
-  const int n_planes = static_cast<int>(gridDim.x / p.n_kvtiles);
-  const int job = order.n ? static_cast<int>(order.job[blockIdx.x]) : static_cast<int>(blockIdx.x);
+  const int n_planes =
+      static_cast<int>(gridDim.x) /
+      (WINDOW ? p.n_kvtiles + p.sink_tiles * (p.sink_parts - 1) : p.n_kvtiles);
+  int job = order.n ? static_cast<int>(order.job[blockIdx.x]) : static_cast<int>(blockIdx.x);
+  // window variant: a key tile with sinks is seen by every later row, many times what a tile of
+  // the window is; its query tiles are cut into sink_parts blocks (numbered first, part major)
+  [[maybe_unused]] int part = 0;
+  if constexpr (WINDOW) {
+    const int n_sink = n_planes * p.sink_tiles;
+    if (job < n_sink * p.sink_parts) {
+      part = job / n_sink;
+      job -= part * n_sink;
+    } else {
+      job -= n_sink * (p.sink_parts - 1);
+    }
+  }
   const int kt = job / n_planes;
   const int bkv = job % n_planes;
   const int b = bkv / p.Hkv;
@@ -292,7 +327,15 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   int qt_hi = p.n_qtiles;
   if constexpr (WINDOW) window_q_tiles(kt, p.n_qtiles, off, p.window, p.sinks, qt_lo, qt_hi);
   const int nq_per = qt_hi - qt_lo;  // query tiles per query head
-  const int n = nq_per > 0 ? p.G * nq_per : 0;
+  int n = nq_per > 0 ? p.G * nq_per : 0;
+  int tile0 = 0;                          // first (query head, query tile) pair of this block
+  [[maybe_unused]] const bool partial = WINDOW && kt < p.sink_tiles && p.sink_parts > 1;
+  if constexpr (WINDOW) {
+    if (partial) {
+      tile0 = static_cast<int>(static_cast<long long>(n) * part / p.sink_parts);
+      n = static_cast<int>(static_cast<long long>(n) * (part + 1) / p.sink_parts) - tile0;
+    }
+  }
   const int n_steps = 2 * n;              // two 64-query steps per query tile
 
   if (threadIdx.x == 0) {
@@ -340,7 +383,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       for (int i = 0; i < n_steps; ++i) {
         const int s = i % QS;
         if (i >= QS && !wait_bounded(ST_EMPTY(s), ((i / QS) - 1) & 1, abort_flag, p.status)) break;
-        const int tile = i >> 1;
+        const int tile = tile0 + (i >> 1);
         const int g = tile / nq_per;
         const int q0 = (qt_lo + tile % nq_per) * kBT + (i & 1) * kStepQ;
         const int bhq = b * p.Hq + hk * p.G + g;
@@ -440,7 +483,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     bool ok = true;
     for (int i = wg; i < n_steps; i += 2) {
       const int s = i % QS;
-      const int tile = i >> 1;
+      const int tile = tile0 + (i >> 1);
       const int q0 = (qt_lo + tile % nq_per) * kBT + (i & 1) * kStepQ;
       const float* lv = reinterpret_cast<const float*>(gbase + L::kStages + s * L::kStage +
                                                        2 * L::kHalf);
@@ -533,7 +576,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       const bool store = kr < p.N_kv;
       const size_t grow = (static_cast<size_t>(bkv) * p.N_kv + (store ? kr : 0)) * D;
       uint16_t* dst = (wg ? p.dk : p.dv) + grow;
-      if (n > 0)
+      if (partial) {
+        const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2 + wg;
+        store_part_row<D>(row_tmem + (wg ? L::kColDK : L::kColDV), p.part + (at * kBT + r) * D, n > 0);
+      } else if (n > 0)
         store_acc_row<D, BF16>(row_tmem + (wg ? L::kColDK : L::kColDV), dst, store);
       else if (store)
         store_zero_row<D>(dst);
@@ -962,6 +1008,32 @@ __global__ void __launch_bounds__(kQThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------------
+// kernel 3 (window variant): dK and dV of the key tiles with sinks from their blocks' partial sums,
+// added in block order.  Four values a thread; grid (elements, key tile of a plane, dV or dK).
+// ------------------------------------------------------------------------------------------
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const BwdParams p) {
+  griddep_wait();
+  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int r = e / D, c = e % D;
+  const int bkv = blockIdx.y / p.sink_tiles, kt = blockIdx.y % p.sink_tiles;
+  const int which = blockIdx.z;
+  const int key = kt * kBT + r;
+  if (key >= p.N_kv) return;
+  const float* src = p.part + (static_cast<size_t>(blockIdx.y) * p.sink_parts * 2 + which) * kBT * D + e;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < p.sink_parts; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(src + static_cast<size_t>(i) * 2 * kBT * D);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  uint16_t* dst = (which ? p.dk : p.dv) + (static_cast<size_t>(bkv) * p.N_kv + key) * D + c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(s.x, s.y), pack2<BF16>(s.z, s.w));
+}
+
+// ------------------------------------------------------------------------------------------
 // launcher
 // ------------------------------------------------------------------------------------------
 size_t bwd_workspace_bytes(int B, int Hq, int N_q) {
@@ -986,12 +1058,51 @@ static int kv_job_steps(int kt, int n_qtiles, int G, int causal, int off, int wi
   return nq_per > 0 ? 2 * G * nq_per : 0;
 }
 
+// How the key tiles with sinks are cut (window variant): into parts of at most half an SM's share
+// of all steps, and 32 steps at least.
+static void sink_split(int n_planes, int n_kvtiles, int n_qtiles, int G, int off, int window,
+                       int sinks, int& tiles, int& parts) {
+  constexpr int kSms = 152;
+  tiles = static_cast<int>(std::min<long long>((static_cast<long long>(sinks) + kBT - 1) / kBT, n_kvtiles));
+  parts = 1;
+  if (tiles == 0) return;
+  long long total = 0, longest = 0;
+  for (int kt = 0; kt < n_kvtiles; ++kt) {
+    const long long w = kv_job_steps(kt, n_qtiles, G, 1, off, window, sinks);
+    total += w * n_planes;
+    if (kt < tiles) longest = std::max(longest, w);
+  }
+  const long long target = std::max<long long>(total / (2 * kSms), 32);
+  parts = static_cast<int>(std::min<long long>((longest + target - 1) / target, 32));
+  if (parts < 1) parts = 1;
+}
+
+// Floats of the partial sums.
+static size_t sink_part_floats(size_t n_planes, int tiles, int parts, int d) {
+  return parts > 1 ? n_planes * tiles * parts * 2 * kBT * static_cast<size_t>(d) : 0;
+}
+
+size_t bwd_window_workspace_bytes(int B, int Hq, int Hkv, int N_q, int N_kv, int d, int window,
+                                  int sinks) {
+  const size_t base = bwd_workspace_bytes(B, Hq, N_q);
+  if (base == 0 || N_kv <= 0) return base;
+  int tiles, parts;
+  sink_split(B * Hkv, (N_kv + kBT - 1) / kBT, (N_q + kBT - 1) / kBT, Hq / Hkv, N_kv - N_q, window,
+             sinks, tiles, parts);
+  return base + sink_part_floats(static_cast<size_t>(B) * Hkv, tiles, parts, d) * 4;
+}
+
 // The packed dispatch order for a grid of n_planes x n_kvtiles jobs on n_sm SMs: writes the job
 // of every block to job[0 .. n) and returns n, or 0 when the default order stands (no causal
 // mask: equal jobs; no more jobs than SMs; more than `cap` jobs).
 int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, int off, int window,
                  int sinks, int n_sm, uint16_t* job, int cap) {
-  const long long n_jobs_ll = static_cast<long long>(n_planes) * n_kvtiles;
+  int sink_tiles = 0, sink_parts = 1;
+  if (window >= 0)
+    sink_split(n_planes, n_kvtiles, n_qtiles, G, off, window, sinks, sink_tiles, sink_parts);
+  const int n_sink = n_planes * sink_tiles;  // jobs cut into sink_parts blocks, numbered first
+  const long long n_jobs_ll = static_cast<long long>(n_planes) * n_kvtiles +
+                              static_cast<long long>(n_sink) * (sink_parts - 1);
   if (!causal || n_sm <= 0 || n_jobs_ll <= n_sm || n_jobs_ll > cap || n_jobs_ll > 65536) return 0;
   const int n_jobs = static_cast<int>(n_jobs_ll);
   // job weights: its steps plus a block's fixed cost (about four steps: setup, K/V load,
@@ -999,7 +1110,9 @@ int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, i
   std::vector<long long> w(n_jobs);
   long long total = 0;
   for (int j = 0; j < n_jobs; ++j) {
-    w[j] = kv_job_steps(j / n_planes, n_qtiles, G, causal, off, window, sinks) + 4;
+    const bool cut = j < n_sink * sink_parts;
+    const int kt = (cut ? j % n_sink : j - n_sink * (sink_parts - 1)) / n_planes;
+    w[j] = kv_job_steps(kt, n_qtiles, G, causal, off, window, sinks) / (cut ? sink_parts : 1) + 4;
     total += w[j];
   }
   std::vector<int> by_size(n_jobs);
@@ -1119,6 +1232,14 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   p.sl2 = a.scale * 1.4426950408889634f;
   p.window = a.window;
   p.sinks = a.sinks;
+  p.sink_tiles = 0;
+  p.sink_parts = 1;
+  p.part = nullptr;
+  if constexpr (WINDOW) {
+    sink_split(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.N_kv - a.N_q, a.window, a.sinks,
+               p.sink_tiles, p.sink_parts);
+    p.part = const_cast<float*>(p.lse2) + 2 * bhq * nqp;
+  }
   const long long rows = static_cast<long long>(bhq) * nqp;
   attn_bwd_pre_kernel<D, BF16><<<static_cast<unsigned>((rows * (D / 8) + 255) / 256), 256, 0, stream>>>(
       static_cast<const uint16_t*>(a.o), static_cast<const uint16_t*>(a.dout), a.lse,
@@ -1129,7 +1250,8 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   if (cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::kBytes) != cudaSuccess ||
       cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, LQ::kBytes) != cudaSuccess)
     return -5;
-  const uint64_t kv_blocks = bhk * p.n_kvtiles;
+  const uint64_t kv_blocks =
+      bhk * (static_cast<uint64_t>(p.n_kvtiles) + static_cast<uint64_t>(p.sink_tiles) * (p.sink_parts - 1));
   const uint64_t q_blocks = bhq * n_qtiles;
   if (kv_blocks > 0x7fffffffull || q_blocks > 0x7fffffffull) return -2;
   const KvOrder* order = kv_order(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.causal,
@@ -1149,6 +1271,16 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kq, tk, tv, tdo, p) != cudaSuccess) return -5;
+  if constexpr (WINDOW) {
+    if (p.sink_parts > 1) {
+      // a dependent of dQ, whose blocks end after the dK/dV kernel has (more than 65,535 tiles are
+      // never cut: together they are over 100 times an SM's share)
+      cfg.gridDim = dim3(kBT * D / 1024, static_cast<unsigned>(bhk * p.sink_tiles), 2);
+      cfg.blockDim = dim3(256);
+      cfg.dynamicSmemBytes = 0;
+      if (cudaLaunchKernelEx(&cfg, attn_bwd_sink_sum_kernel<D, BF16>, p) != cudaSuccess) return -5;
+    }
+  }
   return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 

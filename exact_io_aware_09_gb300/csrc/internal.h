@@ -206,6 +206,8 @@ size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int
                              int sinks, int d);
 int launch_attn_bwd(const BwdArgs& a, cudaStream_t stream);
 size_t bwd_workspace_bytes(int B, int Hq, int N_q);
+size_t bwd_window_workspace_bytes(int B, int Hq, int Hkv, int N_q, int N_kv, int d, int window,
+                                  int sinks);
 size_t decode_workspace_bytes(int B, int Hq, int max_seqlen, int split, int d);
 // Device address and size of the library-owned decode scratch of the current device
 // (set up on the first call per device).  Returns 0 or an attn_status_t value.
