@@ -15,20 +15,19 @@
 // power of two to at most 2 in magnitude before its own conversion to f16, which then loses only
 // what is 2^-25 of the row's largest element.
 //
-// Channel order.  The sum over channels may run in any order, so thread c of a row group takes
-// the contiguous channels D/4 c .. D/4 c + D/4 - 1 of its key (16-byte loads, free of bank
-// conflicts in the swizzled stage), four of them per 16-wide step, and the query fragments are
-// loaded in that order.  Likewise output column (tile t, n) stands for channel n (D/8) + t, so
-// that the values' operand is made from contiguous bytes of four tokens by byte permutes.
+// Channel order.  The sum over channels may run in any order, so thread (g, c) takes the contiguous
+// channels D/4 c .. D/4 c + D/4 - 1 of its keys (16-byte loads, free of bank conflicts in the
+// swizzled stage), four of them per 16-wide step, and the query fragments are loaded in that order.
+// Likewise its output channels are the contiguous g D/8 .., so that the values' operand is made
+// from contiguous bytes of four tokens by byte permutes.
 //
 // Merging.  A call whose sequences have at most eight splits runs each (sequence, head)'s splits as
 // one cluster, whose blocks read one another's states through distributed shared memory: one
 // launch, no workspace.  More splits go through the workspace and the 16-bit decode's merge kernel.
 //
 // Bound by HBM: 2 (d + 4) bytes per cached token and head.
-#include <type_traits>
-
 #include "attn_decode.cuh"
+#include "attn_rows.cuh"
 
 namespace attn {
 
@@ -41,8 +40,6 @@ struct DecFp8Params : DecParams {
   uint16_t* out;          // [B, Hq, D], [B, Hq]: written here when they are
   float* lse;
 };
-
-constexpr int kMaxCluster = 8;  // blocks of a portable cluster
 
 // l adds w_j 2^(-b_j - kSumShift): the sum stays in range for scales from 2^-126 to 2^94.
 constexpr int kSumShift = 32;
@@ -107,13 +104,6 @@ __device__ __forceinline__ int q_biased_exp(float amax) {
   return e == 255 || amax == 0.0f ? 127 : e < 1 ? 1 : e > 253 ? 253 : e;
 }
 
-// Transpose of an 8 x 8 matrix of 16-bit values held as the matrix instructions hold them.
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 // The D / 8 codes of channels g D/8 .. of a stage row.
 template <int D>
 __device__ __forceinline__ void load_v_words(const uint8_t* vbuf, int row, int g,
@@ -127,110 +117,87 @@ __device__ __forceinline__ void load_v_words(const uint8_t* vbuf, int row, int g
 
 }  // namespace
 
-// The compute warps' part for up to eight query heads per key/value head.  The tiles hold keys (or
-// channels) by query heads, so that eight heads fill a tile's eight columns: half the matrix
-// instructions and accumulators of the form below, whose sixteen rows they would half fill.
-//   S^T = K Q^T: token g and g + 8 of the warp's sixteen by heads 2c and 2c + 1 in thread (g, c);
-//   O^T = V^T P^T: channels g D/8 + 2t and + 1 by the same heads in tile t; P^T as the second
-//   operand is the transpose of what the thread holds (movmatrix).
-template <int D, bool BF16>
-struct NarrowWarp {
-  uint32_t qf[D / 16][2];
-  float f[2];              // factors of the two heads' products
-  float m[2], l[2];        // running maximum; partial sum over this thread's tokens
-  float o[D / 16][4];
+// A warp's query rows and state (attn_rows.cuh) and its work on sixteen tokens.
+template <int D, bool BF16, int NT>
+struct Fp8Warp : RowState<D, NT, false> {
+  uint32_t qf[NT][D / 16][2];
+  float f[NT][2];  // factors of the rows' products
 
+  // q: the group's query rows, G of them
   __device__ __forceinline__ void init(const uint16_t* q, int G, float sl2, int lane) {
+    RowState<D, NT, false>::init();
     const int g = lane >> 2, c = lane & 3;
-    float mx = 0.0f;
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const uint2 a = g < G ? *reinterpret_cast<const uint2*>(q + g * D + c * (D / 4) + ks * 4)
-                            : make_uint2(0, 0);
-      qf[ks][0] = a.x;
-      qf[ks][1] = a.y;
-      if constexpr (BF16) mx = fmaxf(mx, fmaxf(pair_amax(a.x), pair_amax(a.y)));
-    }
-    float mine = sl2;
-    if constexpr (BF16) {
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = q_biased_exp(mx);
-      const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-      mine *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+    for (int n = 0; n < NT; ++n) {
+      const int row = n * 8 + g;
+      float mx = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][0] = q_pair<BF16>(qf[ks][0], inv);
-        qf[ks][1] = q_pair<BF16>(qf[ks][1], inv);
+        // channels D/4 c + 4 ks .. + 3: the first pair at the step's k = 2c, 2c + 1, the second at
+        // k = 2c + 8, 2c + 9
+        const uint2 a = row < G ? *reinterpret_cast<const uint2*>(q + row * D + c * (D / 4) + ks * 4)
+                                : make_uint2(0, 0);
+        qf[n][ks][0] = a.x;
+        qf[n][ks][1] = a.y;
+        if constexpr (BF16) mx = fmaxf(mx, fmaxf(pair_amax(a.x), pair_amax(a.y)));
       }
-    }
-    f[0] = __shfl_sync(0xffffffffu, mine, 8 * c);
-    f[1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.0f;
+      float mine = sl2;
+      if constexpr (BF16) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = q_biased_exp(mx);
+        const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        mine *= __uint_as_float(static_cast<uint32_t>(e) << 23);
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
+        for (int ks = 0; ks < D / 16; ++ks) {
+          qf[n][ks][0] = q_pair<BF16>(qf[n][ks][0], inv);
+          qf[n][ks][1] = q_pair<BF16>(qf[n][ks][1], inv);
+        }
+      }
+      f[n][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
+      f[n][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+    }
   }
 
-  // Sixteen tokens, stage rows w0 .. w0 + 15, of which the first `valid` count.
+  // Stage rows w0 .. w0 + 15, of which the first `valid` count.
   __device__ __forceinline__ void tokens(const uint8_t* kbuf, const uint8_t* vbuf,
                                          const float* k_sc, const float* v_sc, int w0, int valid,
                                          int lane) {
     const int g = lane >> 2, c = lane & 3;
-    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+    float sc[NT][4] = {};
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
-      const uint4 w0v = *reinterpret_cast<const uint4*>(kbuf + code_off<D>(w0 + g, c * (D / 64) + h));
-      const uint4 w1v = *reinterpret_cast<const uint4*>(kbuf + code_off<D>(w0 + g + 8, c * (D / 64) + h));
-      const uint32_t wa[4] = {w0v.x, w0v.y, w0v.z, w0v.w}, wb[4] = {w1v.x, w1v.y, w1v.z, w1v.w};
+      const uint4 u = *reinterpret_cast<const uint4*>(kbuf + code_off<D>(w0 + g, c * (D / 64) + h));
+      const uint4 v = *reinterpret_cast<const uint4*>(kbuf + code_off<D>(w0 + g + 8, c * (D / 64) + h));
+      const uint32_t wa[4] = {u.x, u.y, u.z, u.w}, wb[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t a[4] = {e4m3x2_f16x2(wa[i]), e4m3x2_f16x2(wb[i]), e4m3x2_f16x2_hi(wa[i]),
                                e4m3x2_f16x2_hi(wb[i])};
-        mma_m16n8k16<false>(sc, a, qf[h * 4 + i][0], qf[h * 4 + i][1]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma_m16n8k16<false>(sc[n], a, qf[n][h * 4 + i][0], qf[n][h * 4 + i][1]);
       }
     }
-    float x[2][2], inv_b[2];  // [token][head]
+    float x[NT][2][2], inv_b[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int row = w0 + g + 8 * t;
+    for (int k = 0; k < 2; ++k) {
+      const int row = w0 + g + 8 * k;
       const int vb = static_cast<int>(__float_as_uint(v_sc[row]) >> 23) & 0xff;
       const float bj = static_cast<float>(vb - 127);
       const float kj = k_sc[row];
-      inv_b[t] = __uint_as_float(static_cast<uint32_t>(max(254 - kSumShift - vb, 0)) << 23);
-      const bool in = g + 8 * t < valid;
-      x[t][0] = in ? fmaf(sc[2 * t], f[0] * kj, bj) : -INFINITY;
-      x[t][1] = in ? fmaf(sc[2 * t + 1], f[1] * kj, bj) : -INFINITY;
+      inv_b[k] = __uint_as_float(static_cast<uint32_t>(max(254 - kSumShift - vb, 0)) << 23);
+      const bool in = g + 8 * k < valid;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          x[n][k][r] = in ? fmaf(sc[n][2 * k + r], f[n][r] * kj, bj) : -INFINITY;
     }
-    float pr[2][2], a[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = fmaxf(x[0][h], x[1][h]);
-#pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-      const float mn = fmaxf(m[h], mx);
-      a[h] = (m[h] == -INFINITY) ? 0.f : ex2(m[h] - mn);
-      const float mu = (mn == -INFINITY) ? 0.f : mn;
-      m[h] = mn;
-      l[h] *= a[h];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        pr[t][h] = ex2(x[t][h] - mu);
-        l[h] = fmaf(pr[t][h], inv_b[t], l[h]);
-      }
-    }
-    if (__any_sync(0xffffffffu, a[0] != 1.0f || a[1] != 1.0f)) {
-#pragma unroll
-      for (int t = 0; t < D / 16; ++t) {
-        o[t][0] *= a[0];
-        o[t][1] *= a[1];
-        o[t][2] *= a[0];
-        o[t][3] *= a[1];
-      }
-    }
-    const uint32_t p0 = transpose_8x8(pack2<false>(pr[0][0], pr[0][1]));
-    const uint32_t p1 = transpose_8x8(pack2<false>(pr[1][0], pr[1][1]));
-    constexpr int kW = D / 32;  // words of a token: channels g D/8 .. + D/8 - 1
+    uint32_t pb[NT][2];
+    this->step(x, inv_b, pb);
+    // this thread's channels of tile t are g D/8 + 2t and + 1: D/8 contiguous bytes of a token
+    constexpr int kW = D / 32;
     uint32_t v[4][kW];
 #pragma unroll
     for (int r = 0; r < 4; ++r) load_v_words<D>(vbuf, w0 + (r >> 1) * 8 + 2 * c + (r & 1), g, v[r]);
@@ -238,217 +205,22 @@ struct NarrowWarp {
     for (int i = 0; i < kW; ++i)
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t sel = hh ? 0x7362u : 0x5140u;
+        const uint32_t sel = hh ? 0x7362u : 0x5140u;  // bytes 2hh, 2hh + 1 of two tokens, paired
         const uint32_t lo = __byte_perm(v[0][i], v[1][i], sel);
         const uint32_t hi = __byte_perm(v[2][i], v[3][i], sel);
         const uint32_t av[4] = {e4m3x2_f16x2(lo), e4m3x2_f16x2_hi(lo), e4m3x2_f16x2(hi),
                                 e4m3x2_f16x2_hi(hi)};
-        mma_m16n8k16<false>(o[i * 2 + hh], av, p0, p1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma_m16n8k16<false>(this->o[n][i * 2 + hh], av, pb[n][0], pb[n][1]);
       }
-  }
-
-  __device__ __forceinline__ void finish() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], sh);
-  }
-
-  // This warp's state to its part of the merge scratch: [row][D + 2].
-  __device__ __forceinline__ void store(float* rw, int G, int lane) const {
-    const int g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = 2 * c + h;
-      if (row >= G) continue;
-      float* dst = rw + row * (D + 2);
-#pragma unroll
-      for (int t = 0; t < D / 16; ++t) {
-        *reinterpret_cast<float2*>(dst + g * (D / 8) + 2 * t) = make_float2(o[t][h], o[t][2 + h]);
-      }
-      if (g == 0) {
-        dst[D] = m[h];
-        dst[D + 1] = l[h];
-      }
-    }
   }
 };
 
-// The same for up to sixteen: query heads by keys (or channels), heads g and g + 8 in thread (g, c).
-template <int D, bool BF16>
-struct WideWarp {
-  uint32_t qa[D / 16][4];
-  float f0, f1;      // factors of the two rows' products
-  float m[2], l[2];  // running maximum; partial sum over this thread's columns
-  float o[D / 8][4];
-
-  __device__ __forceinline__ void init(const uint16_t* q, int G, float sl2, int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    f0 = f1 = sl2;
-    float mx0 = 0.0f, mx1 = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      // channels D/4 c + 4 ks .. + 3: the first pair at the step's k = 2c, 2c + 1, the second at
-      // k = 2c + 8, 2c + 9
-      const int col = c * (D / 4) + ks * 4;
-      const uint2 a = g < G ? *reinterpret_cast<const uint2*>(q + g * D + col) : make_uint2(0, 0);
-      const uint2 d = g + 8 < G ? *reinterpret_cast<const uint2*>(q + (g + 8) * D + col) : make_uint2(0, 0);
-      qa[ks][0] = a.x;
-      qa[ks][2] = a.y;
-      qa[ks][1] = d.x;
-      qa[ks][3] = d.y;
-      if constexpr (BF16) {
-        mx0 = fmaxf(mx0, fmaxf(pair_amax(a.x), pair_amax(a.y)));
-        mx1 = fmaxf(mx1, fmaxf(pair_amax(d.x), pair_amax(d.y)));
-      }
-    }
-    if constexpr (BF16) {
-#pragma unroll
-      for (int sh = 1; sh < 4; sh <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
-      }
-      const int e0 = q_biased_exp(mx0), e1 = q_biased_exp(mx1);
-      const float i0 = __uint_as_float(static_cast<uint32_t>(254 - e0) << 23);
-      const float i1 = __uint_as_float(static_cast<uint32_t>(254 - e1) << 23);
-      f0 *= __uint_as_float(static_cast<uint32_t>(e0) << 23);
-      f1 *= __uint_as_float(static_cast<uint32_t>(e1) << 23);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qa[ks][0] = q_pair<BF16>(qa[ks][0], i0);
-        qa[ks][2] = q_pair<BF16>(qa[ks][2], i0);
-        qa[ks][1] = q_pair<BF16>(qa[ks][1], i1);
-        qa[ks][3] = q_pair<BF16>(qa[ks][3], i1);
-      }
-    }
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.0f;
-#pragma unroll
-    for (int nd = 0; nd < D / 8; ++nd) o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
-  }
-
-  __device__ __forceinline__ void tokens(const uint8_t* kbuf, const uint8_t* vbuf,
-                                         const float* k_sc, const float* v_sc, int w0, int valid,
-                                         int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    // S = Q K^T: key n of tile nt is stage row w0 + 8 nt + n
-    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        const uint4 w = *reinterpret_cast<const uint4*>(
-            kbuf + code_off<D>(w0 + nt * 8 + g, c * (D / 64) + h));
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma_m16n8k16<false>(sc[nt], qa[h * 4 + i], e4m3x2_f16x2(ww[i]), e4m3x2_f16x2_hi(ww[i]));
-      }
-    }
-    float x[2][4], inv_b[2][2];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const float2 ks = *reinterpret_cast<const float2*>(k_sc + w0 + nt * 8 + 2 * c);
-      const float2 vs = *reinterpret_cast<const float2*>(v_sc + w0 + nt * 8 + 2 * c);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int vb = static_cast<int>(__float_as_uint(e ? vs.y : vs.x) >> 23) & 0xff;
-        const float bj = static_cast<float>(vb - 127);
-        const float kj = e ? ks.y : ks.x;
-        inv_b[nt][e] = __uint_as_float(static_cast<uint32_t>(max(254 - kSumShift - vb, 0)) << 23);
-        const bool in = nt * 8 + 2 * c + e < valid;
-        x[nt][e] = in ? fmaf(sc[nt][e], f0 * kj, bj) : -INFINITY;
-        x[nt][2 + e] = in ? fmaf(sc[nt][2 + e], f1 * kj, bj) : -INFINITY;
-      }
-    }
-    float mx0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-    float mx1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
-    const float a0 = (m[0] == -INFINITY) ? 0.f : ex2(m[0] - mn0);
-    const float a1 = (m[1] == -INFINITY) ? 0.f : ex2(m[1] - mn1);
-    const float mu0 = (mn0 == -INFINITY) ? 0.f : mn0;
-    const float mu1 = (mn1 == -INFINITY) ? 0.f : mn1;
-    m[0] = mn0;
-    m[1] = mn1;
-    float pr[2][4];
-    l[0] *= a0;
-    l[1] *= a1;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        pr[nt][e] = ex2(x[nt][e] - mu0);
-        pr[nt][2 + e] = ex2(x[nt][2 + e] - mu1);
-        l[0] = fmaf(pr[nt][e], inv_b[nt][e], l[0]);
-        l[1] = fmaf(pr[nt][2 + e], inv_b[nt][e], l[1]);
-      }
-#pragma unroll
-    for (int nd = 0; nd < D / 8; ++nd) {
-      o[nd][0] *= a0;
-      o[nd][1] *= a0;
-      o[nd][2] *= a1;
-      o[nd][3] *= a1;
-    }
-    uint32_t pa[4];
-    pa[0] = pack2<false>(pr[0][0], pr[0][1]);
-    pa[1] = pack2<false>(pr[0][2], pr[0][3]);
-    pa[2] = pack2<false>(pr[1][0], pr[1][1]);
-    pa[3] = pack2<false>(pr[1][2], pr[1][3]);
-    // O += P V: tokens 2c, 2c + 1 (tile 0) and 2c + 8, 2c + 9 (tile 1); this thread's output
-    // column of tile t is channel g (D/8) + t
-    constexpr int kW = D / 32;  // words of a token
-    uint32_t v[4][kW];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) load_v_words<D>(vbuf, w0 + (r >> 1) * 8 + 2 * c + (r & 1), g, v[r]);
-#pragma unroll
-    for (int i = 0; i < kW; ++i) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t sel = hh ? 0x7362u : 0x5140u;  // (a_2h, b_2h, a_2h+1, b_2h+1)
-        const uint32_t lo = __byte_perm(v[0][i], v[1][i], sel);
-        const uint32_t hi = __byte_perm(v[2][i], v[3][i], sel);
-        mma_m16n8k16<false>(o[i * 4 + hh * 2], pa, e4m3x2_f16x2(lo), e4m3x2_f16x2(hi));
-        mma_m16n8k16<false>(o[i * 4 + hh * 2 + 1], pa, e4m3x2_f16x2_hi(lo), e4m3x2_f16x2_hi(hi));
-      }
-    }
-  }
-
-  __device__ __forceinline__ void finish() {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
-  }
-
-  __device__ __forceinline__ void store(float* rw, int G, int lane) const {
-    const int g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = e < 2 ? g : g + 8;
-      if (row >= G) continue;
-      float* dst = rw + row * (D + 2) + (2 * c + (e & 1)) * (D / 8);
-#pragma unroll
-      for (int nd = 0; nd < D / 8; ++nd) dst[nd] = o[nd][e];
-    }
-    if (c == 0) {
-      for (int r = 0; r < 2; ++r) {
-        if (g + 8 * r >= G) continue;
-        rw[(g + 8 * r) * (D + 2) + D] = m[r];
-        rw[(g + 8 * r) * (D + 2) + D + 1] = l[r];
-      }
-    }
-  }
-};
-
-// Narrow: four blocks of 160 threads an SM at up to 102 registers (two at the 150 that the wide
-// form needs), which hides the latency of a stage's conversions and products behind other blocks.
-template <int D, bool BF16, bool NARROW>
-__global__ void __launch_bounds__(kDecThreads, NARROW ? 4 : 2)
+// One column tile: four blocks of 160 threads an SM at up to 102 registers (two column tiles need
+// more), which hides the latency of a stage's conversions and products behind other blocks.
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 2)
     attn_decode_fp8_split_kernel(const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v, const DecFp8Params p) {
   using L = Fp8Layout<D>;
@@ -546,7 +318,7 @@ __global__ void __launch_bounds__(kDecThreads, NARROW ? 4 : 2)
 
   // -------------------------------------------------------------------- compute warps
   const int hq0 = hk * p.G;
-  std::conditional_t<NARROW, NarrowWarp<D, BF16>, WideWarp<D, BF16>> st_w;
+  Fp8Warp<D, BF16, NT> st_w;
   st_w.init(p.q + (static_cast<size_t>(b) * p.Hq + hq0) * D, p.G, p.sl2, lane);
 
   bool ok = true;
@@ -582,73 +354,15 @@ __global__ void __launch_bounds__(kDecThreads, NARROW ? 4 : 2)
   named_bar_sync(1, kDecWarps * 32);  // every warp is done with the ring
   ok = ok && (*abort_flag == 0);
   float* red = reinterpret_cast<float*>(gbase);  // [warp][row][D + 2]
-  constexpr int kRow = D + 2;
-  if (ok) st_w.store(red + warp * kMaxGroup * kRow, p.G, lane);
+  const int g = lane >> 2;
+  if (ok)
+    st_w.store(red + warp * kMaxGroup * (D + 2), p.G, lane,
+               [&](int t, int i) { return g * (D / 8) + 2 * t + i; });
   named_bar_sync(1, kDecWarps * 32);
-  constexpr float kUnshift = 1.0f / 4294967296.0f;  // 2^-kSumShift
-  float* fin = reinterpret_cast<float*>(gbase + L::kFin);
-  if (ok || p.cluster) {
-    const size_t part0 = (static_cast<size_t>(b) * p.Hq + hq0) * p.max_splits + split;
-    for (int i = threadIdx.x; i < p.G * D; i += kDecWarps * 32) {
-      const int row = i / D, col = i % D;
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, red[(w * kMaxGroup + row) * kRow + D]);
-      float ll = 0.f, acc = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float mw = red[(w * kMaxGroup + row) * kRow + D];
-        const float wgt = (mw == -INFINITY) ? 0.f : ex2(mw - mm);
-        ll += wgt * red[(w * kMaxGroup + row) * kRow + D + 1];
-        acc += wgt * red[(w * kMaxGroup + row) * kRow + col];
-      }
-      if (p.cluster) {
-        const bool any = ok && n_tok > 0;
-        fin[row * D + col] = any ? acc / ll * kUnshift : 0.0f;
-        if (col == 0) {
-          fin[kMaxGroup * D + row * 2] = any ? mm + static_cast<float>(kSumShift) : -INFINITY;
-          fin[kMaxGroup * D + row * 2 + 1] = any ? ll : 0.0f;
-        }
-        continue;
-      }
-      const size_t part = part0 + static_cast<size_t>(row) * p.max_splits;
-      p.ws_o[part * D + col] = acc / ll * kUnshift;
-      if (col == 0) {
-        p.ws_ml[part * 2] = mm + static_cast<float>(kSumShift);
-        p.ws_ml[part * 2 + 1] = ll;
-      }
-    }
-  }
-  if (!p.cluster) return;
-  __syncwarp();
-  // The cluster's merge: block `split` of n writes every n-th stretch of the rows.
-  cluster_sync();
-  const int n = p.max_splits;
-  const uint32_t fin_u = smem_u32(fin);
-  for (int i = split * (kDecWarps * 32) + threadIdx.x; i < p.G * D; i += n * kDecWarps * 32) {
-    const int row = i / D, col = i % D;
-    float ms[kMaxCluster], mm = -INFINITY;
-#pragma unroll
-    for (int s = 0; s < kMaxCluster; ++s) {
-      ms[s] = s < n ? ld_cluster_f32(fin_u + (kMaxGroup * D + row * 2) * 4, s) : -INFINITY;
-      mm = fmaxf(mm, ms[s]);
-    }
-    float ll = 0.f, acc = 0.f;
-#pragma unroll
-    for (int s = 0; s < kMaxCluster; ++s) {
-      if (s >= n) break;
-      const float ls = ld_cluster_f32(fin_u + (kMaxGroup * D + row * 2 + 1) * 4, s);
-      const float w = ms[s] == -INFINITY ? ls : ex2(ms[s] - mm) * ls;
-      ll += w;
-      acc += w * ld_cluster_f32(fin_u + i * 4, s);
-    }
-    const size_t orow = static_cast<size_t>(b) * p.Hq + hq0 + row;
-    p.out[orow * D + col] =
-        static_cast<uint16_t>(pack2<BF16>(ll == 0.0f ? 0.0f : acc / ll, 0.0f) & 0xffffu);
-    if (col == 0) p.lse[orow] = ll == 0.0f ? -INFINITY : (mm + lg2(ll)) * 0.69314718055994531f;
-  }
-  __syncwarp();
-  cluster_sync();  // no block leaves while another reads its shared memory
+  const RowsOut w{p.ws_o, p.ws_ml, p.out, p.lse, p.max_splits, split, p.cluster != 0};
+  merge_rows<D, BF16, kDecWarps, kMaxGroup, kSumShift>(
+      red, reinterpret_cast<float*>(gbase + L::kFin), p.G, ok, n_tok > 0, w,
+      [&](int row) { return static_cast<size_t>(b) * p.Hq + hq0 + row; });
 #undef FULL
 #undef EMPTY
 }
@@ -693,9 +407,9 @@ static int launch_decode_fp8_variant(const DecodeArgs& a, const CacheFp8& c, cud
   p.cluster = any_keys && max_splits <= kMaxCluster;
   p.out = static_cast<uint16_t*>(a.o);
   p.lse = a.lse;
-  // up to eight heads a group fill the narrow form's tiles; more need the wide one
-  auto kern = p.G <= 8 ? attn_decode_fp8_split_kernel<D, BF16, true>
-                       : attn_decode_fp8_split_kernel<D, BF16, false>;
+  // up to eight heads a group fill one column tile; more need two
+  auto kern = p.G <= 8 ? attn_decode_fp8_split_kernel<D, BF16, 1>
+                       : attn_decode_fp8_split_kernel<D, BF16, 2>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
       cudaSuccess)
     return -5;
@@ -729,15 +443,9 @@ size_t decode_fp8_workspace_bytes(int B, int Hq, int max_seqlen, int split, int 
   return max_seqlen > 0 ? decode_workspace_bytes(B, Hq, max_seqlen, split, d) : 0;
 }
 
-// Tokens of a split.  Four blocks an SM hold one split each.  A call that gives one round of such
-// blocks or less takes splits that fill it, of two stages at least; a larger one 1,024 tokens,
-// where the last round's idle blocks and the partial states' traffic both stay near 3% of the
-// decode workload (512 tokens: 6% of traffic; 4,096: a last round of a quarter of the time).
+// Tokens of a split, with four blocks an SM.
 int decode_fp8_split(int B, int Hkv, int max_seqlen) {
-  const long long total = static_cast<long long>(B) * Hkv * max_seqlen;
-  long long per = (total + 152 * 4 - 1) / (152 * 4);
-  per = (per + kDecTok - 1) / kDecTok * kDecTok;
-  return static_cast<int>(per < 128 ? 128 : per > 1024 ? 1024 : per);
+  return row_split_tokens(static_cast<long long>(B) * Hkv, max_seqlen, 152 * 4);
 }
 
 int launch_attn_decode_fp8(const DecodeArgs& a, const CacheFp8& c, cudaStream_t stream) {

@@ -10,8 +10,10 @@
 // ahead.  (3) When the chunks give fewer tiles than keep the SMs evenly busy, an item's key tiles
 // are split and the parts' normalised rows merged with the (m, l) rule by a second kernel.
 //
-// Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.
+// Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.  Calls of at most
+// 16 rows per key/value head go to attn_paged_few.cu.
 #include "attn_fwd_kernel.cuh"
+#include "attn_rows.cuh"
 
 namespace attn {
 
@@ -61,10 +63,28 @@ size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int
   if (total_q <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > kBlockM ||
       max_q <= 0 || max_k <= 0 || d <= 0)
     return 0;
-  const PagedSplit s = paged_split(B, Hq, Hkv, max_q, max_k, window, sinks);
-  if (s.n_splits == 1) return 0;
-  const size_t parts = static_cast<size_t>(total_q) * Hq * s.n_splits;
+  PagedArgs a = {};
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.max_q = max_q;
+  int n_splits;
+  if (paged_few_rows(a)) {
+    int stages;
+    paged_few_split(B, Hkv, max_q, max_k, window, sinks, d, n_splits, stages);
+    if (n_splits <= kMaxCluster) return 0;
+  } else {
+    n_splits = paged_split(B, Hq, Hkv, max_q, max_k, window, sinks).n_splits;
+    if (n_splits == 1) return 0;
+  }
+  const size_t parts = static_cast<size_t>(total_q) * Hq * n_splits;
   return parts_o_bytes(parts, d) + parts * 8;
+}
+
+void paged_parts(const PagedArgs& a, int d, int n_splits, float*& ws_o, float*& ws_ml) {
+  const size_t parts = static_cast<size_t>(a.total_q) * a.Hq * n_splits;
+  ws_o = static_cast<float*>(a.workspace);
+  ws_ml = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + parts_o_bytes(parts, d));
 }
 
 // One warp per row: the merge of its splits' (m, l, o).  A split without a visible key has
@@ -116,6 +136,37 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (lane == 0) lse[row] = l == 0.0f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
 }
 
+template <int D, bool BF16>
+static int launch_merge_variant(const PagedArgs& a, int n_splits, cudaStream_t stream) {
+  float *ws_o, *ws_ml;
+  paged_parts(a, D, n_splits, ws_o, ws_ml);
+  const size_t rows = static_cast<size_t>(a.total_q) * a.Hq;
+  const uint64_t blocks = (rows + kMergeWarps - 1) / kMergeWarps;
+  if (blocks > 0x7fffffffull) return -2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<D, BF16>, static_cast<const float*>(ws_o),
+                         static_cast<const float*>(ws_ml), a.cu_q, a.B, a.Hq, rows, n_splits,
+                         static_cast<uint16_t*>(a.o), a.lse) != cudaSuccess)
+    return -5;
+  return cudaGetLastError() == cudaSuccess ? 0 : -5;
+}
+
+int launch_paged_merge(const PagedArgs& a, int n_splits, cudaStream_t stream) {
+  if (a.d == 64)
+    return a.bf16 ? launch_merge_variant<64, true>(a, n_splits, stream)
+                  : launch_merge_variant<64, false>(a, n_splits, stream);
+  return a.bf16 ? launch_merge_variant<128, true>(a, n_splits, stream)
+                : launch_merge_variant<128, false>(a, n_splits, stream);
+}
+
 template <int D, bool BF16, int KS, int VS>
 static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
   using L = FwdLayout<D, KS, VS>;
@@ -164,12 +215,7 @@ static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
   p.tile_tokens = sp.tile_tokens;
   p.n_splits = sp.n_splits;
   p.split_tiles = sp.split_tiles;
-  const size_t rows = static_cast<size_t>(a.total_q) * a.Hq;
-  if (sp.n_splits > 1) {
-    const size_t parts = rows * sp.n_splits;
-    p.ws_o = static_cast<float*>(a.workspace);
-    p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + parts_o_bytes(parts, D));
-  }
+  if (sp.n_splits > 1) paged_parts(a, D, sp.n_splits, p.ws_o, p.ws_ml);
   auto kern = attn_fwd_kernel<D, BF16, KS, VS, false, true, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
       cudaSuccess)
@@ -178,27 +224,11 @@ static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
   if (blocks > 0x7fffffffull) return -2;
   kern<<<static_cast<unsigned>(blocks), kFwdThreads, L::kBytes, stream>>>(tq, tk, tv, tq, p);
   if (cudaGetLastError() != cudaSuccess) return -5;
-  if (sp.n_splits == 1) return 0;
-  const uint64_t merge_blocks = (rows + kMergeWarps - 1) / kMergeWarps;
-  if (merge_blocks > 0x7fffffffull) return -2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(merge_blocks));
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<D, BF16>,
-                         static_cast<const float*>(p.ws_o), static_cast<const float*>(p.ws_ml),
-                         a.cu_q, a.B, a.Hq, rows, sp.n_splits, static_cast<uint16_t*>(a.o),
-                         a.lse) != cudaSuccess)
-    return -5;
-  return cudaGetLastError() == cudaSuccess ? 0 : -5;
+  return sp.n_splits == 1 ? 0 : launch_paged_merge(a, sp.n_splits, stream);
 }
 
 int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
+  if (paged_few_rows(a)) return launch_attn_paged_few(a, stream);
   if (a.d == 64)
     return a.bf16 ? launch_paged_variant<64, true, 4, 4>(a, stream)
                   : launch_paged_variant<64, false, 4, 4>(a, stream);

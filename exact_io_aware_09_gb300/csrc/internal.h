@@ -202,6 +202,14 @@ int launch_attn_decode_fp8(const DecodeArgs& a, const CacheFp8& c, cudaStream_t 
 size_t decode_fp8_workspace_bytes(int B, int Hq, int max_seqlen, int split, int d);
 int decode_fp8_split(int B, int Hkv, int max_seqlen);
 int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream);
+// Whether a call has few enough rows for attn_paged_few.cu, how it splits there, and its launch.
+bool paged_few_rows(const PagedArgs& a);
+void paged_few_split(int B, int Hkv, int max_q, int max_k, int window, int sinks, int d,
+                     int& n_splits, int& stages);
+int launch_attn_paged_few(const PagedArgs& a, cudaStream_t stream);
+// The partial states of n_splits splits in the call's workspace, and their merge into o and lse.
+void paged_parts(const PagedArgs& a, int d, int n_splits, float*& ws_o, float*& ws_ml);
+int launch_paged_merge(const PagedArgs& a, int n_splits, cudaStream_t stream);
 size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
                              int sinks, int d);
 int launch_attn_bwd(const BwdArgs& a, cudaStream_t stream);

@@ -90,6 +90,25 @@ def test_group_sizes(attn, Hq, Hkv):
     run_and_check(attn, [700, 130, 64], [1, 1, 1], Hq, Hkv, 64, "f16", 16, seed=Hq + 1)
 
 
+# at most 16 (token, head) rows per key/value head: chunks of 16 / G tokens and fewer
+FEW = [(16, 2, [1, 2, 1, 2, 2, 0, 1, 2, 2, 1]), (6, 2, [1, 5, 4, 3, 5, 0, 2, 5, 5, 1]),
+       (16, 1, [1] * 10), (4, 4, [1, 15, 16, 8, 16, 0, 9, 16, 2, 16]), (8, 1, [1] * 10)]
+
+
+@pytest.mark.parametrize("W,s", [(-1, 0), (0, 2), (63, 65), (200, 4), (1500, 300)])
+@pytest.mark.parametrize("Hq,Hkv,chunks", FEW, ids=lambda x: str(x)[:8])
+def test_few_rows(attn, Hq, Hkv, chunks, W, s):
+    for d, dtype, page in ((128, "bf16", 16), (64, "f16", 64), (128, "f16", 256), (64, "bf16", 32)):
+        run_and_check(attn, LENGTHS, chunks, Hq, Hkv, d, dtype, page, W, s, seed=W + 3 * Hq + d)
+
+
+def test_few_rows_in_a_cluster_and_through_the_workspace(attn):
+    """Eight splits and nine of 128 keys; a long cache, whose splits are longer."""
+    for n in (1, 128, 1024, 1025, 9000, 40000):
+        run_and_check(attn, [n, 3], [1, 1], 8, 1, 128, "bf16", 64, seed=n)
+        run_and_check(attn, [n, 3], [1, 1], 2, 2, 64, "f16", 16, seed=n)
+
+
 @pytest.mark.parametrize("lengths,chunks", [([1], [1]), ([5000], [1]), ([9000, 3], [2, 1]),
                                             ([4097], [9])])
 @pytest.mark.parametrize("W,s", [(-1, 0), (1000, 4)])
