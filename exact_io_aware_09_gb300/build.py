@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn_gb300.so")
-SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_fwd_paged.cu", "attn_paged_few.cu", "attn_fwd_pair.cu",
+SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_fwd_paged.cu", "attn_paged_few.cu", "attn_fwd_window.cu", "attn_fwd_pair.cu",
            "attn_decode.cu", "attn_decode_fp8.cu", "attn_cache_fp8.cu", "attn_bwd.cu", "attn_fp8.cu"]
 HEADERS = [os.path.join(CSRC, h)
            for h in ("ptx.cuh", "internal.h", "attn_fwd_kernel.cuh", "attn_decode.cuh",

@@ -156,7 +156,7 @@ extern "C" {
 static int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                       int Hq, int Hkv, int N_q, int N_kv, int d, int causal, int window,
                       const uint8_t* block_mask, float scale, attn_stream_t stream,
-                      attn_dtype_t dtype, int sinks = 0) {
+                      attn_dtype_t dtype, int sinks = -1) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || N_q < 0 || N_kv < 0 || Hq % Hkv != 0)
     return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.0f)) return ATTN_ERR_INVALID_ARG;

@@ -119,8 +119,9 @@ int launch_attn_fwd(const FwdArgs& a, cudaStream_t stream) {
       attn_empty_rows_kernel<false><<<blocks, 256, 0, stream>>>(static_cast<uint16_t*>(a.o), a.lse, rows, a.d);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
   }
-  if (a.sinks > 0) {
-    // the window with first keys that stay visible (without them: the window alone, below)
+  if (a.sinks >= 0) {
+    // the window with first keys that stay visible
+    if (window_sinks_short(a)) return launch_attn_fwd_window_sinks(a, stream);
     if (a.d == 64)
       return a.bf16 ? launch_fwd_variant<64, true, 4, 4, false, true>(a, stream)
                     : launch_fwd_variant<64, false, 4, 4, false, true>(a, stream);

@@ -111,7 +111,7 @@ struct FwdArgs {
   const float* k_scale = nullptr;
   const float* v_scale = nullptr;
   int nkvp = 0;
-  int sinks = 0;  // with a window: the first keys that stay visible outside it
+  int sinks = -1;  // with a window: the first keys that stay visible outside it; -1 = the plain window
 };
 
 // A chunk of new tokens of each sequence over a paged 16-bit cache.
@@ -173,6 +173,9 @@ struct BwdArgs {
 int launch_attn_fwd(const FwdArgs& a, cudaStream_t stream);
 // d = 64: two query tiles per work item (attn_fwd_pair.cu)
 int launch_attn_fwd_pair(const FwdArgs& a, cudaStream_t stream);
+// window with sinks whose query tiles see few keys (attn_fwd_window.cu), and whether a call's do
+int launch_attn_fwd_window_sinks(const FwdArgs& a, cudaStream_t stream);
+bool window_sinks_short(const FwdArgs& a);
 // The d = 64 kernel choice: 0 automatic, 1 two query tiles per item, 2 one (attn_fwd.cu).
 int set_d64_kernel(int mode);
 int launch_attn_fwd_fp8_kernel(const FwdArgs& a, cudaStream_t stream);
