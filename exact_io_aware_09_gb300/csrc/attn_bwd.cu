@@ -147,6 +147,20 @@ __device__ __forceinline__ void store_part_row(uint32_t row_tmem_col, float* dst
   }
 }
 
+// 32 scores of a row: kept where their column (less col0) lies in [lo, hi] or is at most sk, -inf
+// elsewhere.  By bits, so that a NaN or infinite score of a masked pair leaves no trace; called from a
+// branch of its own, where a test per column in the exponential loop would cost every tile.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], int col0, int lo, int hi, int sk) {
+  const int a = max(lo - col0, 0), b = min(hi - col0, 31), c = min(sk - col0, 31);
+  uint32_t vis = (a > b) ? 0u : ((0xffffffffu >> (31 - b)) & (0xffffffffu << a));
+  vis |= (c < 0) ? 0u : (0xffffffffu >> (31 - c));
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const uint32_t keep = static_cast<uint32_t>(static_cast<int32_t>(vis << (31 - e)) >> 31);
+    s[e] = (s[e] & keep) | (0xff800000u & ~keep);
+  }
+}
+
 template <int D>
 __device__ __forceinline__ void store_zero_row(uint16_t* dst) {
   uint4* out = reinterpret_cast<uint4*>(dst);
@@ -188,7 +202,9 @@ __global__ void attn_bwd_pre_kernel(const uint16_t* o, const uint16_t* dout, con
     // stored negated (and D times the scale), so that the elementwise steps are single FMAs:
     // s * scale log2(e) + (-L log2(e)) and dP * scale + (-scale D)
     dvec[w] = (i < N_q) ? -scale * acc : 0.0f;
-    lse2[w] = (i < N_q) ? -lse[bh * N_q + i] * 1.4426950408889634f : -INFINITY;
+    // a row that sees no key (L = -inf) takes part in nothing, as the padding rows
+    const float L = (i < N_q) ? lse[bh * N_q + i] : -INFINITY;
+    lse2[w] = (L == -INFINITY) ? -INFINITY : -L * 1.4426950408889634f;
   }
 }
 
@@ -507,6 +523,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             WINDOW ? q0 >= q_first_visible && q0 + (kStepQ - 1) <= q_last_visible
                    : !p.causal || q0 >= q_first_visible;
         const bool all_full = __all_sync(0xffffffffu, full);
+        if constexpr (WINDOW) {
+          if (!all_full) {
+            const int lo = max(q_first_visible, 0) - q0, hi = q_last_visible - q0;
+            mask32(sv[0], 0, lo, hi, -1);
+            mask32(sv[1], 32, lo, hi, -1);
+          }
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -517,14 +540,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             fma2(a0, a1, __uint_as_float(sv[h][e]), __uint_as_float(sv[h][e + 1]), sl2, sl2, l4.x, l4.y);
             fma2(a2, a3, __uint_as_float(sv[h][e + 2]), __uint_as_float(sv[h][e + 3]), sl2, sl2, l4.z,
                  l4.w);
-            if (!all_full) {
+            if (!WINDOW && !all_full) {
               const int rel = q_first_visible - (q0 + col);  // columns below rel precede the key
-              // ... and columns past rel_hi are past the window
-              const int rel_hi = WINDOW ? q_last_visible - (q0 + col) : 3;
-              a0 = (0 >= rel && 0 <= rel_hi) ? a0 : -INFINITY;
-              a1 = (1 >= rel && 1 <= rel_hi) ? a1 : -INFINITY;
-              a2 = (2 >= rel && 2 <= rel_hi) ? a2 : -INFINITY;
-              a3 = (3 >= rel && 3 <= rel_hi) ? a3 : -INFINITY;
+              a0 = (0 >= rel) ? a0 : -INFINITY;
+              a1 = (1 >= rel) ? a1 : -INFINITY;
+              a2 = (2 >= rel) ? a2 : -INFINITY;
+              a3 = (3 >= rel) ? a3 : -INFINITY;
             }
             pv[col] = ex2(a0);
             pv[col + 1] = ex2(a1);
@@ -888,6 +909,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const float sl2 = p.sl2, scale = p.scale;
     int lim = p.causal ? row + (p.N_kv - p.N_q) : p.N_kv - 1;  // last visible key of this row
     if (lim > p.N_kv - 1) lim = p.N_kv - 1;
+    [[maybe_unused]] int first_key = 0;  // first key of this row's window
+    if constexpr (WINDOW) {
+      const long long lo = static_cast<long long>(row) + (p.N_kv - p.N_q) - p.window;
+      first_key = static_cast<int>(lo > 0 ? lo : 0);
+    }
     bool ok = true;
     if (n > 0 && wg == 0) {
       // warpgroup 0 writes the Q rows it loaded before the setup
@@ -901,13 +927,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const int j = key_tile(t);
       const bool masked = WINDOW ? j >= first_masked || j < lo_masked : j >= first_masked;
       const int rel = lim - (j * kBT + c0);  // last visible key, relative to this half tile
-      // window variant: the first key of the window and the last sink, likewise
-      [[maybe_unused]] int rel_lo = 0, rel_sink = 0;
-      if constexpr (WINDOW) {
-        const long long lo = static_cast<long long>(row) + (p.N_kv - p.N_q) - p.window;
-        rel_lo = static_cast<int>(lo > 0 ? lo : 0) - (j * kBT + c0);
-        rel_sink = min(p.sinks - 1 - (j * kBT + c0), rel);
-      }
       if (!ew_wait(bar_sfull, t & 1, abort_flag, p.status)) {
         ok = false;
         break;
@@ -919,6 +938,15 @@ __global__ void __launch_bounds__(kQThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(bar_sfree);  // S_{t+1} may overwrite
+      if constexpr (WINDOW) {
+        if (masked) {
+          // the first key of the window and the last sink, relative to this half tile
+          const int lo = max(first_key - (j * kBT + c0), 0);
+          const int sk = min(p.sinks - 1 - (j * kBT + c0), rel);
+          mask32(sv[0], 0, lo, rel, sk);
+          mask32(sv[1], 32, lo, rel, sk);
+        }
+      }
       // p = 2^(s scale log2(e) - L log2(e)), one packed FMA a pair; the mask only on the tiles
       // that need it (the same for every row of the tile)
       float pv[64];
@@ -929,14 +957,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
           const int col = h * 32 + e;
           float a0, a1;
           fma2(a0, a1, __uint_as_float(sv[h][e]), __uint_as_float(sv[h][e + 1]), sl2, sl2, nl2, nl2);
-          if (masked) {
-            if constexpr (WINDOW) {
-              a0 = ((col <= rel && col >= rel_lo) || col <= rel_sink) ? a0 : -INFINITY;
-              a1 = ((col + 1 <= rel && col + 1 >= rel_lo) || col + 1 <= rel_sink) ? a1 : -INFINITY;
-            } else {
-              a0 = (col <= rel) ? a0 : -INFINITY;
-              a1 = (col + 1 <= rel) ? a1 : -INFINITY;
-            }
+          if (!WINDOW && masked) {
+            a0 = (col <= rel) ? a0 : -INFINITY;
+            a1 = (col + 1 <= rel) ? a1 : -INFINITY;
           }
           pv[col] = ex2(a0);
           pv[col + 1] = ex2(a1);
