@@ -137,34 +137,45 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_fp8_kernel(const CacheParams p) {
   constexpr int kLanes = D / 16;  // lanes of a row
   __shared__ int slot[kMaxRun];
+  constexpr int kStep = kCacheThreads / kLanes;  // rows of the block at a time
   const int i0 = blockIdx.x * p.run;
   const int n = min(p.run, p.total - i0);
-  locate_run<true>(p, i0, n, slot);
-  __syncthreads();
   const int lane = threadIdx.x % kLanes;
   const int rows = n * p.Hkv;
   const bool is_v = blockIdx.y != 0;
-  const uint16_t* src0 = (is_v ? p.v : p.k) + static_cast<size_t>(i0) * p.Hkv * D;
+  const uint16_t* src0 = (is_v ? p.v : p.k) + static_cast<size_t>(i0) * p.Hkv * D + lane * 16;
   uint8_t* codes = is_v ? p.c.v_pages : p.c.k_pages;
   float* scales = is_v ? p.c.v_scales : p.c.k_scales;
-  for (int u0 = 0; u0 < rows; u0 += kCacheThreads / kLanes) {
-    const int u = u0 + threadIdx.x / kLanes;  // every lane stays for the row's reductions
+  // Rows are loaded two steps ahead: the first two while the run's cache rows are looked up.
+  uint4 ahead[2][2] = {};
+  auto load = [&](uint4 (&w)[2], int u) {
+    if (u >= rows) return;
+    const uint4* src = reinterpret_cast<const uint4*>(src0 + static_cast<size_t>(u) * D);
+    w[0] = __ldcs(src);
+    w[1] = __ldcs(src + 1);
+  };
+  const int u_first = threadIdx.x / kLanes;
+  load(ahead[0], u_first);
+  load(ahead[1], u_first + kStep);
+  locate_run<true>(p, i0, n, slot);
+  __syncthreads();
+#pragma unroll 2
+  for (int u0 = 0, b = 0; u0 < rows; u0 += kStep, b ^= 1) {
+    const int u = u0 + u_first;  // every lane stays for the row's reductions
     const int at = u < rows ? slot[u / p.Hkv] : -1;
     const int h = u % p.Hkv;
     float x[16];
+    unpack8<BF16>(ahead[b][0], x);
+    unpack8<BF16>(ahead[b][1], x + 8);
+    load(ahead[b], u + 2 * kStep);
     float amax = 0.0f;
-    if (at >= 0) {
-      const uint4* src = reinterpret_cast<const uint4*>(src0 + static_cast<size_t>(u) * D + lane * 16);
-      unpack8<BF16>(src[0], x);
-      unpack8<BF16>(src[1], x + 8);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float a = fabsf(x[c]);
-        if (a <= 3.402823466e38f)
-          amax = fmaxf(amax, a);
-        else
-          x[c] = __uint_as_float(0x7fffffffu);  // not finite: the NaN code
-      }
+    for (int c = 0; c < 16; ++c) {
+      const float a = fabsf(x[c]);
+      if (a <= 3.402823466e38f)
+        amax = fmaxf(amax, a);
+      else
+        x[c] = __uint_as_float(0x7fffffffu);  // not finite: the NaN code
     }
 #pragma unroll
     for (int sh = kLanes / 2; sh > 0; sh >>= 1)

@@ -19,16 +19,19 @@ namespace attn {
 
 namespace {
 
-constexpr int kSms = 152;       // SMs of a GB300, the split rule's unit
-constexpr int kUnitsPerSm = 4;  // work items per SM below which items are split
-constexpr int kMinSplitTiles = 4;
+constexpr int kSms = 152;        // SMs of a GB300, one block each
+constexpr int kItemTiles = 8;    // a work item's start and end, in key tiles' time (about 6 us)
+constexpr int kMergeTiles = 8;   // the merge's launch, likewise
+constexpr int kMaxSplits = 128;
 
 struct PagedSplit {
   int tile_tokens, n_qtiles, n_splits, split_tiles;
 };
 
-// How a call's work is cut.  An item is one query tile of one key/value head of a sequence; its
-// key tiles are cut so that about kUnitsPerSm items exist per SM.
+// How a call's work is cut.  An item is one query tile of one key/value head of a sequence; its key
+// tiles are cut into the number of splits that finishes first by this count: rounds of items over
+// the SMs, each its key tiles and its fixed cost, and the merge.  (The lengths are the caller's
+// bounds: what the sequences really hold is on the device.)
 PagedSplit paged_split(int B, int Hq, int Hkv, int max_q, int max_k, int window, int sinks) {
   PagedSplit s;
   s.tile_tokens = kBlockM / (Hq / Hkv);
@@ -42,12 +45,15 @@ PagedSplit paged_split(int B, int Hq, int Hkv, int max_q, int max_k, int window,
   const long long items = static_cast<long long>(B) * Hkv * s.n_qtiles;
   s.n_splits = 1;
   s.split_tiles = static_cast<int>(tiles);
-  if (items > 0 && items < kSms * kUnitsPerSm && tiles > kMinSplitTiles) {
-    const long long want = (kSms * kUnitsPerSm + items - 1) / items;
-    long long per = (tiles + want - 1) / want;
-    if (per < kMinSplitTiles) per = kMinSplitTiles;
-    s.split_tiles = static_cast<int>(per);
-    s.n_splits = static_cast<int>((tiles + per - 1) / per);
+  long long best = -1;
+  for (int n = 1; n <= kMaxSplits && n <= tiles; ++n) {
+    const long long per = (tiles + n - 1) / n;
+    const long long cost = (items * n + kSms - 1) / kSms * (per + kItemTiles) + (n > 1 ? kMergeTiles : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      s.split_tiles = static_cast<int>(per);
+      s.n_splits = static_cast<int>((tiles + per - 1) / per);
+    }
   }
   return s;
 }

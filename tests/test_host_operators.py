@@ -69,10 +69,11 @@ def test_paged_refusals(attn):
     assert f(table=ctypes.c_void_p((1 << 20) + 2)) == -3
     assert f(dt=3) == -1
     assert f(B=0) == 0 and f(total=0) == 0 and f(mq=0) == 0
-    need = attn.attn_fwd_paged_workspace_bytes(40, 3, 16, 2, 20, 1024, 128)
-    assert need > 0 and f(n=need - 1) == -4 and f(ws=NUL) == -4
+    long = dict(page=64, width=512, mk=32768)     # a few query tiles over many key tiles: split
+    need = attn.attn_fwd_paged_workspace_bytes(40, 3, 16, 2, 20, 32768, 128)
+    assert need > 0 and f(n=need - 1, **long) == -4 and f(ws=NUL, **long) == -4
     if _no_cuda():
-        assert f() == -7 and f(n=need) == -7
+        assert f(ws=NUL, n=0) == -7 and f(n=need, **long) == -7
 
 
 def test_paged_workspace(attn):
