@@ -329,6 +329,11 @@ def attn_fwd_window_sinks(q, k, v, window: int, sinks: int, o=None, lse=None,
 
     Shapes and return value as attn_fwd.
     """
+    torch = _torch()
+    if o is not None:
+        _expect("attn_fwd_window_sinks", o, "o", q.dtype, q.shape)
+    if lse is not None:
+        _expect("attn_fwd_window_sinks", lse, "lse", torch.float32, q.shape[:3])
     B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
     with _on_device("attn_fwd_window_sinks", q, k, v, o, lse):
         st = lib.attn_fwd_window_sinks(_dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),

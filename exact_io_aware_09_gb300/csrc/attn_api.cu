@@ -194,8 +194,9 @@ int attn_fwd_window_sinks(const void* q, const void* k, const void* v, void* o, 
                           int Hq, int Hkv, int N_q, int N_kv, int d, int window, int sinks,
                           float scale, attn_stream_t stream, attn_dtype_t dtype) {
   if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
-  return fwd_common(q, k, v, o, lse, B, Hq, Hkv, N_q, N_kv, d, 1, window, nullptr, scale,
-                    stream, dtype, sinks);
+  // more than all keys means all keys; the kernels round both up and subtract them from positions
+  return fwd_common(q, k, v, o, lse, B, Hq, Hkv, N_q, N_kv, d, 1, window < N_kv ? window : N_kv,
+                    nullptr, scale, stream, dtype, sinks < N_kv ? sinks : N_kv);
 }
 
 int attn_fwd_block_sparse(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -309,7 +310,8 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const v
 size_t attn_bwd_window_sinks_workspace_bytes(int B, int Hq, int Hkv, int N_q, int N_kv, int d,
                                              int window, int sinks) {
   if (Hkv <= 0 || Hq % Hkv || N_kv < 0 || (d != 64 && d != 128) || window < 0 || sinks < 0) return 0;
-  return bwd_window_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window, sinks);
+  return bwd_window_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window < N_kv ? window : N_kv,
+                                    sinks < N_kv ? sinks : N_kv);
 }
 
 int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const void* o,
@@ -318,8 +320,9 @@ int attn_bwd_window_sinks(const void* q, const void* k, const void* v, const voi
                           float scale, attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
                           attn_stream_t stream) {
   if (window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
-  return bwd_common(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, N_q, N_kv, d, 1, window, sinks,
-                    scale, dtype, workspace, workspace_bytes, stream);
+  return bwd_common(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, N_q, N_kv, d, 1,
+                    window < N_kv ? window : N_kv, sinks < N_kv ? sinks : N_kv, scale, dtype,
+                    workspace, workspace_bytes, stream);
 }
 
 size_t attn_decode_workspace_bytes(int B, int Hq, int max_seqlen_k, int split_size, int d) {
@@ -434,8 +437,13 @@ int attn_decode_splitkv_static(const void* q, const void* k_cache, const void* v
 
 size_t attn_fwd_paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_seqlen_q,
                                       int max_seqlen_k, int window, int sinks, int d) {
-  return paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, window, sinks, d);
+  return paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k,
+                               window < max_seqlen_k ? window : max_seqlen_k,
+                               sinks < max_seqlen_k ? sinks : max_seqlen_k, d);
 }
+
+// Positions are 32-bit and rounded up to whole tiles.
+constexpr int64_t kMaxPagedTokens = int64_t(1) << 30;
 
 // Checks of a page pool and its block table, for tables that reach max_tokens tokens a sequence.
 static int check_pages(int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens) {
@@ -444,6 +452,7 @@ static int check_pages(int num_pages, int page_size, int max_pages_per_seq, int6
     return ATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_pages) * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_pages_per_seq) * page_size < max_tokens) return ATTN_ERR_INVALID_ARG;
+  if (max_tokens > kMaxPagedTokens) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -472,14 +481,15 @@ int attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
       !aligned16(workspace) || !aligned4(lse) || !aligned4(block_table) ||
       !aligned4(cu_seqlens_q) || !aligned4(seqlens_k))
     return ATTN_ERR_MISALIGNED;
-  const size_t need = paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, window,
-                                            sinks, d);
+  const size_t need = attn_fwd_paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k,
+                                                     window, sinks, d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   const int dev_ok = check_device(q);
   if (dev_ok != ATTN_OK) return dev_ok;
   const PagedArgs a{q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, num_pages, page_size,
                     max_pages_per_seq, total_q, max_seqlen_q, max_seqlen_k, o, lse, B, Hq, Hkv, d,
-                    window, sinks, scale, dtype == ATTN_BF16, workspace};
+                    window < max_seqlen_k ? window : max_seqlen_k,
+                    sinks < max_seqlen_k ? sinks : max_seqlen_k, scale, dtype == ATTN_BF16, workspace};
   return launch_attn_fwd_paged(a, reinterpret_cast<cudaStream_t>(stream));
 }
 

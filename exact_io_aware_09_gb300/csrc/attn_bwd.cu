@@ -1198,15 +1198,19 @@ static const KvOrder* kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G,
   static std::map<Key, std::unique_ptr<KvOrder>> cache;
   static std::mutex mu;
   const Key key{n_planes, n_kvtiles, n_qtiles, G, off, window, sinks, n_sm};
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(key);
-  if (it != cache.end()) return it->second.get();
-  auto order = std::make_unique<KvOrder>();
-  order->n = bwd_kv_order(n_planes, n_kvtiles, n_qtiles, G, causal, off, window, sinks, n_sm,
-                          order->job, kMaxKvOrder);
-  const KvOrder* out = order.get();
-  cache.emplace(key, std::move(order));
-  return out;
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = cache.find(key);
+    if (it != cache.end()) return it->second.get();
+    auto order = std::make_unique<KvOrder>();
+    order->n = bwd_kv_order(n_planes, n_kvtiles, n_qtiles, G, causal, off, window, sinks, n_sm,
+                            order->job, kMaxKvOrder);
+    const KvOrder* out = order.get();
+    cache.emplace(key, std::move(order));
+    return out;
+  } catch (...) {  // out of host memory: the default order serves
+    return &kDefault;
+  }
 }
 
 template <int D, bool BF16, bool WINDOW>

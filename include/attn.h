@@ -358,7 +358,8 @@ size_t attn_fwd_paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int m
  *   cu_seqlens_q  [B + 1] int32 device, non-decreasing
  *   seqlens_k     [B] int32 device: cached tokens, the new ones included
  *   max_seqlen_q, max_seqlen_k   upper bounds of n_b and seqlens_k (max_seqlen_k >= max_seqlen_q,
- *                 <= max_pages_per_seq * page_size); they size the grid and the workspace
+ *                 <= max_pages_per_seq * page_size and <= 2^30); they size the grid and the
+ *                 workspace and choose the kernel
  *   o             [total_q, Hq, d] out;  lse [total_q, Hq] out, fp32 (natural log)
  *   window, sinks the token at position p sees key j iff j <= p and (window == -1 or
  *                 p - j <= window or j < sinks); sinks without a window change nothing

@@ -273,6 +273,53 @@ def test_write_then_decode_equals_reading_back(attn):
     assert torch.all((k.float() - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -10 * x.abs().amax(-1, keepdim=True))
 
 
+def test_cache_past_2_31_codes(attn):
+    """Codes past byte 2^31 of the pool: written, read back and attended to as in a small pool."""
+    import torch
+
+    lengths, Hq, Hkv, d, page = [100, 333], 16, 8, 128, 64
+    table, n_pages, _, _ = syn.paged_layout(lengths, page, seed=2)
+    far = 2 ** 31 // (page * Hkv * d) + n_pages
+    dt = torch.bfloat16
+    k, v = (torch.randn((433, Hkv, d), device="cuda").to(dt) for _ in range(2))
+    q = torch.randn((2, Hq, d), device="cuda").to(dt)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    cu, seq = i32([0, 100, 433]), i32(lengths)
+    out = []
+    for shift in (0, far - n_pages):
+        cache = pool(n_pages + shift, page, Hkv, d)
+        tab = torch.from_numpy(table).cuda()
+        tab = torch.where(tab >= 0, tab + shift, tab)
+        attn.attn_cache_write_fp8(k, v, *cache, tab, cu, seq)
+        out.append([*attn.attn_cache_read_fp8(*cache, tab, cu, 433),
+                    *attn.attn_decode_paged_fp8(q, *cache, tab, seq, 333)])
+        assert attn.attn_poll_status() == 0
+        del cache
+    assert all(torch.equal(x, y) for x, y in zip(*out))
+    torch.cuda.empty_cache()
+
+
+def test_nothing_to_do(attn):
+    import torch
+
+    Hkv, d, page = 2, 64, 16
+    cache = pool(2, page, Hkv, d)
+    before = [x.clone() for x in cache]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    x = torch.ones((0, Hkv, d), dtype=torch.float16, device="cuda")
+    attn.attn_cache_write_fp8(x, x, *cache, i32([[0], [1]]), i32([0, 0, 0]), i32([5, 0]))
+    k, v = attn.attn_cache_read_fp8(*cache, i32([[0], [1]]), i32([0, 0, 0]), 0)
+    assert k.shape == (0, Hkv, d) and attn.attn_poll_status() == 0
+    for a, b in zip(cache, before):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # every sequence empty
+    q = torch.ones((2, 4, d), dtype=torch.float16, device="cuda")
+    for most in (0, 16):
+        o, lse = attn.attn_decode_paged_fp8(q, *cache, i32([[0], [1]]), i32([0, 0]), most)
+        assert attn.attn_poll_status() == 0
+        assert not o.any() and torch.isneginf(lse).all()
+
+
 def test_bad_tables_are_reported(attn):
     import torch
 

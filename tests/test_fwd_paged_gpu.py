@@ -196,7 +196,9 @@ def test_pool_past_2_31_elements(attn):
 
     lengths, chunks, page, Hkv, d = [3000, 500], [100, 1], 16, 8, 128
     args, _ = build(lengths, chunks, 16, Hkv, d, "bf16", page, 17)
+    few = build(lengths, [2, 1], 16, Hkv, d, "bf16", page, 17)[0]  # the same cache, 4 rows a head
     want = attn.attn_fwd_paged(*args)
+    want_few = attn.attn_fwd_paged(*few)
     n = args[1].shape[0]
     big_pages = 2 ** 31 // (page * Hkv * d) + 2 * n
     a = list(args)
@@ -208,6 +210,9 @@ def test_pool_past_2_31_elements(attn):
     got = attn.attn_fwd_paged(*a)
     assert attn.attn_poll_status() == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    got = attn.attn_fwd_paged(few[0], a[1], a[2], a[3], *few[4:])
+    assert attn.attn_poll_status() == 0
+    assert torch.equal(got[0], want_few[0]) and torch.equal(got[1], want_few[1])
     del a, pool
     torch.cuda.empty_cache()
 
@@ -235,6 +240,56 @@ def test_side_stream_and_graph_with_new_lengths(attn):
     want = attn.attn_fwd_paged(*args)
     assert attn.attn_poll_status() == 0
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_largest_window_and_sinks(attn):
+    import torch
+
+    args, _ = build([300, 900], [40, 200], 8, 2, 128, "bf16", 16, 27)
+    few, _ = build([300, 900], [1, 2], 8, 2, 128, "bf16", 16, 28)
+    for a in (args, few):
+        want = attn.attn_fwd_paged(*a)
+        for W, s in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (0, 2 ** 31 - 1), (-1, 2 ** 31 - 1)):
+            got = attn.attn_fwd_paged(*a, window=W, sinks=s)
+            assert attn.attn_poll_status() == 0
+            big = want[0].float().abs().amax(-1, keepdim=True)
+            assert torch.all((got[0].float() - want[0].float()).abs() <= 4 * 2.0 ** -8 * (big + 5.0))
+            assert torch.all((got[1] - want[1]).abs() <= 1e-4)
+
+
+def test_packed_rows_that_start_later(attn):
+    """cu_seqlens_q[0] > 0: rows before the first sequence are left as they were, too."""
+    import torch
+
+    for chunks in ([2, 1], [60, 9]):
+        args, _ = build([3000, 700], chunks, 16, 2, 128, "bf16", 32, 33)
+        want = attn.attn_fwd_paged(*args)
+        q = torch.cat([torch.randn_like(args[0][:3]), args[0]])
+        o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        attn.attn_fwd_paged(q, *args[1:4], args[4] + 3, *args[5:], o=o, lse=lse)
+        assert attn.attn_poll_status() == 0
+        assert torch.all(o[:3] == 7.0) and torch.all(lse[:3] == 7.0)
+        assert torch.equal(o[3:], want[0]) and torch.equal(lse[3:], want[1])
+
+
+def test_two_streams_at_once(attn):
+    """Calls of both kernels on two streams, each with its own workspace."""
+    import torch
+
+    a, _ = build([5000, 800], [3, 1], 16, 4, 128, "bf16", 16, 23)
+    b, _ = build([9000], [1], 8, 8, 64, "f16", 16, 24)
+    want = [attn.attn_fwd_paged(*x) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(4):
+        for st, x in zip(streams, (a, b)):
+            with torch.cuda.stream(st):
+                got.append(attn.attn_fwd_paged(*x))
+    torch.cuda.synchronize()
+    assert attn.attn_poll_status() == 0
+    for i, g in enumerate(got):
+        assert torch.equal(g[0], want[i % 2][0]) and torch.equal(g[1], want[i % 2][1])
 
 
 def test_repeated_calls_are_bit_identical(attn):

@@ -170,6 +170,59 @@ def test_wide_window_backward_is_the_causal_one(attn, d):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("nq,nkv", [(600, 600), (900, 300)])
+def test_largest_window_and_sinks_are_all_keys(attn, nq, nkv):
+    """2^31 - 1 of either: the causal result and gradients, rows without keys among them."""
+    import torch
+
+    cfg, (q, k, v) = _inputs((1, 4, 2, nq, nkv, 128, "bf16"), 23)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v)]
+    do = torch.randn_like(t[0])
+    o, lse = attn.attn_fwd(*t, causal=True, scale=cfg.scale)
+    g = attn.attn_bwd(*t, o, do, lse, causal=True, scale=cfg.scale)
+    rows = _oracle(cfg, q, k, v, -1, 0)
+    big = 2 ** 31 - 1
+    for W, s in ((big, 0), (big, big), (0, big)):
+        a, l = attn.attn_fwd_window_sinks(*t, W, s, scale=cfg.scale)
+        assert attn.attn_poll_status() == 0
+        _check(cfg, a, l, rows, f"W={W} sinks={s}")
+        h = attn.attn_bwd_window_sinks(*t, o, do, lse, W, s, scale=cfg.scale)
+        assert attn.attn_poll_status() == 0
+        # the same products in other groups of tiles: sums of them in fp32, rounded once
+        for x, y in zip(g, h):
+            lim = 2.0 ** -7 * x.float().abs() + 2.0 ** -12 * x.float().abs().amax()
+            assert torch.all((x.float() - y.float()).abs() <= lim)
+
+
+def test_past_2_31_elements_sampled(attn):
+    """Q, O, dO and dQ of 2.29e9 elements under a narrow window: sampled rows against a one-row
+    problem over the keys the row sees."""
+    import torch
+
+    W, s = 200, 5
+    cfg = syn.PrefillConfig("big", 1, 128, 8, 140000, 140000, 128, "bf16", True, 6201)
+    q, k, v = cfg.device_inputs("cuda")
+    do = syn.device_normal(q.shape, cfg.seed + 7, cfg.dtype, "cuda")
+    o, lse = attn.attn_fwd_window_sinks(q, k, v, W, s, scale=cfg.scale)
+    dq, dk, dv = attn.attn_bwd_window_sinks(q, k, v, o, do, lse, W, s, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    bits = lambda t: syn.tensor_to_bits(t.contiguous())
+    for h in (0, 61, cfg.Hq - 1):
+        for i in (0, 3, 127, 128, 204, 100001, cfg.N_q - 1):
+            keys = sorted(set(range(max(0, i - W), i + 1)) | set(range(min(s, i + 1))))
+            kr, vr = bits(k[0, h // 16][keys]), bits(v[0, h // 16][keys])
+            qr, dor = bits(q[0, h, i:i + 1]), bits(do[0, h, i:i + 1])
+            rq, _, _, _, _, sc = attention_backward(qr, kr, vr, dor, cfg.dtype, 1, 1, 1, 1, len(keys),
+                                                    cfg.d, False, cfg.scale, error_scales=True)
+            got = dq[0, h, i].float().cpu().numpy().reshape(1, 1, 1, cfg.d)
+            check_grad("dq", got, rq, sc.row[0], sc.elem[0], cfg.dtype, f"head {h} row {i}")
+            x = [bits_to_double(b, cfg.dtype) for b in (qr, kr, vr)]
+            rows = chunk.attend(x[0], x[1], x[2], [len(keys) - 1], cfg.scale)
+            _check(cfg, o[0, h, i], lse[0, h, i], rows, f"head {h} row {i}")
+    del q, k, v, do, o, lse, dq, dk, dv
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("nq,nkv", [(0, 300), (300, 0)], ids=["no_queries", "no_keys"])
 def test_empty_side(attn, nq, nkv):
     import torch
@@ -263,6 +316,10 @@ def test_refusals(attn):
             attn.attn_fwd_window_sinks(q, q, q, W, s)
         with pytest.raises(attn.AttnError):
             attn.attn_bwd_window_sinks(q, q, q, q, q, lse, W, s)
+    with pytest.raises(attn.AttnError):
+        attn.attn_fwd_window_sinks(q, q, q, 10, 4, o=q.half())
+    with pytest.raises(attn.AttnError):
+        attn.attn_fwd_window_sinks(q, q, q, 10, 4, lse=lse[:, :, :9])
     with pytest.raises(attn.AttnError):
         attn.attn_bwd_window_sinks(q, q, q, q, q.half(), lse, 10, 4)
     with pytest.raises(attn.AttnError):
