@@ -165,6 +165,28 @@ def _on_device(where, first, *others):
     return torch.cuda.device(first.device)
 
 
+def _pointers(where, names, tensors):
+    """The device index of the first tensor and every tensor's address (None for None), checked to
+    be contiguous CUDA tensors of that device: one pass, since a call's host time is mostly this."""
+    index = tensors[0].get_device()
+    out = []
+    for i, t in enumerate(tensors):
+        if t is None:
+            out.append(None)
+        elif index < 0 or t.get_device() != index or not t.is_contiguous():
+            raise AttnError(-1, f"{where}: {names[i]} must be a contiguous CUDA tensor"
+                                + (f" on {tensors[0].device}" if index >= 0 else ""))
+        else:
+            out.append(t.data_ptr())
+    return index, out
+
+
+def _device(index):
+    """A context with CUDA device ``index`` current; nothing to do where it is already."""
+    torch = _torch()
+    return _NO_SWITCH if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.float16:
@@ -330,17 +352,17 @@ def attn_fwd_window_sinks(q, k, v, window: int, sinks: int, o=None, lse=None,
     Shapes and return value as attn_fwd.
     """
     torch = _torch()
+    where = "attn_fwd_window_sinks"
     if o is not None:
-        _expect("attn_fwd_window_sinks", o, "o", q.dtype, q.shape)
+        _expect(where, o, "o", q.dtype, q.shape)
     if lse is not None:
-        _expect("attn_fwd_window_sinks", lse, "lse", torch.float32, q.shape[:3])
+        _expect(where, lse, "lse", torch.float32, q.shape[:3])
     B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
-    with _on_device("attn_fwd_window_sinks", q, k, v, o, lse):
-        st = lib.attn_fwd_window_sinks(_dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
-                                       _dev_ptr(o, "o"), _dev_ptr(lse, "lse"), B, Hq, Hkv, N_q,
-                                       N_kv, d, int(window), int(sinks), scale,
+    index, p = _pointers(where, ("q", "k", "v", "o", "lse"), (q, k, v, o, lse))
+    with _device(index):
+        st = lib.attn_fwd_window_sinks(*p, B, Hq, Hkv, N_q, N_kv, d, int(window), int(sinks), scale,
                                        _stream_handle(stream, q.device), _dtype_code(q))
-    _check(st, "attn_fwd_window_sinks")
+    _check(st, where)
     return o, lse
 
 
@@ -375,13 +397,13 @@ def attn_bwd_window_sinks(q, k, v, o, dout, lse, window: int, sinks: int,
     if workspace is None:
         need = attn_bwd_window_sinks_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window, sinks)
         workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
-    with _on_device(where, q, k, v, o, dout, lse, dq, dk, dv, workspace):
-        st = lib.attn_bwd_window_sinks(
-            _dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(o, "o"),
-            _dev_ptr(dout, "dout"), _dev_ptr(lse, "lse"), _dev_ptr(dq, "dq"), _dev_ptr(dk, "dk"),
-            _dev_ptr(dv, "dv"), B, Hq, Hkv, N_q, N_kv, d, int(window), int(sinks), float(scale),
-            _dtype_code(q), _dev_ptr(workspace, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream, q.device))
+    index, (*p, ws) = _pointers(
+        where, ("q", "k", "v", "o", "dout", "lse", "dq", "dk", "dv", "workspace"),
+        (q, k, v, o, dout, lse, dq, dk, dv, workspace))
+    with _device(index):
+        st = lib.attn_bwd_window_sinks(*p, B, Hq, Hkv, N_q, N_kv, d, int(window), int(sinks),
+                                       float(scale), _dtype_code(q), ws, workspace.nbytes,
+                                       _stream_handle(stream, q.device))
     _check(st, where)
     return dq, dk, dv
 
@@ -499,17 +521,16 @@ def attn_fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, ma
         need = attn_fwd_paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d,
                                               window, sinks)
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
-    with _on_device(where, q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, o, lse,
-                    workspace):
-        st = lib.attn_fwd_paged(
-            _dev_ptr(q, "q"), _dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"),
-            _dev_ptr(block_table, "block_table"), _dev_ptr(cu_seqlens_q, "cu_seqlens_q"),
-            _dev_ptr(seqlens_k, "seqlens_k"), num_pages, page_size, block_table.shape[1], total_q,
-            int(max_seqlen_q), int(max_seqlen_k), _dev_ptr(o, "o"), _dev_ptr(lse, "lse"), B, Hq,
-            Hkv, d, int(window), int(sinks), float(scale), _dtype_code(q),
-            _dev_ptr(workspace, "workspace"),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            _stream_handle(stream, q.device))
+    index, (*p, op, lp, ws) = _pointers(
+        where, ("q", "k_pages", "v_pages", "block_table", "cu_seqlens_q", "seqlens_k", "o", "lse",
+                "workspace"),
+        (q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, o, lse, workspace))
+    with _device(index):
+        st = lib.attn_fwd_paged(*p, num_pages, page_size, block_table.shape[1], total_q,
+                                int(max_seqlen_q), int(max_seqlen_k), op, lp, B, Hq, Hkv, d,
+                                int(window), int(sinks), float(scale), _dtype_code(q), ws,
+                                0 if workspace is None else workspace.nbytes,
+                                _stream_handle(stream, q.device))
     _check(st, where)
     return o, lse
 
@@ -517,11 +538,14 @@ def attn_fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, ma
 def _check_cache_fp8(where, k_pages, v_pages, k_scales, v_scales, block_table, B):
     """The (num_pages, page_size, Hkv, d) of a quantised cache, its tensors checked."""
     torch = _torch()
-    num_pages, page_size, Hkv, d = k_pages.shape
-    _expect(where, k_pages, "k_pages", torch.float8_e4m3fn, k_pages.shape)
-    _expect(where, v_pages, "v_pages", torch.float8_e4m3fn, k_pages.shape)
-    _expect(where, k_scales, "k_scales", torch.float32, (num_pages, Hkv, page_size))
-    _expect(where, v_scales, "v_scales", torch.float32, (num_pages, Hkv, page_size))
+    shape = k_pages.shape
+    num_pages, page_size, Hkv, d = shape
+    rows = (num_pages, Hkv, page_size)
+    if not (k_pages.dtype == v_pages.dtype == torch.float8_e4m3fn and v_pages.shape == shape
+            and k_scales.dtype == v_scales.dtype == torch.float32
+            and k_scales.shape == v_scales.shape == rows):
+        raise AttnError(-1, f"{where}: the pools must be float8_e4m3fn [num_pages, page_size, Hkv, d]"
+                            " and their scales float32 [num_pages, Hkv, page_size]")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
         raise AttnError(-1, f"{where}: block_table must be int32 [B, max_pages]")
     return num_pages, page_size, Hkv, d
@@ -548,15 +572,13 @@ def attn_cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, block_table
     _expect(where, v, "v", k.dtype, (total, Hkv, d))
     _expect(where, seqlens_k, "seqlens_k", torch.int32, (B,))
     _expect(where, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
-    with _on_device(where, k, v, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_q,
-                    seqlens_k):
-        st = lib.attn_cache_write_fp8(
-            _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(k_pages, "k_pages"),
-            _dev_ptr(v_pages, "v_pages"), _dev_ptr(k_scales, "k_scales"),
-            _dev_ptr(v_scales, "v_scales"), _dev_ptr(block_table, "block_table"),
-            _dev_ptr(cu_seqlens_q, "cu_seqlens_q"), _dev_ptr(seqlens_k, "seqlens_k"), num_pages,
-            page_size, block_table.shape[1], total, B, Hkv, d, _dtype_code(k),
-            _stream_handle(stream, k.device))
+    index, p = _pointers(
+        where, ("k", "v", "k_pages", "v_pages", "k_scales", "v_scales", "block_table",
+                "cu_seqlens_q", "seqlens_k"),
+        (k, v, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_q, seqlens_k))
+    with _device(index):
+        st = lib.attn_cache_write_fp8(*p, num_pages, page_size, block_table.shape[1], total, B, Hkv,
+                                      d, _dtype_code(k), _stream_handle(stream, k.device))
     _check(st, where)
 
 
@@ -583,13 +605,13 @@ def attn_cache_read_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_se
         v = torch.empty((total, Hkv, d), device=k_pages.device, dtype=dtype)
     _expect(where, k, "k", dtype, (total, Hkv, d))
     _expect(where, v, "v", dtype, (total, Hkv, d))
-    with _on_device(where, k, v, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_k):
-        st = lib.attn_cache_read_fp8(
-            _dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"),
-            _dev_ptr(k_scales, "k_scales"), _dev_ptr(v_scales, "v_scales"),
-            _dev_ptr(block_table, "block_table"), _dev_ptr(cu_seqlens_k, "cu_seqlens_k"),
-            num_pages, page_size, block_table.shape[1], _dev_ptr(k, "k"), _dev_ptr(v, "v"), total,
-            B, Hkv, d, _dtype_code(k), _stream_handle(stream, k.device))
+    index, (*p, kp, vp) = _pointers(
+        where, ("k_pages", "v_pages", "k_scales", "v_scales", "block_table", "cu_seqlens_k", "k",
+                "v"),
+        (k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_k, k, v))
+    with _device(index):
+        st = lib.attn_cache_read_fp8(*p, num_pages, page_size, block_table.shape[1], kp, vp, total,
+                                     B, Hkv, d, _dtype_code(k), _stream_handle(stream, k.device))
     _check(st, where)
     return k, v
 
@@ -628,17 +650,16 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     if workspace is None:
         need = attn_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d, split_size)
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
-    with _on_device(where, q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, o, lse,
-                    workspace):
-        st = lib.attn_decode_paged_fp8(
-            _dev_ptr(q, "q"), _dev_ptr(k_pages, "k_pages"), _dev_ptr(v_pages, "v_pages"),
-            _dev_ptr(k_scales, "k_scales"), _dev_ptr(v_scales, "v_scales"),
-            _dev_ptr(block_table, "block_table"), _dev_ptr(seqlens_k, "seqlens_k"), num_pages,
-            page_size, block_table.shape[1], int(max_seqlen_k), _dev_ptr(o, "o"),
-            _dev_ptr(lse, "lse"), B, Hq, Hkv, d, int(split_size), float(scale), _dtype_code(q),
-            _dev_ptr(workspace, "workspace"),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            _stream_handle(stream, q.device))
+    index, (*p, op, lp, ws) = _pointers(
+        where, ("q", "k_pages", "v_pages", "k_scales", "v_scales", "block_table", "seqlens_k", "o",
+                "lse", "workspace"),
+        (q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, o, lse, workspace))
+    with _device(index):
+        st = lib.attn_decode_paged_fp8(*p, num_pages, page_size, block_table.shape[1],
+                                       int(max_seqlen_k), op, lp, B, Hq, Hkv, d, int(split_size),
+                                       float(scale), _dtype_code(q), ws,
+                                       0 if workspace is None else workspace.nbytes,
+                                       _stream_handle(stream, q.device))
     _check(st, where)
     return o, lse
 
