@@ -19,7 +19,7 @@ namespace attn {
 namespace {
 
 constexpr int kFewRows = 16;
-constexpr int kFewMaxStages = 1024 / kDecTok;  // of a split (row_split_tokens)
+constexpr int kFewMaxStages = 2048 / kDecTok;  // of a split (row_split_tokens)
 
 struct FewParams {
   const uint16_t* q;  // [total_q, Hq, D]

@@ -197,15 +197,20 @@ __device__ __forceinline__ void merge_rows(const float* red, float* fin, int row
   cluster_sync();  // no block leaves while another reads its shared memory
 }
 
-// Splits of `tokens` keys for `pairs` (sequence, head) pairs when `slots` blocks run at a time, in
-// multiples of 64 keys: as many as fill one round of blocks, at least 128 keys each; where that
-// leaves over 1,024 keys, 1,024 (several rounds, of which the last one's idle blocks and the
-// partial states' traffic both stay near 3%).
+// Keys of a split, in multiples of 64, for `pairs` (sequence, head) pairs of at most `tokens` keys
+// when `slots` blocks run at a time: as many splits as fill one round of blocks, at least 128 keys
+// each; where that leaves over 2,048 keys, equal splits of at most 2,048 in several rounds.  A block
+// costs 4-5 us besides its keys (it reads its lengths, then its pages, then the first stage), which
+// speaks for long splits, the last round's idle blocks for short ones.  Measured with at most
+// 1,024 / 2,048 / 4,096 keys, us: the 8-bit decode of 64 sequences of 1k-32k tokens (Hq=64 Hkv=8
+// d=128) 406 / 398 / 475, one 16-bit token of the same 623 / 594 / 703, of 32 sequences of 2k-4k 76 /
+// 64 / 62, one token under a 4,095-key window (16 sequences, Hkv=8, d=64) 35 / 26 / 27.
 inline int row_split_tokens(long long pairs, long long tokens, int slots) {
-  const long long n = pairs > 0 && slots / pairs > 1 ? slots / pairs : 1;
+  long long n = pairs > 0 && slots / pairs > 1 ? slots / pairs : 1;
+  if ((tokens + n - 1) / n > 2048) n = (tokens + 2047) / 2048;
   long long per = (tokens + n - 1) / n;
   per = (per + 63) / 64 * 64;
-  return static_cast<int>(per < 128 ? 128 : per > 1024 ? 1024 : per);
+  return static_cast<int>(per < 128 ? 128 : per);
 }
 
 }  // namespace attn
