@@ -50,6 +50,17 @@ __device__ __forceinline__ float pow2i(int e) {  // 2^e for -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// Magnitudes of a 16-bit pair, and the larger of two pairs (a NaN stays one).
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("{\n\t.reg .b32 t;\n\tabs.f16x2 t, %2;\n\tmax.NaN.f16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4 w, float* v) {
   const uint32_t h[4] = {w.x, w.y, w.z, w.w};
@@ -167,19 +178,37 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_fp8_kernel(const Ca
     float x[16];
     unpack8<BF16>(ahead[b][0], x);
     unpack8<BF16>(ahead[b][1], x + 8);
-    load(ahead[b], u + 2 * kStep);
-    float amax = 0.0f;
+    // the row's largest magnitude, in 16-bit pairs (exact): the kernel is near the ALU's rate
+    uint32_t m2 = 0;
+    {
+      const uint32_t w[8] = {ahead[b][0].x, ahead[b][0].y, ahead[b][0].z, ahead[b][0].w,
+                             ahead[b][1].x, ahead[b][1].y, ahead[b][1].z, ahead[b][1].w};
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float a = fabsf(x[c]);
-      if (a <= 3.402823466e38f)
-        amax = fmaxf(amax, a);
-      else
-        x[c] = __uint_as_float(0x7fffffffu);  // not finite: the NaN code
+      for (int c = 0; c < 8; ++c) m2 = max_abs2<BF16>(m2, w[c]);
     }
 #pragma unroll
     for (int sh = kLanes / 2; sh > 0; sh >>= 1)
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, sh));
+      m2 = max_abs2<BF16>(m2, __shfl_xor_sync(0xffffffffu, m2, sh));
+    load(ahead[b], u + 2 * kStep);
+    float pair[8];
+    unpack8<BF16>(make_uint4(m2, 0, 0, 0), pair);
+    float amax = fmaxf(pair[0], pair[1]);
+    const bool odd = !(pair[0] <= 3.402823466e38f) || !(pair[1] <= 3.402823466e38f);
+    if (__any_sync(0xffffffffu, odd)) {
+      // a value that is not finite: it becomes the NaN code and takes no part in the maximum
+      amax = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float a = fabsf(x[c]);
+        if (a <= 3.402823466e38f)
+          amax = fmaxf(amax, a);
+        else
+          x[c] = __uint_as_float(0x7fffffffu);
+      }
+#pragma unroll
+      for (int sh = kLanes / 2; sh > 0; sh >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, sh));
+    }
     if (at < 0) continue;
     const int e = row_scale_exp(amax);
     const float inv = pow2i(-e);
