@@ -142,6 +142,21 @@ __device__ __forceinline__ void locate_run(const CacheParams& p, int i0, int n, 
   }
 }
 
+// (token, head) of row u of a block's run, advanced by a fixed number of rows without a division.
+struct RunRow {
+  int tok, h, dt, dh, Hkv;
+  __device__ __forceinline__ RunRow(int u, int step, int Hkv_)
+      : tok(u / Hkv_), h(u % Hkv_), dt(step / Hkv_), dh(step % Hkv_), Hkv(Hkv_) {}
+  __device__ __forceinline__ void advance() {
+    tok += dt;
+    h += dh;
+    if (h >= Hkv) {
+      h -= Hkv;
+      ++tok;
+    }
+  }
+};
+
 }  // namespace
 
 template <int D, bool BF16>
@@ -170,11 +185,13 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_fp8_kernel(const Ca
   load(ahead[1], u_first + kStep);
   locate_run<true>(p, i0, n, slot);
   __syncthreads();
+  RunRow rr(u_first, kStep, p.Hkv);
 #pragma unroll 2
   for (int u0 = 0, b = 0; u0 < rows; u0 += kStep, b ^= 1) {
     const int u = u0 + u_first;  // every lane stays for the row's reductions
-    const int at = u < rows ? slot[u / p.Hkv] : -1;
-    const int h = u % p.Hkv;
+    const int at = u < rows ? slot[rr.tok] : -1;
+    const int h = rr.h;
+    rr.advance();
     float x[16];
     unpack8<BF16>(ahead[b][0], x);
     unpack8<BF16>(ahead[b][1], x + 8);
