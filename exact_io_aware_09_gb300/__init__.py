@@ -149,6 +149,17 @@ def _stream_handle(stream, device=None):
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _allocating(stream, device):
+    """A context in which torch allocates for ``stream``, the stream the call runs on: a workspace
+    given back when the call returns is then reused behind the call's kernels and not beside them."""
+    if stream is None:
+        return _NO_SWITCH
+    handle = _stream_handle(stream, device)
+    cuda = _torch().cuda
+    return cuda.stream(stream if hasattr(stream, "cuda_stream")
+                       else cuda.ExternalStream(handle, device=device))
+
+
 def _on_device(where, first, *others):
     """Checks that every given tensor sits on ``first``'s CUDA device and returns a context
     that makes that device current, so that the library's launches, its per-device state and
@@ -349,7 +360,8 @@ def attn_fwd_window_sinks(q, k, v, window: int, sinks: int, o=None, lse=None,
     """Sliding-window prefill whose first ``sinks`` keys stay visible: key j visible to row i,
     p = i + N_kv - N_q, iff j <= p and (p - j <= window or j < sinks).
 
-    Shapes and return value as attn_fwd.
+    Shapes and return value as attn_fwd.  What this call and those below allocate, results and
+    workspace, belongs to ``stream``.
     """
     torch = _torch()
     where = "attn_fwd_window_sinks"
@@ -357,7 +369,8 @@ def attn_fwd_window_sinks(q, k, v, window: int, sinks: int, o=None, lse=None,
         _expect(where, o, "o", q.dtype, q.shape)
     if lse is not None:
         _expect(where, lse, "lse", torch.float32, q.shape[:3])
-    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
+    with _allocating(stream, q.device):
+        B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
     index, p = _pointers(where, ("q", "k", "v", "o", "lse"), (q, k, v, o, lse))
     with _device(index):
         st = lib.attn_fwd_window_sinks(*p, B, Hq, Hkv, N_q, N_kv, d, int(window), int(sinks), scale,
@@ -389,14 +402,15 @@ def attn_bwd_window_sinks(q, k, v, o, dout, lse, window: int, sinks: int,
     if k.shape[0] != B or k.shape[3] != d or k.dtype != q.dtype:
         raise AttnError(-1, f"{where}: q/k/v shapes or dtypes disagree")
     _expect(where, lse, "lse", torch.float32, (B, Hq, N_q))
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if workspace is None:
-        need = attn_bwd_window_sinks_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window, sinks)
-        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    with _allocating(stream, q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            need = attn_bwd_window_sinks_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d, window, sinks)
+            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
     index, (*p, ws) = _pointers(
         where, ("q", "k", "v", "o", "dout", "lse", "dq", "dk", "dv", "workspace"),
         (q, k, v, o, dout, lse, dq, dk, dv, workspace))
@@ -507,20 +521,20 @@ def attn_fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, ma
     _expect(where, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
         raise AttnError(-1, f"{where}: block_table must be int32 [B, max_pages]")
-    if o is None:
-        o = torch.empty_like(q)
-    else:
+    if o is not None:
         _expect(where, o, "o", q.dtype, q.shape)
-    if lse is None:
-        lse = torch.empty((total_q, Hq), device=q.device, dtype=torch.float32)
-    else:
+    if lse is not None:
         _expect(where, lse, "lse", torch.float32, (total_q, Hq))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if workspace is None:
-        need = attn_fwd_paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d,
-                                              window, sinks)
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+    with _allocating(stream, q.device):
+        o = torch.empty_like(q) if o is None else o
+        if lse is None:
+            lse = torch.empty((total_q, Hq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            need = attn_fwd_paged_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d,
+                                                  window, sinks)
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
     index, (*p, op, lp, ws) = _pointers(
         where, ("q", "k_pages", "v_pages", "block_table", "cu_seqlens_q", "seqlens_k", "o", "lse",
                 "workspace"),
@@ -599,10 +613,11 @@ def attn_cache_read_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_se
     if dtype is None:
         dtype = k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16
     total = int(total)
-    if k is None:
-        k = torch.empty((total, Hkv, d), device=k_pages.device, dtype=dtype)
-    if v is None:
-        v = torch.empty((total, Hkv, d), device=k_pages.device, dtype=dtype)
+    with _allocating(stream, k_pages.device):
+        if k is None:
+            k = torch.empty((total, Hkv, d), device=k_pages.device, dtype=dtype)
+        if v is None:
+            v = torch.empty((total, Hkv, d), device=k_pages.device, dtype=dtype)
     _expect(where, k, "k", dtype, (total, Hkv, d))
     _expect(where, v, "v", dtype, (total, Hkv, d))
     index, (*p, kp, vp) = _pointers(
@@ -637,19 +652,19 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     if dk != d:
         raise AttnError(-1, f"{where}: page pools disagree with q")
     _expect(where, seqlens_k, "seqlens_k", torch.int32, (B,))
-    if o is None:
-        o = torch.empty_like(q)
-    else:
+    if o is not None:
         _expect(where, o, "o", q.dtype, q.shape)
-    if lse is None:
-        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
-    else:
+    if lse is not None:
         _expect(where, lse, "lse", torch.float32, (B, Hq))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if workspace is None:
-        need = attn_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d, split_size)
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+    with _allocating(stream, q.device):
+        o = torch.empty_like(q) if o is None else o
+        if lse is None:
+            lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            need = attn_decode_paged_fp8_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d, split_size)
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
     index, (*p, op, lp, ws) = _pointers(
         where, ("q", "k_pages", "v_pages", "k_scales", "v_scales", "block_table", "seqlens_k", "o",
                 "lse", "workspace"),

@@ -198,7 +198,8 @@ size_t attn_bwd_window_sinks_workspace_bytes(int B, int Hq, int Hkv, int N_q, in
  * attn_bwd_window_sinks -- gradients of attn_fwd_window_sinks (and, with sinks = 0, of
  * attn_fwd_window): attn_bwd's formulas under that mask.  Arguments as attn_bwd with `causal`
  * replaced by window and sinks, and the workspace of attn_bwd_window_sinks_workspace_bytes.
- * Tiles no row sees are neither loaded nor computed.  Deterministic: no atomics.
+ * Tiles no row sees are neither loaded nor computed; in a tile that a row sees, the operands of the
+ * masked pairs have to be finite too.  Deterministic: no atomics.
  */
 int attn_bwd_window_sinks(const void *q, const void *k, const void *v, const void *o,
                           const void *dout, const float *lse, void *dq, void *dk, void *dv, int B,
@@ -366,6 +367,9 @@ size_t attn_fwd_paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int m
  *   Query head h reads key/value head h / (Hq / Hkv); Hq / Hkv <= 128.
  *   workspace     device scratch of attn_fwd_paged_workspace_bytes(...) bytes, caller-owned, its
  *                 contents need no initialisation; calls that share it must not overlap
+ * Under a window a page is read only where it overlaps the 128-key tiles (from position 0) that hold
+ * sinks or keys from the first new token's window on: the table entries of the pages before those may
+ * be anything.  Inside those tiles the values of keys that no new token sees have to be finite.
  * A sequence may have no new tokens.  Rows of o and lse outside cu_seqlens_q[0] .. cu_seqlens_q[B]-1
  * are left as they were.  Lengths past their bounds (n_b > seqlens_k[b] among them) and block-table
  * entries outside [0, num_pages) are reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status (that

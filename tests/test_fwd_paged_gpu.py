@@ -328,3 +328,49 @@ def test_nothing_to_do_and_refusals(attn):
               (q, kp[:, :24 - 16].contiguous(), vp[:, :8].contiguous(), table, cu, seq, mq, 8)):
         with pytest.raises(attn.AttnError):
             attn.attn_fwd_paged(*a)
+
+
+@pytest.mark.parametrize("chunks,G", [((1, 1), 4), ((5, 1), 2), ((200, 33), 4), ((1, 130), 1)])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("sinks", [0, 20])
+def test_pages_behind_the_window_need_no_entry(attn, chunks, G, page, sinks):
+    """Table entries of pages outside the 128-key tiles of the sinks and the window: any number."""
+    import torch
+
+    window, lengths = 300, [4000, 2100]
+    args, _ = build(lengths, list(chunks), 2 * G, 2, 128, "bf16", page, seed=5)
+    o, lse = attn.attn_fwd_paged(*args, window=window, sinks=sinks)
+    table = args[3].clone()
+    freed = 0
+    for b, n in enumerate(chunks):
+        first = (-(-sinks // 128) * 128 + page - 1) // page
+        last = (lengths[b] - n - window) // 128 * 128 // page
+        for i in range(first, last):
+            table[b, i] = (-1, 1 << 30)[i % 2]
+            freed += 1
+    assert freed > 0
+    o2, lse2 = attn.attn_fwd_paged(*args[:3], table, *args[4:], window=window, sinks=sinks)
+    assert attn.attn_poll_status() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_workspace_belongs_to_the_calls_stream(attn, as_int):
+    """A call handed a busy stream, its workspace allocated inside: what the current stream
+    allocates and fills while the call waits leaves its result alone."""
+    import torch
+
+    args, _ = build([3000, 5000], [4, 4], 16, 2, 128, "bf16", 64, seed=6)
+    need = attn.attn_fwd_paged_workspace_bytes(8, 2, 16, 2, 4, 5000, 128)
+    assert need > 0
+    want, want_l = attn.attn_fwd_paged(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    o, lse = attn.attn_fwd_paged(*args, stream=side.cuda_stream if as_int else side)
+    filled = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+              for n in (need, o.nbytes, lse.nbytes) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_l)
+    del filled
