@@ -25,7 +25,11 @@
 // one cluster, whose blocks read one another's states through distributed shared memory: one
 // launch, no workspace.  More splits go through the workspace and the 16-bit decode's merge kernel.
 //
-// Bound by HBM: 2 (d + 4) bytes per cached token and head.
+// Bound by HBM: 2 (d + 4) bytes per cached token and head.  64 sequences of 1k-32k tokens (Hq=64 Hkv=8
+// d=128, 64-token pages, 2.45 GB): 412 us, 5.9 TB/s, against 723 for the 16-bit cache; the split
+// kernel runs at 1.8 instructions a cycle (converting the codes is most of them) and the merge, whose
+// launch the split kernel allows early, takes the rest of the gap.  One sequence of 1,001 tokens (Hq=16
+// Hkv=4 d=64): 12 us on the device, one launch.
 #include "attn_decode.cuh"
 #include "attn_rows.cuh"
 

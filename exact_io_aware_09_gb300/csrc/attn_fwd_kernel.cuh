@@ -32,6 +32,12 @@
 // Every barrier phase is counted over the block's whole tile sequence (all items), so the rings,
 // buffers and hand-offs need no reset between items.
 //
+// Variants.  FP8: E4M3 operands (attn_fp8.cu).  SINKS: the first keys stay visible outside the
+// sliding window; an item's key tiles are those that hold sinks, then the window's.  PAGED: a chunk
+// of new tokens of each sequence over a paged cache (attn_fwd_paged.cu).  A masked score of the last
+// two is replaced by bits, so that a NaN of a key no row sees does not spread; the dense variants add
+// -inf, which costs one operation less per score.
+//
 // Departures from the pages' kernels (prior art for A100/H100/B200): accumulators live in tensor
 // memory instead of registers, P is handed to the second MMA through tensor memory instead of
 // shared memory or registers, exponentials are base 2 with the scale folded into one FMA, and the
@@ -1253,23 +1259,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               x[c] = __uint_as_float((__float_as_uint(x[c]) & keep) | (0xff800000u & ~keep));
             }
           } else {
-          if (j >= it.first_masked) {
-            int lim = causal ? row + off : n_kv - 1;  // last visible key of this row
-            if (lim > n_kv - 1) lim = n_kv - 1;
-            hi = min(lim - j * kBlockN, kBlockN - 1);
-          }
-          if (j < it.lo_masked) lo = max(row + off - window - j * kBlockN, 0);
-          uint32_t vis[kBlockN / 32];
+            if (j >= it.first_masked) {
+              int lim = causal ? row + off : n_kv - 1;  // last visible key of this row
+              if (lim > n_kv - 1) lim = n_kv - 1;
+              hi = min(lim - j * kBlockN, kBlockN - 1);
+            }
+            if (j < it.lo_masked) lo = max(row + off - window - j * kBlockN, 0);
+            uint32_t vis[kBlockN / 32];
 #pragma unroll
-          for (int g = 0; g < kBlockN / 32; ++g) {
-            const int a = max(lo - 32 * g, 0), bb = min(hi - 32 * g, 31);
-            vis[g] = (a > bb) ? 0u : ((0xffffffffu >> (31 - bb)) & (0xffffffffu << a));
-          }
-          // x + 0 where visible, x + (-inf) where not: integer arithmetic, no per-column
-          // condition (each of which could otherwise become a divergent branch)
+            for (int g = 0; g < kBlockN / 32; ++g) {
+              const int a = max(lo - 32 * g, 0), bb = min(hi - 32 * g, 31);
+              vis[g] = (a > bb) ? 0u : ((0xffffffffu >> (31 - bb)) & (0xffffffffu << a));
+            }
+            // x + 0 where visible, x + (-inf) where not: integer arithmetic, no per-column
+            // condition (each of which could otherwise become a divergent branch)
 #pragma unroll
-          for (int c = 0; c < kBlockN; ++c)
-            x[c] += __uint_as_float((((vis[c >> 5] >> (c & 31)) & 1u) - 1u) & 0xff800000u);
+            for (int c = 0; c < kBlockN; ++c)
+              x[c] += __uint_as_float((((vis[c >> 5] >> (c & 31)) & 1u) - 1u) & 0xff800000u);
           }
         }
         // Row maximum of the tile: three-input max, sixteen independent chains.

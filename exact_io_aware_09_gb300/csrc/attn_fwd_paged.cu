@@ -10,8 +10,11 @@
 // ahead.  (3) When the chunks give fewer tiles than keep the SMs evenly busy, an item's key tiles
 // are split and the parts' normalised rows merged with the (m, l) rule by a second kernel.
 //
-// Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.  Calls of at most
-// 16 rows per key/value head go to attn_paged_few.cu.
+// Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.  Hq=64 Hkv=8
+// d=128 bf16: two chunks of 2,048 tokens over 12k-16k cached ones 1,550 us in 16-token pages (1,150
+// TFLOP/s), where the producer's 32 copies a tile are as long as the tile, within 3% of the
+// contiguous prefill from 64-token pages on; 64 sequences of 3-8 tokens over 1k-32k 750 us (6.3 TB/s).
+// Calls of at most 16 rows per key/value head go to attn_paged_few.cu.
 #include "attn_fwd_kernel.cuh"
 #include "attn_rows.cuh"
 
@@ -22,6 +25,8 @@ namespace {
 constexpr int kSms = 152;        // SMs of a GB300, one block each
 constexpr int kItemTiles = 8;    // a work item's start and end, in key tiles' time (about 6 us)
 constexpr int kMergeTiles = 8;   // the merge's launch, likewise
+// (against four items an SM, Hq=64 Hkv=8 d=128: 16 tokens over 32k 70 -> 45 us, 4 x 64 tokens over 8k
+// 108 -> 70)
 constexpr int kMaxSplits = 128;
 
 struct PagedSplit {
