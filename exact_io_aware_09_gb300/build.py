@@ -18,10 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn_gb300.so")
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_fwd_paged.cu", "attn_paged_few.cu", "attn_fwd_window.cu", "attn_fwd_pair.cu",
-           "attn_decode.cu", "attn_decode_fp8.cu", "attn_cache_fp8.cu", "attn_bwd.cu", "attn_fp8.cu"]
+           "attn_decode.cu", "attn_decode_fp8.cu", "attn_cache_fp8.cu", "attn_bwd.cu", "attn_bwd_window.cu", "attn_fp8.cu"]
 HEADERS = [os.path.join(CSRC, h)
            for h in ("ptx.cuh", "internal.h", "attn_fwd_kernel.cuh", "attn_decode.cuh",
-                     "attn_rows.cuh")] + [
+                     "attn_rows.cuh", "attn_bwd.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
