@@ -68,6 +68,26 @@ __device__ __forceinline__ void mma_grad(uint32_t d_tmem, uint32_t a_tmem, uint3
   mma_tmem_rows_d<kStepQ>(d_tmem, a_tmem, make_sdesc_sw128(b_smem, kBwStep, 1024), idesc, accumulate);
 }
 
+// Row r of a 128 x 64 accumulator as 16-bit values in a swizzled tile of shared memory, from where one
+// TMA store takes the rows that exist: written row by row from the threads that hold them, a warp's
+// stores would touch 32 lines each (a block's end took a microsecond longer).
+template <bool BF16>
+__device__ __forceinline__ void stage_acc_row(uint32_t row_tmem_col, uint8_t* tile, int r) {
+#pragma unroll 1
+  for (int c = 0; c < kBwD / 32; ++c) {
+    uint32_t a[32];
+    tmem_ld32(row_tmem_col + c * 32, a);
+    tmem_wait_ld();
+#pragma unroll
+    for (int q4 = 0; q4 < 4; ++q4)
+      *reinterpret_cast<uint4*>(tile + sw128(r, c * 4 + q4)) =
+          make_uint4(pack2<BF16>(__uint_as_float(a[8 * q4 + 0]), __uint_as_float(a[8 * q4 + 1])),
+                     pack2<BF16>(__uint_as_float(a[8 * q4 + 2]), __uint_as_float(a[8 * q4 + 3])),
+                     pack2<BF16>(__uint_as_float(a[8 * q4 + 4]), __uint_as_float(a[8 * q4 + 5])),
+                     pack2<BF16>(__uint_as_float(a[8 * q4 + 6]), __uint_as_float(a[8 * q4 + 7])));
+  }
+}
+
 }  // namespace
 
 template <bool BF16>
@@ -75,7 +95,9 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     attn_bwd_short_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                                const __grid_constant__ CUtensorMap tm_k,
                                const __grid_constant__ CUtensorMap tm_v,
-                               const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+                               const __grid_constant__ CUtensorMap tm_do,
+                               const __grid_constant__ CUtensorMap tm_dk,
+                               const __grid_constant__ CUtensorMap tm_dv, const BwdParams p) {
   using L = KvShort;
   constexpr int QS = L::kQS;
   extern __shared__ uint8_t smem_raw[];
@@ -169,7 +191,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
       mbar_arrive_expect_tx(bar_kv, 2 * kBwTile);
       tma_load_3d(base + L::kK, &tm_k, bar_kv, 0, kt * kBT, bkv);
       tma_load_3d(base + L::kV, &tm_v, bar_kv, 0, kt * kBT, bkv);
-      for (int i = 0; i < QS && i < n; ++i) load_stage(i);
+      load_stage(0);
     }
   }
   if (warp == 5) {
@@ -184,9 +206,9 @@ __global__ void __launch_bounds__(kBwThreads, 2)
   if (warp == 4) {
     // ----------------------------------------------------------------- TMA producer
     if (lane == 0 && n > 0) {
-      int issued = min(QS, n);
-      for (int i = QS; i < n; ++i) {
-        if (!wait_bounded(ST_EMPTY(i % QS), ((i / QS) - 1) & 1, abort_flag, p.status)) break;
+      int issued = 1;
+      for (int i = 1; i < n; ++i) {
+        if (i >= QS && !wait_bounded(ST_EMPTY(i % QS), ((i / QS) - 1) & 1, abort_flag, p.status)) break;
         load_stage(i);
         issued = i + 1;
       }
@@ -341,8 +363,17 @@ __global__ void __launch_bounds__(kBwThreads, 2)
         store_part_row<kBwD>(row_tmem + L::kColDV, p.part + (at * kBT + r) * kBwD, n > 0);
         store_part_row<kBwD>(row_tmem + L::kColDK, p.part + ((at + 1) * kBT + r) * kBwD, n > 0);
       } else if (n > 0) {
-        store_acc_row<kBwD, BF16>(row_tmem + L::kColDV, p.dv + row, store);
-        store_acc_row<kBwD, BF16>(row_tmem + L::kColDK, p.dk + row, store);
+        // over K and V, whose products are done
+        stage_acc_row<BF16>(row_tmem + L::kColDV, gbase + L::kK, r);
+        stage_acc_row<BF16>(row_tmem + L::kColDK, gbase + L::kV, r);
+        fence_proxy_async_smem();
+        named_bar_sync(1, kBT);
+        if (threadIdx.x == 0) {
+          tma_store_3d(&tm_dv, base + L::kK, 0, kt * kBT, bkv);
+          tma_store_3d(&tm_dk, base + L::kV, 0, kt * kBT, bkv);
+          tma_store_commit();
+          tma_store_wait_read0();  // the block's shared memory may go
+        }
       } else if (store) {
         store_zero_row<kBwD>(p.dv + row);
         store_zero_row<kBwD>(p.dk + row);
@@ -364,7 +395,8 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     attn_bwd_short_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
                              const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v,
-                             const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+                             const __grid_constant__ CUtensorMap tm_do,
+                             const __grid_constant__ CUtensorMap tm_dq, const BwdParams p) {
   using L = QShort;
   constexpr int KS = L::kKS, VS = L::kVS;
   extern __shared__ uint8_t smem_raw[];
@@ -438,10 +470,6 @@ __global__ void __launch_bounds__(kBwThreads, 2)
       load_k(0);
       tma_load_3d(base + L::kDO, &tm_do, bar_q, 0, qt * kBT, bh);
       load_v(0);
-      for (int t = 1; t < KS && t < n; ++t) {
-        load_k(t);
-        if (t < VS) load_v(t);
-      }
     }
   }
   if (warp == 5) {
@@ -456,16 +484,14 @@ __global__ void __launch_bounds__(kBwThreads, 2)
   if (warp == 4) {
     // ----------------------------------------------------------------- TMA producer
     if (lane == 0 && n > 0) {
-      int issued_k = min(KS, n), issued_v = min(VS, n);
-      // a V step leaves its slot before the K step of the same number does
-      for (int t = VS; t < n; ++t) {
-        if (!wait_bounded(V_EMPTY(t % VS), ((t / VS) - 1) & 1, abort_flag, p.status)) break;
-        load_v(t);
-        issued_v = t + 1;
-        if (t < KS) continue;
-        if (!wait_bounded(K_EMPTY(t % KS), ((t / KS) - 1) & 1, abort_flag, p.status)) break;
+      int issued_k = 1, issued_v = 1;
+      for (int t = 1; t < n; ++t) {
+        if (t >= KS && !wait_bounded(K_EMPTY(t % KS), ((t / KS) - 1) & 1, abort_flag, p.status)) break;
         load_k(t);
         issued_k = t + 1;
+        if (t >= VS && !wait_bounded(V_EMPTY(t % VS), ((t / VS) - 1) & 1, abort_flag, p.status)) break;
+        load_v(t);
+        issued_v = t + 1;
       }
       // Every asynchronous write into this block's shared memory lands before it may exit.
       wait_bounded(bar_q, 0, nullptr, p.status, kBwdDrainNs);
@@ -592,12 +618,18 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     if (ok && n > 0) ok = ew_wait(DQ_DONE((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.status);
     if (ok) {
       tc_fence_after();
-      const bool store = row < p.N_q;
-      uint16_t* dst = p.dq + (static_cast<size_t>(bh) * p.N_q + (store ? row : 0)) * kBwD;
-      if (n > 0)
-        store_acc_row<kBwD, BF16>(row_tmem + L::kColDQ, dst, store);
-      else if (store)
-        store_zero_row<kBwD>(dst);
+      if (n > 0) {
+        stage_acc_row<BF16>(row_tmem + L::kColDQ, gbase + L::kQ, r);  // over Q, whose products are done
+        fence_proxy_async_smem();
+        named_bar_sync(1, kBT);
+        if (threadIdx.x == 0) {
+          tma_store_3d(&tm_dq, base + L::kQ, 0, qt * kBT, bh);
+          tma_store_commit();
+          tma_store_wait_read0();  // the block's shared memory may go
+        }
+      } else if (row < p.N_q) {
+        store_zero_row<kBwD>(p.dq + (static_cast<size_t>(bh) * p.N_q + row) * kBwD);
+      }
     }
   }
 #undef K_FULL
@@ -632,19 +664,26 @@ bool bwd_window_short(const BwdArgs& a) {
 }
 
 int launch_bwd_window_dkdv(const BwdArgs& a, const BwdParams& p, unsigned blocks, cudaStream_t stream) {
-  CUtensorMap m[4];
-  if (!short_maps(a, kStepQ, kBT, m)) return -5;
+  CUtensorMap m[4], dk, dv;
+  const uint64_t bhk = static_cast<uint64_t>(a.B) * a.Hkv, rb = kBwD * 2;
+  if (!short_maps(a, kStepQ, kBT, m) ||
+      !make_tmap_3d(&dk, a.dk, a.bf16, kBwD, a.N_kv, bhk, rb, rb * a.N_kv, 64, kBT, 1) ||
+      !make_tmap_3d(&dv, a.dv, a.bf16, kBwD, a.N_kv, bhk, rb, rb * a.N_kv, 64, kBT, 1))
+    return -5;
   auto kern = a.bf16 ? attn_bwd_short_dkdv_kernel<true> : attn_bwd_short_dkdv_kernel<false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, KvShort::kBytes) != cudaSuccess)
     return -5;
-  kern<<<blocks, kBwThreads, KvShort::kBytes, stream>>>(m[0], m[1], m[2], m[3], p);
+  kern<<<blocks, kBwThreads, KvShort::kBytes, stream>>>(m[0], m[1], m[2], m[3], dk, dv, p);
   return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
 // A programmatic dependent of dK/dV: its blocks fill the SMs of that kernel's tail.
 int launch_bwd_window_dq(const BwdArgs& a, const BwdParams& p, unsigned blocks, cudaStream_t stream) {
-  CUtensorMap m[4];
-  if (!short_maps(a, kBT, kStepQ, m)) return -5;
+  CUtensorMap m[4], dq;
+  const uint64_t bhq = static_cast<uint64_t>(a.B) * a.Hq, rb = kBwD * 2;
+  if (!short_maps(a, kBT, kStepQ, m) ||
+      !make_tmap_3d(&dq, a.dq, a.bf16, kBwD, a.N_q, bhq, rb, rb * a.N_q, 64, kBT, 1))
+    return -5;
   auto kern = a.bf16 ? attn_bwd_short_dq_kernel<true> : attn_bwd_short_dq_kernel<false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, QShort::kBytes) != cudaSuccess)
     return -5;
@@ -658,7 +697,7 @@ int launch_bwd_window_dq(const BwdArgs& a, const BwdParams& p, unsigned blocks, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], p) == cudaSuccess ? 0 : -5;
+  return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], dq, p) == cudaSuccess ? 0 : -5;
 }
 
 }  // namespace attn
