@@ -95,10 +95,7 @@ __device__ __forceinline__ void mask32(uint32_t (&s)[32], int col0, int lo, int 
   uint32_t vis = (a > b) ? 0u : ((0xffffffffu >> (31 - b)) & (0xffffffffu << a));
   vis |= (c < 0) ? 0u : (0xffffffffu >> (31 - c));
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    const uint32_t keep = static_cast<uint32_t>(static_cast<int32_t>(vis << (31 - e)) >> 31);
-    s[e] = (s[e] & keep) | (0xff800000u & ~keep);
-  }
+  for (int e = 0; e < 32; ++e) s[e] = (vis & (1u << e)) ? s[e] : 0xff800000u;
 }
 
 template <int D>

@@ -290,10 +290,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
           // the score where visible, -inf where not: by bits, so that a NaN or infinite score of a
           // masked key leaves no trace
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint32_t keep = static_cast<uint32_t>(static_cast<int32_t>(vis << (31 - c)) >> 31);
-            sr[g][c] = (sr[g][c] & keep) | (0xff800000u & ~keep);
-          }
+          for (int c = 0; c < 32; ++c) sr[g][c] = (vis & (1u << c)) ? sr[g][c] : 0xff800000u;
         }
       }
       float mx[8];
