@@ -1152,7 +1152,8 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
       static_cast<const uint16_t*>(a.o), static_cast<const uint16_t*>(a.dout), a.lse,
       const_cast<float*>(p.lse2), const_cast<float*>(p.dvec), a.N_q, nqp, rows, a.scale);
   if (cudaGetLastError() != cudaSuccess) return -5;
-  const bool two_blocks = WINDOW && D == 64 && bwd_window_short(a);
+  // two blocks on an SM (attn_bwd_window.cu) for either kernel
+  const bool kv_two = WINDOW && D == 64 && bwd_window_two_kv(a), q_two = WINDOW && D == 64 && bwd_window_two_q(a);
   auto kkv = attn_bwd_dkdv_kernel<D, BF16, QS, WINDOW>;
   auto kq = attn_bwd_dq_kernel<D, BF16, KR, VR, WINDOW>;
   if (cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::kBytes) != cudaSuccess ||
@@ -1162,7 +1163,7 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
       bhk * (static_cast<uint64_t>(p.n_kvtiles) + static_cast<uint64_t>(p.sink_tiles) * (p.sink_parts - 1));
   const uint64_t q_blocks = bhq * n_qtiles;
   if (kv_blocks > 0x7fffffffull || q_blocks > 0x7fffffffull) return -2;
-  if (two_blocks) {
+  if (kv_two) {
     const int st = launch_bwd_window_dkdv(a, p, static_cast<unsigned>(kv_blocks), stream);
     if (st != 0) return st;
   } else {
@@ -1183,7 +1184,7 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (two_blocks) {
+  if (q_two) {
     const int st = launch_bwd_window_dq(a, p, static_cast<unsigned>(q_blocks), stream);
     if (st != 0) return st;
   } else if (cudaLaunchKernelEx(&cfg, kq, tk, tv, tdo, p) != cudaSuccess) {

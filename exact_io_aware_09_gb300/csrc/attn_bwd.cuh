@@ -130,8 +130,10 @@ __device__ __forceinline__ void mma_tmem_rows_d(uint32_t d_tmem, uint32_t a_tmem
            (accumulate || kk > 0) ? 1u : 0u);
 }
 
-// d = 64, a short window: two blocks an SM (attn_bwd_window.cu), and whether a call's tiles are short.
-bool bwd_window_short(const BwdArgs& a);
+// d = 64 under a window: the gradient kernels with two blocks on an SM (attn_bwd_window.cu), and
+// whether a call's dK/dV and dQ take them.
+bool bwd_window_two_kv(const BwdArgs& a);
+bool bwd_window_two_q(const BwdArgs& a);
 int launch_bwd_window_dkdv(const BwdArgs& a, const BwdParams& p, unsigned blocks, cudaStream_t stream);
 int launch_bwd_window_dq(const BwdArgs& a, const BwdParams& p, unsigned blocks, cudaStream_t stream);
 

@@ -106,6 +106,45 @@ def test_backward(attn, shape, W, s):
     assert all(torch.equal(x, y) for x, y in zip(got, again))
 
 
+MANY = [
+    # d = 64 with enough tiles for the gradient kernels of two blocks an SM
+    ((8, 96, 96, 33, 33, 64, "f16"), 10, 3),
+    ((8, 96, 96, 1, 130, 64, "bf16"), 64, 64),      # one row
+    ((4, 64, 64, 200, 333, 64, "bf16"), 100, 0),    # N_kv > N_q
+    ((4, 128, 64, 333, 300, 64, "bf16"), 90, 7),    # top rows see no key, grouped heads
+    ((2, 130, 130, 300, 300, 64, "f16"), 5000, 9),  # causal
+    ((2, 40, 10, 700, 700, 64, "bf16"), 200, 150),  # dQ alone
+]
+
+
+@pytest.mark.parametrize("shape,W,s", MANY, ids=ids)
+def test_backward_with_many_tiles(attn, shape, W, s):
+    test_backward(attn, shape, W, s)
+
+
+def test_sink_tiles_cut_in_parts_with_many_tiles(attn):
+    """The first key tile's query steps in several blocks, next to 800 short ones: four heads."""
+    import torch
+
+    shape, W, s = (1, 48, 48, 2100, 2100, 64, "bf16"), 100, 4
+    cfg, (q, k, v) = _inputs(shape, 4501)
+    do = syn.host_normal_bits(q.shape, 4502, cfg.dtype)
+    t = [syn.bits_to_tensor(x, cfg.dtype, "cuda") for x in (q, k, v, do)]
+    need = attn.attn_bwd_window_sinks_workspace_bytes(*shape[:6], W, s)
+    assert need > attn.attn_bwd_window_sinks_workspace_bytes(*shape[:6], W, 0)  # partial sums
+    o, lse = attn.attn_fwd_window_sinks(*t[:3], W, s, scale=cfg.scale)
+    got = attn.attn_bwd_window_sinks(*t[:3], o, t[3], lse, W, s, scale=cfg.scale)
+    assert attn.attn_poll_status() == 0
+    hs = [0, 17, 31, 47]
+    part = [np.ascontiguousarray(x[:, hs]) for x in (q, k, v, do)]
+    r = attention_backward(*part, cfg.dtype, 1, 4, 4, 2100, 2100, 64, True, cfg.scale, window=W,
+                           sinks=s, error_scales=True)
+    for i, (name, g) in enumerate(zip(("dq", "dk", "dv"), got)):
+        check_grad(name, g[:, hs].float().cpu().numpy(), r[i], r[5].row[i], r[5].elem[i], cfg.dtype,
+                   "parts")
+    assert all(bool(torch.isfinite(g).all()) for g in got)
+
+
 def test_gradient_against_differences(attn):
     """The directional derivative of sum(do * o) along random directions, by central differences of
     the fp64 definition, against the GPU gradients: each gradient g lies within the row scales'
