@@ -40,18 +40,18 @@ struct KvShort {
   static_assert(2 * (kBytes + 1024) <= 233472, "two blocks on an SM");
 };
 
-// dQ: Q, dO and rings of 64-key K and V steps.  Tensor memory: S[2] 0-127, dP 128-191, dQ 192-255; dS
-// as 16-bit pairs over the first half of its S buffer.
+// dQ: Q, dO and rings of 64-key K and V steps.  Tensor memory: S 0-63, dS[2] 64-127 (16-bit pairs), dP
+// 128-191, dQ 192-255.
 struct QShort {
   static constexpr int kKS = 5, kVS = 4;
   static constexpr uint32_t kQ = 0, kDO = kBwTile, kK = 2 * kBwTile, kV = kK + kKS * kBwStep;
   static constexpr uint32_t kBar = kV + kVS * kBwStep;
-  // q and dO, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], ds_ready[2], dq_done[2],
-  // dp_full, dp_free, drain
+  // q and dO, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full, s_free, ds_ready[2],
+  // dq_done[2], dp_full, dp_free, drain
   static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 9;
   static constexpr uint32_t kMisc = kBar + kNumBars * 8;
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
-  static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 192;
+  static constexpr uint32_t kColS = 0, kColDS = 64, kColDP = 128, kColDQ = 192;
   static_assert(2 * (kBytes + 1024) <= 233472, "two blocks on an SM");
 };
 
@@ -409,9 +409,10 @@ __global__ void __launch_bounds__(kBwThreads, 2)
 #define V_FULL(s) (bar_q + 8u * (1 + 2 * KS + (s)))
 #define V_EMPTY(s) (bar_q + 8u * (1 + 2 * KS + VS + (s)))
   const uint32_t bar_b = bar_q + 8u * (1 + 2 * KS + 2 * VS);
-#define S_FULL(b) (bar_b + 8u * (b))         // S_t written (MMA commit)
+  const uint32_t bar_s = bar_b;           // S_t written (MMA commit)
+  const uint32_t bar_sfree = bar_b + 8u;  // S_t read (128 arrivals)
 #define DS_READY(b) (bar_b + 8u * (2 + (b)))  // dS_t stored (128 arrivals)
-#define DQ_DONE(b) (bar_b + 8u * (4 + (b)))   // dQ += dS_t K_t done: S buffer free
+#define DQ_DONE(b) (bar_b + 8u * (4 + (b)))   // dQ += dS_t K_t done: dS buffer free
   const uint32_t bar_dp = bar_b + 48u;      // dP_t written
   const uint32_t bar_dpfree = bar_b + 56u;  // dP_t read (128 arrivals)
   const uint32_t bar_drain = bar_b + 64u;
@@ -454,10 +455,11 @@ __global__ void __launch_bounds__(kBwThreads, 2)
       mbar_init(V_EMPTY(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(S_FULL(b), 1);
       mbar_init(DS_READY(b), kBT);
       mbar_init(DQ_DONE(b), 1);
     }
+    mbar_init(bar_s, 1);
+    mbar_init(bar_sfree, kBT);
     mbar_init(bar_dp, 1);
     mbar_init(bar_dpfree, kBT);
     mbar_init(bar_drain, 1);
@@ -506,12 +508,11 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     if (lane == 0 && n > 0) {
       constexpr uint32_t idesc_s = make_idesc_f16(BF16, kBT, kStepQ, false);
       constexpr uint32_t idesc_g = make_idesc_f16(BF16, kBT, kBwD, true);
-      auto issue_s = [&](int t) -> bool {  // S_t into buffer t % 2
+      auto issue_s = [&](int t) -> bool {
         if (!wait_bounded(K_FULL(t % KS), (t / KS) & 1, abort_flag, p.status)) return false;
         tc_fence_after();
-        mma_scores(tmem + L::kColS + (t & 1) * kStepQ, base + L::kQ, base + L::kK + (t % KS) * kBwStep,
-                   idesc_s);
-        mma_commit(S_FULL(t & 1));
+        mma_scores(tmem + L::kColS, base + L::kQ, base + L::kK + (t % KS) * kBwStep, idesc_s);
+        mma_commit(bar_s);
         return true;
       };
       auto issue_dp = [&](int t) -> bool {
@@ -523,23 +524,20 @@ __global__ void __launch_bounds__(kBwThreads, 2)
         return true;
       };
       bool ok = wait_bounded(bar_q, 0, abort_flag, p.status) && issue_s(0) && issue_dp(0);
-      if (ok && n > 1) ok = issue_s(1);
       for (int t = 0; ok && t < n; ++t) {
         const int b = t & 1;
-        if (t + 1 < n) {
+        if (t + 1 < n) {  // the next step's products, each as soon as this step's have been read
+          if (!wait_bounded(bar_sfree, t & 1, abort_flag, p.status)) break;
+          if (!issue_s(t + 1)) break;
           if (!wait_bounded(bar_dpfree, t & 1, abort_flag, p.status)) break;
           if (!issue_dp(t + 1)) break;
         }
         if (!wait_bounded(DS_READY(b), (t >> 1) & 1, abort_flag, p.status)) break;
         tc_fence_after();
-        mma_grad(tmem + L::kColDQ, tmem + L::kColS + b * kStepQ, base + L::kK + (t % KS) * kBwStep,
+        mma_grad(tmem + L::kColDQ, tmem + L::kColDS + b * (kStepQ / 2), base + L::kK + (t % KS) * kBwStep,
                  idesc_g, t > 0);  // dQ += dS K
         mma_commit(K_EMPTY(t % KS));
         mma_commit(DQ_DONE(b));
-        if (t + 2 < n) {  // S_{t+2} goes over dS_t
-          if (!wait_bounded(DQ_DONE(b), (t >> 1) & 1, abort_flag, p.status)) break;
-          ok = issue_s(t + 2);
-        }
       }
       // every MMA this thread issued completes before the block frees its tensor memory
       mma_commit(bar_drain);
@@ -561,16 +559,17 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     for (int t = 0; t < n; ++t) {
       const int j = key_step(t);
       const int b = t & 1;
-      const uint32_t s_addr = row_tmem + L::kColS + b * kStepQ;
-      if (!ew_wait(S_FULL(b), (t >> 1) & 1, abort_flag, p.status)) {
+      if (!ew_wait(bar_s, t & 1, abort_flag, p.status)) {
         ok = false;
         break;
       }
       tc_fence_after();
       uint32_t sv[2][32];
-      tmem_ld32(s_addr, sv[0]);
-      tmem_ld32(s_addr + 32, sv[1]);
+      tmem_ld32(row_tmem + L::kColS, sv[0]);
+      tmem_ld32(row_tmem + L::kColS + 32, sv[1]);
       tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(bar_sfree);
       if (j >= hi_masked || j < lo_masked) {
         const int hi = lim - j * kStepQ;
         const int lo = max(first_key - j * kStepQ, 0);
@@ -610,7 +609,14 @@ __global__ void __launch_bounds__(kBwThreads, 2)
           w[(h * 32 + e) >> 1] = pack2<BF16>(g0, g1);
         }
       }
-      tmem_st32(s_addr, w);  // dS over the scores already read
+      if (t > 1) {  // dQ's product of step t - 2 read this buffer
+        if (!ew_wait(DQ_DONE(b), ((t - 2) >> 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      tmem_st32(row_tmem + L::kColDS + b * (kStepQ / 2), w);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(DS_READY(b));
@@ -636,7 +642,6 @@ __global__ void __launch_bounds__(kBwThreads, 2)
 #undef K_EMPTY
 #undef V_FULL
 #undef V_EMPTY
-#undef S_FULL
 #undef DS_READY
 #undef DQ_DONE
   tc_fence_before();

@@ -35,7 +35,7 @@ constexpr int kWThreads = 192;
 constexpr uint32_t kWSubQ = kWM * 128;   // one 64-column sub-tile of Q
 constexpr uint32_t kWSubKV = kWN * 128;  // ... of a K or V step
 constexpr uint32_t kWTmemCols = 256;
-constexpr uint32_t kWColS = 0, kWColO = 128;  // S buffers at 0 and 64
+constexpr uint32_t kWColP = 0, kWColS = 64;  // P buffers at 0 and 32; S buffers, then O
 constexpr float kWRescale = 8.0f;  // log2 units
 constexpr uint64_t kWDrainNs = 100000000ull;
 
@@ -50,13 +50,16 @@ struct WinParams {
 template <int D>
 struct WinLayout {
   static constexpr int kKS = D == 128 ? 2 : 3, kVS = D == 128 ? 2 : 3;  // ring slots
+  static constexpr int kNS = D == 128 ? 1 : 2;                          // S buffers
+  static constexpr uint32_t kColO = kWColS + kNS * kWN;
+  static_assert(kColO + D <= kWTmemCols, "tensor memory");
   static constexpr uint32_t kQBytes = kWM * D * 2;
   static constexpr uint32_t kStep = kWN * D * 2;
   static constexpr uint32_t kK = kQBytes;
   static constexpr uint32_t kV = kK + kKS * kStep;
   static constexpr uint32_t kBar = kV + kVS * kStep;
-  // q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_ready[2], pv_done[2], drain
-  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 7;
+  // q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_ready[2], pv_done[2], drain, s_free[2]
+  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 9;
   static constexpr uint32_t kMisc = kBar + kNumBars * 8;
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;  // + alignment
   static_assert(2 * (kBytes + 1024) <= 233472, "two blocks on an SM");
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ CUtensorMap tm_o, const WinParams p) {
   using L = WinLayout<D>;
-  constexpr int KS = L::kKS, VS = L::kVS;
+  constexpr int KS = L::kKS, VS = L::kVS, NS = L::kNS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -123,6 +126,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #define P_READY(b) (bar_b + 8u * (2 + (b)))
 #define PV_DONE(b) (bar_b + 8u * (4 + (b)))
   const uint32_t bar_drain = bar_b + 8u * 6;
+#define S_FREE(b) (bar_b + 8u * (7 + (b)))
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   const int warp = threadIdx.x >> 5;
@@ -162,6 +166,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
       mbar_init(S_FULL(b), 1);
       mbar_init(P_READY(b), kWM);
       mbar_init(PV_DONE(b), 1);
+      mbar_init(S_FREE(b), kWM);
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
@@ -212,24 +217,29 @@ __global__ void __launch_bounds__(kWThreads, 2)
       constexpr uint32_t idesc_qk = make_idesc_f16(BF16, kWM, kWN, false);
       constexpr uint32_t idesc_pv = make_idesc_f16(BF16, kWM, D, true);
       const uint64_t q_desc = make_sdesc_sw128(base, 16, 1024);
-      auto issue_qk = [&](int t) -> bool {  // S_t into buffer t % 2
+      auto issue_qk = [&](int t) -> bool {  // S_t into buffer t % NS
         const int s = t % KS;
         if (!wait_bounded(K_FULL(s), (t / KS) & 1, abort_flag, p.status)) return false;
         tc_fence_after();
         const uint64_t k_desc = make_sdesc_sw128(base + L::kK + s * L::kStep, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + kWColS + (t & 1) * kWN, q_desc + (((kk >> 2) * kWSubQ + (kk & 3) * 32) >> 4),
+          mma_ss(tmem + kWColS + (t % NS) * kWN, q_desc + (((kk >> 2) * kWSubQ + (kk & 3) * 32) >> 4),
                  k_desc + (((kk >> 2) * kWSubKV + (kk & 3) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
-        mma_commit(S_FULL(t & 1));
+        mma_commit(S_FULL(t % NS));
         mma_commit(K_EMPTY(s));
         return true;
       };
       bool ok = wait_bounded(bar_q, 0, abort_flag, p.status);
       if (ok) ok = issue_qk(0);
-      if (ok && n > 1) ok = issue_qk(1);
+      if (ok && NS > 1 && n > 1) ok = issue_qk(1);
       for (int t = 0; ok && t < n; ++t) {
         const int s = t % VS, b = t & 1;
+        // the next scores go out as soon as this step's have been read, ahead of P_t V_t
+        if (t + NS < n) {
+          if (!wait_bounded(S_FREE(t % NS), (t / NS) & 1, abort_flag, p.status)) break;
+          if (!issue_qk(t + NS)) break;
+        }
         if (!wait_bounded(P_READY(b), (t >> 1) & 1, abort_flag, p.status)) break;
         if (!wait_bounded(V_FULL(s), (t / VS) & 1, abort_flag, p.status)) break;
         tc_fence_after();
@@ -237,15 +247,10 @@ __global__ void __launch_bounds__(kWThreads, 2)
         const uint64_t v_desc = make_sdesc_sw128(base + L::kV + s * L::kStep, kWSubKV, 1024);
 #pragma unroll
         for (int kk = 0; kk < kWN / 16; ++kk)
-          mma_ts(tmem + kWColO, tmem + kWColS + b * kWN + kk * 8, v_desc + ((kk * 16 * 128) >> 4),
+          mma_ts(tmem + L::kColO, tmem + kWColP + b * (kWN / 2) + kk * 8, v_desc + ((kk * 16 * 128) >> 4),
                  idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
         mma_commit(PV_DONE(b));
-        // S_{t+2} goes over P_t, so P_t V_t has to be done; S_{t+1} is under way meanwhile
-        if (t + 2 < n) {
-          if (!wait_bounded(PV_DONE(b), (t >> 1) & 1, abort_flag, p.status)) break;
-          mbar_arrive(V_EMPTY(s));
-          ok = issue_qk(t + 2);
-        }
+        mma_commit(V_EMPTY(s));
       }
       // every MMA this thread issued completes before the block frees its tensor memory
       mma_commit(bar_drain);
@@ -266,16 +271,18 @@ __global__ void __launch_bounds__(kWThreads, 2)
     for (int t = 0; t < n; ++t) {
       const int j = it.key_step(t);
       const int b = t & 1;
-      if (!win_wait(S_FULL(b), (t >> 1) & 1, abort_flag, p.status)) {
+      if (!win_wait(S_FULL(t % NS), (t / NS) & 1, abort_flag, p.status)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t s_addr = row_tmem + kWColS + b * kWN;
+      const uint32_t s_addr = row_tmem + kWColS + (t % NS) * kWN;
       uint32_t sr[2][32];
       tmem_ld32(s_addr, sr[0]);
       tmem_ld32(s_addr + 32, sr[1]);
       tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(S_FREE(t % NS));
       if (j >= it.hi_masked || j < it.lo_masked) {
         // visible columns: [lo, hi] and the sinks up to sk
         const int hi = min(last - j * kWN, kWN - 1);
@@ -345,14 +352,21 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          tmem_ld32(row_tmem + kWColO + c * 32, o);
+          tmem_ld32(row_tmem + L::kColO + c * 32, o);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(row_tmem + kWColO + c * 32, o);
+          tmem_st32(row_tmem + L::kColO + c * 32, o);
         }
       }
-      tmem_st32(s_addr, pk);  // over the scores already read
+      if (t > 1) {  // P V_{t-2} read this buffer
+        if (!win_wait(PV_DONE(b), ((t - 2) >> 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      tmem_st32(row_tmem + kWColP + b * (kWN / 2), pk);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(P_READY(b));
@@ -372,7 +386,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        tmem_ld32(row_tmem + kWColO + c * 32, o);
+        tmem_ld32(row_tmem + L::kColO + c * 32, o);
         tmem_wait_ld();
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
@@ -406,6 +420,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #undef S_FULL
 #undef P_READY
 #undef PV_DONE
+#undef S_FREE
   tc_fence_before();
   __syncthreads();
   if (warp == 5) {
