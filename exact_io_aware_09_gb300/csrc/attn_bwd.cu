@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ CUtensorMap tm_do, const BwdParams p,
+                         const __grid_constant__ CUtensorMap tm_do,
+                         const __grid_constant__ CUtensorMap tm_dk,
+                         const __grid_constant__ CUtensorMap tm_dv, const BwdParams p,
                          const __grid_constant__ KvOrder order) {
   using L = KvLayout<D, QS>;
   extern __shared__ uint8_t smem_raw[];
@@ -472,18 +474,20 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     }
     // epilogue: warpgroup 0 stores dV, warpgroup 1 dK, once the last MMA has finished
     if (ok && n > 0) ok = ew_wait(bar_drain, 0, abort_flag, p.status);
-    if (ok) {
-      tc_fence_after();
-      const bool store = kr < p.N_kv;
-      const size_t grow = (static_cast<size_t>(bkv) * p.N_kv + (store ? kr : 0)) * D;
-      uint16_t* dst = (wg ? p.dk : p.dv) + grow;
-      if (partial) {
-        const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2 + wg;
-        store_part_row<D>(row_tmem + (wg ? L::kColDK : L::kColDV), p.part + (at * kBT + r) * D, n > 0);
-      } else if (n > 0)
-        store_acc_row<D, BF16>(row_tmem + (wg ? L::kColDK : L::kColDV), dst, store);
-      else if (store)
-        store_zero_row<D>(dst);
+    if (ok) tc_fence_after();
+    const uint32_t col = wg ? L::kColDK : L::kColDV;
+    if (partial) {
+      const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2 + wg;
+      if (ok) store_part_row<D>(row_tmem + col, p.part + (at * kBT + r) * D, n > 0);
+    } else if (n > 0) {
+      // dV over K, dK over V, whose products are done; each warpgroup its own
+      const uint32_t tile = wg ? L::kV : L::kK;
+      if (ok) stage_acc_row<BF16>(row_tmem + col, gbase + tile, r, 0, D);
+      fence_proxy_async_smem();
+      named_bar_sync(1 + wg, kEwThreads);
+      if (r == 0 && *abort_flag == 0) store_staged<D>(wg ? &tm_dk : &tm_dv, base + tile, kt * kBT, bkv);
+    } else if (kr < p.N_kv) {
+      store_zero_row<D>((wg ? p.dk : p.dv) + (static_cast<size_t>(bkv) * p.N_kv + kr) * D);
     }
   }
 #undef ST_FULL
@@ -586,7 +590,8 @@ template <int D, bool BF16, int KR, int VR, bool WINDOW>
 __global__ void __launch_bounds__(kQThreads, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+                       const __grid_constant__ CUtensorMap tm_do,
+                       const __grid_constant__ CUtensorMap tm_dq, const BwdParams p) {
   using L = QLayout<D, KR, VR>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -882,14 +887,19 @@ __global__ void __launch_bounds__(kQThreads, 1)
       mbar_arrive(DS_READY(wg));
     }
     if (ok && n > 0) ok = ew_wait(bar_drain, 0, abort_flag, p.status);
-    if (ok && wg == 0) {
-      tc_fence_after();
-      const bool store = row < p.N_q;
-      const size_t grow = (static_cast<size_t>(bh) * p.N_q + (store ? row : 0)) * D;
-      if (n > 0)
-        store_acc_row<D, BF16>(row_tmem + L::kColDQ, p.dq + grow, store);
-      else if (store)
-        store_zero_row<D>(p.dq + grow);
+    if (n > 0) {
+      // over dO, whose products are done; each warpgroup half of the columns
+      if (ok) {
+        tc_fence_after();
+        stage_acc_row<BF16>(row_tmem + L::kColDQ, gbase + L::kDO, quarter * 32 + lane, wg * (D / 2),
+                            (wg + 1) * (D / 2));
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(1, 2 * kEwThreads);
+      if (threadIdx.x == 0 && *abort_flag == 0)
+        store_staged<D>(&tm_dq, base + L::kDO, qt * kBT, bh);
+    } else if (wg == 0 && row < p.N_q) {
+      store_zero_row<D>(p.dq + (static_cast<size_t>(bh) * p.N_q + row) * D);
     }
   }
 #undef K_FULL
@@ -1112,6 +1122,11 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
       !make_tmap_3d(&tk, a.k, BF16, D, a.N_kv, bhk, rb, rb * a.N_kv, 64, kBT, 1) ||
       !make_tmap_3d(&tv, a.v, BF16, D, a.N_kv, bhk, rb, rb * a.N_kv, 64, kBT, 1))
     return -5;
+  CUtensorMap tdq, tdk, tdv;
+  if (!make_tmap_3d(&tdq, a.dq, BF16, D, a.N_q, bhq, rb, rb * a.N_q, 64, kBT, 1) ||
+      !make_tmap_3d(&tdk, a.dk, BF16, D, a.N_kv, bhk, rb, rb * a.N_kv, 64, kBT, 1) ||
+      !make_tmap_3d(&tdv, a.dv, BF16, D, a.N_kv, bhk, rb, rb * a.N_kv, 64, kBT, 1))
+    return -5;
   BwdParams p;
   const int n_qtiles = (a.N_q + kBT - 1) / kBT;
   const int nqp = n_qtiles * kBT;
@@ -1169,8 +1184,8 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   } else {
     const KvOrder* order = kv_order(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.causal,
                                     a.N_kv - a.N_q, a.window, a.sinks);
-    kkv<<<static_cast<unsigned>(kv_blocks), kKvThreads, LK::kBytes, stream>>>(tq64, tk, tv, tdo64, p,
-                                                                              *order);
+    kkv<<<static_cast<unsigned>(kv_blocks), kKvThreads, LK::kBytes, stream>>>(tq64, tk, tv, tdo64, tdk,
+                                                                              tdv, p, *order);
     if (cudaGetLastError() != cudaSuccess) return -5;
   }
   // dQ as a programmatic dependent of dK/dV: its blocks fill the SMs of dK/dV's tail.
@@ -1187,7 +1202,7 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   if (q_two) {
     const int st = launch_bwd_window_dq(a, p, static_cast<unsigned>(q_blocks), stream);
     if (st != 0) return st;
-  } else if (cudaLaunchKernelEx(&cfg, kq, tk, tv, tdo, p) != cudaSuccess) {
+  } else if (cudaLaunchKernelEx(&cfg, kq, tk, tv, tdo, tdq, p) != cudaSuccess) {
     return -5;
   }
   if constexpr (WINDOW) {

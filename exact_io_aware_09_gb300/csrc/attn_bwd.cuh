@@ -48,27 +48,38 @@ __device__ __forceinline__ bool ew_wait(uint32_t bar, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, ok);
 }
 
-// One 128 x D tile row r of a tensor-memory accumulator -> 16-bit values of global row `dst`.
-template <int D, bool BF16>
-__device__ __forceinline__ void store_acc_row(uint32_t row_tmem_col, uint16_t* dst, bool store) {
+// Columns [c0, c1) (multiples of 32) of row r of a 128 x D accumulator as 16-bit values in a tile of
+// shared memory (64-column sub-tiles kSub apart, 128-byte swizzle), from where TMA stores take the rows
+// that exist: written to memory by the threads that hold them, a warp's stores would touch 32 lines each
+// (a block's end took a microsecond longer).
+template <bool BF16>
+__device__ __forceinline__ void stage_acc_row(uint32_t row_tmem_col, uint8_t* tile, int r, int c0, int c1) {
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
+  for (int c = c0 / 32; c < c1 / 32; ++c) {
     uint32_t a[32];
     tmem_ld32(row_tmem_col + c * 32, a);
     tmem_wait_ld();
-    if (store) {
-      uint4* out = reinterpret_cast<uint4*>(dst + c * 32);
+    uint8_t* sub = tile + (c >> 1) * kSub;
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4)
-        out[q4] = make_uint4(pack2<BF16>(__uint_as_float(a[8 * q4 + 0]), __uint_as_float(a[8 * q4 + 1])),
-                             pack2<BF16>(__uint_as_float(a[8 * q4 + 2]), __uint_as_float(a[8 * q4 + 3])),
-                             pack2<BF16>(__uint_as_float(a[8 * q4 + 4]), __uint_as_float(a[8 * q4 + 5])),
-                             pack2<BF16>(__uint_as_float(a[8 * q4 + 6]), __uint_as_float(a[8 * q4 + 7])));
-    }
+    for (int q4 = 0; q4 < 4; ++q4)
+      *reinterpret_cast<uint4*>(sub + sw128(r, (c & 1) * 4 + q4)) =
+          make_uint4(pack2<BF16>(__uint_as_float(a[8 * q4 + 0]), __uint_as_float(a[8 * q4 + 1])),
+                     pack2<BF16>(__uint_as_float(a[8 * q4 + 2]), __uint_as_float(a[8 * q4 + 3])),
+                     pack2<BF16>(__uint_as_float(a[8 * q4 + 4]), __uint_as_float(a[8 * q4 + 5])),
+                     pack2<BF16>(__uint_as_float(a[8 * q4 + 6]), __uint_as_float(a[8 * q4 + 7])));
   }
 }
 
-// The same as fp32 values (zeros for an accumulator nothing was added to).
+// A staged tile out to rows row0 .. of plane z (one thread; the stages' writes fenced before).
+template <int D>
+__device__ __forceinline__ void store_staged(const CUtensorMap* m, uint32_t tile, int row0, int z) {
+#pragma unroll
+  for (int sub = 0; sub < D / 64; ++sub) tma_store_3d(m, tile + sub * kSub, sub * 64, row0, z);
+  tma_store_commit();
+  tma_store_wait_read0();  // the block's shared memory may go
+}
+
+// Row of a 128 x D accumulator as fp32 values (zeros for an accumulator nothing was added to).
 template <int D>
 __device__ __forceinline__ void store_part_row(uint32_t row_tmem_col, float* dst, bool any) {
 #pragma unroll 1

@@ -68,26 +68,6 @@ __device__ __forceinline__ void mma_grad(uint32_t d_tmem, uint32_t a_tmem, uint3
   mma_tmem_rows_d<kStepQ>(d_tmem, a_tmem, make_sdesc_sw128(b_smem, kBwStep, 1024), idesc, accumulate);
 }
 
-// Row r of a 128 x 64 accumulator as 16-bit values in a swizzled tile of shared memory, from where one
-// TMA store takes the rows that exist: written row by row from the threads that hold them, a warp's
-// stores would touch 32 lines each (a block's end took a microsecond longer).
-template <bool BF16>
-__device__ __forceinline__ void stage_acc_row(uint32_t row_tmem_col, uint8_t* tile, int r) {
-#pragma unroll 1
-  for (int c = 0; c < kBwD / 32; ++c) {
-    uint32_t a[32];
-    tmem_ld32(row_tmem_col + c * 32, a);
-    tmem_wait_ld();
-#pragma unroll
-    for (int q4 = 0; q4 < 4; ++q4)
-      *reinterpret_cast<uint4*>(tile + sw128(r, c * 4 + q4)) =
-          make_uint4(pack2<BF16>(__uint_as_float(a[8 * q4 + 0]), __uint_as_float(a[8 * q4 + 1])),
-                     pack2<BF16>(__uint_as_float(a[8 * q4 + 2]), __uint_as_float(a[8 * q4 + 3])),
-                     pack2<BF16>(__uint_as_float(a[8 * q4 + 4]), __uint_as_float(a[8 * q4 + 5])),
-                     pack2<BF16>(__uint_as_float(a[8 * q4 + 6]), __uint_as_float(a[8 * q4 + 7])));
-  }
-}
-
 }  // namespace
 
 template <bool BF16>
@@ -354,30 +334,29 @@ __global__ void __launch_bounds__(kBwThreads, 2)
       mbar_arrive(bar_ds);
     }
     if (ok && n > 0) ok = ew_wait(bar_drain, 0, abort_flag, p.status);
-    if (ok) {
-      tc_fence_after();
-      const bool store = kr < p.N_kv;
-      const size_t row = (static_cast<size_t>(bkv) * p.N_kv + (store ? kr : 0)) * kBwD;
-      if (partial) {
-        const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2;
+    if (ok) tc_fence_after();
+    if (partial) {
+      const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2;
+      if (ok) {
         store_part_row<kBwD>(row_tmem + L::kColDV, p.part + (at * kBT + r) * kBwD, n > 0);
         store_part_row<kBwD>(row_tmem + L::kColDK, p.part + ((at + 1) * kBT + r) * kBwD, n > 0);
-      } else if (n > 0) {
-        // over K and V, whose products are done
-        stage_acc_row<BF16>(row_tmem + L::kColDV, gbase + L::kK, r);
-        stage_acc_row<BF16>(row_tmem + L::kColDK, gbase + L::kV, r);
-        fence_proxy_async_smem();
-        named_bar_sync(1, kBT);
-        if (threadIdx.x == 0) {
-          tma_store_3d(&tm_dv, base + L::kK, 0, kt * kBT, bkv);
-          tma_store_3d(&tm_dk, base + L::kV, 0, kt * kBT, bkv);
-          tma_store_commit();
-          tma_store_wait_read0();  // the block's shared memory may go
-        }
-      } else if (store) {
-        store_zero_row<kBwD>(p.dv + row);
-        store_zero_row<kBwD>(p.dk + row);
       }
+    } else if (n > 0) {
+      // over K and V, whose products are done
+      if (ok) {
+        stage_acc_row<BF16>(row_tmem + L::kColDV, gbase + L::kK, r, 0, kBwD);
+        stage_acc_row<BF16>(row_tmem + L::kColDK, gbase + L::kV, r, 0, kBwD);
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(1, kBT);
+      if (threadIdx.x == 0 && *abort_flag == 0) {
+        store_staged<kBwD>(&tm_dv, base + L::kK, kt * kBT, bkv);
+        store_staged<kBwD>(&tm_dk, base + L::kV, kt * kBT, bkv);
+      }
+    } else if (kr < p.N_kv) {
+      const size_t row = (static_cast<size_t>(bkv) * p.N_kv + kr) * kBwD;
+      store_zero_row<kBwD>(p.dv + row);
+      store_zero_row<kBwD>(p.dk + row);
     }
   }
 #undef ST_FULL
@@ -621,21 +600,17 @@ __global__ void __launch_bounds__(kBwThreads, 2)
       tc_fence_before();
       mbar_arrive(DS_READY(b));
     }
-    if (ok && n > 0) ok = ew_wait(DQ_DONE((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.status);
-    if (ok) {
-      tc_fence_after();
-      if (n > 0) {
-        stage_acc_row<BF16>(row_tmem + L::kColDQ, gbase + L::kQ, r);  // over Q, whose products are done
-        fence_proxy_async_smem();
-        named_bar_sync(1, kBT);
-        if (threadIdx.x == 0) {
-          tma_store_3d(&tm_dq, base + L::kQ, 0, qt * kBT, bh);
-          tma_store_commit();
-          tma_store_wait_read0();  // the block's shared memory may go
-        }
-      } else if (row < p.N_q) {
-        store_zero_row<kBwD>(p.dq + (static_cast<size_t>(bh) * p.N_q + row) * kBwD);
+    if (n > 0) {
+      if (ok) ok = ew_wait(DQ_DONE((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.status);
+      if (ok) {
+        tc_fence_after();
+        stage_acc_row<BF16>(row_tmem + L::kColDQ, gbase + L::kQ, r, 0, kBwD);  // over Q, whose products are done
       }
+      fence_proxy_async_smem();
+      named_bar_sync(1, kBT);
+      if (threadIdx.x == 0 && *abort_flag == 0) store_staged<kBwD>(&tm_dq, base + L::kQ, qt * kBT, bh);
+    } else if (row < p.N_q) {
+      store_zero_row<kBwD>(p.dq + (static_cast<size_t>(bh) * p.N_q + row) * kBwD);
     }
   }
 #undef K_FULL

@@ -379,32 +379,36 @@ __global__ void __launch_bounds__(kWThreads, 2)
         for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
         p.lse[row_index] = -INFINITY;
       }
-    } else if (ok && win_wait(PV_DONE((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.status)) {
-      // O / l into Q's shared memory (its products are done) and out by one TMA store per 64 columns
-      tc_fence_after();
-      const float inv_l = (l > 0.0f) ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // a NaN sum stays one
+    } else {
+      // O / l into Q's shared memory (its products are done) and out by one TMA store per 64 columns; a
+      // warp whose wait ran out still meets the others at the barrier
+      if (ok) ok = win_wait(PV_DONE((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.status);
+      if (ok) {
+        tc_fence_after();
+        const float inv_l = (l > 0.0f) ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // a NaN sum stays one
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(row_tmem + L::kColO + c * 32, o);
-        tmem_wait_ld();
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(row_tmem + L::kColO + c * 32, o);
+          tmem_wait_ld();
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const uint4 w = make_uint4(
-              pack2<BF16>(__uint_as_float(o[q4 * 8 + 0]) * inv_l, __uint_as_float(o[q4 * 8 + 1]) * inv_l),
-              pack2<BF16>(__uint_as_float(o[q4 * 8 + 2]) * inv_l, __uint_as_float(o[q4 * 8 + 3]) * inv_l),
-              pack2<BF16>(__uint_as_float(o[q4 * 8 + 4]) * inv_l, __uint_as_float(o[q4 * 8 + 5]) * inv_l),
-              pack2<BF16>(__uint_as_float(o[q4 * 8 + 6]) * inv_l, __uint_as_float(o[q4 * 8 + 7]) * inv_l));
-          const uint32_t chunk = c * 4 + q4;
-          *reinterpret_cast<uint4*>(gbase + (chunk >> 3) * kWSubQ + sw128(r, chunk & 7)) = w;
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const uint4 w = make_uint4(
+                pack2<BF16>(__uint_as_float(o[q4 * 8 + 0]) * inv_l, __uint_as_float(o[q4 * 8 + 1]) * inv_l),
+                pack2<BF16>(__uint_as_float(o[q4 * 8 + 2]) * inv_l, __uint_as_float(o[q4 * 8 + 3]) * inv_l),
+                pack2<BF16>(__uint_as_float(o[q4 * 8 + 4]) * inv_l, __uint_as_float(o[q4 * 8 + 5]) * inv_l),
+                pack2<BF16>(__uint_as_float(o[q4 * 8 + 6]) * inv_l, __uint_as_float(o[q4 * 8 + 7]) * inv_l));
+            const uint32_t chunk = c * 4 + q4;
+            *reinterpret_cast<uint4*>(gbase + (chunk >> 3) * kWSubQ + sw128(r, chunk & 7)) = w;
+          }
         }
+        if (row < p.N_q)
+          p.lse[row_index] = (l == 0.0f) ? -INFINITY
+                                         : ((m == -INFINITY ? 0.0f : m) + lg2(l)) * 0.69314718055994531f;
       }
-      if (row < p.N_q)
-        p.lse[row_index] = (l == 0.0f) ? -INFINITY
-                                       : ((m == -INFINITY ? 0.0f : m) + lg2(l)) * 0.69314718055994531f;
       fence_proxy_async_smem();
       named_bar_sync(1, kWM);
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && *abort_flag == 0) {
 #pragma unroll
         for (int sub = 0; sub < D / 64; ++sub)
           tma_store_3d(&tm_o, base + sub * kWSubQ, sub * 64, it.qt * kWM, it.bh);
