@@ -235,8 +235,25 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     }
   }
   const int n_steps = 2 * n;              // two 64-query steps per query tile
+  auto load_stage = [&](int i) {
+    const int s = i % QS;
+    const int tile = tile0 + (i >> 1);
+    const int g = tile / nq_per;
+    const int q0 = (qt_lo + tile % nq_per) * kBT + (i & 1) * kStepQ;
+    const int bhq = b * p.Hq + hk * p.G + g;
+    const uint32_t st = base + L::kStages + s * L::kStage;
+    mbar_arrive_expect_tx(ST_FULL(s), 2 * L::kHalf + 512);
+#pragma unroll
+    for (int sub = 0; sub < D / 64; ++sub) {
+      tma_load_3d(st + sub * L::kHalfSub, &tm_q, ST_FULL(s), sub * 64, q0, bhq);
+      tma_load_3d(st + L::kHalf + sub * L::kHalfSub, &tm_do, ST_FULL(s), sub * 64, q0, bhq);
+    }
+    const size_t vec = static_cast<size_t>(bhq) * p.nqp + static_cast<size_t>(q0);
+    bulk_load(st + 2 * L::kHalf, p.lse2 + vec, kStepQ * 4, ST_FULL(s));
+    bulk_load(st + 2 * L::kHalf + 256, p.dvec + vec, kStepQ * 4, ST_FULL(s));
+  };
 
-  if (threadIdx.x == 0) {
+  if (warp == kBwdProducerWarp && lane == 0) {
     mbar_init(bar_kv, 1);
     for (int s = 0; s < QS; ++s) {
       mbar_init(ST_FULL(s), 1);
@@ -255,6 +272,16 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     mbar_init(bar_drain_dp, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    // the first loads go out before the block's setup is done
+    if (n > 0) {
+      mbar_arrive_expect_tx(bar_kv, 2 * L::kTile);
+#pragma unroll
+      for (int sub = 0; sub < D / 64; ++sub) {
+        tma_load_3d(base + L::kK + sub * kSub, &tm_k, bar_kv, sub * 64, kt * kBT, bkv);
+        tma_load_3d(base + L::kV + sub * kSub, &tm_v, bar_kv, sub * 64, kt * kBT, bkv);
+      }
+      load_stage(0);
+    }
   }
   if (warp == kBwdIssuerWarp) {
     tmem_alloc(smem_u32(tmem_slot), kBwdTmemCols);
@@ -267,34 +294,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 
   if (warp == kBwdProducerWarp) {
     if (lane == 0 && n > 0) {
-      prefetch_tmap(&tm_q);
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-      prefetch_tmap(&tm_do);
-      mbar_arrive_expect_tx(bar_kv, 2 * L::kTile);
-#pragma unroll
-      for (int sub = 0; sub < D / 64; ++sub) {
-        tma_load_3d(base + L::kK + sub * kSub, &tm_k, bar_kv, sub * 64, kt * kBT, bkv);
-        tma_load_3d(base + L::kV + sub * kSub, &tm_v, bar_kv, sub * 64, kt * kBT, bkv);
-      }
-      int issued = 0;
-      for (int i = 0; i < n_steps; ++i) {
-        const int s = i % QS;
-        if (i >= QS && !wait_bounded(ST_EMPTY(s), ((i / QS) - 1) & 1, abort_flag, p.status)) break;
-        const int tile = tile0 + (i >> 1);
-        const int g = tile / nq_per;
-        const int q0 = (qt_lo + tile % nq_per) * kBT + (i & 1) * kStepQ;
-        const int bhq = b * p.Hq + hk * p.G + g;
-        const uint32_t st = base + L::kStages + s * L::kStage;
-        mbar_arrive_expect_tx(ST_FULL(s), 2 * L::kHalf + 512);
-#pragma unroll
-        for (int sub = 0; sub < D / 64; ++sub) {
-          tma_load_3d(st + sub * L::kHalfSub, &tm_q, ST_FULL(s), sub * 64, q0, bhq);
-          tma_load_3d(st + L::kHalf + sub * L::kHalfSub, &tm_do, ST_FULL(s), sub * 64, q0, bhq);
-        }
-        const size_t vec = static_cast<size_t>(bhq) * p.nqp + static_cast<size_t>(q0);
-        bulk_load(st + 2 * L::kHalf, p.lse2 + vec, kStepQ * 4, ST_FULL(s));
-        bulk_load(st + 2 * L::kHalf + 256, p.dvec + vec, kStepQ * 4, ST_FULL(s));
+      int issued = 1;
+      for (int i = 1; i < n_steps; ++i) {
+        if (i >= QS && !wait_bounded(ST_EMPTY(i % QS), ((i / QS) - 1) & 1, abort_flag, p.status)) break;
+        load_stage(i);
         issued = i + 1;
       }
       wait_bounded(bar_kv, 0, nullptr, p.status, kBwdDrainNs);
@@ -647,7 +650,21 @@ __global__ void __launch_bounds__(kQThreads, 1)
                 q_row);
   }
 
-  if (threadIdx.x == 0) {
+  auto load_k = [&](int t) {
+    mbar_arrive_expect_tx(K_FULL(t % KR), L::kTile);
+#pragma unroll
+    for (int sub = 0; sub < D / 64; ++sub)
+      tma_load_3d(base + L::kK + (t % KR) * L::kTile + sub * kSub, &tm_k, K_FULL(t % KR), sub * 64,
+                  key_tile(t) * kBT, kv_plane);
+  };
+  auto load_v = [&](int t) {
+    mbar_arrive_expect_tx(V_FULL(t % VR), L::kTile);
+#pragma unroll
+    for (int sub = 0; sub < D / 64; ++sub)
+      tma_load_3d(base + L::kV + (t % VR) * L::kTile + sub * kSub, &tm_v, V_FULL(t % VR), sub * 64,
+                  key_tile(t) * kBT, kv_plane);
+  };
+  if (warp == kBwdProducerWarp && lane == 0) {
     for (int s = 0; s < KR; ++s) {
       mbar_init(K_FULL(s), 1);
       mbar_init(K_EMPTY(s), 1);
@@ -670,6 +687,15 @@ __global__ void __launch_bounds__(kQThreads, 1)
     mbar_init(bar_drain_dp, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    // the first loads go out before the block's setup is done
+    if (n > 0) {
+      load_k(0);
+      mbar_arrive_expect_tx(bar_do, L::kTile);
+#pragma unroll
+      for (int sub = 0; sub < D / 64; ++sub)
+        tma_load_3d(base + L::kDO + sub * kSub, &tm_do, bar_do, sub * 64, qt * kBT, bh);
+      load_v(0);
+    }
   }
   if (warp == kBwdIssuerWarp) {
     tmem_alloc(smem_u32(tmem_slot), kBwdTmemCols);
@@ -682,29 +708,13 @@ __global__ void __launch_bounds__(kQThreads, 1)
 
   if (warp == kBwdProducerWarp) {
     if (lane == 0 && n > 0) {
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-      prefetch_tmap(&tm_do);
-      mbar_arrive_expect_tx(bar_do, L::kTile);
-#pragma unroll
-      for (int sub = 0; sub < D / 64; ++sub)
-        tma_load_3d(base + L::kDO + sub * kSub, &tm_do, bar_do, sub * 64, qt * kBT, bh);
-      int issued_k = 0, issued_v = 0;
-      for (int t = 0; t < n; ++t) {
-        const int sk = t % KR, sv = t % VR;
-        if (t >= KR && !wait_bounded(K_EMPTY(sk), ((t / KR) - 1) & 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(K_FULL(sk), L::kTile);
-#pragma unroll
-        for (int sub = 0; sub < D / 64; ++sub)
-          tma_load_3d(base + L::kK + sk * L::kTile + sub * kSub, &tm_k, K_FULL(sk), sub * 64,
-                      key_tile(t) * kBT, kv_plane);
+      int issued_k = 1, issued_v = 1;
+      for (int t = 1; t < n; ++t) {
+        if (t >= KR && !wait_bounded(K_EMPTY(t % KR), ((t / KR) - 1) & 1, abort_flag, p.status)) break;
+        load_k(t);
         issued_k = t + 1;
-        if (t >= VR && !wait_bounded(V_EMPTY(sv), ((t / VR) - 1) & 1, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(V_FULL(sv), L::kTile);
-#pragma unroll
-        for (int sub = 0; sub < D / 64; ++sub)
-          tma_load_3d(base + L::kV + sv * L::kTile + sub * kSub, &tm_v, V_FULL(sv), sub * 64,
-                      key_tile(t) * kBT, kv_plane);
+        if (t >= VR && !wait_bounded(V_EMPTY(t % VR), ((t / VR) - 1) & 1, abort_flag, p.status)) break;
+        load_v(t);
         issued_v = t + 1;
       }
       wait_bounded(bar_do, 0, nullptr, p.status, kBwdDrainNs);
