@@ -10,7 +10,7 @@
 //
 // Both kernels step through 64 rows of the other side, one elementwise warpgroup (thread = row of the
 // block's own tile) and one issuing thread.  Roles (192 threads): warps 0-3 elementwise and epilogue,
-// warp 4 TMA producer, warp 5 tcgen05 issuer (it owns the tensor memory).  Every wait on a barrier is
+// warp 4 TMA producer, warps 5 and 6 tcgen05 issuers (warp 5 owns the tensor memory).  Every wait on a barrier is
 // bounded.
 #include "attn_bwd.cuh"
 
@@ -18,7 +18,7 @@ namespace attn {
 
 namespace {
 
-constexpr int kBwThreads = 192;
+constexpr int kBwThreads = 224;
 constexpr int kBwD = 64;
 constexpr uint32_t kBwTmemCols = 256;
 constexpr uint32_t kBwTile = kBT * kBwD * 2;     // 128 rows
@@ -32,8 +32,9 @@ struct KvShort {
   static constexpr uint32_t kStage = (2 * kBwStep + 512 + 1023) / 1024 * 1024;
   static constexpr uint32_t kK = 0, kV = kBwTile, kStages = 2 * kBwTile;
   static constexpr uint32_t kBar = kStages + kQS * kStage;
-  // kv_full, st_full[QS], st_empty[QS], s_full, dp_full, p_ready, ds_ready, p_free, ds_free, drain
-  static constexpr uint32_t kNumBars = 1 + 2 * kQS + 7;
+  // kv_full, st_full[QS], st_empty[QS], s_full, dp_full, p_ready, ds_ready, p_free, ds_free,
+  // drains of the two issuers
+  static constexpr uint32_t kNumBars = 1 + 2 * kQS + 8;
   static constexpr uint32_t kMisc = kBar + kNumBars * 8;
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;  // + alignment
   static constexpr uint32_t kColS = 0, kColDP = 64, kColDV = 128, kColDK = 192;
@@ -47,8 +48,8 @@ struct QShort {
   static constexpr uint32_t kQ = 0, kDO = kBwTile, kK = 2 * kBwTile, kV = kK + kKS * kBwStep;
   static constexpr uint32_t kBar = kV + kVS * kBwStep;
   // q and dO, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full, s_free, ds_ready[2],
-  // dq_done[2], dp_full, dp_free, drain
-  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 9;
+  // dq_done[2], dp_full, dp_free, drains of the two issuers
+  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 10;
   static constexpr uint32_t kMisc = kBar + kNumBars * 8;
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;
   static constexpr uint32_t kColS = 0, kColDS = 64, kColDP = 128, kColDQ = 192;
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
   const uint32_t bar_ds = bar_b + 24u;      // dS^T stored (128)
   const uint32_t bar_pfree = bar_b + 32u;   // dV product done: S^T columns free
   const uint32_t bar_dsfree = bar_b + 40u;  // dK product done: dP^T columns free
-  const uint32_t bar_drain = bar_b + 48u;
+  const uint32_t bar_drain = bar_b + 48u, bar_drain2 = bar_b + 56u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   const int warp = threadIdx.x >> 5;
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     mbar_init(bar_kv, 1);
     for (int s = 0; s < QS; ++s) {
       mbar_init(ST_FULL(s), 1);
-      mbar_init(ST_EMPTY(s), 1);
+      mbar_init(ST_EMPTY(s), 2);
     }
     mbar_init(bar_s, 1);
     mbar_init(bar_dp, 1);
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     mbar_init(bar_pfree, 1);
     mbar_init(bar_dsfree, 1);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_drain2, 1);
     *abort_flag = 0;
     fence_barrier_init();
     // the first loads go out before the block's setup is done
@@ -199,50 +201,53 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     }
     __syncwarp();
   } else if (warp == 5) {
-    // ----------------------------------------------------------------- tcgen05 issuer
+    // ------------------------------------------ tcgen05 issuer of S^T = K Q^T and dV += P^T dO
     if (lane == 0 && n > 0) {
       constexpr uint32_t idesc_s = make_idesc_f16(BF16, kBT, kStepQ, false);
       constexpr uint32_t idesc_g = make_idesc_f16(BF16, kBT, kBwD, true);
       auto stage = [&](int i) { return base + L::kStages + (i % QS) * L::kStage; };
-      bool ok = wait_bounded(bar_kv, 0, abort_flag, p.status) &&
-                wait_bounded(ST_FULL(0), 0, abort_flag, p.status);
-      if (ok) {
-        tc_fence_after();
-        mma_scores(tmem + L::kColS, base + L::kK, stage(0), idesc_s);
-        mma_commit(bar_s);
-        mma_scores(tmem + L::kColDP, base + L::kV, stage(0) + kBwStep, idesc_s);
-        mma_commit(bar_dp);
-      }
-      for (int i = 0; ok && i < n; ++i) {
-        const bool more = i + 1 < n;
-        if (!wait_bounded(bar_p, i & 1, abort_flag, p.status)) break;
-        tc_fence_after();
-        mma_grad(tmem + L::kColDV, tmem + L::kColS, stage(i) + kBwStep, idesc_g, i > 0);  // dV += P^T dO
-        mma_commit(bar_pfree);
-        if (more) {
-          // S^T_{i+1} goes over P^T_i, dP^T_{i+1} over dS^T_i: each once the product that reads it is
-          // done; the first meanwhile runs under the elementwise step of dS^T_i
-          if (!wait_bounded(ST_FULL((i + 1) % QS), ((i + 1) / QS) & 1, abort_flag, p.status)) break;
-          if (!wait_bounded(bar_pfree, i & 1, abort_flag, p.status)) break;
+      if (wait_bounded(bar_kv, 0, abort_flag, p.status)) {
+        for (int i = 0; i < n; ++i) {
+          if (!wait_bounded(ST_FULL(i % QS), (i / QS) & 1, abort_flag, p.status)) break;
+          // S^T_i goes over P^T_{i-1}, once the product that reads it is done
+          if (i > 0 && !wait_bounded(bar_pfree, (i - 1) & 1, abort_flag, p.status)) break;
           tc_fence_after();
-          mma_scores(tmem + L::kColS, base + L::kK, stage(i + 1), idesc_s);
+          mma_scores(tmem + L::kColS, base + L::kK, stage(i), idesc_s);
           mma_commit(bar_s);
-        }
-        if (!wait_bounded(bar_ds, i & 1, abort_flag, p.status)) break;
-        tc_fence_after();
-        mma_grad(tmem + L::kColDK, tmem + L::kColDP, stage(i), idesc_g, i > 0);  // dK += dS^T Q
-        mma_commit(ST_EMPTY(i % QS));
-        mma_commit(bar_dsfree);
-        if (more) {
-          if (!wait_bounded(bar_dsfree, i & 1, abort_flag, p.status)) break;
+          if (!wait_bounded(bar_p, i & 1, abort_flag, p.status)) break;
           tc_fence_after();
-          mma_scores(tmem + L::kColDP, base + L::kV, stage(i + 1) + kBwStep, idesc_s);
-          mma_commit(bar_dp);
+          mma_grad(tmem + L::kColDV, tmem + L::kColS, stage(i) + kBwStep, idesc_g, i > 0);
+          mma_commit(bar_pfree);
+          mma_commit(ST_EMPTY(i % QS));
         }
       }
       // every MMA this thread issued completes before the block frees its tensor memory
       mma_commit(bar_drain);
       wait_bounded(bar_drain, 0, nullptr, p.status, kBwdDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------ tcgen05 issuer of dP^T = V dO^T and dK += dS^T Q
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_s = make_idesc_f16(BF16, kBT, kStepQ, false);
+      constexpr uint32_t idesc_g = make_idesc_f16(BF16, kBT, kBwD, true);
+      auto stage = [&](int i) { return base + L::kStages + (i % QS) * L::kStage; };
+      if (wait_bounded(bar_kv, 0, abort_flag, p.status)) {
+        for (int i = 0; i < n; ++i) {
+          if (!wait_bounded(ST_FULL(i % QS), (i / QS) & 1, abort_flag, p.status)) break;
+          if (i > 0 && !wait_bounded(bar_dsfree, (i - 1) & 1, abort_flag, p.status)) break;
+          tc_fence_after();
+          mma_scores(tmem + L::kColDP, base + L::kV, stage(i) + kBwStep, idesc_s);
+          mma_commit(bar_dp);
+          if (!wait_bounded(bar_ds, i & 1, abort_flag, p.status)) break;
+          tc_fence_after();
+          mma_grad(tmem + L::kColDK, tmem + L::kColDP, stage(i), idesc_g, i > 0);
+          mma_commit(bar_dsfree);
+          mma_commit(ST_EMPTY(i % QS));
+        }
+      }
+      mma_commit(bar_drain2);
+      wait_bounded(bar_drain2, 0, nullptr, p.status, kBwdDrainNs);
     }
     __syncwarp();
   } else {
@@ -333,7 +338,8 @@ __global__ void __launch_bounds__(kBwThreads, 2)
       tc_fence_before();
       mbar_arrive(bar_ds);
     }
-    if (ok && n > 0) ok = ew_wait(bar_drain, 0, abort_flag, p.status);
+    if (ok && n > 0)
+      ok = ew_wait(bar_drain, 0, abort_flag, p.status) && ew_wait(bar_drain2, 0, abort_flag, p.status);
     if (ok) tc_fence_after();
     if (partial) {
       const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2;
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
 #define DQ_DONE(b) (bar_b + 8u * (4 + (b)))   // dQ += dS_t K_t done: dS buffer free
   const uint32_t bar_dp = bar_b + 48u;      // dP_t written
   const uint32_t bar_dpfree = bar_b + 56u;  // dP_t read (128 arrivals)
-  const uint32_t bar_drain = bar_b + 64u;
+  const uint32_t bar_drain = bar_b + 64u, bar_drain2 = bar_b + 72u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   const int warp = threadIdx.x >> 5;
@@ -442,6 +448,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     mbar_init(bar_dp, 1);
     mbar_init(bar_dpfree, kBT);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_drain2, 1);
     *abort_flag = 0;
     fence_barrier_init();
     // the first loads go out before the block's setup is done
@@ -483,7 +490,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     }
     __syncwarp();
   } else if (warp == 5) {
-    // ----------------------------------------------------------------- tcgen05 issuer
+    // ------------------------------------------ tcgen05 issuer of S = Q K^T and dQ += dS K
     if (lane == 0 && n > 0) {
       constexpr uint32_t idesc_s = make_idesc_f16(BF16, kBT, kStepQ, false);
       constexpr uint32_t idesc_g = make_idesc_f16(BF16, kBT, kBwD, true);
@@ -494,33 +501,41 @@ __global__ void __launch_bounds__(kBwThreads, 2)
         mma_commit(bar_s);
         return true;
       };
-      auto issue_dp = [&](int t) -> bool {
-        if (!wait_bounded(V_FULL(t % VS), (t / VS) & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-        mma_scores(tmem + L::kColDP, base + L::kDO, base + L::kV + (t % VS) * kBwStep, idesc_s);
-        mma_commit(bar_dp);
-        mma_commit(V_EMPTY(t % VS));
-        return true;
-      };
-      bool ok = wait_bounded(bar_q, 0, abort_flag, p.status) && issue_s(0) && issue_dp(0);
+      bool ok = wait_bounded(bar_q, 0, abort_flag, p.status) && issue_s(0);
       for (int t = 0; ok && t < n; ++t) {
         const int b = t & 1;
-        if (t + 1 < n) {  // the next step's products, each as soon as this step's have been read
+        if (t + 1 < n) {  // the next step's scores as soon as this step's have been read
           if (!wait_bounded(bar_sfree, t & 1, abort_flag, p.status)) break;
           if (!issue_s(t + 1)) break;
-          if (!wait_bounded(bar_dpfree, t & 1, abort_flag, p.status)) break;
-          if (!issue_dp(t + 1)) break;
         }
         if (!wait_bounded(DS_READY(b), (t >> 1) & 1, abort_flag, p.status)) break;
         tc_fence_after();
         mma_grad(tmem + L::kColDQ, tmem + L::kColDS + b * (kStepQ / 2), base + L::kK + (t % KS) * kBwStep,
-                 idesc_g, t > 0);  // dQ += dS K
+                 idesc_g, t > 0);
         mma_commit(K_EMPTY(t % KS));
         mma_commit(DQ_DONE(b));
       }
       // every MMA this thread issued completes before the block frees its tensor memory
       mma_commit(bar_drain);
       wait_bounded(bar_drain, 0, nullptr, p.status, kBwdDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------ tcgen05 issuer of dP = dO V^T
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_s = make_idesc_f16(BF16, kBT, kStepQ, false);
+      if (wait_bounded(bar_q, 0, abort_flag, p.status)) {
+        for (int t = 0; t < n; ++t) {
+          if (!wait_bounded(V_FULL(t % VS), (t / VS) & 1, abort_flag, p.status)) break;
+          if (t > 0 && !wait_bounded(bar_dpfree, (t - 1) & 1, abort_flag, p.status)) break;
+          tc_fence_after();
+          mma_scores(tmem + L::kColDP, base + L::kDO, base + L::kV + (t % VS) * kBwStep, idesc_s);
+          mma_commit(bar_dp);
+          mma_commit(V_EMPTY(t % VS));
+        }
+      }
+      mma_commit(bar_drain2);
+      wait_bounded(bar_drain2, 0, nullptr, p.status, kBwdDrainNs);
     }
     __syncwarp();
   } else {

@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kWM = 128;        // query rows
 constexpr int kWN = 64;         // keys of a step
-constexpr int kWThreads = 192;
+constexpr int kWThreads = 224;
 constexpr uint32_t kWSubQ = kWM * 128;   // one 64-column sub-tile of Q
 constexpr uint32_t kWSubKV = kWN * 128;  // ... of a K or V step
 constexpr uint32_t kWTmemCols = 256;
@@ -58,8 +58,9 @@ struct WinLayout {
   static constexpr uint32_t kK = kQBytes;
   static constexpr uint32_t kV = kK + kKS * kStep;
   static constexpr uint32_t kBar = kV + kVS * kStep;
-  // q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_ready[2], pv_done[2], drain, s_free[2]
-  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 9;
+  // q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_ready[2], pv_done[2], drain, s_free[2],
+  // drain of the S issuer
+  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 10;
   static constexpr uint32_t kMisc = kBar + kNumBars * 8;
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;  // + alignment
   static_assert(2 * (kBytes + 1024) <= 233472, "two blocks on an SM");
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
 #define PV_DONE(b) (bar_b + 8u * (4 + (b)))
   const uint32_t bar_drain = bar_b + 8u * 6;
 #define S_FREE(b) (bar_b + 8u * (7 + (b)))
+  const uint32_t bar_drain_s = bar_b + 8u * 9;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   const int warp = threadIdx.x >> 5;
@@ -169,6 +171,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
       mbar_init(S_FREE(b), kWM);
     }
     mbar_init(bar_drain, 1);
+    mbar_init(bar_drain_s, 1);
     *abort_flag = 0;
     fence_barrier_init();
     // the first loads go out before the block's setup is done
@@ -212,36 +215,38 @@ __global__ void __launch_bounds__(kWThreads, 2)
     }
     __syncwarp();
   } else if (warp == 5) {
-    // ----------------------------------------------------------------- tcgen05 issuer
+    // ----------------------------------------------------------------- tcgen05 issuer of S
     if (lane == 0 && n > 0) {
       constexpr uint32_t idesc_qk = make_idesc_f16(BF16, kWM, kWN, false);
-      constexpr uint32_t idesc_pv = make_idesc_f16(BF16, kWM, D, true);
       const uint64_t q_desc = make_sdesc_sw128(base, 16, 1024);
-      auto issue_qk = [&](int t) -> bool {  // S_t into buffer t % NS
-        const int s = t % KS;
-        if (!wait_bounded(K_FULL(s), (t / KS) & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-        const uint64_t k_desc = make_sdesc_sw128(base + L::kK + s * L::kStep, 16, 1024);
+      if (wait_bounded(bar_q, 0, abort_flag, p.status)) {
+        for (int t = 0; t < n; ++t) {  // S_t into buffer t % NS, once S_{t-NS} has been read
+          const int s = t % KS, b = t % NS;
+          if (!wait_bounded(K_FULL(s), (t / KS) & 1, abort_flag, p.status)) break;
+          if (t >= NS && !wait_bounded(S_FREE(b), ((t / NS) - 1) & 1, abort_flag, p.status)) break;
+          tc_fence_after();
+          const uint64_t k_desc = make_sdesc_sw128(base + L::kK + s * L::kStep, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + kWColS + (t % NS) * kWN, q_desc + (((kk >> 2) * kWSubQ + (kk & 3) * 32) >> 4),
-                 k_desc + (((kk >> 2) * kWSubKV + (kk & 3) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
-        mma_commit(S_FULL(t % NS));
-        mma_commit(K_EMPTY(s));
-        return true;
-      };
-      bool ok = wait_bounded(bar_q, 0, abort_flag, p.status);
-      if (ok) ok = issue_qk(0);
-      if (ok && NS > 1 && n > 1) ok = issue_qk(1);
-      for (int t = 0; ok && t < n; ++t) {
-        const int s = t % VS, b = t & 1;
-        // the next scores go out as soon as this step's have been read, ahead of P_t V_t
-        if (t + NS < n) {
-          if (!wait_bounded(S_FREE(t % NS), (t / NS) & 1, abort_flag, p.status)) break;
-          if (!issue_qk(t + NS)) break;
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + kWColS + b * kWN, q_desc + (((kk >> 2) * kWSubQ + (kk & 3) * 32) >> 4),
+                   k_desc + (((kk >> 2) * kWSubKV + (kk & 3) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
+          mma_commit(S_FULL(b));
+          mma_commit(K_EMPTY(s));
         }
-        if (!wait_bounded(P_READY(b), (t >> 1) & 1, abort_flag, p.status)) break;
+      }
+      // every MMA this thread issued completes before the block frees its tensor memory
+      mma_commit(bar_drain_s);
+      wait_bounded(bar_drain_s, 0, nullptr, p.status, kWDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ----------------------------------------------------------------- tcgen05 issuer of O += P V
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_pv = make_idesc_f16(BF16, kWM, D, true);
+      for (int t = 0; t < n; ++t) {
+        const int s = t % VS, b = t & 1;
         if (!wait_bounded(V_FULL(s), (t / VS) & 1, abort_flag, p.status)) break;
+        if (!wait_bounded(P_READY(b), (t >> 1) & 1, abort_flag, p.status)) break;
         tc_fence_after();
         // V is [keys, d] with d contiguous: an MN-major operand, 16 keys per step of the product
         const uint64_t v_desc = make_sdesc_sw128(base + L::kV + s * L::kStep, kWSubKV, 1024);
@@ -252,7 +257,6 @@ __global__ void __launch_bounds__(kWThreads, 2)
         mma_commit(PV_DONE(b));
         mma_commit(V_EMPTY(s));
       }
-      // every MMA this thread issued completes before the block frees its tensor memory
       mma_commit(bar_drain);
       wait_bounded(bar_drain, 0, nullptr, p.status, kWDrainNs);
     }
