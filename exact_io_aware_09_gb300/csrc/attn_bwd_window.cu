@@ -654,31 +654,31 @@ static bool short_maps(const BwdArgs& a, uint32_t q_rows, uint32_t k_rows, CUten
          make_tmap_3d(&m[3], a.dout, a.bf16, kBwD, a.N_q, bhq, rb, rb * a.N_q, 64, q_rows, 1);
 }
 
-// dK/dV with one / two blocks an SM, us of all three gradient kernels (bf16, 4 sinks):
-//   many key tiles   B=8 H=12 N=1024 (768 tiles): W=64 62 / 53, 256 72 / 64, 1023 86 / 77;
-//                    B=8 H=8 N=2048 (1,024) W=2047 167 / 157; B=1 H=32 N=8192 (2,048): W=2048 523 /
-//                    504, 4095 766 / 755; B=1 Hq=32 Hkv=8 N=16384 (1,024) W=1024 637 / 645
-//   fewer            B=4 H=8 N=2048 (512) W=256 52 / 53; B=2 Hq=32 Hkv=4 N=4096 (256) W=1024 298 / 308;
-//                    B=2 H=8 N=2048 (256) W=256 29 / 42; B=1 H=12 N=1024 (96) W=256 18 / 25
-// A step alone on an SM takes longer here than there: it pays from about five tiles an SM on, which
-// keep both blocks of every SM running.
+// dK/dV with one / two blocks an SM, us of all three gradient kernels (bf16, 4 sinks; dQ with two):
+//   many key tiles, few steps   B=8 H=12 N=1024 (768 tiles): W=64 60 / 52, 256 69 / 61, 1023 81 / 73;
+//                               B=8 H=8 N=2048 (1,024) W=256 95 / 83, 2047 155 / 147; B=1 H=32 N=8192
+//                               (2,048) W=2048 483 / 472
+//   more steps                  B=1 H=32 N=8192 W=4095 (67 a tile) 715 / 720; B=1 Hq=32 Hkv=8 N=16384
+//                               W=1024 (76) 598 / 623; B=1 Hq=16 Hkv=4 N=8192 W=4096 (268) 359 / 431
+//   fewer tiles                 B=4 H=12 N=1024 (384) W=256 36 / 38; B=4 H=8 N=2048 (512) W=256 49 / 61;
+//                               B=1 H=12 N=1024 (96) 18 / 26
+// A step here takes longer than there: it pays where starts and ends are many and both blocks of every
+// SM stay busy, from about five tiles an SM on and up to 64 steps a tile.
 bool bwd_window_two_kv(const BwdArgs& a) {
-  return a.d == kBwD && a.window >= 0 &&
+  long long rows = static_cast<long long>(a.window) + kBT + kStepQ;  // of a head that see a key tile
+  if (rows > a.N_q) rows = a.N_q;
+  return a.d == kBwD && a.window >= 0 && rows * (a.Hq / a.Hkv) <= 64 * kStepQ &&
          static_cast<long long>(a.B) * a.Hkv * ((a.N_kv + kBT - 1) / kBT) >= 5 * 152;
 }
 
-// dQ likewise (dK/dV as chosen above, or with one block an SM):
-//   short spans   B=8 H=12 N=1024 (768 tiles): W=64 70 / 53, 256 78 / 64, 1023 87 / 77; B=1 Hq=16 Hkv=4
-//                 N=8192 (1,024): W=256 110 / 93, 1024 173 / 160, 2048 266 / 259; B=2 H=8 N=2048 (256)
-//                 W=256 36 / 29, B=3 (384) W=2047 68 / 69
-//   long          B=1 Hq=16 Hkv=4 N=8192: W=4096 382 / 382, 8191 449 / 468; B=1 H=32 N=8192 (2,048)
-//                 W=4095 755 / 772
-//   few tiles     B=1 H=8 N=2048 (128) W=256 27 / 27; B=1 H=2 N=4096 (64) W=4095 42 / 58
+// dQ with one / two blocks an SM likewise (dK/dV with one):
+//   more query tiles than SMs   B=8 H=12 N=1024 (768): W=64 76 / 60, 1023 93 / 81; B=1 Hq=16 Hkv=4 N=8192
+//                               (1,024): W=256 108 / 91, 2048 266 / 245, 8191 450 / 428; B=2 H=8 N=2048
+//                               (256) W=256 35 / 28; B=3 (384) W=2047 66 / 63
+//   fewer                       B=1 H=8 N=2048 (128) W=256 28 / 28; B=1 H=2 N=4096 (64) W=4095 43 / 45
 bool bwd_window_two_q(const BwdArgs& a) {
-  const long long tiles = static_cast<long long>(a.B) * a.Hq * ((a.N_q + kBT - 1) / kBT);
-  long long keys = static_cast<long long>(a.window) + kBT + a.sinks;  // a query tile sees
-  if (keys > a.N_kv) keys = a.N_kv;
-  return a.d == kBwD && a.window >= 0 && tiles > 152 && keys <= 2560;
+  return a.d == kBwD && a.window >= 0 &&
+         static_cast<long long>(a.B) * a.Hq * ((a.N_q + kBT - 1) / kBT) > 152;
 }
 
 int launch_bwd_window_dkdv(const BwdArgs& a, const BwdParams& p, unsigned blocks, cudaStream_t stream) {

@@ -478,18 +478,17 @@ static int launch_window_variant(const FwdArgs& a, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
-// This kernel against the prefill kernel's sinks variant, us (bf16, sinks 4):
-//   more query tiles than SMs   B=1 Hq=64 Hkv=8 N=8192 d=128: W=0 101 / 149, 1024 275 / 335,
-//                               2048 428 / 456, 3000 559 / 568, 4096 681 / 654, 8192 874 / 811
-//                               B=1 Hq=16 Hkv=4 N=8192 d=64: W=1024 63 / 80, 8192 185 / 193
-//   fewer (one block an SM)     B=1 Hq=Hkv=4 N=4096 d=128: W=512 14.6 / 14.9, 1024 20.3 / 18.7,
-//                               4096 50 / 34; d=64: W=512 12.9 / 14.7, 1024 18.5 / 16.8, 4096 44 / 31
+// This kernel against the prefill kernel's sinks variant, us (bf16, 4 sinks):
+//   more query tiles than SMs   B=1 Hq=64 Hkv=8 N=8192 d=128: W=0 99 / 146, 1024 248 / 334, 4096 594 /
+//                               667, 8192 762 / 828; B=1 Hq=16 Hkv=4 N=8192 d=64: W=256 35 / 58, 8192
+//                               156 / 192; B=4 H=16 N=1024 d=128: W=256 19 / 31
+//   fewer (one block an SM)     B=1 Hq=Hkv=4 N=4096 d=128: W=256 9.5 / 11.9, 512 11.9 / 13.5, 1024 16.8 /
+//                               16.4, 4096 43 / 32; d=64: W=512 10.8 / 12.4, 1024 14.9 / 15.0, 2048 23 / 21
 bool window_sinks_short(const FwdArgs& a) {
   const long long items = static_cast<long long>(a.B) * a.Hq * ((a.N_q + kWM - 1) / kWM);
   long long keys = static_cast<long long>(a.window) + kWM + a.sinks;  // a query tile sees
   if (keys > a.N_kv) keys = a.N_kv;
-  if (items <= 152) return keys <= 800;
-  return a.d == 64 || keys <= 3500;
+  return items > 152 || keys <= 1024;
 }
 
 int launch_attn_fwd_window_sinks(const FwdArgs& a, cudaStream_t stream) {
