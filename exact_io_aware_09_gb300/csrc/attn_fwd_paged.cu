@@ -15,49 +15,53 @@
 // TFLOP/s), where the producer's 32 copies a tile are as long as the tile, within 3% of the
 // contiguous prefill from 64-token pages on; 64 sequences of 3-8 tokens over 1k-32k 750 us (6.3 TB/s).
 // Calls of at most 16 rows per key/value head go to attn_paged_few.cu.
-#include "attn_fwd_kernel.cuh"
+#include "attn_fwd_two.cuh"
 #include "attn_rows.cuh"
 
 namespace attn {
 
 namespace {
 
-constexpr int kSms = 152;        // SMs of a GB300, one block each
-constexpr int kItemTiles = 8;    // a work item's start and end, in key tiles' time (about 6 us)
-constexpr int kMergeTiles = 8;   // the merge's launch, likewise
-// (against four items an SM, Hq=64 Hkv=8 d=128: 16 tokens over 32k 70 -> 45 us, 4 x 64 tokens over 8k
-// 108 -> 70)
+constexpr int kSms = 152;  // SMs of a GB300, two blocks each
 constexpr int kMaxSplits = 128;
+// Measured, us: a 64-key step and a block's start and end with two blocks on an SM, with one alone; the
+// merge's launch, and its bytes (written and read) per us.
+constexpr double kStepTwo = 0.88, kItemTwo = 4.0, kStepOne = 0.6, kItemOne = 3.5;
+constexpr double kMerge = 4.0, kMergeBytes = 5e6;
 
 struct PagedSplit {
-  int tile_tokens, n_qtiles, n_splits, split_tiles;
+  int tile_tokens, n_qtiles, n_splits, split_steps;
 };
 
-// How a call's work is cut.  An item is one query tile of one key/value head of a sequence; its key
-// tiles are cut into the number of splits that finishes first by this count: rounds of items over
-// the SMs, each its key tiles and its fixed cost, and the merge.  (The lengths are the caller's
-// bounds: what the sequences really hold is on the device.)
-PagedSplit paged_split(int B, int Hq, int Hkv, int max_q, int max_k, int window, int sinks) {
+// How a call's work is cut.  An item is one query tile of one key/value head of a sequence; its 64-key
+// steps are cut into the number of splits that is estimated to finish first: rounds of blocks over the
+// SMs, two on each, a last round of few blocks running one on an SM, and the merge.  (The lengths are
+// the caller's bounds: what the sequences really hold is on the device.)
+PagedSplit paged_split(int B, int Hq, int Hkv, int max_q, int max_k, int window, int sinks, int d) {
   PagedSplit s;
-  s.tile_tokens = kBlockM / (Hq / Hkv);
+  s.tile_tokens = kWM / (Hq / Hkv);
   s.n_qtiles = (max_q + s.tile_tokens - 1) / s.tile_tokens;
-  long long tiles = (static_cast<long long>(max_k) + kBlockN - 1) / kBlockN;
+  long long steps = (static_cast<long long>(max_k) + kWN - 1) / kWN;
   if (window >= 0) {
-    const long long near = (static_cast<long long>(window) + s.tile_tokens) / kBlockN + 2 +
-                           (static_cast<long long>(sinks) + kBlockN - 1) / kBlockN;
-    if (near < tiles) tiles = near;
+    const long long near = (static_cast<long long>(window) + s.tile_tokens) / kWN + 2 +
+                           (static_cast<long long>(sinks) + kWN - 1) / kWN;
+    if (near < steps) steps = near;
   }
   const long long items = static_cast<long long>(B) * Hkv * s.n_qtiles;
+  const double part_bytes = 2.0 * 4.0 * d * B * static_cast<double>(max_q) * Hq;
   s.n_splits = 1;
-  s.split_tiles = static_cast<int>(tiles);
-  long long best = -1;
-  for (int n = 1; n <= kMaxSplits && n <= tiles; ++n) {
-    const long long per = (tiles + n - 1) / n;
-    const long long cost = (items * n + kSms - 1) / kSms * (per + kItemTiles) + (n > 1 ? kMergeTiles : 0);
+  s.split_steps = static_cast<int>(steps);
+  double best = -1.0;
+  for (int n = 1; n <= kMaxSplits && n <= steps; ++n) {
+    const long long per = (steps + n - 1) / n, blocks = items * n;
+    const double two = per * kStepTwo + kItemTwo, one = per * kStepOne + kItemOne;
+    const long long left = blocks % (2 * kSms);
+    double cost = static_cast<double>(blocks / (2 * kSms)) * two + (left == 0 ? 0.0 : left <= kSms ? one : two);
+    if (n > 1) cost += kMerge + n * part_bytes / kMergeBytes;
     if (best < 0 || cost < best) {
       best = cost;
-      s.split_tiles = static_cast<int>(per);
-      s.n_splits = static_cast<int>((tiles + per - 1) / per);
+      s.split_steps = static_cast<int>(per);
+      s.n_splits = static_cast<int>((steps + per - 1) / per);
     }
   }
   return s;
@@ -71,7 +75,7 @@ size_t parts_o_bytes(size_t parts, int d) {
 
 size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
                              int sinks, int d) {
-  if (total_q <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > kBlockM ||
+  if (total_q <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > kWM ||
       max_q <= 0 || max_k <= 0 || d <= 0)
     return 0;
   PagedArgs a = {};
@@ -85,7 +89,7 @@ size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int
     paged_few_split(B, Hkv, max_q, max_k, window, sinks, d, n_splits, stages);
     if (n_splits <= kMaxCluster) return 0;
   } else {
-    n_splits = paged_split(B, Hq, Hkv, max_q, max_k, window, sinks).n_splits;
+    n_splits = paged_split(B, Hq, Hkv, max_q, max_k, window, sinks, d).n_splits;
     if (n_splits == 1) return 0;
   }
   const size_t parts = static_cast<size_t>(total_q) * Hq * n_splits;
@@ -178,20 +182,21 @@ int launch_paged_merge(const PagedArgs& a, int n_splits, cudaStream_t stream) {
                 : launch_merge_variant<128, false>(a, n_splits, stream);
 }
 
-template <int D, bool BF16, int KS, int VS>
+template <int D, bool BF16>
 static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
-  using L = FwdLayout<D, KS, VS>;
-  const PagedSplit sp = paged_split(a.B, a.Hq, a.Hkv, a.max_q, a.max_k, a.window, a.sinks);
+  using L = WinLayout<D>;
+  const PagedSplit sp = paged_split(a.B, a.Hq, a.Hkv, a.max_q, a.max_k, a.window, a.sinks, D);
   const int G = a.Hq / a.Hkv;
   const uint64_t row = static_cast<uint64_t>(D) * 2;
   const uint64_t tokens = static_cast<uint64_t>(a.num_pages) * a.page_size;
-  const uint32_t box = static_cast<uint32_t>(a.page_size < kBlockN ? a.page_size : kBlockN);
-  CUtensorMap tq, tk, tv;
+  const uint32_t box = static_cast<uint32_t>(a.page_size < kWN ? a.page_size : kWN);
+  CUtensorMap tq, tk, tv, to;
   if (!make_tmap_3d(&tq, a.q, BF16, D, a.Hq, a.total_q, row, row * a.Hq, 64, G, sp.tile_tokens) ||
+      !make_tmap_3d(&to, a.o, BF16, D, a.Hq, a.total_q, row, row * a.Hq, 64, G, sp.tile_tokens) ||
       !make_tmap_3d(&tk, a.k_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box) ||
       !make_tmap_3d(&tv, a.v_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box))
     return -5;
-  FwdParamsPaged p = {};
+  PagedParams p = {};
   p.o = a.o;
   p.lse = a.lse;
   p.status = device_status_ptr();
@@ -199,8 +204,7 @@ static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
   p.n_qtiles = sp.n_qtiles;
-  p.group = G;
-  p.causal = 1;
+  p.G = G;
   p.window = a.window;
   p.sinks = a.sinks;
   const uint64_t planes = static_cast<uint64_t>(a.B) * a.Hkv;
@@ -225,15 +229,15 @@ static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
   p.max_k = a.max_k;
   p.tile_tokens = sp.tile_tokens;
   p.n_splits = sp.n_splits;
-  p.split_tiles = sp.split_tiles;
+  p.split_steps = sp.split_steps;
   if (sp.n_splits > 1) paged_parts(a, D, sp.n_splits, p.ws_o, p.ws_ml);
-  auto kern = attn_fwd_kernel<D, BF16, KS, VS, false, true, true>;
+  auto kern = attn_fwd_two_kernel<D, BF16, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
       cudaSuccess)
     return -5;
   const uint64_t blocks = planes * sp.n_qtiles * sp.n_splits;
   if (blocks > 0x7fffffffull) return -2;
-  kern<<<static_cast<unsigned>(blocks), kFwdThreads, L::kBytes, stream>>>(tq, tk, tv, tq, p);
+  kern<<<static_cast<unsigned>(blocks), two_threads(true), L::kBytes, stream>>>(tq, tk, tv, to, p);
   if (cudaGetLastError() != cudaSuccess) return -5;
   return sp.n_splits == 1 ? 0 : launch_paged_merge(a, sp.n_splits, stream);
 }
@@ -241,11 +245,9 @@ static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
 int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
   if (paged_few_rows(a)) return launch_attn_paged_few(a, stream);
   if (a.d == 64)
-    return a.bf16 ? launch_paged_variant<64, true, 4, 4>(a, stream)
-                  : launch_paged_variant<64, false, 4, 4>(a, stream);
+    return a.bf16 ? launch_paged_variant<64, true>(a, stream) : launch_paged_variant<64, false>(a, stream);
   if (a.d == 128)
-    return a.bf16 ? launch_paged_variant<128, true, 3, 2>(a, stream)
-                  : launch_paged_variant<128, false, 3, 2>(a, stream);
+    return a.bf16 ? launch_paged_variant<128, true>(a, stream) : launch_paged_variant<128, false>(a, stream);
   return -2;
 }
 

@@ -1,441 +1,8 @@
-// Prefill under a sliding window whose first keys (sinks) stay visible.
-//
-// A 128-row query tile sees few keys here (window + 128 and the sinks), so the work around its key
-// loop counts: the prefill kernel (attn_fwd_kernel.cuh), one long-lived block on an SM, spends about
-// 6 us per work item between the last tile of one and a full pipeline on the next, as much as nine
-// 128-key tiles.  This kernel takes one work item per block and runs two blocks on an SM, so that
-// one block's start and end lie under the other's key loop.  What a block may hold is halved: 256
-// tensor-memory columns, 113 KB of shared memory, 168 registers for each of 192 threads.
-//
-// Keys go in steps of 64: S = Q K_t^T is 128 x 64 in one of two tensor-memory buffers, the online
-// softmax (one warpgroup, thread = query row) writes P_t as 16-bit pairs over the first half of the
-// buffer it read, and O += P_t V_t follows; the product S_{t+1} runs while the softmax works on S_t.
-// The finer steps also cut what the window's edges and a few sinks leave of a tile.  The running
-// maximum is the thread's own; the accumulator is rescaled when it rises by more than 2^8, the
-// division by the row sum at the end undoing the difference.
-//
-// Roles (192 threads): warps 0-3 softmax and epilogue, warp 4 TMA producer, warp 5 tcgen05 issuer
-// (it owns the tensor memory).  Every wait on a barrier is bounded.
-//
-// Bound by the latency of a step's chain (scores, softmax, P V) at two blocks an SM: at B=1 Hq=64
-// Hkv=8 N=8192 d=128 bf16, W=1024, 4 sinks it takes 275 us (940 TFLOP/s of visible products; the
-// tensor pipe 47% busy, 1.7 instructions a cycle), the prefill kernel 335; at B=8 H=12 N=1024 d=64,
-// W=256 25 us.  Tried and slower at the first shape: a persistent grid of two blocks an SM (321 us),
-// the same with 128-key tiles (319); three blocks an SM at d=64, one S buffer each (27 us against 25).
-#include "internal.h"
-#include "ptx.cuh"
+// Prefill under a sliding window whose first keys (sinks) stay visible: the launcher of the kernel with
+// two blocks on an SM (attn_fwd_two.cuh).
+#include "attn_fwd_two.cuh"
 
 namespace attn {
-
-namespace {
-
-constexpr int kWM = 128;        // query rows
-constexpr int kWN = 64;         // keys of a step
-constexpr int kWThreads = 224;
-constexpr uint32_t kWSubQ = kWM * 128;   // one 64-column sub-tile of Q
-constexpr uint32_t kWSubKV = kWN * 128;  // ... of a K or V step
-constexpr uint32_t kWTmemCols = 256;
-constexpr uint32_t kWColP = 0, kWColS = 64;  // P buffers at 0 and 32; S buffers, then O
-constexpr float kWRescale = 8.0f;  // log2 units
-constexpr uint64_t kWDrainNs = 100000000ull;
-
-struct WinParams {
-  void* o;
-  float* lse;
-  int* status;
-  int Hq, Hkv, G, N_q, N_kv, n_qtiles, BH, head_group, window, sinks;
-  float sl2;
-};
-
-template <int D>
-struct WinLayout {
-  static constexpr int kKS = D == 128 ? 2 : 3, kVS = D == 128 ? 2 : 3;  // ring slots
-  static constexpr int kNS = D == 128 ? 1 : 2;                          // S buffers
-  static constexpr uint32_t kColO = kWColS + kNS * kWN;
-  static_assert(kColO + D <= kWTmemCols, "tensor memory");
-  static constexpr uint32_t kQBytes = kWM * D * 2;
-  static constexpr uint32_t kStep = kWN * D * 2;
-  static constexpr uint32_t kK = kQBytes;
-  static constexpr uint32_t kV = kK + kKS * kStep;
-  static constexpr uint32_t kBar = kV + kVS * kStep;
-  // q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_ready[2], pv_done[2], drain, s_free[2],
-  // drain of the S issuer
-  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 10;
-  static constexpr uint32_t kMisc = kBar + kNumBars * 8;
-  static constexpr uint32_t kBytes = kMisc + 16 + 1024;  // + alignment
-  static_assert(2 * (kBytes + 1024) <= 233472, "two blocks on an SM");
-};
-
-// One work item: a 128-row query tile of one (batch, query head).
-struct WinItem {
-  int qt, bh, kv_plane;
-  int j_begin, lo_masked, hi_masked;  // first step of the window; steps below / from which on masked
-  int sink_steps, n;                  // steps that hold sinks and lie before the window; all steps
-  __device__ __forceinline__ int key_step(int t) const {
-    return t < sink_steps ? t : j_begin + t - sink_steps;
-  }
-};
-
-// (batch, query head) pairs in groups whose K/V planes fill about half of L2, a group's items longest
-// query tile first across its heads.
-__device__ __forceinline__ WinItem win_item(int id, const WinParams& p) {
-  WinItem it;
-  const int span = p.head_group * p.n_qtiles;
-  const int grp = id / span;
-  const int rem = id - grp * span;
-  const int h0 = grp * p.head_group;
-  const int gh = min(p.head_group, p.BH - h0);
-  it.qt = p.n_qtiles - 1 - rem / gh;
-  it.bh = h0 + rem % gh;
-  it.kv_plane = (it.bh / p.Hq) * p.Hkv + (it.bh % p.Hq) / p.G;
-  int j_end;
-  kv_tile_span(it.qt, kWM, kWN, p.N_q, p.N_kv, 1, p.window, it.j_begin, j_end, it.lo_masked,
-               it.hi_masked);
-  it.sink_steps = min((p.sinks + kWN - 1) / kWN, it.j_begin);
-  it.n = it.sink_steps + j_end - it.j_begin;
-  return it;
-}
-
-__device__ __forceinline__ bool win_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                         int* status) {
-  const bool ok = wait_bounded(bar, parity, abort, status);
-  return __all_sync(0xffffffffu, ok);
-}
-
-}  // namespace
-
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kWThreads, 2)
-    attn_fwd_window_kernel(const __grid_constant__ CUtensorMap tm_q,
-                           const __grid_constant__ CUtensorMap tm_k,
-                           const __grid_constant__ CUtensorMap tm_v,
-                           const __grid_constant__ CUtensorMap tm_o, const WinParams p) {
-  using L = WinLayout<D>;
-  constexpr int KS = L::kKS, VS = L::kVS, NS = L::kNS;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t bars = base + L::kBar;
-  const uint32_t bar_q = bars;
-#define K_FULL(s) (bars + 8u * (1 + (s)))
-#define K_EMPTY(s) (bars + 8u * (1 + KS + (s)))
-#define V_FULL(s) (bars + 8u * (1 + 2 * KS + (s)))
-#define V_EMPTY(s) (bars + 8u * (1 + 2 * KS + VS + (s)))
-  const uint32_t bar_b = bars + 8u * (1 + 2 * KS + 2 * VS);
-#define S_FULL(b) (bar_b + 8u * (b))
-#define P_READY(b) (bar_b + 8u * (2 + (b)))
-#define PV_DONE(b) (bar_b + 8u * (4 + (b)))
-  const uint32_t bar_drain = bar_b + 8u * 6;
-#define S_FREE(b) (bar_b + 8u * (7 + (b)))
-  const uint32_t bar_drain_s = bar_b + 8u * 9;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-
-  const WinItem it = win_item(static_cast<int>(blockIdx.x), p);
-  const int n = it.n;
-  auto load_k = [&](int t) {
-    mbar_arrive_expect_tx(K_FULL(t % KS), L::kStep);
-#pragma unroll
-    for (int sub = 0; sub < D / 64; ++sub)
-      tma_load_3d(base + L::kK + (t % KS) * L::kStep + sub * kWSubKV, &tm_k, K_FULL(t % KS), sub * 64,
-                  it.key_step(t) * kWN, it.kv_plane);
-  };
-  auto load_v = [&](int t) {
-    mbar_arrive_expect_tx(V_FULL(t % VS), L::kStep);
-#pragma unroll
-    for (int sub = 0; sub < D / 64; ++sub)
-      tma_load_3d(base + L::kV + (t % VS) * L::kStep + sub * kWSubKV, &tm_v, V_FULL(t % VS), sub * 64,
-                  it.key_step(t) * kWN, it.kv_plane);
-  };
-
-  if (warp == 4 && lane == 0) {
-    prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
-    mbar_init(bar_q, 1);
-    for (int s = 0; s < KS; ++s) {
-      mbar_init(K_FULL(s), 1);
-      mbar_init(K_EMPTY(s), 1);
-    }
-    for (int s = 0; s < VS; ++s) {
-      mbar_init(V_FULL(s), 1);
-      mbar_init(V_EMPTY(s), 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(S_FULL(b), 1);
-      mbar_init(P_READY(b), kWM);
-      mbar_init(PV_DONE(b), 1);
-      mbar_init(S_FREE(b), kWM);
-    }
-    mbar_init(bar_drain, 1);
-    mbar_init(bar_drain_s, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-    // the first loads go out before the block's setup is done
-    if (n > 0) {
-      mbar_arrive_expect_tx(bar_q, L::kQBytes);
-#pragma unroll
-      for (int sub = 0; sub < D / 64; ++sub)
-        tma_load_3d(base + sub * kWSubQ, &tm_q, bar_q, sub * 64, it.qt * kWM, it.bh);
-      for (int t = 0; t < KS && t < n; ++t) load_k(t);
-      for (int t = 0; t < VS && t < n; ++t) load_v(t);
-    }
-  }
-  if (warp == 5) {
-    tmem_alloc(smem_u32(tmem_slot), kWTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  if (warp == 4) {
-    // ----------------------------------------------------------------- TMA producer
-    if (lane == 0 && n > 0) {
-      int issued_k = min(KS, n), issued_v = min(VS, n);
-      static_assert(KS == VS, "one loop for both rings");
-      for (int t = KS; t < n; ++t) {
-        if (!wait_bounded(K_EMPTY(t % KS), ((t / KS) - 1) & 1, abort_flag, p.status)) break;
-        load_k(t);
-        issued_k = t + 1;
-        if (!wait_bounded(V_EMPTY(t % VS), ((t / VS) - 1) & 1, abort_flag, p.status)) break;
-        load_v(t);
-        issued_v = t + 1;
-      }
-      // Every asynchronous write into this block's shared memory lands before it may exit.
-      wait_bounded(bar_q, 0, nullptr, p.status, kWDrainNs);
-      for (int t = (issued_k > KS ? issued_k - KS : 0); t < issued_k; ++t)
-        wait_bounded(K_FULL(t % KS), (t / KS) & 1, nullptr, p.status, kWDrainNs);
-      for (int t = (issued_v > VS ? issued_v - VS : 0); t < issued_v; ++t)
-        wait_bounded(V_FULL(t % VS), (t / VS) & 1, nullptr, p.status, kWDrainNs);
-    }
-    __syncwarp();
-  } else if (warp == 5) {
-    // ----------------------------------------------------------------- tcgen05 issuer of S
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t idesc_qk = make_idesc_f16(BF16, kWM, kWN, false);
-      const uint64_t q_desc = make_sdesc_sw128(base, 16, 1024);
-      if (wait_bounded(bar_q, 0, abort_flag, p.status)) {
-        for (int t = 0; t < n; ++t) {  // S_t into buffer t % NS, once S_{t-NS} has been read
-          const int s = t % KS, b = t % NS;
-          if (!wait_bounded(K_FULL(s), (t / KS) & 1, abort_flag, p.status)) break;
-          if (t >= NS && !wait_bounded(S_FREE(b), ((t / NS) - 1) & 1, abort_flag, p.status)) break;
-          tc_fence_after();
-          const uint64_t k_desc = make_sdesc_sw128(base + L::kK + s * L::kStep, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + kWColS + b * kWN, q_desc + (((kk >> 2) * kWSubQ + (kk & 3) * 32) >> 4),
-                   k_desc + (((kk >> 2) * kWSubKV + (kk & 3) * 32) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
-          mma_commit(S_FULL(b));
-          mma_commit(K_EMPTY(s));
-        }
-      }
-      // every MMA this thread issued completes before the block frees its tensor memory
-      mma_commit(bar_drain_s);
-      wait_bounded(bar_drain_s, 0, nullptr, p.status, kWDrainNs);
-    }
-    __syncwarp();
-  } else if (warp == 6) {
-    // ----------------------------------------------------------------- tcgen05 issuer of O += P V
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t idesc_pv = make_idesc_f16(BF16, kWM, D, true);
-      for (int t = 0; t < n; ++t) {
-        const int s = t % VS, b = t & 1;
-        if (!wait_bounded(V_FULL(s), (t / VS) & 1, abort_flag, p.status)) break;
-        if (!wait_bounded(P_READY(b), (t >> 1) & 1, abort_flag, p.status)) break;
-        tc_fence_after();
-        // V is [keys, d] with d contiguous: an MN-major operand, 16 keys per step of the product
-        const uint64_t v_desc = make_sdesc_sw128(base + L::kV + s * L::kStep, kWSubKV, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kWN / 16; ++kk)
-          mma_ts(tmem + L::kColO, tmem + kWColP + b * (kWN / 2) + kk * 8, v_desc + ((kk * 16 * 128) >> 4),
-                 idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(PV_DONE(b));
-        mma_commit(V_EMPTY(s));
-      }
-      mma_commit(bar_drain);
-      wait_bounded(bar_drain, 0, nullptr, p.status, kWDrainNs);
-    }
-    __syncwarp();
-  } else {
-    // ----------------------------------------------------------------- softmax + epilogue
-    const int r = warp * 32 + lane;
-    const uint32_t row_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const float sl2 = p.sl2;
-    const int row = it.qt * kWM + r;
-    const int pos = row + p.N_kv - p.N_q;
-    const int last = min(pos, p.N_kv - 1);
-    const size_t row_index = static_cast<size_t>(it.bh) * p.N_q + row;
-    float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int t = 0; t < n; ++t) {
-      const int j = it.key_step(t);
-      const int b = t & 1;
-      if (!win_wait(S_FULL(t % NS), (t / NS) & 1, abort_flag, p.status)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t s_addr = row_tmem + kWColS + (t % NS) * kWN;
-      uint32_t sr[2][32];
-      tmem_ld32(s_addr, sr[0]);
-      tmem_ld32(s_addr + 32, sr[1]);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(S_FREE(t % NS));
-      if (j >= it.hi_masked || j < it.lo_masked) {
-        // visible columns: [lo, hi] and the sinks up to sk
-        const int hi = min(last - j * kWN, kWN - 1);
-        const int lo = j < it.lo_masked ? max(pos - p.window - j * kWN, 0) : 0;
-        const int sk = min(p.sinks - 1 - j * kWN, hi);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int a = max(lo - 32 * g, 0), bb = min(hi - 32 * g, 31);
-          const int ss = min(sk - 32 * g, 31);
-          uint32_t vis = (a > bb) ? 0u : ((0xffffffffu >> (31 - bb)) & (0xffffffffu << a));
-          vis |= (ss < 0) ? 0u : (0xffffffffu >> (31 - ss));
-          // the score where visible, -inf where not: by bits, so that a NaN or infinite score of a
-          // masked key leaves no trace
-#pragma unroll
-          for (int c = 0; c < 32; ++c) sr[g][c] = (vis & (1u << c)) ? sr[g][c] : 0xff800000u;
-        }
-      }
-      float mx[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        mx[e] = fmaxf(__uint_as_float(sr[0][e]), __uint_as_float(sr[1][e]));
-#pragma unroll
-      for (int c = 8; c < 32; c += 8)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          mx[e] = max3f(mx[e], __uint_as_float(sr[0][c + e]), __uint_as_float(sr[1][c + e]));
-      const float tile_max = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]),
-                                   fmaxf(mx[6], mx[7]));
-      // the maximum moves when it rises by more than 2^8 (and at the first finite one)
-      const float m_new = fmaxf(m, tile_max * sl2);
-      float alpha = 1.0f;
-      if (m_new - m > kWRescale) {
-        alpha = ex2(m - m_new);
-        m = m_new;
-        l *= alpha;
-      }
-      const float neg_mu = (m == -INFINITY) ? 0.0f : -m;
-      uint32_t pk[32];
-      float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          float a0, a1;
-          fma2(a0, a1, __uint_as_float(sr[g][c]), __uint_as_float(sr[g][c + 1]), sl2, sl2, neg_mu,
-               neg_mu);
-          sr[g][c] = __float_as_uint(ex2(a0));
-          sr[g][c + 1] = __float_as_uint(ex2(a1));
-        }
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const float p0 = __uint_as_float(sr[g][c]), p1 = __uint_as_float(sr[g][c + 1]);
-          const int k2 = c & 6;
-          add2(ps[k2], ps[k2 + 1], p0, p1);
-          pk[(g * 32 + c) >> 1] = pack2<BF16>(p0, p1);
-        }
-      l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-      if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-        // P V_{t-1} done; P V_t waits for this step's P, so nothing else touches O meanwhile
-        if (!win_wait(PV_DONE(b ^ 1), ((t - 1) >> 1) & 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(row_tmem + L::kColO + c * 32, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(row_tmem + L::kColO + c * 32, o);
-        }
-      }
-      if (t > 1) {  // P V_{t-2} read this buffer
-        if (!win_wait(PV_DONE(b), ((t - 2) >> 1) & 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-      }
-      tmem_st32(row_tmem + kWColP + b * (kWN / 2), pk);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(P_READY(b));
-    }
-    if (n == 0) {
-      // No key visible to any row of this tile: O = 0, L = -inf.
-      if (row < p.N_q) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row_index * D);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-        p.lse[row_index] = -INFINITY;
-      }
-    } else {
-      // O / l into Q's shared memory (its products are done) and out by one TMA store per 64 columns; a
-      // warp whose wait ran out still meets the others at the barrier
-      if (ok) ok = win_wait(PV_DONE((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.status);
-      if (ok) {
-        tc_fence_after();
-        const float inv_l = (l > 0.0f) ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // a NaN sum stays one
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(row_tmem + L::kColO + c * 32, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const uint4 w = make_uint4(
-                pack2<BF16>(__uint_as_float(o[q4 * 8 + 0]) * inv_l, __uint_as_float(o[q4 * 8 + 1]) * inv_l),
-                pack2<BF16>(__uint_as_float(o[q4 * 8 + 2]) * inv_l, __uint_as_float(o[q4 * 8 + 3]) * inv_l),
-                pack2<BF16>(__uint_as_float(o[q4 * 8 + 4]) * inv_l, __uint_as_float(o[q4 * 8 + 5]) * inv_l),
-                pack2<BF16>(__uint_as_float(o[q4 * 8 + 6]) * inv_l, __uint_as_float(o[q4 * 8 + 7]) * inv_l));
-            const uint32_t chunk = c * 4 + q4;
-            *reinterpret_cast<uint4*>(gbase + (chunk >> 3) * kWSubQ + sw128(r, chunk & 7)) = w;
-          }
-        }
-        if (row < p.N_q)
-          p.lse[row_index] = (l == 0.0f) ? -INFINITY
-                                         : ((m == -INFINITY ? 0.0f : m) + lg2(l)) * 0.69314718055994531f;
-      }
-      fence_proxy_async_smem();
-      named_bar_sync(1, kWM);
-      if (threadIdx.x == 0 && *abort_flag == 0) {
-#pragma unroll
-        for (int sub = 0; sub < D / 64; ++sub)
-          tma_store_3d(&tm_o, base + sub * kWSubQ, sub * 64, it.qt * kWM, it.bh);
-        tma_store_commit();
-        tma_store_wait_read0();  // the block's shared memory may go
-      }
-    }
-  }
-#undef K_FULL
-#undef K_EMPTY
-#undef V_FULL
-#undef V_EMPTY
-#undef S_FULL
-#undef P_READY
-#undef PV_DONE
-#undef S_FREE
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 5) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kWTmemCols);
-  }
-}
 
 template <int D, bool BF16>
 static int launch_window_variant(const FwdArgs& a, cudaStream_t stream) {
@@ -470,11 +37,11 @@ static int launch_window_variant(const FwdArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.sinks = a.sinks;
   p.sl2 = a.scale * 1.4426950408889634f;
-  auto kern = attn_fwd_window_kernel<D, BF16>;
+  auto kern = attn_fwd_two_kernel<D, BF16, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
       cudaSuccess)
     return -5;
-  kern<<<static_cast<unsigned>(blocks), kWThreads, L::kBytes, stream>>>(tq, tk, tv, to, p);
+  kern<<<static_cast<unsigned>(blocks), two_threads(false), L::kBytes, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
