@@ -185,9 +185,8 @@ def profiled_traffic(kernel: str, sources):
         return None
 
 
-FWD_SOURCES = ["exact_io_aware_09_gb300/csrc/attn_fwd.cu",
-               "exact_io_aware_09_gb300/csrc/attn_fwd_kernel.cuh",
-               "exact_io_aware_09_gb300/csrc/ptx.cuh", "exact_io_aware_09_gb300/csrc/internal.h"]
+FWD_SOURCES = ["exact_io_aware_09_gb300/csrc/attn_fwd.cu", "exact_io_aware_09_gb300/csrc/ptx.cuh",
+               "exact_io_aware_09_gb300/csrc/internal.h"]
 DEC_SOURCES = ["exact_io_aware_09_gb300/csrc/attn_decode.cu",
                "exact_io_aware_09_gb300/csrc/attn_decode.cuh",
                "exact_io_aware_09_gb300/csrc/ptx.cuh", "exact_io_aware_09_gb300/csrc/internal.h"]

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libattn_gb300.so")
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_fwd_paged.cu", "attn_paged_few.cu", "attn_fwd_window.cu", "attn_fwd_pair.cu",
            "attn_decode.cu", "attn_decode_fp8.cu", "attn_cache_fp8.cu", "attn_bwd.cu", "attn_bwd_window.cu", "attn_fp8.cu"]
 HEADERS = [os.path.join(CSRC, h)
-           for h in ("ptx.cuh", "internal.h", "attn_fwd_kernel.cuh", "attn_fwd_two.cuh", "attn_decode.cuh",
+           for h in ("ptx.cuh", "internal.h", "attn_fwd_two.cuh", "attn_decode.cuh",
                      "attn_rows.cuh", "attn_bwd.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,7 +1,7 @@
 // A chunk of new tokens of each sequence over a paged KV cache: causal attention of the last
 // positions of every sequence, with or without a sliding window and sinks.
 //
-// The prefill kernel (attn_fwd_kernel.cuh) runs it with three changes.  (1) A query tile's 128
+// The prefill kernel (attn_fwd.cu) runs it with three changes.  (1) A query tile's 128
 // rows are (token, query head) pairs of one key/value head, 128 / G tokens of the G heads that
 // share it, so that a tile reads each cache row once for all its heads and a chunk of a few
 // tokens still fills the tile: the number of products is that of one head per tile, the diagonal

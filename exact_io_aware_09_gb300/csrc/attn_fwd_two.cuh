@@ -2,7 +2,7 @@
 // paged cache (attn_fwd_paged.cu).
 //
 // A 128-row query tile sees few keys here (window + 128 and the sinks), so the work around its key
-// loop counts: the prefill kernel (attn_fwd_kernel.cuh), one long-lived block on an SM, spends about
+// loop counts: the prefill kernel (attn_fwd.cu), one long-lived block on an SM, spends about
 // 6 us per work item between the last tile of one and a full pipeline on the next, as much as nine
 // 128-key tiles.  This kernel takes one work item per block and runs two blocks on an SM, so that
 // one block's start and end lie under the other's key loop.  What a block may hold is halved: 256
