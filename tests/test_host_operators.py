@@ -73,7 +73,7 @@ def test_paged_refusals(attn):
     need = attn.attn_fwd_paged_workspace_bytes(40, 3, 16, 2, 20, 32768, 128)
     assert need > 0 and f(n=need - 1, **long) == -4 and f(ws=NUL, **long) == -4
     if _no_cuda():
-        assert f(ws=NUL, n=0) == -7 and f(n=need, **long) == -7
+        assert f(ws=NUL, n=0, mk=64) == -7 and f(n=need, **long) == -7  # (one step of keys: no split)
 
 
 def test_paged_workspace(attn):
