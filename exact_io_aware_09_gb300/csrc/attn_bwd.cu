@@ -38,8 +38,9 @@
 // tile of the window is: its query tiles are cut into parts, blocks of their own whose fp32 sums a
 // last kernel adds in order (B=1 Hq=64 Hkv=8 N=8192 d=128, W=1024, 64 sinks: forward and gradients
 // 1,788 -> 1,369 us).  The masks sit in a branch of their own: as tests per column inside the
-// exponential loop they cost every tile (gradients 1,028 -> 882 us at 4 sinks).  The same shape now: D 50 us, dK/dV 447 (tensor pipe 69%
-// busy), dQ 399 (53%: nine key tiles a block do not hide its start and end), sums 5.
+// exponential loop they cost every tile (gradients 1,028 -> 882 us at 4 sinks).  The same shape now: D
+// 42 us, dK/dV 437 (tensor pipe 70% busy), dQ 376 (56%: nine key tiles a block do not hide its start and
+// end), sums 5.  At d = 64 calls of many short tiles take the kernels of attn_bwd_window.cu.
 #include <algorithm>
 #include <map>
 #include <memory>

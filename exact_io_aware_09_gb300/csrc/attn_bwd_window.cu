@@ -4,14 +4,21 @@
 // A tile of a short window runs a handful of steps, so a block's start and end (tensor-memory
 // allocation, first loads, first products, the gradients' way out) cost as much as its steps; with one
 // block on an SM nothing covers them.  Here a block holds half of what an SM has: 256 tensor-memory
-// columns, about 105 KB of shared memory, 192 threads of up to 168 registers, so that one block's
+// columns, about 105 KB of shared memory, 224 threads of up to 128 registers, so that one block's
 // start and end, and its waits, lie under the other's steps.  At d = 128 the two accumulators of dK and
 // dV alone fill the 256 columns, and Q, dO and two steps of K and V the shared memory.
 //
 // Both kernels step through 64 rows of the other side, one elementwise warpgroup (thread = row of the
-// block's own tile) and one issuing thread.  Roles (192 threads): warps 0-3 elementwise and epilogue,
+// block's own tile) and two issuing threads.  Roles (224 threads): warps 0-3 elementwise and epilogue,
 // warp 4 TMA producer, warps 5 and 6 tcgen05 issuers (warp 5 owns the tensor memory).  Every wait on a barrier is
 // bounded.
+//
+// Bound by a step's chain of products and elementwise work at two blocks an SM (tensor pipe 25% busy,
+// 1.4 instructions a cycle).  B=8 H=12 N=1024 bf16, W=256, 4 sinks: dK/dV 37 us, dQ 26.5 (one block an
+// SM: 48 and 43).  Steps that count there: the gradients through shared memory and TMA 43 -> 40 and 30 ->
+// 28; dQ's scores in a buffer of their own, and a thread each for the two pairs of products 39 -> 37 and
+// 27.5 -> 26.5.  Tried for dK/dV and slower: P^T and dS^T in shared memory, which frees the scores early
+// but leaves two stages for Q and dO (46 us against 40); S^T in two halves of 32 queries (46 against 39).
 #include "attn_bwd.cuh"
 
 namespace attn {

@@ -10,14 +10,14 @@
 // finite takes no part in a and is stored as the NaN code: E4M3 has no infinity, and a finite
 // code would hide it.
 //
-// Both kernels are bound by memory; the writer's ALU is 70% busy beside it (amax, scale and
-// conversion of every value).  Hkv=8 d=128: 77k prompt tokens into 16-token pages 82 us (499 MB, 6.1
-// TB/s), 440k cached tokens back out of 32-token pages 415 us (2.73 GB, 6.6 TB/s, a copy's rate); 64
-// sequences' single tokens 9 us on the device, launch and latency.  A block takes a run of packed tokens: its threads find their
-// sequences and cache rows first (one token each, a binary search of the packed offsets), then the
-// block streams the run's rows, d / 16 lanes per row with 32 bytes of 16-bit values and 16 bytes
-// of codes each.  Packed rows are consecutive, and so are cache rows inside a page, so every
-// access of a warp is whole lines but for the scales.
+// Both kernels are bound by memory; the writer's ALU is 45% busy beside it (amax, scale and conversion of
+// every value).  Hkv=8 d=128: 77k prompt tokens into 16-token pages 82 us (499 MB, 6.1 TB/s), 440k cached
+// tokens back out of 32-token pages 413 us (2.73 GB, 6.6 TB/s, a copy's rate); 64 sequences' single tokens
+// 9 us on the device, launch and latency.  A block takes a run of packed tokens: its threads find their
+// sequences and cache rows first (one token each, a binary search of the packed offsets), then the block
+// streams the run's rows, d / 16 lanes per row with 32 bytes of 16-bit values and 16 bytes of codes each.
+// Packed rows are consecutive, and so are cache rows inside a page, so every access of a warp is whole
+// lines but for the scales.
 #include "internal.h"
 #include "ptx.cuh"
 

@@ -1,19 +1,18 @@
 // A chunk of new tokens of each sequence over a paged KV cache: causal attention of the last
 // positions of every sequence, with or without a sliding window and sinks.
 //
-// The prefill kernel (attn_fwd.cu) runs it with three changes.  (1) A query tile's 128
-// rows are (token, query head) pairs of one key/value head, 128 / G tokens of the G heads that
-// share it, so that a tile reads each cache row once for all its heads and a chunk of a few
-// tokens still fills the tile: the number of products is that of one head per tile, the diagonal
-// takes G times fewer masked tiles.  (2) A 128-key tile comes in page by page, each page's TMA
-// copy issued by its own lane of the producer warp, with the block-table entries read one tile
-// ahead.  (3) When the chunks give fewer tiles than keep the SMs evenly busy, an item's key tiles
-// are split and the parts' normalised rows merged with the (m, l) rule by a second kernel.
+// The kernel with two blocks on an SM (attn_fwd_two.cuh) runs it.  A query tile's 128 rows are (token,
+// query head) pairs of one key/value head, 128 / G tokens of the G heads that share it, so that a tile
+// reads each cache row once for all its heads and a chunk of a few tokens still fills the tile: the
+// number of products is that of one head per tile, the diagonal takes G times fewer masked steps.  When
+// the chunks give fewer tiles than keep the SMs evenly busy, an item's keys are split and the parts'
+// normalised rows merged with the (m, l) rule by a second kernel.
 //
-// Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.  Hq=64 Hkv=8
-// d=128 bf16: two chunks of 2,048 tokens over 12k-16k cached ones 1,550 us in 16-token pages (1,150
-// TFLOP/s), where the producer's 32 copies a tile are as long as the tile, within 3% of the
-// contiguous prefill from 64-token pages on; 64 sequences of 3-8 tokens over 1k-32k 750 us (6.3 TB/s).
+// Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.  Hq=64 Hkv=8 d=128
+// bf16: two chunks of 2,048 tokens over 16k cached ones 1,335 us in 16-token pages (1,540 TFLOP/s, tensor
+// pipe 67% busy) and 1,300 in 64-token pages, the contiguous prefill of the same 1,320-1,390 (on the
+// prefill kernel, one block an SM: 1,750 and 1,400, its producers' 16 copies a tile being as long as the
+// tile); 64 sequences of 3-8 tokens over 1k-32k 750 us (6.3 TB/s).
 // Calls of at most 16 rows per key/value head go to attn_paged_few.cu.
 #include "attn_fwd_two.cuh"
 #include "attn_rows.cuh"

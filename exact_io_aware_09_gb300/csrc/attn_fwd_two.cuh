@@ -1,28 +1,30 @@
 // Prefill with two blocks on an SM: the sliding window with sinks (attn_fwd_window.cu) and chunks over a
 // paged cache (attn_fwd_paged.cu).
 //
-// A 128-row query tile sees few keys here (window + 128 and the sinks), so the work around its key
-// loop counts: the prefill kernel (attn_fwd.cu), one long-lived block on an SM, spends about
-// 6 us per work item between the last tile of one and a full pipeline on the next, as much as nine
-// 128-key tiles.  This kernel takes one work item per block and runs two blocks on an SM, so that
-// one block's start and end lie under the other's key loop.  What a block may hold is halved: 256
-// tensor-memory columns, 113 KB of shared memory, 168 registers for each of 192 threads.
+// The prefill kernel (attn_fwd.cu) runs one long-lived block on an SM and spends about 6 us per work
+// item between the last tile of one and a full pipeline on the next, as much as nine 128-key tiles.
+// This kernel takes one work item per block and runs two blocks on an SM, so that one block's start
+// and end, and its waits, lie under the other's key loop.  What a block may hold is halved: 256
+// tensor-memory columns, 113 KB of shared memory, 128 registers a thread.
 //
-// Keys go in steps of 64: S = Q K_t^T is 128 x 64 in one of two tensor-memory buffers, the online
-// softmax (one warpgroup, thread = query row) writes P_t as 16-bit pairs over the first half of the
-// buffer it read, and O += P_t V_t follows; the product S_{t+1} runs while the softmax works on S_t.
-// The finer steps also cut what the window's edges and a few sinks leave of a tile.  The running
-// maximum is the thread's own; the accumulator is rescaled when it rises by more than 2^8, the
-// division by the row sum at the end undoing the difference.
+// Keys go in steps of 64: S = Q K_t^T is 128 x 64 in a tensor-memory buffer that is free as soon as the
+// softmax (one warpgroup, thread = query row) has read it; P_t goes as 16-bit pairs into one of two
+// buffers of its own, and O += P_t V_t follows.  So S_{t+1} is made under the softmax of S_t, and
+// nothing waits for P_t V_t but the step after the next (with P_t over the scores, as before, S_{t+2}
+// had to: 278 us against 266 at the first shape below).  The finer steps also cut what the window's
+// edges and a few sinks leave of a tile.  The running maximum is the thread's own; the accumulator is
+// rescaled when it rises by more than 2^8, the division by the row sum at the end undoing the difference.
 //
-// Roles (192 threads): warps 0-3 softmax and epilogue, warp 4 TMA producer, warp 5 tcgen05 issuer
-// (it owns the tensor memory).  Every wait on a barrier is bounded.
+// Roles: warps 0-3 softmax and epilogue; warp 4 TMA producer (paged: of Q and K, page by page, a page's
+// copy issued by its own lane, the block-table entries read a step ahead); warp 5 tcgen05 issuer of S
+// (it owns the tensor memory), warp 6 of P V (one thread for both: 268 us against 260); paged: warp 7
+// producer of V.  Every wait on a barrier is bounded.
 //
-// Bound by the latency of a step's chain (scores, softmax, P V) at two blocks an SM: at B=1 Hq=64
-// Hkv=8 N=8192 d=128 bf16, W=1024, 4 sinks it takes 275 us (940 TFLOP/s of visible products; the
-// tensor pipe 47% busy, 1.7 instructions a cycle), the prefill kernel 335; at B=8 H=12 N=1024 d=64,
-// W=256 25 us.  Tried and slower at the first shape: a persistent grid of two blocks an SM (321 us),
-// the same with 128-key tiles (319); three blocks an SM at d=64, one S buffer each (27 us against 25).
+// Bound by the tensor pipe's 64-wide products and a step's chain at two blocks an SM.  B=1 Hq=64 Hkv=8
+// N=8192 d=128 bf16, W=1024, 4 sinks: 250 us (1,030 TFLOP/s of visible products; tensor pipe 52% busy,
+// 1.8 instructions a cycle), the prefill kernel 334; B=8 H=12 N=1024 d=64, W=256: 25 us.  Tried and
+// slower: a persistent grid of two blocks an SM (321 us when this kernel took 282), the same with
+// 128-key tiles (319); three blocks an SM at d=64 (27 us against 25).
 #pragma once
 #include "internal.h"
 #include "ptx.cuh"
