@@ -173,7 +173,7 @@ struct BwdArgs {
 int launch_attn_fwd(const FwdArgs& a, cudaStream_t stream);
 // d = 64: two query tiles per work item (attn_fwd_pair.cu)
 int launch_attn_fwd_pair(const FwdArgs& a, cudaStream_t stream);
-// window with sinks whose query tiles see few keys (attn_fwd_window.cu), and whether a call's do
+// window with sinks, two blocks on an SM (attn_fwd_window.cu), and whether a call takes that kernel
 int launch_attn_fwd_window_sinks(const FwdArgs& a, cudaStream_t stream);
 bool window_sinks_short(const FwdArgs& a);
 // The d = 64 kernel choice: 0 automatic, 1 two query tiles per item, 2 one (attn_fwd.cu).
