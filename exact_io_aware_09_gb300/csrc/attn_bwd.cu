@@ -33,6 +33,12 @@
 // hand-offs between them run through the elementwise warps' barriers.  Every wait on a barrier
 // is bounded.
 //
+// Roundings.  P and dS enter their products in the operands' 16-bit type, since the tensor cores multiply
+// operands of one type: each term of dV, dK and dQ is off by at most half a step (2^-9 of it in bf16,
+// 2^-12 in fp16), about as much as rounding the gradients themselves; products with what the roundings
+// leave would add three to seven.  D is formed from O as stored.  Sums, S, dP and the exponentials are
+// fp32.
+//
 // The window variant (WINDOW; a sliding window whose first keys, the sinks, stay visible) walks only
 // the tiles a row sees.  A key tile with sinks is seen by every later query row, many times what a
 // tile of the window is: its query tiles are cut into parts, blocks of their own whose fp32 sums a

@@ -13,6 +13,8 @@
 // warp 4 TMA producer, warps 5 and 6 tcgen05 issuers (warp 5 owns the tensor memory).  Every wait on a barrier is
 // bounded.
 //
+// Roundings as in attn_bwd.cu: P and dS to the operands' type, everything else fp32.
+//
 // Bound by a step's chain of products and elementwise work at two blocks an SM (tensor pipe 25% busy,
 // 1.4 instructions a cycle).  B=8 H=12 N=1024 bf16, W=256, 4 sinks: dK/dV 37 us, dQ 26.5 (one block an
 // SM: 48 and 43).  Steps that count there: the gradients through shared memory and TMA 43 -> 40 and 30 ->

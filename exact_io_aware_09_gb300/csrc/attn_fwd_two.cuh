@@ -15,6 +15,10 @@
 // edges and a few sinks leave of a tile.  The running maximum is the thread's own; the accumulator is
 // rescaled when it rises by more than 2^8, the division by the row sum at the end undoing the difference.
 //
+// P is rounded to V's 16-bit type for its product (the tensor cores multiply operands of one type), which
+// moves each weight by at most half a step; the row sums take the unrounded weights, and scores, statistics
+// and O are fp32 until O is stored.
+//
 // Roles: warps 0-3 softmax and epilogue; warp 4 TMA producer (paged: of Q and K, page by page, a page's
 // copy issued by its own lane, the block-table entries read a step ahead); warp 5 tcgen05 issuer of S
 // (it owns the tensor memory), warp 6 of P V (one thread for both: 268 us against 260); paged: warp 7

@@ -8,6 +8,9 @@
 //                 holds keys g and g + 8 of rows 2c and 2c + 1 of each column tile;
 //   O^T += V^T P^T   channels by rows, P^T being the transpose of what the thread holds (movmatrix);
 //                 tile t holds two channels of thread (g, c) for the same two rows.
+//
+// P is rounded to the 16 bits of the second product's other operand (half a step of each weight); the row
+// sums take the unrounded weights, and scores, statistics and O are fp32.
 #pragma once
 #include "ptx.cuh"
 
