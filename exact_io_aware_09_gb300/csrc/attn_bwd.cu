@@ -34,9 +34,9 @@
 // is bounded.
 //
 // Roundings.  P and dS enter their products in the operands' 16-bit type, since the tensor cores multiply
-// operands of one type: each term of dV, dK and dQ is off by at most half a step (2^-9 of it in bf16,
-// 2^-12 in fp16), about as much as rounding the gradients themselves; products with what the roundings
-// leave would add three to seven.  D is formed from O as stored.  Sums, S, dP and the exponentials are
+// operands of one type: each term of dV, dK and dQ is off by at most half a step (2^-8 of it in bf16,
+// 2^-11 in fp16), about as much as rounding the gradients themselves; products with what the roundings
+// leave would add three to the seven.  D is formed from O as stored.  Sums, S, dP and the exponentials are
 // fp32.
 //
 // The window variant (WINDOW; a sliding window whose first keys, the sinks, stay visible) walks only
