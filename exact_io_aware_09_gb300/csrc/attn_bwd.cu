@@ -96,6 +96,7 @@ __global__ void attn_bwd_pre_kernel(const uint16_t* o, const uint16_t* dout, con
                                     float scale) {
   // D / 8 lanes per row, 16-byte loads of O and dO
   constexpr int kLanes = D / 8;
+  if (threadIdx.x == 0) griddep_launch_dependents();  // dK/dV's setup and first loads may start
   const long long w0 =
       (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes * kPreRows;
   const int lane = threadIdx.x % kLanes;
@@ -212,8 +213,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // The dQ kernel needs nothing this one writes: its blocks may take the SMs this grid's
-  // blocks leave, as soon as every block of this grid has started.
-  if (threadIdx.x == 0) griddep_launch_dependents();
+  // blocks leave, as soon as every block of this grid has started and kernel 0 has ended (dQ
+  // reads its vectors too).
+  if (threadIdx.x == 0) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
 
   // job: key tile kt of (batch, key/value head) bkv, numbered key tile major; the launch order
   // is the packed one of KvOrder when the launcher gives one
@@ -269,6 +274,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       tma_load_3d(st + sub * L::kHalfSub, &tm_q, ST_FULL(s), sub * 64, q0, bhq);
       tma_load_3d(st + L::kHalf + sub * L::kHalfSub, &tm_do, ST_FULL(s), sub * 64, q0, bhq);
     }
+    if (i == 0) griddep_wait();  // kernel 0's vectors
     const size_t vec = static_cast<size_t>(bhq) * p.nqp + static_cast<size_t>(q0);
     bulk_load(st + 2 * L::kHalf, p.lse2 + vec, kStepQ * 4, ST_FULL(s));
     bulk_load(st + 2 * L::kHalf + 256, p.dvec + vec, kStepQ * 4, ST_FULL(s));
@@ -1209,27 +1215,30 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
       bhk * (static_cast<uint64_t>(p.n_kvtiles) + static_cast<uint64_t>(p.sink_tiles) * (p.sink_parts - 1));
   const uint64_t q_blocks = bhq * n_qtiles;
   if (kv_blocks > 0x7fffffffull || q_blocks > 0x7fffffffull) return -2;
-  if (kv_two) {
-    const int st = launch_bwd_window_dkdv(a, p, static_cast<unsigned>(kv_blocks), stream);
-    if (st != 0) return st;
-  } else {
-    const KvOrder* order = kv_order(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.causal,
-                                    a.N_kv - a.N_q, a.window, a.sinks);
-    kkv<<<static_cast<unsigned>(kv_blocks), kKvThreads, LK::kBytes, stream>>>(tq64, tk, tv, tdo64, tdk,
-                                                                              tdv, p, *order);
-    if (cudaGetLastError() != cudaSuccess) return -5;
-  }
-  // dQ as a programmatic dependent of dK/dV: its blocks fill the SMs of dK/dV's tail.
+  // dK/dV as a programmatic dependent of kernel 0 (its setup and first loads under that kernel's end),
+  // dQ as one of dK/dV.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(q_blocks));
-  cfg.blockDim = dim3(kQThreads);
-  cfg.dynamicSmemBytes = LQ::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (kv_two) {
+    const int st = launch_bwd_window_dkdv(a, p, static_cast<unsigned>(kv_blocks), stream);
+    if (st != 0) return st;
+  } else {
+    const KvOrder* order = kv_order(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.causal,
+                                    a.N_kv - a.N_q, a.window, a.sinks);
+    cfg.gridDim = dim3(static_cast<unsigned>(kv_blocks));
+    cfg.blockDim = dim3(kKvThreads);
+    cfg.dynamicSmemBytes = LK::kBytes;
+    if (cudaLaunchKernelEx(&cfg, kkv, tq64, tk, tv, tdo64, tdk, tdv, p, *order) != cudaSuccess) return -5;
+  }
+  // dQ's blocks fill the SMs of dK/dV's tail.
+  cfg.gridDim = dim3(static_cast<unsigned>(q_blocks));
+  cfg.blockDim = dim3(kQThreads);
+  cfg.dynamicSmemBytes = LQ::kBytes;
   if (q_two) {
     const int st = launch_bwd_window_dq(a, p, static_cast<unsigned>(q_blocks), stream);
     if (st != 0) return st;

@@ -109,7 +109,10 @@ __global__ void __launch_bounds__(kBwThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) griddep_launch_dependents();  // dQ needs nothing of this kernel
+  if (threadIdx.x == 0) {
+    griddep_wait();  // (dQ reads kernel 0's vectors too)
+    griddep_launch_dependents();  // dQ needs nothing of this kernel
+  }
 
   // job: key tile kt of (batch, key/value head) bkv, key tile major; the tiles with sinks come first,
   // cut into sink_parts blocks each (part major)
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     mbar_arrive_expect_tx(ST_FULL(s), 2 * kBwStep + 512);
     tma_load_3d(st, &tm_q, ST_FULL(s), 0, q0, bhq0 + g);
     tma_load_3d(st + kBwStep, &tm_do, ST_FULL(s), 0, q0, bhq0 + g);
+    if (i == 0) griddep_wait();  // kernel 0's vectors
     const size_t vec = static_cast<size_t>(bhq0 + g) * p.nqp + static_cast<size_t>(q0);
     bulk_load(st + 2 * kBwStep, p.lse2 + vec, kStepQ * 4, ST_FULL(s));
     bulk_load(st + 2 * kBwStep + 256, p.dvec + vec, kStepQ * 4, ST_FULL(s));
@@ -700,8 +704,17 @@ int launch_bwd_window_dkdv(const BwdArgs& a, const BwdParams& p, unsigned blocks
   auto kern = a.bf16 ? attn_bwd_short_dkdv_kernel<true> : attn_bwd_short_dkdv_kernel<false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, KvShort::kBytes) != cudaSuccess)
     return -5;
-  kern<<<blocks, kBwThreads, KvShort::kBytes, stream>>>(m[0], m[1], m[2], m[3], dk, dv, p);
-  return cudaGetLastError() == cudaSuccess ? 0 : -5;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kBwThreads);
+  cfg.dynamicSmemBytes = KvShort::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], dk, dv, p) == cudaSuccess ? 0 : -5;
 }
 
 // A programmatic dependent of dK/dV: its blocks fill the SMs of that kernel's tail.
