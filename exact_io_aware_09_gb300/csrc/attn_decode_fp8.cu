@@ -57,10 +57,9 @@ struct Fp8Layout {
   // the block's merged state for its cluster: [row][D] and (m, l) per row
   static constexpr uint32_t kFin = kRed;
   static_assert(kFin + kMaxGroup * (D + 2) * 4 <= kRing, "merge scratch must fit in the ring");
-  static constexpr uint32_t kScales = kRing;  // [stage][K, V][64] floats
-  static constexpr uint32_t kBar = kScales + kDecStages * 2 * kDecTok * 4;
+  static constexpr uint32_t kBar = kRing;
   static constexpr uint32_t kMisc = kBar + 2 * kDecStages * 8;
-  static constexpr uint32_t kPages = kMisc + 16;  // first pool row of the split's pages, or -1
+  static constexpr uint32_t kPages = kMisc + 16;  // the split's pages, or -1
   static constexpr int kMaxSplitPages = 8192 / 16;
   static constexpr uint32_t kBytes = kPages + kMaxSplitPages * 4 + 1024;
 };
@@ -163,10 +162,10 @@ struct Fp8Warp : RowState<D, NT, false> {
     }
   }
 
-  // Stage rows w0 .. w0 + 15, of which the first `valid` count.
-  __device__ __forceinline__ void tokens(const uint8_t* kbuf, const uint8_t* vbuf,
-                                         const float* k_sc, const float* v_sc, int w0, int valid,
-                                         int lane) {
+  // Stage rows w0 .. w0 + 15, of which the first `valid` count.  scale: lane i holds the key scale of
+  // row i, lane 16 + i its value scale.
+  __device__ __forceinline__ void tokens(const uint8_t* kbuf, const uint8_t* vbuf, float scale, int w0,
+                                         int valid, int lane) {
     const int g = lane >> 2, c = lane & 3;
     float sc[NT][4] = {};
 #pragma unroll
@@ -186,10 +185,10 @@ struct Fp8Warp : RowState<D, NT, false> {
     float x[NT][2][2], inv_b[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int row = w0 + g + 8 * k;
-      const int vb = static_cast<int>(__float_as_uint(v_sc[row]) >> 23) & 0xff;
+      const float vj = __shfl_sync(0xffffffffu, scale, 16 + g + 8 * k);
+      const float kj = __shfl_sync(0xffffffffu, scale, g + 8 * k);
+      const int vb = static_cast<int>(__float_as_uint(vj) >> 23) & 0xff;
       const float bj = static_cast<float>(vb - 127);
-      const float kj = k_sc[row];
       inv_b[k] = __uint_as_float(static_cast<uint32_t>(max(254 - kSumShift - vb, 0)) << 23);
       const bool in = g + 8 * k < valid;
 #pragma unroll
@@ -261,27 +260,27 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 2)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  __syncthreads();
-
-  if (warp == kDecWarps) {
-    // ------------------------------------------------------------------ TMA producer
-    // Lane i brings the i-th page of a stage: its codes of K and V as one box each, its scales as
-    // two short copies.
-    int* page_row = reinterpret_cast<int*>(gbase + L::kPages);
+  int* page_row = reinterpret_cast<int*>(gbase + L::kPages);
+  const int first = t0 >> p.page_log2;
+  {
     const int32_t* tbl = p.block_table + static_cast<size_t>(b) * p.max_pages;
-    const int first = t0 >> p.page_log2;
     const int n_pg_all = n_tok > 0 ? ((t0 + n_tok - 1) >> p.page_log2) - first + 1 : 0;
-    for (int i = lane; i < n_pg_all; i += 32) {
+    for (int i = threadIdx.x; i < n_pg_all; i += kDecThreads) {
       const int pg = tbl[first + i];
       const bool good = pg >= 0 && pg < p.num_pages;
       if (!good) latch_status(p.status, kStatusBadLengths);
       page_row[i] = good ? pg : -1;
     }
-    __syncwarp();
+  }
+  __syncthreads();
+
+  if (warp == kDecWarps) {
+    // ------------------------------------------------------------------ TMA producer
+    // Lane i brings the i-th page of a stage: its codes of K and V as one box each.
     const uint64_t stream_policy = l2_policy_evict_first();
     const int rows = min(p.page_size, kDecTok);
     const int n_pg = kDecTok / rows;
-    const uint32_t page_bytes = 2u * rows * D + 2u * rows * 4u;
+    const uint32_t page_bytes = 2u * rows * D;
     int issued = 0;
     for (int st = 0; st < n_stages; ++st) {
       const int s = st % kDecStages;
@@ -291,7 +290,6 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 2)
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       const uint32_t kbuf = base + s * L::kStage;
       const uint32_t vbuf = kbuf + L::kTensor;
-      const uint32_t sbuf = base + L::kScales + s * (2 * kDecTok * 4);
       int page = -1, off = 0;
       if (lane < n_pg) {
         const int t = t0 + st * kDecTok + lane * rows;
@@ -308,9 +306,6 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 2)
         const int row = (page << p.page_log2) + off;
         tma_load_3d_hint(kbuf + box_off, &tm_k, FULL(s), 0, hk, row, stream_policy);
         tma_load_3d_hint(vbuf + box_off, &tm_v, FULL(s), 0, hk, row, stream_policy);
-        const size_t sc = ((static_cast<size_t>(page) * p.Hkv + hk) << p.page_log2) + off;
-        bulk_load(sbuf + lane * rows * 4, p.k_scales + sc, rows * 4, FULL(s));
-        bulk_load(sbuf + kDecTok * 4 + lane * rows * 4, p.v_scales + sc, rows * 4, FULL(s));
       }
       issued = st + 1;
     }
@@ -325,17 +320,31 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 2)
   Fp8Warp<D, BF16, NT> st_w;
   st_w.init(p.q + (static_cast<size_t>(b) * p.Hq + hq0) * D, p.G, p.sl2, lane);
 
+  // The scales go straight to registers, two stages ahead: a warp's sixteen tokens lie in one page, and
+  // lane i < 16 loads the key scale of token i, lane 16 + i its value scale.  (As copies into the stage,
+  // two of 256 bytes each, they cost 408 us against 392 back to back at the 64 sequences above.)
+  auto scale_at = [&](int st) -> float {
+    const int t = t0 + st * kDecTok + warp * 16;
+    if (t >= t_stop || st >= n_stages) return 0.0f;
+    const int page = page_row[(t >> p.page_log2) - first];
+    if (page < 0) return 0.0f;
+    return __ldcs((lane < 16 ? p.k_scales : p.v_scales) +
+                  ((static_cast<size_t>(page) * p.Hkv + hk) << p.page_log2) + (t & (p.page_size - 1)) +
+                  (lane & 15));
+  };
+  float sc0 = scale_at(0), sc1 = scale_at(1);
   bool ok = true;
   for (int st = 0; st < n_stages; ++st) {
     const int s = st % kDecStages;
+    const float scale = sc0;
+    sc0 = sc1;
+    sc1 = scale_at(st + 2);
     if (!dec_warp_wait(FULL(s), (st / kDecStages) & 1, abort_flag, p.status)) {
       ok = false;
       break;
     }
     uint8_t* kbuf = gbase + s * L::kStage;
     uint8_t* vbuf = kbuf + L::kTensor;
-    const float* k_sc = reinterpret_cast<const float*>(gbase + L::kScales) + s * 2 * kDecTok;
-    const float* v_sc = k_sc + kDecTok;
     const int w0 = warp * 16;                     // first stage row of this warp
     const int valid = n_tok - st * kDecTok - w0;  // rows of this warp that belong to the chunk
     if (valid > 0) {
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 2)
               make_uint4(0, 0, 0, 0);
         __syncwarp();
       }
-      st_w.tokens(kbuf, vbuf, k_sc, v_sc, w0, valid, lane);
+      st_w.tokens(kbuf, vbuf, scale, w0, valid, lane);
       if (valid < 16) fence_proxy_async_smem();  // generic zeros before the next TMA write
     }
     __syncwarp();
