@@ -26,10 +26,10 @@
 // launch, no workspace.  More splits go through the workspace and the 16-bit decode's merge kernel.
 //
 // Bound by HBM: 2 (d + 4) bytes per cached token and head.  64 sequences of 1k-32k tokens (Hq=64 Hkv=8
-// d=128, 64-token pages, 2.45 GB): 412 us, 5.9 TB/s, against 723 for the 16-bit cache; the split
-// kernel runs at 1.8 instructions a cycle (converting the codes is most of them) and the merge, whose
-// launch the split kernel allows early, takes the rest of the gap.  One sequence of 1,001 tokens (Hq=16
-// Hkv=4 d=64): 12 us on the device, one launch.
+// d=128, 64-token pages, 2.45 GB): 396 us, 6.2 TB/s, against 723 for the 16-bit cache.  Without its
+// arithmetic it takes as long; what counts is how the bytes are asked for: codes and scales both with the
+// policy that evicts their lines first (codes with the default one 411 us, scales as short asynchronous
+// copies with it 408).  One sequence of 1,001 tokens (Hq=16 Hkv=4 d=64): 12 us on the device, one launch.
 #include "attn_decode.cuh"
 #include "attn_rows.cuh"
 

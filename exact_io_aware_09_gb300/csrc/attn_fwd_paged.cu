@@ -12,7 +12,7 @@
 // bf16: two chunks of 2,048 tokens over 16k cached ones 1,335 us in 16-token pages (1,540 TFLOP/s, tensor
 // pipe 67% busy) and 1,300 in 64-token pages, the contiguous prefill of the same 1,320-1,390 (on the
 // prefill kernel, one block an SM: 1,750 and 1,400, its producers' 16 copies a tile being as long as the
-// tile); 64 sequences of 3-8 tokens over 1k-32k 750 us (6.3 TB/s).
+// tile); 64 sequences of 3-8 tokens over 1k-32k 736 us (6.5 TB/s).
 // Calls of at most 16 rows per key/value head go to attn_paged_few.cu.
 #include "attn_fwd_two.cuh"
 #include "attn_rows.cuh"
@@ -230,7 +230,7 @@ static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
   p.n_splits = sp.n_splits;
   p.split_steps = sp.split_steps;
   if (sp.n_splits > 1) paged_parts(a, D, sp.n_splits, p.ws_o, p.ws_ml);
-  auto kern = attn_fwd_two_kernel<D, BF16, true>;
+  auto kern = sp.n_qtiles == 1 ? attn_fwd_two_kernel<D, BF16, true, true> : attn_fwd_two_kernel<D, BF16, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
       cudaSuccess)
     return -5;
