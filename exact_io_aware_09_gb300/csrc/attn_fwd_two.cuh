@@ -5,7 +5,7 @@
 // item between the last tile of one and a full pipeline on the next, as much as nine 128-key tiles.
 // This kernel takes one work item per block and runs two blocks on an SM, so that one block's start
 // and end, and its waits, lie under the other's key loop.  What a block may hold is halved: 256
-// tensor-memory columns, 113 KB of shared memory, 128 registers a thread.
+// tensor-memory columns, about 100 KB of shared memory (113 at most), 128 registers a thread.
 //
 // Keys go in steps of 64: S = Q K_t^T is 128 x 64 in a tensor-memory buffer that is free as soon as the
 // softmax (one warpgroup, thread = query row) has read it; P_t goes as 16-bit pairs into one of two
