@@ -3,10 +3,13 @@
 // (token, key/value head) row.
 //
 // With codes kc_j, vc_j and scales 2^a_j, 2^b_j:  x_j = scale log2(e) 2^a_j (q . kc_j),
-// p_j = 2^(x_j - m), o = sum_j p_j 2^b_j vc_j / sum_j p_j.  The values' scale joins the exponent:
-// the running maximum is taken of x_j + b_j, the weight of vc_j is w_j = 2^(x_j + b_j - m) <= 1,
-// and the row sum adds w_j 2^-b_j.  So w_j goes into the second product as a 16-bit number
-// whatever the scales are, at the cost of one multiply.
+// p_j = 2^(x_j - m), o = sum_j p_j 2^b_j vc_j / sum_j p_j.  m and the row sum are those of the scores
+// alone.  The weights of the second product take the values' scales into their exponent, y_j = x_j + b_j,
+// and have a reference of their own: w_j = 2^(y_j - r + 7), r at most 8 below the largest y_j so far, so
+// that w_j <= 2^15 fits a 16-bit number and o is off by at most half a step of each w_j (2^-12 of it) and,
+// where w_j is below fp16's normal numbers, by 2^-32 of the largest p_j 2^b_j for each code.  A value row
+// of zeros adds nothing to o whatever its scale (the writer's is 1, often far above the other rows'), so
+// it takes no part in r: a tile that would raise r looks at its codes first.
 //
 // The split kernel is the 16-bit one's (attn_decode.cu) with half the bytes: blocks of (split,
 // key/value head, sequence), a producer warp bringing 64-token stages page by page with TMA, four
@@ -26,7 +29,7 @@
 // launch, no workspace.  More splits go through the workspace and the 16-bit decode's merge kernel.
 //
 // Bound by HBM: 2 (d + 4) bytes per cached token and head.  64 sequences of 1k-32k tokens (Hq=64 Hkv=8
-// d=128, 64-token pages, 2.45 GB): 396 us, 6.2 TB/s, against 723 for the 16-bit cache.  Without its
+// d=128, 64-token pages, 2.45 GB): 398 us, 6.2 TB/s, against 723 for the 16-bit cache.  Without its
 // arithmetic it takes as long; what counts is how the bytes are asked for: codes and scales both with the
 // policy that evicts their lines first (codes with the default one 411 us, scales as short asynchronous
 // copies with it 408).  One sequence of 1,001 tokens (Hq=16 Hkv=4 d=64): 12 us on the device, one launch.
@@ -45,8 +48,8 @@ struct DecFp8Params : DecParams {
   float* lse;
 };
 
-// l adds w_j 2^(-b_j - kSumShift): the sum stays in range for scales from 2^-126 to 2^94.
-constexpr int kSumShift = 32;
+// The weights' reference r rises when a key exceeds it by more than 2^kRise; a key at r weighs 2^kTop.
+constexpr float kRise = 8.0f, kTop = 7.0f;
 
 template <int D>
 struct Fp8Layout {
@@ -120,11 +123,13 @@ __device__ __forceinline__ void load_v_words(const uint8_t* vbuf, int row, int g
 
 }  // namespace
 
-// A warp's query rows and state (attn_rows.cuh) and its work on sixteen tokens.
+// A warp's query rows and state (attn_rows.cuh) and its work on sixteen tokens.  The state's m and l are
+// those of the scores, its o counts in units of 2^(ref - kTop).
 template <int D, bool BF16, int NT>
 struct Fp8Warp : RowState<D, NT, false> {
   uint32_t qf[NT][D / 16][2];
-  float f[NT][2];  // factors of the rows' products
+  float f[NT][2];    // factors of the rows' products
+  float ref[NT][2];  // the weights' reference; -inf before the first value row that is not zero
 
   // q: the group's query rows, G of them
   __device__ __forceinline__ void init(const uint16_t* q, int G, float sl2, int lane) {
@@ -132,6 +137,7 @@ struct Fp8Warp : RowState<D, NT, false> {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      ref[n][0] = ref[n][1] = -INFINITY;
       const int row = n * 8 + g;
       float mx = 0.0f;
 #pragma unroll
@@ -182,23 +188,53 @@ struct Fp8Warp : RowState<D, NT, false> {
           mma_m16n8k16<false>(sc[n], a, qf[n][h * 4 + i][0], qf[n][h * 4 + i][1]);
       }
     }
-    float x[NT][2][2], inv_b[2];
+    float y[NT][2][2];  // scores, then scores with the values' exponents
+    float bj[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float vj = __shfl_sync(0xffffffffu, scale, 16 + g + 8 * k);
       const float kj = __shfl_sync(0xffffffffu, scale, g + 8 * k);
-      const int vb = static_cast<int>(__float_as_uint(vj) >> 23) & 0xff;
-      const float bj = static_cast<float>(vb - 127);
-      inv_b[k] = __uint_as_float(static_cast<uint32_t>(max(254 - kSumShift - vb, 0)) << 23);
+      bj[k] = static_cast<float>((static_cast<int>(__float_as_uint(vj) >> 23) & 0xff) - 127);
       const bool in = g + 8 * k < valid;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          x[n][k][r] = in ? fmaf(sc[n][2 * k + r], f[n][r] * kj, bj) : -INFINITY;
+        for (int r = 0; r < 2; ++r) y[n][k][r] = in ? sc[n][2 * k + r] * (f[n][r] * kj) : -INFINITY;
     }
+    bool rise = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float& m = this->m[n][r];
+        float mx = fmaxf(y[n][0][r], y[n][1][r]);
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        const float mn = fmaxf(m, mx);
+        const float mu = (mn == -INFINITY) ? 0.f : mn;
+        this->l[n][r] = this->l[n][r] * ((m == -INFINITY) ? 0.f : ex2(m - mn)) + ex2(y[n][0][r] - mu) +
+                        ex2(y[n][1][r] - mu);
+        m = mn;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          y[n][k][r] += bj[k];
+          rise = rise || y[n][k][r] > ref[n][r] + kRise;
+        }
+      }
+    if (__any_sync(0xffffffffu, rise)) raise(y, vbuf, w0, lane);
     uint32_t pb[NT][2];
-    this->step(x, inv_b, pb);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float w[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float shift = (ref[n][r] == -INFINITY) ? 0.f : kTop - ref[n][r];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) w[k][r] = ex2(y[n][k][r] + shift);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) pb[n][k] = transpose_8x8(pack2<false>(w[k][0], w[k][1]));
+    }
     // this thread's channels of tile t are g D/8 + 2t and + 1: D/8 contiguous bytes of a token
     constexpr int kW = D / 32;
     uint32_t v[4][kW];
@@ -217,6 +253,63 @@ struct Fp8Warp : RowState<D, NT, false> {
         for (int n = 0; n < NT; ++n)
           mma_m16n8k16<false>(this->o[n][i * 2 + hh], av, pb[n][0], pb[n][1]);
       }
+  }
+
+  // Takes value rows of zeros out of y and raises the references to the largest of the rest where that
+  // exceeds them by more than 2^kRise.  Lane i looks at half a row's codes.
+  __device__ __forceinline__ void raise(float (&y)[NT][2][2], const uint8_t* vbuf, int w0, int lane) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(
+          vbuf + code_off<D>(w0 + (lane >> 1), (lane & 1) * (D / 32) + i));
+      any |= u.x | u.y | u.z | u.w;
+    }
+    const uint32_t some = __ballot_sync(0xffffffffu, (any & 0x7f7f7f7fu) != 0);  // two bits a row
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float a[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!((some >> (2 * ((lane >> 2) + 8 * k))) & 3u)) y[n][k][r] = -INFINITY;
+          mx = fmaxf(mx, y[n][k][r]);
+        }
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        a[r] = 1.0f;
+        if (mx > ref[n][r] + kRise) {
+          a[r] = (ref[n][r] == -INFINITY) ? 0.f : ex2(ref[n][r] - mx);
+          ref[n][r] = mx;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        this->o[n][t][0] *= a[0];
+        this->o[n][t][1] *= a[1];
+        this->o[n][t][2] *= a[0];
+        this->o[n][t][3] *= a[1];
+      }
+    }
+  }
+
+  // The state to the merge scratch, its rows divided by their sums: o 2^(ref - kTop - m) / l, the power
+  // of two in two halves, each of which is a normal number.
+  __device__ __forceinline__ void store(float* rw, int rows, int lane) const {
+    float h[NT][2], hl[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool none = ref[n][r] == -INFINITY;  // no key, or no value row that is not zero
+        h[n][r] = none ? 1.0f : ex2(0.5f * (ref[n][r] - kTop - this->m[n][r]));
+        hl[n][r] = this->l[n][r] == 0.f ? 0.f : h[n][r] / this->l[n][r];
+      }
+    RowState<D, NT, false>::store(
+        rw, rows, lane, [&](int t, int i) { return (lane >> 2) * (D / 8) + 2 * t + i; },
+        [&](int n, int r, float x) { return x * h[n][r] * hl[n][r]; });
   }
 };
 
@@ -367,13 +460,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 2)
   named_bar_sync(1, kDecWarps * 32);  // every warp is done with the ring
   ok = ok && (*abort_flag == 0);
   float* red = reinterpret_cast<float*>(gbase);  // [warp][row][D + 2]
-  const int g = lane >> 2;
-  if (ok)
-    st_w.store(red + warp * kMaxGroup * (D + 2), p.G, lane,
-               [&](int t, int i) { return g * (D / 8) + 2 * t + i; });
+  if (ok) st_w.store(red + warp * kMaxGroup * (D + 2), p.G, lane);
   named_bar_sync(1, kDecWarps * 32);
   const RowsOut w{p.ws_o, p.ws_ml, p.out, p.lse, p.max_splits, split, p.cluster != 0};
-  merge_rows<D, BF16, kDecWarps, kMaxGroup, kSumShift>(
+  merge_rows<D, BF16, kDecWarps, kMaxGroup, true>(
       red, reinterpret_cast<float*>(gbase + L::kFin), p.G, ok, n_tok > 0, w,
       [&](int row) { return static_cast<size_t>(b) * p.Hq + hq0 + row; });
 #undef FULL

@@ -204,7 +204,6 @@ __global__ void __launch_bounds__(kDecThreads, few_blocks_per_sm<D>())
     k_row[h] = stage_off(warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), h);
     v_row[h] = stage_off(warp * 16 + (lane >> 4) * 8 + (lane & 7), h);
   }
-  const float one[2] = {1.0f, 1.0f};
 
   bool ok = true;
   for (int st = 0; st < n_stages; ++st) {
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kDecThreads, few_blocks_per_sm<D>())
             x[u][k][r] = in ? sc[u][2 * k + r] * p.sl2 : -INFINITY;
           }
       uint32_t pb[NT][2];
-      rs.step(x, one, pb);
+      rs.step(x, pb);
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) {
         const int chunk = 2 * t + ((lane >> 3) & 1);
@@ -271,11 +270,12 @@ __global__ void __launch_bounds__(kDecThreads, few_blocks_per_sm<D>())
   ok = ok && (*abort_flag == 0);
   float* red = reinterpret_cast<float*>(gbase);  // [warp][row][D + 2]
   if (ok)
-    rs.store(red + warp * kFewRows * (D + 2), rows, lane, [&](int t, int i) { return 16 * t + 8 * i + g; });
+    rs.store(red + warp * kFewRows * (D + 2), rows, lane, [&](int t, int i) { return 16 * t + 8 * i + g; },
+             [](int, int, float x) { return x; });
   named_bar_sync(1, kDecWarps * 32);
   const RowsOut w{p.ws_o, p.ws_ml, p.out, p.lse, p.n_splits, split, p.cluster != 0};
-  merge_rows<D, BF16, kDecWarps, kFewRows, 0>(red, reinterpret_cast<float*>(gbase + L::kFin), rows,
-                                              ok, n_stages > 0, w, out_row);
+  merge_rows<D, BF16, kDecWarps, kFewRows, false>(red, reinterpret_cast<float*>(gbase + L::kFin), rows,
+                                                  ok, n_stages > 0, w, out_row);
 #undef FULL
 #undef EMPTY
 }

@@ -41,10 +41,9 @@ struct RowState {
   }
 
   // Online softmax over sixteen keys: x[n][k][r] the score of key g + 8k and row 2c + r (log2 units,
-  // -inf where masked), lw[k] what a weight of key g + 8k counts for in the row sum.  Rescales the
-  // state and gives the weights as the second operand of the next product.
-  __device__ __forceinline__ void step(const float (&x)[NT][2][2], const float (&lw)[2],
-                                       uint32_t (&pb)[NT][2]) {
+  // -inf where masked).  Rescales the state and gives the weights as the second operand of the next
+  // product.
+  __device__ __forceinline__ void step(const float (&x)[NT][2][2], uint32_t (&pb)[NT][2]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float p[2][2], a[2];
@@ -61,7 +60,7 @@ struct RowState {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           p[k][r] = ex2(x[n][k][r] - mu);
-          l[n][r] = fmaf(p[k][r], lw[k], l[n][r]);
+          l[n][r] += p[k][r];
         }
       }
       if (__any_sync(0xffffffffu, a[0] != 1.0f || a[1] != 1.0f)) {
@@ -88,9 +87,9 @@ struct RowState {
   }
 
   // The state to the warp's part of the merge scratch, [row][D + 2]; channel(t, i) is the channel
-  // of the thread's i-th row of tile t.
-  template <typename F>
-  __device__ __forceinline__ void store(float* rw, int rows, int lane, F channel) const {
+  // of the thread's i-th row of tile t, value(n, r, x) what is stored for x of row 2c + r of tile n.
+  template <typename F, typename V>
+  __device__ __forceinline__ void store(float* rw, int rows, int lane, F channel, V value) const {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -101,8 +100,8 @@ struct RowState {
         float* dst = rw + row * (D + 2);
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) {
-          dst[channel(t, 0)] = o[n][t][r];
-          dst[channel(t, 1)] = o[n][t][2 + r];
+          dst[channel(t, 0)] = value(n, r, o[n][t][r]);
+          dst[channel(t, 1)] = value(n, r, o[n][t][2 + r]);
         }
         if (g == 0) {
           dst[D] = m[n][r];
@@ -126,13 +125,12 @@ struct RowsOut {
 // Merges the states of WARPS warps (red: [warp][MAXR][D + 2]) for `rows` rows and writes them out;
 // every one of the WARPS * 32 threads calls it, after the last of them has stored its state and a
 // barrier.  fin: shared scratch of MAXR (D + 2) floats at the same address in every block.  ok: the
-// block's state is sound; any: it has keys.  The weights stand for 2^-SHIFT of what the maximum says
-// (the row sum carries that factor).  grow(row): the output row.
-template <int D, bool BF16, int WARPS, int MAXR, int SHIFT, typename F>
+// block's state is sound; any: it has keys.  NORM: the stored rows are divided by their sums already.
+// grow(row): the output row.
+template <int D, bool BF16, int WARPS, int MAXR, bool NORM, typename F>
 __device__ __forceinline__ void merge_rows(const float* red, float* fin, int rows, bool ok, bool any,
                                            const RowsOut& w, F grow) {
   constexpr int kRow = D + 2;
-  const float unshift = __uint_as_float(static_cast<uint32_t>(127 - SHIFT) << 23);
   if (ok || w.cluster) {
     for (int i = threadIdx.x; i < rows * D; i += WARPS * 32) {
       const int row = i / D, col = i % D;
@@ -147,22 +145,21 @@ __device__ __forceinline__ void merge_rows(const float* red, float* fin, int row
         // (no key: weight 0; a NaN sum stays one)
         const float wgt = (mw == -INFINITY) ? (lw == 0.f ? 0.f : lw) : ex2(mw - mm);
         ll += wgt * lw;
-        acc += wgt * red[(u * MAXR + row) * kRow + col];
+        acc += (NORM ? wgt * lw : wgt) * red[(u * MAXR + row) * kRow + col];
       }
-      const float o = ll == 0.f ? 0.f : acc / ll * unshift;
-      const float mo = mm + static_cast<float>(SHIFT);
+      const float o = ll == 0.f ? 0.f : acc / ll;
       if (w.cluster) {
         const bool use = ok && any;
         fin[row * D + col] = use ? o : 0.0f;
         if (col == 0) {
-          fin[MAXR * D + row * 2] = use ? mo : -INFINITY;
+          fin[MAXR * D + row * 2] = use ? mm : -INFINITY;
           fin[MAXR * D + row * 2 + 1] = use ? ll : 0.0f;
         }
       } else {
         const size_t part = grow(row) * w.n_splits + w.split;
         w.ws_o[part * D + col] = o;
         if (col == 0) {
-          w.ws_ml[part * 2] = mo;
+          w.ws_ml[part * 2] = mm;
           w.ws_ml[part * 2 + 1] = ll;
         }
       }

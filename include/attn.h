@@ -433,12 +433,14 @@ size_t attn_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int max_seq
 
 /*
  * attn_decode_paged_fp8 -- attn_decode_paged over a quantised cache: keys and values are code times
- * scale, read as attn_cache_write_fp8 stores them (the scales powers of two; V's from 2^-126 to
- * 2^94).  Arguments as attn_decode_paged with the two scale arrays added; q, o in `dtype`;
- * split_size 0 leaves the choice to the library; the workspace is that of
- * attn_decode_paged_fp8_workspace_bytes.  Both
+ * scale, read as attn_cache_write_fp8 stores them (the scales powers of two, any the writer makes).
+ * Arguments as attn_decode_paged with the two scale arrays added; q, o in `dtype`; split_size 0 leaves
+ * the choice to the library; the workspace is that of attn_decode_paged_fp8_workspace_bytes.  Both
  * products take the codes as they are (exact in fp16); a bf16 query is scaled by a power of two
- * per row and rounded to fp16, the weights are rounded to fp16, sums are fp32.
+ * per row and rounded to fp16; sums and the softmax statistics are fp32, so a value's magnitude times
+ * the sequence's tokens has to stay within fp32's range.  The weights p_j take the value rows' scales
+ * 2^b_j and are rounded to fp16: o is off by at most 2^-12 sum_j p_j |v_j| and, from what fp16's
+ * subnormals lose, 2^-32 max_j(p_j 2^b_j) sum_j |code_j|, the maximum over value rows that are not zero.
  */
 int attn_decode_paged_fp8(const void *q, const void *k_pages, const void *v_pages,
                           const float *k_scales, const float *v_scales,

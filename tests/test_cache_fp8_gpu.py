@@ -411,3 +411,116 @@ def test_refusals(attn):
     with pytest.raises(E):
         attn.attn_decode_paged_fp8(q, *cache, i32([[0] * 40]), seq, 640, split_size=64,
                                    workspace=torch.empty(4, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------------------- value rows far apart within a head
+def written(attn, ks, vs, page, dtype):
+    """A cache that attn_cache_write_fp8 filled with the sequences ks, vs (float64 [L, Hkv, d], rounded
+    to dtype), its table, the lengths, and each sequence's (codes, scale) of K and V as float64."""
+    import torch
+
+    lengths = [len(x) for x in ks]
+    Hkv, d = ks[0].shape[1:]
+    table, n_pages, _, _ = syn.paged_layout(lengths, page, seed=page)
+    cache = pool(n_pages, page, Hkv, d)
+    tab = torch.from_numpy(table).cuda()
+    cu = syn.cu_seqlens(lengths)
+    seq = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    bits = [syn.round_bits(np.concatenate(x).astype(np.float32), dtype) for x in (ks, vs)]
+    attn.attn_cache_write_fp8(*(syn.bits_to_tensor(x, dtype, "cuda") for x in bits), *cache, tab,
+                              torch.from_numpy(cu).cuda(), seq)
+    seqs = []
+    for x in bits:
+        s, c = chunk.quantise(bits_to_double(x, dtype))
+        seqs.append([(c[cu[b]:cu[b + 1]], s[cu[b]:cu[b + 1]]) for b in range(len(lengths))])
+    return cache, tab, seq, seqs
+
+
+def check_decode(attn, q, cache, tab, seq, seqs, Hkv, dtype, what, **kw):
+    """The decode step against the definition over the dequantised cache.
+
+    Tolerance: that of chunk.row_tolerance for weights of 11 bits, o's subnormals those of its own type
+    (values may be as small as 2^-120).  A weight is held as 2^7 times its share of
+    a reference that lies at most 2^8 below the largest p_j 2^(b_j) among the keys whose value row is not
+    zero (a row of zeros has no part in O, whatever its scale) and never above it, so that what fp16's
+    subnormals lose, 2^-25 at most, is 2^-32 of that largest one.  The value scale's exponent is added to
+    the score and taken out again: numbers of up to 2^7, rounded by 2^-18 each."""
+    B, Hq, d = q.shape
+    G, scale = Hq // Hkv, 1.0 / np.sqrt(d)
+    qt = syn.bits_to_tensor(q, dtype, "cuda")
+    o, lse = attn.attn_decode_paged_fp8(qt, *cache, tab, seq, int(seq.max()), scale=scale, **kw)
+    assert attn.attn_poll_status() == 0
+    qd = bits_to_double(q, dtype)
+    parts, sub = [], np.zeros((B * Hq, d))
+    for b in range(B):
+        (kc, ks), (vc, vs) = seqs[0][b], seqs[1][b]
+        for h in range(Hq):
+            k, v = (c[:, h // G] * s[:, h // G, None] for c, s in ((kc, ks), (vc, vs)))
+            parts.append(chunk.attend(qd[b, h][None], k, v, np.array([len(k) - 1]), scale))
+            x = scale * (k @ qd[b, h])
+            p = np.exp(x - x.max())
+            w = p / p.sum() * vs[:, h // G] * np.any(vc[:, h // G] != 0, axis=1)
+            sub[b * Hq + h] = 2.0 ** -32 * w.max(initial=0.0) * np.abs(vc[:, h // G]).sum(axis=0)
+    rows = chunk.Rows(*(np.concatenate(x) for x in zip(*parts)))
+    qk = np.abs(qd).reshape(B * Hq, d).max(axis=1) * np.array(
+        [scale * np.abs(seqs[0][b][0][:, h // G] * seqs[0][b][1][:, h // G, None]).sum(axis=1).max()
+         for b in range(B) for h in range(Hq)])
+    bf16 = dtype == "bf16"
+    t = 2.0 ** -20 * rows.score + 2.0 ** -17 + (2.0 ** -24 * qk if bf16 else 0.0)
+    el = (np.expm1(2.0 * t)[:, None] + 2.0 ** -11 + 2.0 ** -17) * rows.pv + sub
+    el += 2.0 ** (-8 if bf16 else -11) * (np.abs(rows.o) + el) + 2.0 ** (-134 if bf16 else -25)
+    ls = 2.0 * t + 2.0 ** -18 + 2.0 ** -21 * np.abs(rows.lse)
+    chunk.check(o.double().cpu().numpy().reshape(-1, d), lse.cpu().numpy().reshape(-1), rows, (el, ls),
+                what)
+
+
+# one block, a cluster of them, the workspace (33 splits); two column tiles
+@pytest.mark.parametrize("split", [0, 64, 2048])
+@pytest.mark.parametrize("Hq,Hkv,d,dtype,std", [(8, 2, 128, "bf16", 0.02), (8, 2, 128, "bf16", 1e-4),
+                                                (6, 1, 64, "bf16", 1e-6), (16, 1, 64, "f16", 0.02),
+                                                (8, 2, 128, "f16", 1e-2)])
+def test_decode_over_zero_value_rows(attn, Hq, Hkv, d, dtype, std, split):
+    """Tokens whose value rows are zero (padding, null tokens) and score highest: they take most of the
+    softmax and nothing of O, which the small values of the others make."""
+    rng = np.random.default_rng(7)
+    lengths = [2048, 333, 40, 1]
+    q = syn.host_normal_bits((len(lengths), Hq, d), 5, dtype)
+    qd = bits_to_double(q, dtype)
+    ks, vs = [], []
+    for b, n in enumerate(lengths):
+        k, v = rng.standard_normal((n, Hkv, d)), std * rng.standard_normal((n, Hkv, d))
+        zero = np.arange(min(16, n)) if b < 2 else np.arange(n)  # of b = 2, 3: every row
+        zero = np.concatenate([zero, rng.integers(0, n, n // 100)])
+        v[zero] = 0.0
+        k[zero] = 0.7 * qd[b, ::Hq // Hkv][None]  # a score of about 0.7 sqrt(d) for one query head a group
+        ks.append(k)
+        vs.append(v)
+    cache, tab, seq, seqs = written(attn, ks, vs, 64, dtype)
+    check_decode(attn, q, cache, tab, seq, seqs, Hkv, dtype, f"zero rows, std {std}", split_size=split)
+
+
+@pytest.mark.parametrize("split", [0, 64])
+@pytest.mark.parametrize("Hq,Hkv,d,dtype,spread", [(8, 2, 128, "bf16", 15), (3, 3, 64, "f16", 7),
+                                                   (16, 1, 128, "bf16", 60), (11, 1, 64, "bf16", 15)])
+def test_decode_with_value_scales_per_token(attn, Hq, Hkv, d, dtype, spread, split):
+    """Value rows whose magnitudes differ from token to token by up to 2^(2 spread)."""
+    rng = np.random.default_rng(8)
+    lengths = [1500, 90, 700]
+    q = syn.host_normal_bits((len(lengths), Hq, d), 6, dtype)
+    row = lambda n: np.exp2(rng.integers(-spread, spread + 1, size=(n, Hkv, 1)).astype(np.float64))
+    ks = [rng.standard_normal((n, Hkv, d)) for n in lengths]
+    vs = [rng.standard_normal((n, Hkv, d)) * row(n) for n in lengths]
+    cache, tab, seq, seqs = written(attn, ks, vs, 16, dtype)
+    check_decode(attn, q, cache, tab, seq, seqs, Hkv, dtype, f"2^+-{spread}", split_size=split)
+
+
+@pytest.mark.parametrize("split", [0, 64])
+@pytest.mark.parametrize("exponent", [-110, 87, 100, 112])
+def test_decode_of_the_largest_and_smallest_values(attn, exponent, split):
+    """bf16 values about 2^exponent, whose scales lie 7 below: any the writer makes is read."""
+    rng = np.random.default_rng(9)
+    q = syn.host_normal_bits((2, 8, 128), 7, "bf16")
+    ks = [rng.standard_normal((n, 2, 128)) for n in (900, 20)]
+    vs = [rng.standard_normal((n, 2, 128)) * 2.0 ** exponent for n in (900, 20)]
+    cache, tab, seq, seqs = written(attn, ks, vs, 32, "bf16")
+    check_decode(attn, q, cache, tab, seq, seqs, 2, "bf16", f"2^{exponent}", split_size=split)
