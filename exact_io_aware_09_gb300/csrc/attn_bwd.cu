@@ -36,8 +36,9 @@
 // Roundings.  P and dS enter their products in the operands' 16-bit type, since the tensor cores multiply
 // operands of one type: each term of dV, dK and dQ is off by at most half a step (2^-8 of it in bf16,
 // 2^-11 in fp16), about as much as rounding the gradients themselves; products with what the roundings
-// leave would add three to the seven.  D is formed from O as stored.  Sums, S, dP and the exponentials are
-// fp32.
+// leave would add three to the seven.  In fp16 both are held times powers of two that keep them within
+// its normal numbers (grad_scale in attn_bwd.cuh; kernel 0 takes the ranges, which costs it a pass over V).
+// D is formed from O as stored.  Sums, S, dP and the exponentials are fp32.
 //
 // The window variant (WINDOW; a sliding window whose first keys, the sinks, stay visible) walks only
 // the tiles a row sees.  A key tile with sinks is seen by every later query row, many times what a
@@ -90,17 +91,69 @@ __device__ __forceinline__ float half_to_f32(uint32_t h) {
 // Hq=64 N=8192 d=128 (268 MB, 6.4 TB/s), one row a lane 50.
 constexpr int kPreRows = 4;
 
+// The largest of a block's values (none negative) into N words that start at 0.  (With a warp's each
+// straight to the words the gradients of fp16 B=4 H=32 N=4096 d=128, W=256, take 700 us and not 633.)
+template <int N>
+__device__ __forceinline__ void block_max_to(uint32_t* word, const float (&v)[N]) {
+  __shared__ uint32_t top[N][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]));
+    if (lane == 0) top[i][warp] = w;
+  }
+  __syncthreads();
+  if (warp < N) {
+    const uint32_t w = __reduce_max_sync(0xffffffffu, lane < 8 ? top[warp][lane] : 0u);
+    if (lane == 0 && w > __ldcg(word + warp)) atomicMax(word + warp, w);
+  }
+}
+
+// fp16: also the ranges of each plane (grad_scale); the blocks from q_blocks on take the rows of V.  The
+// ranges, their use and the words' clearing cost, W=256: B=8 H=12 N=1024 d=64 65 -> 68 us, B=1 Hq=64 Hkv=8
+// N=8192 d=128 492 -> 508, B=4 H=32 N=4096 d=128 591 -> 633.
 template <int D, bool BF16>
-__global__ void attn_bwd_pre_kernel(const uint16_t* o, const uint16_t* dout, const float* lse,
-                                    float* lse2, float* dvec, int N_q, int nqp, long long rows,
-                                    float scale) {
+__global__ void __launch_bounds__(256)
+    attn_bwd_pre_kernel(const uint16_t* o, const uint16_t* dout, const uint16_t* v, const float* lse,
+                        float* lse2, float* dvec, uint32_t* range, int N_q, int nqp, int N_kv, int Hq,
+                        int Hkv, long long rows, unsigned q_blocks, float scale) {
   // D / 8 lanes per row, 16-byte loads of O and dO
   constexpr int kLanes = D / 8;
   if (threadIdx.x == 0) griddep_launch_dependents();  // dK/dV's setup and first loads may start
+  const int lane = threadIdx.x % kLanes;
+  if constexpr (!BF16) {
+    if (blockIdx.x >= q_blocks) {
+      constexpr int kRows = 256 / kLanes * kPreRows;  // of a block
+      const unsigned per = (static_cast<unsigned>(N_kv) + kRows - 1) / kRows;
+      const unsigned vb = blockIdx.x - q_blocks;
+      const int j0 = static_cast<int>(vb % per) * kRows + static_cast<int>(threadIdx.x / kLanes) * kPreRows;
+      float top = 0.0f;
+      uint4 a[kPreRows];
+#pragma unroll
+      for (int u = 0; u < kPreRows; ++u)
+        a[u] = j0 + u < N_kv ? *reinterpret_cast<const uint4*>(
+                                   v + (static_cast<size_t>(vb / per) * N_kv + j0 + u) * D + lane * 8)
+                             : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < kPreRows; ++u) {
+        const uint32_t av[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+        float sq = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float lo = half_to_f32<BF16>(av[c] & 0xffffu), hi = half_to_f32<BF16>(av[c] >> 16);
+          sq = fmaf(lo, lo, fmaf(hi, hi, sq));
+        }
+#pragma unroll
+        for (int sh = kLanes / 2; sh > 0; sh >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, sh);
+        top = fmaxf(top, sq);
+      }
+      block_max_to<1>(range + vb / per * 4 + 2, {sqrtf(top)});
+      return;
+    }
+  }
   const long long w0 =
       (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes * kPreRows;
-  const int lane = threadIdx.x % kLanes;
-  // the first row's (batch, query head) and index; nqp is a multiple of the rows a lane takes
+  // the first row's (batch, query head) and index; nqp is a multiple of the rows a block takes
   const long long bh = w0 < rows ? w0 / nqp : 0;
   const int i0 = w0 < rows ? static_cast<int>(w0 - bh * nqp) : N_q;
   uint4 a[kPreRows], b[kPreRows];
@@ -113,17 +166,28 @@ __global__ void attn_bwd_pre_kernel(const uint16_t* o, const uint16_t* dout, con
       b[u] = *reinterpret_cast<const uint4*>(dout + base);
     }
   }
+  [[maybe_unused]] float top_do = 0.0f, top_d = 0.0f;
 #pragma unroll
   for (int u = 0; u < kPreRows; ++u) {
     const uint32_t av[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bv[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
     float acc = 0.0f;
+    [[maybe_unused]] float sq = 0.0f;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      acc = fmaf(half_to_f32<BF16>(av[c] & 0xffffu), half_to_f32<BF16>(bv[c] & 0xffffu), acc);
-      acc = fmaf(half_to_f32<BF16>(av[c] >> 16), half_to_f32<BF16>(bv[c] >> 16), acc);
+      const float lo = half_to_f32<BF16>(bv[c] & 0xffffu), hi = half_to_f32<BF16>(bv[c] >> 16);
+      acc = fmaf(half_to_f32<BF16>(av[c] & 0xffffu), lo, acc);
+      acc = fmaf(half_to_f32<BF16>(av[c] >> 16), hi, acc);
+      if constexpr (!BF16) sq = fmaf(lo, lo, fmaf(hi, hi, sq));
     }
 #pragma unroll
-    for (int sh = kLanes / 2; sh > 0; sh >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, sh);
+    for (int sh = kLanes / 2; sh > 0; sh >>= 1) {
+      acc += __shfl_xor_sync(0xffffffffu, acc, sh);
+      if constexpr (!BF16) sq += __shfl_xor_sync(0xffffffffu, sq, sh);
+    }
+    if constexpr (!BF16) {
+      top_do = fmaxf(top_do, sq);
+      top_d = fmaxf(top_d, fabsf(scale * acc));
+    }
     if (w0 < rows && lane == 0) {
       // stored negated (and D times the scale), so that the elementwise steps are single FMAs:
       // s * scale log2(e) + (-L log2(e)) and dP * scale + (-scale D)
@@ -131,8 +195,13 @@ __global__ void attn_bwd_pre_kernel(const uint16_t* o, const uint16_t* dout, con
       dvec[w0 + u] = (i < N_q) ? -scale * acc : 0.0f;
       // a row that sees no key (L = -inf) takes part in nothing, as the padding rows
       const float L = (i < N_q) ? lse[bh * N_q + i] : -INFINITY;
-      lse2[w0 + u] = (L == -INFINITY) ? -INFINITY : -L * 1.4426950408889634f;
+      const float shift = BF16 ? 0.0f : static_cast<float>(kPShift);
+      lse2[w0 + u] = (L == -INFINITY) ? -INFINITY : fmaf(-L, 1.4426950408889634f, shift);
     }
+  }
+  if constexpr (!BF16) {
+    uint32_t* w = range + ((bh / Hq) * Hkv + (bh % Hq) / (Hq / Hkv)) * 4;
+    block_max_to<2>(w, {sqrtf(top_do), top_d});
   }
 }
 
@@ -399,7 +468,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     const int r = quarter * 32 + lane;
     const int kr = kt * kBT + r;  // this thread's key
     const uint32_t row_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const float sl2 = p.sl2, scale = p.scale;
+    if constexpr (!BF16) griddep_wait();  // kernel 0's ranges
+    const GradScale gs = grad_scale<BF16>(p, bkv);
+    const float sl2 = p.sl2, scale = p.scale * gs.u;
     const int q_first_visible = kr - off;  // the smallest query row that sees this key
     // window variant: the largest
     [[maybe_unused]] int q_last_visible = 0x7fffffff;
@@ -487,7 +558,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const int col = h * 32 + e;
-          const float4 d4 = *reinterpret_cast<const float4*>(dvv + col);
+          float4 d4 = *reinterpret_cast<const float4*>(dvv + col);
+          if constexpr (!BF16) {
+            fma2(d4.x, d4.y, d4.x, d4.y, gs.u, gs.u, 0.0f, 0.0f);
+            fma2(d4.z, d4.w, d4.z, d4.w, gs.u, gs.u, 0.0f, 0.0f);
+          }
           float u0, u1, u2, u3, g0, g1, g2, g3;
           fma2(u0, u1, __uint_as_float(dpv[h][e]), __uint_as_float(dpv[h][e + 1]), scale, scale, d4.x, d4.y);
           fma2(u2, u3, __uint_as_float(dpv[h][e + 2]), __uint_as_float(dpv[h][e + 3]), scale, scale, d4.z,
@@ -508,11 +583,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     const uint32_t col = wg ? L::kColDK : L::kColDV;
     if (partial) {
       const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2 + wg;
-      if (ok) store_part_row<D>(row_tmem + col, p.part + (at * kBT + r) * D, n > 0);
+      if (ok) store_part_row<D, BF16>(row_tmem + col, p.part + (at * kBT + r) * D, n > 0, wg ? gs.ds : gs.p);
     } else if (n > 0) {
       // dV over K, dK over V, whose products are done; each warpgroup its own
       const uint32_t tile = wg ? L::kV : L::kK;
-      if (ok) stage_acc_row<BF16>(row_tmem + col, gbase + tile, r, 0, D);
+      if (ok) stage_acc_row<BF16>(row_tmem + col, gbase + tile, r, 0, D, wg ? gs.ds : gs.p);
       fence_proxy_async_smem();
       named_bar_sync(1 + wg, kEwThreads);
       if (r == 0 && *abort_flag == 0) store_staged<D>(wg ? &tm_dk : &tm_dv, base + tile, kt * kBT, bkv);
@@ -826,9 +901,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const int row = qt * kBT + r;
     const uint32_t row_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const size_t vec = static_cast<size_t>(bh) * p.nqp + row;
-    const float nl2 = p.lse2[vec];  // -L log2(e)
-    const float nsd = p.dvec[vec];  // -scale D
-    const float sl2 = p.sl2, scale = p.scale;
+    const GradScale gs = grad_scale<BF16>(p, kv_plane);
+    const float nl2 = p.lse2[vec];         // -L log2(e)
+    const float nsd = p.dvec[vec] * gs.u;  // -scale D
+    const float sl2 = p.sl2, scale = p.scale * gs.u;
     int lim = p.causal ? row + (p.N_kv - p.N_q) : p.N_kv - 1;  // last visible key of this row
     if (lim > p.N_kv - 1) lim = p.N_kv - 1;
     [[maybe_unused]] int first_key = 0;  // first key of this row's window
@@ -929,7 +1005,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       if (ok) {
         tc_fence_after();
         stage_acc_row<BF16>(row_tmem + L::kColDQ, gbase + L::kDO, quarter * 32 + lane, wg * (D / 2),
-                            (wg + 1) * (D / 2));
+                            (wg + 1) * (D / 2), gs.ds);
       }
       fence_proxy_async_smem();
       named_bar_sync(1, 2 * kEwThreads);
@@ -989,7 +1065,8 @@ __global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(const BwdParams 
 size_t bwd_workspace_bytes(int B, int Hq, int N_q) {
   if (B <= 0 || Hq <= 0 || N_q <= 0) return 0;
   const size_t nqp = (static_cast<size_t>(N_q) + kBT - 1) / kBT * kBT;
-  return static_cast<size_t>(B) * Hq * nqp * 8;  // L log2(e) and D, fp32
+  // L log2(e) and D, fp32; four words of ranges a plane (at most one a query head)
+  return static_cast<size_t>(B) * Hq * (nqp * 8 + 16);
 }
 
 // 64-query steps of the dK/dV job for key tile kt (as the kernel counts them).
@@ -1197,12 +1274,22 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
   if constexpr (WINDOW) {
     sink_split(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.N_kv - a.N_q, a.window, a.sinks,
                p.sink_tiles, p.sink_parts);
-    p.part = const_cast<float*>(p.lse2) + 2 * bhq * nqp;
+    p.part = const_cast<float*>(p.lse2) + bhq * (2 * static_cast<uint64_t>(nqp) + 4);
   }
+  uint32_t* range = reinterpret_cast<uint32_t*>(const_cast<float*>(p.lse2) + 2 * bhq * nqp);
+  p.range = range;
   const long long rows = static_cast<long long>(bhq) * nqp;
-  attn_bwd_pre_kernel<D, BF16><<<static_cast<unsigned>((rows / kPreRows * (D / 8) + 255) / 256), 256, 0, stream>>>(
-      static_cast<const uint16_t*>(a.o), static_cast<const uint16_t*>(a.dout), a.lse,
-      const_cast<float*>(p.lse2), const_cast<float*>(p.dvec), a.N_q, nqp, rows, a.scale);
+  const unsigned pre_blocks = static_cast<unsigned>((rows / kPreRows * (D / 8) + 255) / 256);
+  unsigned v_blocks = 0;
+  if (!BF16) {
+    constexpr int kRows = 256 / (D / 8) * kPreRows;
+    v_blocks = static_cast<unsigned>(bhk * ((a.N_kv + kRows - 1) / kRows));
+    if (cudaMemsetAsync(range, 0, bhk * 16, stream) != cudaSuccess) return -5;
+  }
+  attn_bwd_pre_kernel<D, BF16><<<pre_blocks + v_blocks, 256, 0, stream>>>(
+      static_cast<const uint16_t*>(a.o), static_cast<const uint16_t*>(a.dout), p.v, a.lse,
+      const_cast<float*>(p.lse2), const_cast<float*>(p.dvec), range, a.N_q, nqp, a.N_kv, a.Hq, a.Hkv, rows,
+      pre_blocks, a.scale);
   if (cudaGetLastError() != cudaSuccess) return -5;
   // two blocks on an SM (attn_bwd_window.cu) for either kernel
   const bool kv_two = WINDOW && D == 64 && bwd_window_two_kv(a), q_two = WINDOW && D == 64 && bwd_window_two_q(a);

@@ -11,7 +11,7 @@ constexpr uint32_t kSub = 128 * 128;  // bytes of one 64-column, 128-row swizzle
 constexpr uint64_t kBwdDrainNs = 100000000ull;
 
 struct BwdParams {
-  const float* lse2;  // [B*Hq, nqp]  -L * log2(e); -inf on padding rows
+  const float* lse2;  // [B*Hq, nqp]  -L * log2(e), fp16: + kPShift; -inf on padding rows
   const float* dvec;  // [B*Hq, nqp]  -scale * D; 0 on padding rows
   const uint16_t* q;     // [B, Hq, N_q, d]
   const uint16_t* k;     // [B, Hkv, N_kv, d]
@@ -27,7 +27,35 @@ struct BwdParams {
   int window, sinks;  // window variant: keys behind the diagonal, first keys always visible
   int sink_tiles, sink_parts;  // ... its key tiles with sinks, each cut into that many blocks
   float* part;        // [B*Hkv, sink_tiles, sink_parts][dV, dK][128, d] their partial sums
+  // fp16: [B*Hkv][4] the largest |dO_i|, scale |D_i| and |V_j| (row norms) of a plane, as bits
+  const uint32_t* range;
 };
+
+// fp16 holds numbers from 2^-14 to 2^16 with all their bits.  P and dS enter their products there times
+// powers of two that the gradients are divided by at the end: P times 2^kPShift (P <= 1; lse2 carries the
+// shift), dS of a (batch, key/value head) plane times 2^t, the largest for which
+//   |dS_ij| <= scale (|dP_ij| + |D_i|) <= scale max |dO_i| max |V_j| + max scale |D_i|
+// stays below 2^15.  Error of dQ and dK, N=2048 W=1024 d=128, of their norm, without / with: dO ~ 1 2.9e-4
+// / 2.9e-4, 2^-6 4.6e-4 / 2.9e-4, 2^-10 5.9e-3 / 3.4e-4 (rounding the result alone: 2.6e-4); of all three,
+// 131,072 keys a row: 1.3e-3 / 3.4e-4.  bf16 has fp32's range.
+constexpr int kPShift = 6;  // a weight is normal down to 2^-20; some room above 1
+struct GradScale {
+  float u;   // of dP and D, beside the 2^kPShift that P brings
+  float p;   // of dV's sum
+  float ds;  // of dQ's and dK's sums
+};
+template <bool BF16>
+__device__ __forceinline__ GradScale grad_scale(const BwdParams& p, int plane) {
+  if constexpr (BF16) return {1.0f, 1.0f, 1.0f};
+  const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p.range) + plane);
+  const float bound = p.scale * __uint_as_float(w.x) * __uint_as_float(w.z) + __uint_as_float(w.y);
+  int t = 0;  // a plane of zeros, or one that is not finite
+  if (bound > 0.0f && bound < INFINITY) t = 14 - (static_cast<int>(__float_as_uint(bound) >> 23) - 127);
+  t = max(-80, min(t, 80));
+  return {__uint_as_float(static_cast<uint32_t>(127 + t - kPShift) << 23),
+          __uint_as_float(static_cast<uint32_t>(127 - kPShift) << 23),
+          __uint_as_float(static_cast<uint32_t>(127 - t) << 23)};
+}
 
 // Window variant: the query tiles [qt_lo, qt_hi) that see key tile kt.  A tile with a sink is seen
 // from its diagonal to the last row, any other until the window has passed its last key.
@@ -48,17 +76,23 @@ __device__ __forceinline__ bool ew_wait(uint32_t bar, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, ok);
 }
 
-// Columns [c0, c1) (multiples of 32) of row r of a 128 x D accumulator as 16-bit values in a tile of
+// Columns [c0, c1) (multiples of 32) of row r of a 128 x D accumulator, times mul where the operands are
+// fp16 (a power of two; 1 for bf16), as 16-bit values in a tile of
 // shared memory (64-column sub-tiles kSub apart, 128-byte swizzle), from where TMA stores take the rows
 // that exist: written to memory by the threads that hold them, a warp's stores would touch 32 lines each
 // (a block's end took a microsecond longer).
 template <bool BF16>
-__device__ __forceinline__ void stage_acc_row(uint32_t row_tmem_col, uint8_t* tile, int r, int c0, int c1) {
+__device__ __forceinline__ void stage_acc_row(uint32_t row_tmem_col, uint8_t* tile, int r, int c0, int c1,
+                                              [[maybe_unused]] float mul) {
 #pragma unroll 1
   for (int c = c0 / 32; c < c1 / 32; ++c) {
     uint32_t a[32];
     tmem_ld32(row_tmem_col + c * 32, a);
     tmem_wait_ld();
+    if constexpr (!BF16) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * mul);
+    }
     uint8_t* sub = tile + (c >> 1) * kSub;
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4)
@@ -79,15 +113,21 @@ __device__ __forceinline__ void store_staged(const CUtensorMap* m, uint32_t tile
   tma_store_wait_read0();  // the block's shared memory may go
 }
 
-// Row of a 128 x D accumulator as fp32 values (zeros for an accumulator nothing was added to).
-template <int D>
-__device__ __forceinline__ void store_part_row(uint32_t row_tmem_col, float* dst, bool any) {
+// Row of a 128 x D accumulator as fp32 values (zeros for an accumulator nothing was added to); mul as
+// above.
+template <int D, bool BF16>
+__device__ __forceinline__ void store_part_row(uint32_t row_tmem_col, float* dst, bool any,
+                                               [[maybe_unused]] float mul) {
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     uint32_t a[32];
     if (any) {
       tmem_ld32(row_tmem_col + c * 32, a);
       tmem_wait_ld();
+      if constexpr (!BF16) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * mul);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 32; ++e) a[e] = 0;

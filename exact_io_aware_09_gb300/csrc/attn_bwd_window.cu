@@ -13,7 +13,8 @@
 // warp 4 TMA producer, warps 5 and 6 tcgen05 issuers (warp 5 owns the tensor memory).  Every wait on a barrier is
 // bounded.
 //
-// Roundings as in attn_bwd.cu: P and dS to the operands' type, everything else fp32.
+// Roundings as in attn_bwd.cu: P and dS to the operands' type (in fp16 times powers of two), everything
+// else fp32.
 //
 // Bound by a step's chain of products and elementwise work at two blocks an SM (tensor pipe 25% busy,
 // 1.4 instructions a cycle).  B=8 H=12 N=1024 bf16, W=256, 4 sinks: dK/dV 37 us, dQ 26.5 (one block an
@@ -268,7 +269,9 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     const int r = warp * 32 + lane;
     const int kr = kt * kBT + r;
     const uint32_t row_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const float sl2 = p.sl2, scale = p.scale;
+    if constexpr (!BF16) griddep_wait();  // kernel 0's ranges
+    const GradScale gs = grad_scale<BF16>(p, bkv);
+    const float sl2 = p.sl2, scale = p.scale * gs.u;
     // the query rows [q_first, q_last] see this key
     const int q_first = kr - off;
     int q_last = 0x7fffffff;
@@ -336,7 +339,11 @@ __global__ void __launch_bounds__(kBwThreads, 2)
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 d4 = *reinterpret_cast<const float4*>(lv + kStepQ + h * 32 + e);
+          float4 d4 = *reinterpret_cast<const float4*>(lv + kStepQ + h * 32 + e);
+          if constexpr (!BF16) {
+            fma2(d4.x, d4.y, d4.x, d4.y, gs.u, gs.u, 0.0f, 0.0f);
+            fma2(d4.z, d4.w, d4.z, d4.w, gs.u, gs.u, 0.0f, 0.0f);
+          }
           float u0, u1, u2, u3, g0, g1, g2, g3;
           fma2(u0, u1, __uint_as_float(dpv[e]), __uint_as_float(dpv[e + 1]), scale, scale, d4.x, d4.y);
           fma2(u2, u3, __uint_as_float(dpv[e + 2]), __uint_as_float(dpv[e + 3]), scale, scale, d4.z, d4.w);
@@ -357,14 +364,14 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     if (partial) {
       const size_t at = ((static_cast<size_t>(bkv) * p.sink_tiles + kt) * p.sink_parts + part) * 2;
       if (ok) {
-        store_part_row<kBwD>(row_tmem + L::kColDV, p.part + (at * kBT + r) * kBwD, n > 0);
-        store_part_row<kBwD>(row_tmem + L::kColDK, p.part + ((at + 1) * kBT + r) * kBwD, n > 0);
+        store_part_row<kBwD, BF16>(row_tmem + L::kColDV, p.part + (at * kBT + r) * kBwD, n > 0, gs.p);
+        store_part_row<kBwD, BF16>(row_tmem + L::kColDK, p.part + ((at + 1) * kBT + r) * kBwD, n > 0, gs.ds);
       }
     } else if (n > 0) {
       // over K and V, whose products are done
       if (ok) {
-        stage_acc_row<BF16>(row_tmem + L::kColDV, gbase + L::kK, r, 0, kBwD);
-        stage_acc_row<BF16>(row_tmem + L::kColDK, gbase + L::kV, r, 0, kBwD);
+        stage_acc_row<BF16>(row_tmem + L::kColDV, gbase + L::kK, r, 0, kBwD, gs.p);
+        stage_acc_row<BF16>(row_tmem + L::kColDK, gbase + L::kV, r, 0, kBwD, gs.ds);
       }
       fence_proxy_async_smem();
       named_bar_sync(1, kBT);
@@ -556,9 +563,10 @@ __global__ void __launch_bounds__(kBwThreads, 2)
     const int r = warp * 32 + lane;
     const int row = qt * kBT + r;
     const uint32_t row_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const float sl2 = p.sl2, scale = p.scale;
+    const GradScale gs = grad_scale<BF16>(p, kv_plane);
+    const float sl2 = p.sl2, scale = p.scale * gs.u;
     const size_t vec = static_cast<size_t>(bh) * p.nqp + row;
-    const float nl2 = p.lse2[vec], nd = p.dvec[vec];
+    const float nl2 = p.lse2[vec], nd = p.dvec[vec] * gs.u;
     const int pos = row + (p.N_kv - p.N_q);
     const int lim = min(pos, p.N_kv - 1);          // last visible key
     const int first_key = max(pos - p.window, 0);  // first key of the window
@@ -632,7 +640,8 @@ __global__ void __launch_bounds__(kBwThreads, 2)
       if (ok) ok = ew_wait(DQ_DONE((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, p.status);
       if (ok) {
         tc_fence_after();
-        stage_acc_row<BF16>(row_tmem + L::kColDQ, gbase + L::kQ, r, 0, kBwD);  // over Q, whose products are done
+        // over Q, whose products are done
+        stage_acc_row<BF16>(row_tmem + L::kColDQ, gbase + L::kQ, r, 0, kBwD, gs.ds);
       }
       fence_proxy_async_smem();
       named_bar_sync(1, kBT);

@@ -94,7 +94,8 @@ int attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse, i
 
 /*
  * attn_bwd_workspace_bytes -- bytes of the workspace attn_bwd needs: two fp32 values (L log2 e
- * and D) per query row, rounded up to whole 128-row tiles.  0 for invalid arguments.
+ * and D) per query row, rounded up to whole 128-row tiles, and 16 bytes per query head.  0 for
+ * invalid arguments.
  */
 size_t attn_bwd_workspace_bytes(int B, int Hq, int N_q);
 
