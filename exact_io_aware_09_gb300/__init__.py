@@ -4,6 +4,9 @@ The functions below only marshal arguments (torch tensors -> device pointers, si
 current CUDA stream) and call the C ABI declared in ``include/attn.h``; every step of the
 computation runs in the library's CUDA kernels.  There is no CPU or PyTorch fallback: if the
 library is missing the import fails, and an unsupported request raises ``AttnError``.
+
+What a call allocates, results and workspace, belongs to the stream it runs on (``stream``, or
+torch's current one): another stream uses a result after waiting for that one.
 """
 from __future__ import annotations
 
@@ -152,7 +155,7 @@ def _stream_handle(stream, device=None):
 def _allocating(stream, device):
     """A context in which torch allocates for ``stream``, the stream the call runs on: a workspace
     given back when the call returns is then reused behind the call's kernels and not beside them."""
-    if stream is None:
+    if stream is None or device.type != "cuda":  # (tensors off the GPU are refused later)
         return _NO_SWITCH
     handle = _stream_handle(stream, device)
     cuda = _torch().cuda
@@ -232,12 +235,13 @@ def attn_fwd(q, k, v, o=None, lse=None, causal: bool = False, scale: float | Non
     _, Hkv, N_kv, _ = k.shape
     if k.shape != v.shape or k.shape[0] != B or k.shape[3] != d or k.dtype != q.dtype or v.dtype != q.dtype:
         raise AttnError(-1, "attn_fwd: q/k/v shapes or dtypes disagree")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq, N_q), device=q.device, dtype=torch.float32)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    with _allocating(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, N_q), device=q.device, dtype=torch.float32)
     with _on_device("attn_fwd", q, k, v, o, lse):
         st = lib.attn_fwd(_dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(o, "o"),
                           _dev_ptr(lse, "lse"), B, Hq, Hkv, N_q, N_kv, d, int(bool(causal)),
@@ -252,16 +256,17 @@ def _expect(where, t, name, dtype, shape):
                             f"got {t.dtype} {tuple(t.shape)}")
 
 
-def _fwd_prep(q, k, v, o, lse, scale):
+def _fwd_prep(q, k, v, o, lse, scale, stream):
     torch = _torch()
     B, Hq, N_q, d = q.shape
     _, Hkv, N_kv, _ = k.shape
     if k.shape != v.shape or k.shape[0] != B or k.shape[3] != d or k.dtype != q.dtype or v.dtype != q.dtype:
         raise AttnError(-1, "attn_fwd: q/k/v shapes or dtypes disagree")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq, N_q), device=q.device, dtype=torch.float32)
+    with _allocating(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, N_q), device=q.device, dtype=torch.float32)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     return B, Hq, Hkv, N_q, N_kv, d, o, lse, float(scale)
@@ -286,14 +291,15 @@ def attn_bwd(q, k, v, o, dout, lse, causal: bool = False, scale: float | None = 
             raise AttnError(-1, f"attn_bwd: {nm} must match q")
     if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype or lse.dtype != torch.float32:
         raise AttnError(-1, "attn_bwd: k/v/lse shapes or dtypes disagree")
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if workspace is None:
-        workspace = torch.empty(max(int(lib.attn_bwd_workspace_bytes(B, Hq, N_q)), 1),
-                                device=q.device, dtype=torch.uint8)
+    with _allocating(stream, q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            workspace = torch.empty(max(int(lib.attn_bwd_workspace_bytes(B, Hq, N_q)), 1),
+                                    device=q.device, dtype=torch.uint8)
     with _on_device("attn_bwd", q, k, v, o, dout, lse, dq, dk, dv, workspace):
         st = lib.attn_bwd(_dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(o, "o"),
                           _dev_ptr(dout, "dout"), _dev_ptr(lse, "lse"), _dev_ptr(dq, "dq"),
@@ -322,12 +328,13 @@ def attn_fwd_fp8(q, k, v, signs=None, o=None, lse=None, causal: bool = False,
     """FP8 prefill with incoherent processing.  signs: int8 CUDA tensor [d] of +-1 (None: no
     rotation).  Shapes and return value as attn_fwd (d = 128)."""
     torch = _torch()
-    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
+    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale, stream)
     if signs is not None and (signs.dtype != torch.int8 or tuple(signs.shape) != (d,)):
         raise AttnError(-1, "attn_fwd_fp8: signs must be int8 [d]")
     if workspace is None:
-        workspace = torch.empty(max(1, attn_fwd_fp8_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d)),
-                                device=q.device, dtype=torch.uint8)
+        with _allocating(stream, q.device):
+            workspace = torch.empty(max(1, attn_fwd_fp8_workspace_bytes(B, Hq, Hkv, N_q, N_kv, d)),
+                                    device=q.device, dtype=torch.uint8)
     with _on_device("attn_fwd_fp8", q, k, v, o, lse, signs, workspace):
         st = lib.attn_fwd_fp8(_dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
                               _dev_ptr(o, "o"), _dev_ptr(lse, "lse"), B, Hq, Hkv, N_q, N_kv, d,
@@ -345,7 +352,7 @@ def attn_fwd_window(q, k, v, window: int, o=None, lse=None, scale: float | None 
 
     Shapes and return value as attn_fwd.
     """
-    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
+    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale, stream)
     with _on_device("attn_fwd_window", q, k, v, o, lse):
         st = lib.attn_fwd_window(_dev_ptr(q, "q"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
                                  _dev_ptr(o, "o"), _dev_ptr(lse, "lse"), B, Hq, Hkv, N_q, N_kv, d,
@@ -360,8 +367,7 @@ def attn_fwd_window_sinks(q, k, v, window: int, sinks: int, o=None, lse=None,
     """Sliding-window prefill whose first ``sinks`` keys stay visible: key j visible to row i,
     p = i + N_kv - N_q, iff j <= p and (p - j <= window or j < sinks).
 
-    Shapes and return value as attn_fwd.  What this call and those below allocate, results and
-    workspace, belongs to ``stream``.
+    Shapes and return value as attn_fwd.
     """
     torch = _torch()
     where = "attn_fwd_window_sinks"
@@ -369,8 +375,7 @@ def attn_fwd_window_sinks(q, k, v, window: int, sinks: int, o=None, lse=None,
         _expect(where, o, "o", q.dtype, q.shape)
     if lse is not None:
         _expect(where, lse, "lse", torch.float32, q.shape[:3])
-    with _allocating(stream, q.device):
-        B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
+    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale, stream)
     index, p = _pointers(where, ("q", "k", "v", "o", "lse"), (q, k, v, o, lse))
     with _device(index):
         st = lib.attn_fwd_window_sinks(*p, B, Hq, Hkv, N_q, N_kv, d, int(window), int(sinks), scale,
@@ -428,7 +433,7 @@ def attn_fwd_block_sparse(q, k, v, block_mask, causal: bool = False, o=None, lse
     nonzero = compute that (query tile, key tile) block.  Shapes and return value as attn_fwd.
     """
     torch = _torch()
-    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale)
+    B, Hq, Hkv, N_q, N_kv, d, o, lse, scale = _fwd_prep(q, k, v, o, lse, scale, stream)
     shape = ((N_q + 127) // 128, (N_kv + 127) // 128)
     if (block_mask.dtype != torch.uint8 or tuple(block_mask.shape) != shape
             or not block_mask.is_contiguous()):
@@ -469,15 +474,16 @@ def attn_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k:
         raise AttnError(-1, "attn_decode_paged: block_table must be int32 [B, max_pages]")
     if seqlens_k.dtype != torch.int32 or tuple(seqlens_k.shape) != (B,):
         raise AttnError(-1, "attn_decode_paged: seqlens_k must be int32 [B]")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     need = attn_decode_workspace_bytes(B, Hq, max_seqlen_k, split_size, d)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
+    with _allocating(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
     with _on_device("attn_decode_paged", q, k_pages, v_pages, block_table, seqlens_k, o, lse,
                     workspace):
         st = lib.attn_decode_paged(_dev_ptr(q, "q"), _dev_ptr(k_pages, "k_pages"),
@@ -697,15 +703,16 @@ def attn_decode_splitkv(q, k_cache, v_cache, cu_seqlens_k, max_seqlen_k: int, o=
     cap, Hkv, _ = k_cache.shape
     if cu_seqlens_k.dtype != torch.int32 or cu_seqlens_k.numel() != B + 1:
         raise AttnError(-1, "attn_decode_splitkv: cu_seqlens_k must be int32 [B+1]")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     need = attn_decode_workspace_bytes(B, Hq, max_seqlen_k, split_size, d)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+    with _allocating(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
     with _on_device("attn_decode_splitkv", q, k_cache, v_cache, cu_seqlens_k, o, lse,
                     workspace):
         st = lib.attn_decode_splitkv(_dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
@@ -740,12 +747,13 @@ def attn_decode_splitkv_static(q, k_cache, v_cache, cu_seqlens_k, max_seqlen_k: 
     cap, Hkv, _ = k_cache.shape
     if cu_seqlens_k.dtype != torch.int32 or cu_seqlens_k.numel() != B + 1:
         raise AttnError(-1, "attn_decode_splitkv_static: cu_seqlens_k must be int32 [B+1]")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    with _allocating(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
     with _on_device("attn_decode_splitkv_static", q, k_cache, v_cache, cu_seqlens_k, o, lse):
         st = lib.attn_decode_splitkv_static(_dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
                                             _dev_ptr(v_cache, "v_cache"),
