@@ -159,8 +159,11 @@ def _allocating(stream, device):
         return _NO_SWITCH
     handle = _stream_handle(stream, device)
     cuda = _torch().cuda
-    return cuda.stream(stream if hasattr(stream, "cuda_stream")
-                       else cuda.ExternalStream(handle, device=device))
+    if hasattr(stream, "cuda_stream"):
+        return cuda.stream(stream)
+    # handle 0, the legacy default stream, makes a stream of torch's pool of an ExternalStream
+    return cuda.stream(cuda.ExternalStream(handle, device=device) if handle
+                       else cuda.default_stream(device))
 
 
 def _on_device(where, first, *others):

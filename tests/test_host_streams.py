@@ -87,3 +87,16 @@ def test_allocations_belong_to_the_calls_stream(attn, monkeypatch, name):
                             lambda *a, real_f=real_f, **kw: (made.append(owner[-1]), real_f(*a, **kw))[1])
     call(stream="the call's")
     assert made and all(o == "the call's" for o in made), made
+
+
+def test_handle_zero_is_the_default_stream(attn, monkeypatch):
+    """The legacy default stream's handle is 0, which no external stream object stands for (torch makes a
+    stream of its pool of it): the allocations are the device's default stream's."""
+    import torch
+
+    dev = torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: ("external", handle, device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert attn._allocating(0, dev) == ("default", dev)
+    assert attn._allocating(1 << 20, dev) == ("external", 1 << 20, dev)

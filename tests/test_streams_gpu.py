@@ -77,3 +77,21 @@ def test_a_busy_stream_keeps_what_the_call_allocated(attn, name, as_int):
     assert attn.attn_poll_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(got, want)), name
     del filled
+
+
+def test_the_default_stream_by_its_handle(attn):
+    """The same with the busy stream the legacy default one, handed over as its handle, 0."""
+    import torch
+
+    call, need = cases(attn)["attn_decode_splitkv"]
+    want = call()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = call(stream=0)
+        filled = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+                  for n in (need, *(t.nbytes for t in got)) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert attn.attn_poll_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del filled
