@@ -49,8 +49,8 @@
 // 42 us, dK/dV 437 (tensor pipe 70% busy), dQ 376 (56%: nine key tiles a block do not hide its start and
 // end), sums 5.  At d = 64 calls of many short tiles take the kernels of attn_bwd_window.cu.
 #include <algorithm>
+#include <list>
 #include <map>
-#include <memory>
 #include <mutex>
 #include <queue>
 #include <tuple>
@@ -1189,31 +1189,54 @@ int bwd_kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, i
   return n == n_jobs ? n : 0;
 }
 
-// The packed dispatch order (KvOrder) for one shape on the current device, computed once and
-// kept.
-static const KvOrder* kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal,
-                               int off, int window, int sinks) {
-  static const KvOrder kDefault = {0, {}};
+// The packed dispatch order (KvOrder) for one shape on the current device.  Packing takes a few
+// milliseconds, so the orders of the last kKeptOrders shapes are kept (4 KB each; a shape in the default
+// order needs none).
+constexpr size_t kKeptOrders = 512;
+
+static void kv_order(int n_planes, int n_kvtiles, int n_qtiles, int G, int causal, int off, int window,
+                     int sinks, KvOrder& order) {
+  order.n = 0;
   int dev = 0, n_sm = 0;
   if (!causal || cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return &kDefault;
+    return;
   using Key = std::tuple<int, int, int, int, int, int, int, int>;
-  static std::map<Key, std::unique_ptr<KvOrder>> cache;
+  struct Kept {
+    KvOrder order;
+    std::list<Key>::iterator at;
+  };
+  static std::map<Key, Kept> cache;
+  static std::list<Key> used;  // last used first
   static std::mutex mu;
   const Key key{n_planes, n_kvtiles, n_qtiles, G, off, window, sinks, n_sm};
   try {
+    {
+      std::lock_guard<std::mutex> lock(mu);
+      auto it = cache.find(key);
+      if (it != cache.end()) {
+        used.splice(used.begin(), used, it->second.at);
+        order = it->second.order;
+        return;
+      }
+    }
+    order.n = bwd_kv_order(n_planes, n_kvtiles, n_qtiles, G, causal, off, window, sinks, n_sm, order.job,
+                           kMaxKvOrder);
+    if (order.n == 0) return;
     std::lock_guard<std::mutex> lock(mu);
-    auto it = cache.find(key);
-    if (it != cache.end()) return it->second.get();
-    auto order = std::make_unique<KvOrder>();
-    order->n = bwd_kv_order(n_planes, n_kvtiles, n_qtiles, G, causal, off, window, sinks, n_sm,
-                            order->job, kMaxKvOrder);
-    const KvOrder* out = order.get();
-    cache.emplace(key, std::move(order));
-    return out;
-  } catch (...) {  // out of host memory: the default order serves
-    return &kDefault;
+    if (cache.count(key)) return;  // another thread has packed it meanwhile
+    while (cache.size() >= kKeptOrders) {
+      cache.erase(used.back());
+      used.pop_back();
+    }
+    used.push_front(key);
+    try {
+      cache.emplace(key, Kept{order, used.begin()});
+    } catch (...) {
+      used.pop_front();
+      throw;
+    }
+  } catch (...) {  // out of host memory: the default order, or this one unkept, serves
   }
 }
 
@@ -1315,12 +1338,13 @@ static int launch_bwd_variant(const BwdArgs& a, cudaStream_t stream) {
     const int st = launch_bwd_window_dkdv(a, p, static_cast<unsigned>(kv_blocks), stream);
     if (st != 0) return st;
   } else {
-    const KvOrder* order = kv_order(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.causal,
-                                    a.N_kv - a.N_q, a.window, a.sinks);
+    KvOrder order;
+    kv_order(static_cast<int>(bhk), p.n_kvtiles, n_qtiles, p.G, a.causal, a.N_kv - a.N_q, a.window, a.sinks,
+             order);
     cfg.gridDim = dim3(static_cast<unsigned>(kv_blocks));
     cfg.blockDim = dim3(kKvThreads);
     cfg.dynamicSmemBytes = LK::kBytes;
-    if (cudaLaunchKernelEx(&cfg, kkv, tq64, tk, tv, tdo64, tdk, tdv, p, *order) != cudaSuccess) return -5;
+    if (cudaLaunchKernelEx(&cfg, kkv, tq64, tk, tv, tdo64, tdk, tdv, p, order) != cudaSuccess) return -5;
   }
   // dQ's blocks fill the SMs of dK/dV's tail.
   cfg.gridDim = dim3(static_cast<unsigned>(q_blocks));

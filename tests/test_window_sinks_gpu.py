@@ -366,3 +366,38 @@ def test_refusals(attn):
     with pytest.raises(attn.AttnError):
         attn.attn_bwd_window_sinks(q, q, q, q, q, lse, 10, 4,
                                    workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_many_shapes_hold_no_host_memory(attn):
+    """What the backward launcher keeps of a shape (the order of its blocks) is bounded: 3,000 masks of
+    160 heads, 4 KB each, leave less than half of that behind."""
+    import os
+
+    import torch
+
+    q, k, v, do = (torch.randn((1, 160, 64, 64), device="cuda").bfloat16() for _ in range(4))
+    grads = [torch.empty_like(x) for x in (q, k, v)]
+    ws = torch.empty(attn.attn_bwd_window_sinks_workspace_bytes(1, 160, 160, 64, 64, 64, 0, 64) * 4,
+                     device="cuda", dtype=torch.uint8)
+    o, lse = attn.attn_fwd_window_sinks(q, k, v, 3, 2)
+
+    def step(w, s):
+        attn.attn_bwd_window_sinks(q, k, v, o, do, lse, w, s, dq=grads[0], dk=grads[1], dv=grads[2],
+                                   workspace=ws)
+
+    def resident():
+        with open("/proc/self/statm") as f:
+            return int(f.read().split()[1]) * os.sysconf("SC_PAGE_SIZE")
+
+    step(3, 2)
+    first = [x.clone() for x in grads]
+    torch.cuda.synchronize()
+    before = resident()
+    for w in range(4, 54):
+        for s in range(60):
+            step(w, s)
+    torch.cuda.synchronize()
+    assert resident() - before < 6 << 20
+    step(3, 2)  # forgotten meanwhile: the same bits
+    assert attn.attn_poll_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(first, grads))
