@@ -130,3 +130,29 @@ def test_weights_of_a_long_row(attn):
     got, ref = gradients(attn, *x, False)
     for name, a, b in zip(("dq", "dk", "dv"), got, ref):
         check(name, a, b, "long rows")
+
+
+@pytest.mark.parametrize("window", [None, 300])
+def test_replayed_with_a_smaller_gradient(attn, window):
+    """A captured backward pass takes the ranges of what it is replayed on: a large dO first, then one of
+    2^-10 in the same buffers, the same bits as eager calls."""
+    import torch
+
+    q, k, v, do = inputs(1, 4, 2, 600, 600, 128, 6, 6)
+    if window is None:
+        o, lse = attn.attn_fwd(q, k, v, causal=True)
+        step = lambda: attn.attn_bwd(q, k, v, o, do, lse, causal=True)
+    else:
+        o, lse = attn.attn_fwd_window_sinks(q, k, v, window, 4)
+        step = lambda: attn.attn_bwd_window_sinks(q, k, v, o, do, lse, window, 4)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(2):
+        graph.replay()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        do.mul_(2.0 ** -16)
+    assert attn.attn_poll_status() == 0

@@ -524,3 +524,25 @@ def test_decode_of_the_largest_and_smallest_values(attn, exponent, split):
     vs = [rng.standard_normal((n, 2, 128)) * 2.0 ** exponent for n in (900, 20)]
     cache, tab, seq, seqs = written(attn, ks, vs, 32, "bf16")
     check_decode(attn, q, cache, tab, seq, seqs, 2, "bf16", f"2^{exponent}", split_size=split)
+
+
+@pytest.mark.parametrize("split", [0, 64])
+def test_decode_keeps_what_is_not_finite(attn, split):
+    """A value that is not finite (a NaN code) shows in its channel and no other; a key's in every channel
+    of its sequence; what lies behind a sequence's end in none."""
+    import torch
+
+    rng = np.random.default_rng(11)
+    n, Hq, Hkv, d = 700, 8, 2, 128
+    ks, vs = ([rng.standard_normal((n, Hkv, d)) for _ in range(3)] for _ in range(2))
+    vs[0][333, 1, 17] = np.inf
+    ks[1][5, 0, 3] = np.nan
+    cache, tab, seq, seqs = written(attn, ks, vs, 64, "bf16")
+    q = syn.bits_to_tensor(syn.host_normal_bits((3, Hq, d), 3, "bf16"), "bf16", "cuda")
+    o, lse = attn.attn_decode_paged_fp8(q, *cache, tab, seq, n, split_size=split)
+    assert attn.attn_poll_status() == 0
+    bad = torch.zeros_like(o, dtype=torch.bool)
+    bad[0, 4:, 17] = True
+    bad[1, :4] = True
+    assert torch.equal(torch.isnan(o), bad)
+    assert torch.equal(torch.isnan(lse), bad.all(-1))

@@ -374,3 +374,11 @@ def test_workspace_belongs_to_the_calls_stream(attn, as_int):
     torch.cuda.synchronize()
     assert torch.equal(o, want) and torch.equal(lse, want_l)
     del filled
+
+
+@pytest.mark.parametrize("W,s", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (0, 2 ** 31 - 1),
+                                 (-1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("chunks", [[40, 200], [1, 2]], ids=str)  # query tiles, few rows
+def test_largest_window_and_sinks_by_the_definition(attn, chunks, W, s):
+    run_and_check(attn, [300, 900], chunks, 8, 2, 128, "bf16", 16, W, s, seed=27)
+    run_and_check(attn, [300, 900], chunks, 4, 2, 64, "f16", 64, W, s, seed=28)
