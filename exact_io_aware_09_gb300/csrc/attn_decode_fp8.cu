@@ -9,7 +9,8 @@
 // that w_j <= 2^15 fits a 16-bit number and o is off by at most half a step of each w_j (2^-12 of it) and,
 // where w_j is below fp16's normal numbers, by 2^-32 of the largest p_j 2^b_j for each code.  A value row
 // of zeros adds nothing to o whatever its scale (the writer's is 1, often far above the other rows'), so
-// it takes no part in r: a tile that would raise r looks at its codes first.
+// it takes no part in r: sixteen tokens that would raise r look at their codes first.  m, too, only
+// follows a score that exceeds it by 8: most steps find neither, and need no maximum over the warp.
 //
 // The split kernel is the 16-bit one's (attn_decode.cu) with half the bytes: blocks of (split,
 // key/value head, sequence), a producer warp bringing 64-token stages page by page with TMA, four
@@ -48,7 +49,7 @@ struct DecFp8Params : DecParams {
   float* lse;
 };
 
-// The weights' reference r rises when a key exceeds it by more than 2^kRise; a key at r weighs 2^kTop.
+// m and the weights' reference r rise when a key exceeds them by more than 2^kRise; a key at r weighs 2^kTop.
 constexpr float kRise = 8.0f, kTop = 7.0f;
 
 template <int D>
@@ -188,49 +189,37 @@ struct Fp8Warp : RowState<D, NT, false> {
           mma_m16n8k16<false>(sc[n], a, qf[n][h * 4 + i][0], qf[n][h * 4 + i][1]);
       }
     }
-    float y[NT][2][2];  // scores, then scores with the values' exponents
-    float bj[2];
+    float x[NT][2][2], y[NT][2][2];  // scores, and with the values' exponents
+    bool rise = false;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float vj = __shfl_sync(0xffffffffu, scale, 16 + g + 8 * k);
       const float kj = __shfl_sync(0xffffffffu, scale, g + 8 * k);
-      bj[k] = static_cast<float>((static_cast<int>(__float_as_uint(vj) >> 23) & 0xff) - 127);
+      const float bj = static_cast<float>((static_cast<int>(__float_as_uint(vj) >> 23) & 0xff) - 127);
       const bool in = g + 8 * k < valid;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) y[n][k][r] = in ? sc[n][2 * k + r] * (f[n][r] * kj) : -INFINITY;
-    }
-    bool rise = false;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float& m = this->m[n][r];
-        float mx = fmaxf(y[n][0][r], y[n][1][r]);
-#pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-        const float mn = fmaxf(m, mx);
-        const float mu = (mn == -INFINITY) ? 0.f : mn;
-        this->l[n][r] = this->l[n][r] * ((m == -INFINITY) ? 0.f : ex2(m - mn)) + ex2(y[n][0][r] - mu) +
-                        ex2(y[n][1][r] - mu);
-        m = mn;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          y[n][k][r] += bj[k];
-          rise = rise || y[n][k][r] > ref[n][r] + kRise;
+        for (int r = 0; r < 2; ++r) {
+          x[n][k][r] = in ? sc[n][2 * k + r] * (f[n][r] * kj) : -INFINITY;
+          y[n][k][r] = x[n][k][r] + bj;
+          rise = rise || x[n][k][r] > this->m[n][r] + kRise || y[n][k][r] > ref[n][r] + kRise;
         }
-      }
-    if (__any_sync(0xffffffffu, rise)) raise(y, vbuf, w0, lane);
+    }
+    if (__any_sync(0xffffffffu, rise)) raise(x, y, vbuf, w0, lane);
     uint32_t pb[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float w[2][2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        const float mu = (this->m[n][r] == -INFINITY) ? 0.f : this->m[n][r];
         const float shift = (ref[n][r] == -INFINITY) ? 0.f : kTop - ref[n][r];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) w[k][r] = ex2(y[n][k][r] + shift);
+        for (int k = 0; k < 2; ++k) {
+          this->l[n][r] += ex2(x[n][k][r] - mu);
+          w[k][r] = ex2(y[n][k][r] + shift);
+        }
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) pb[n][k] = transpose_8x8(pack2<false>(w[k][0], w[k][1]));
@@ -255,9 +244,10 @@ struct Fp8Warp : RowState<D, NT, false> {
       }
   }
 
-  // Takes value rows of zeros out of y and raises the references to the largest of the rest where that
-  // exceeds them by more than 2^kRise.  Lane i looks at half a row's codes.
-  __device__ __forceinline__ void raise(float (&y)[NT][2][2], const uint8_t* vbuf, int w0, int lane) {
+  // Takes value rows of zeros out of y, and raises m to the largest x, the references to the largest y left,
+  // where those exceed them by more than 2^kRise.  Lane i looks at half a row's codes.
+  __device__ __forceinline__ void raise(const float (&x)[NT][2][2], float (&y)[NT][2][2], const uint8_t* vbuf,
+                                        int w0, int lane) {
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -271,18 +261,24 @@ struct Fp8Warp : RowState<D, NT, false> {
       float a[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 2; ++k)
           if (!((some >> (2 * ((lane >> 2) + 8 * k))) & 3u)) y[n][k][r] = -INFINITY;
-          mx = fmaxf(mx, y[n][k][r]);
-        }
+        float mx = fmaxf(x[n][0][r], x[n][1][r]), my = fmaxf(y[n][0][r], y[n][1][r]);
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, sh));
+        }
+        float& m = this->m[n][r];
+        if (mx > m + kRise) {
+          this->l[n][r] *= (m == -INFINITY) ? 0.f : ex2(m - mx);
+          m = mx;
+        }
         a[r] = 1.0f;
-        if (mx > ref[n][r] + kRise) {
-          a[r] = (ref[n][r] == -INFINITY) ? 0.f : ex2(ref[n][r] - mx);
-          ref[n][r] = mx;
+        if (my > ref[n][r] + kRise) {
+          a[r] = (ref[n][r] == -INFINITY) ? 0.f : ex2(ref[n][r] - my);
+          ref[n][r] = my;
         }
       }
 #pragma unroll
