@@ -30,7 +30,7 @@
 // launch, no workspace.  More splits go through the workspace and the 16-bit decode's merge kernel.
 //
 // Bound by HBM: 2 (d + 4) bytes per cached token and head.  64 sequences of 1k-32k tokens (Hq=64 Hkv=8
-// d=128, 64-token pages, 2.45 GB): 398 us, 6.2 TB/s, against 723 for the 16-bit cache.  Without its
+// d=128, 64-token pages, 2.45 GB): 394 us, 6.2 TB/s, against 723 for the 16-bit cache.  Without its
 // arithmetic it takes as long; what counts is how the bytes are asked for: codes and scales both with the
 // policy that evicts their lines first (codes with the default one 411 us, scales as short asynchronous
 // copies with it 408).  One sequence of 1,001 tokens (Hq=16 Hkv=4 d=64): 12 us on the device, one launch.

@@ -9,10 +9,10 @@
 // normalised rows merged with the (m, l) rule by a second kernel.
 //
 // Bound by the tensor cores for long chunks, by the cache's bytes for a few tokens.  Hq=64 Hkv=8 d=128
-// bf16: two chunks of 2,048 tokens over 16k cached ones 1,335 us in 16-token pages (1,540 TFLOP/s, tensor
-// pipe 67% busy) and 1,300 in 64-token pages, the contiguous prefill of the same 1,320-1,390 (on the
-// prefill kernel, one block an SM: 1,750 and 1,400, its producers' 16 copies a tile being as long as the
-// tile); 64 sequences of 3-8 tokens over 1k-32k 736 us (6.5 TB/s).
+// bf16: two chunks of 2,048 tokens, both over 16,384 cached ones, 1,330-1,380 us in 16-token pages (1,500-1,550
+// TFLOP/s, tensor pipe 67% busy) and 1,300-1,410 in 64-token pages, the contiguous prefill of the same
+// 1,320-1,480, box by box (on the prefill kernel, one block an SM: 1,750 and 1,400, its producers' 16 copies
+// a tile being as long as the tile); over 12k-16k 1,260-1,280; 64 sequences of 3-8 tokens over 1k-32k 736 us (6.5 TB/s).
 // Calls of at most 16 rows per key/value head go to attn_paged_few.cu.
 #include "attn_fwd_two.cuh"
 #include "attn_rows.cuh"
