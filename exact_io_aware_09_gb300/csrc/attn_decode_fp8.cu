@@ -292,7 +292,7 @@ struct Fp8Warp : RowState<D, NT, false> {
   }
 
   // The state to the merge scratch, its rows divided by their sums: o 2^(ref - kTop - m) / l, the power
-  // of two in two halves, each of which is a normal number.
+  // of two in two halves, so that it leaves fp32's range only where the result does.
   __device__ __forceinline__ void store(float* rw, int rows, int lane) const {
     float h[NT][2], hl[NT][2];
 #pragma unroll
