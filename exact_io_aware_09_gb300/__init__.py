@@ -22,6 +22,8 @@ __all__ = [
     "attn_fwd_paged", "attn_fwd_paged_workspace_bytes",
     "attn_cache_write_fp8", "attn_cache_read_fp8",
     "attn_decode_paged_fp8", "attn_decode_paged_fp8_workspace_bytes",
+    "attn_pages_extend", "attn_pages_trim",
+    "attn_cache_write_fp4", "attn_cache_read_fp4",
     "attn_bwd", "attn_bwd_workspace_bytes",
     "attn_decode_splitkv", "attn_decode_workspace_bytes", "attn_decode_paged",
     "attn_decode_splitkv_static", "attn_decode_static_scratch_bytes",
@@ -80,6 +82,14 @@ lib.attn_decode_paged_fp8.argtypes = [_P] * 7 + [_I] * 4 + [_P, _P] + [_I] * 5 +
 lib.attn_decode_paged_fp8.restype = _I
 lib.attn_decode_paged_fp8_workspace_bytes.argtypes = [_I] * 6
 lib.attn_decode_paged_fp8_workspace_bytes.restype = _SZ
+lib.attn_cache_write_fp4.argtypes = [_P] * 7 + [_I] * 6 + [_P]
+lib.attn_cache_write_fp4.restype = _I
+lib.attn_cache_read_fp4.argtypes = [_P] * 7 + [_I] * 3 + [_P, _P] + [_I] * 5 + [_P]
+lib.attn_cache_read_fp4.restype = _I
+lib.attn_pages_extend.argtypes = [_P] * 6 + [_I] * 5 + [_P]
+lib.attn_pages_extend.restype = _I
+lib.attn_pages_trim.argtypes = [_P] * 5 + [_I] * 4 + [_P]
+lib.attn_pages_trim.restype = _I
 lib.attn_fwd_block_sparse.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _F, _P,
                                       _I]
 lib.attn_fwd_block_sparse.restype = _I
@@ -686,6 +696,149 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
                                        _stream_handle(stream, q.device))
     _check(st, where)
     return o, lse
+
+
+def _check_cache_fp4(where, k_codes, v_codes, k_scales, v_scales):
+    """The (num_pages, page_size, Hkv, d) of a 4-bit cache, its tensors checked."""
+    torch = _torch()
+    if not (k_codes.dim() == 4 and k_codes.dtype == v_codes.dtype == k_scales.dtype == v_scales.dtype
+            == torch.uint8 and v_codes.shape == k_codes.shape and k_scales.shape == v_scales.shape
+            == k_codes.shape[:3] + (k_codes.shape[3] // 8,)):
+        raise AttnError(-1, f"{where}: the codes must be uint8 [num_pages, Hkv, page_size, d/2] and their"
+                            " scales uint8 [num_pages, Hkv, page_size, d/16]")
+    num_pages, Hkv, page_size, half = k_codes.shape
+    return num_pages, page_size, Hkv, 2 * half
+
+
+def _check_table(where, block_table, B):
+    torch = _torch()
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise AttnError(-1, f"{where}: block_table must be int32 [B, max_pages]")
+
+
+def attn_cache_write_fp4(k, v, k_codes, v_codes, k_scales, v_scales, slots, stream=None) -> None:
+    """New tokens into a paged cache held in 4 bits.
+
+    k/v [total,Hkv,d] packed new tokens (fp16/bf16); k_codes/v_codes uint8 [num_pages, Hkv, page_size,
+    d/2] (two E2M1 codes a byte) and k_scales/v_scales uint8 [num_pages, Hkv, page_size, d/16] (fp16's
+    bits shifted right by seven, one for 16 channels), written in place; slots int32 CUDA [total] as
+    attn_pages_extend gives them, -1 for a token that is not kept.
+    """
+    torch = _torch()
+    where = "attn_cache_write_fp4"
+    num_pages, page_size, Hkv, d = _check_cache_fp4(where, k_codes, v_codes, k_scales, v_scales)
+    total = k.shape[0]
+    _expect(where, k, "k", k.dtype, (total, Hkv, d))
+    _expect(where, v, "v", k.dtype, (total, Hkv, d))
+    _expect(where, slots, "slots", torch.int32, (total,))
+    index, p = _pointers(where, ("k", "v", "k_codes", "v_codes", "k_scales", "v_scales", "slots"),
+                         (k, v, k_codes, v_codes, k_scales, v_scales, slots))
+    with _device(index):
+        st = lib.attn_cache_write_fp4(*p, num_pages, page_size, total, Hkv, d, _dtype_code(k),
+                                      _stream_handle(stream, k.device))
+    _check(st, where)
+
+
+def attn_cache_read_fp4(k_codes, v_codes, k_scales, v_scales, block_table, cu_seqlens_k, total: int,
+                        starts=None, dtype=None, k=None, v=None, stream=None):
+    """Tokens of each sequence of a 4-bit cache as a packed 16-bit cache.
+
+    Sequence b's tokens starts[b] .. (int32 CUDA [B]; None: from the first) go to rows
+    cu_seqlens_k[b] .. cu_seqlens_k[b+1]-1 of (k, v) [total,Hkv,d], allocated here in ``dtype``
+    (bfloat16 when omitted) unless given; exact in both types.  The cache as attn_cache_write_fp4
+    takes it, block_table int32 CUDA [B, max_pages_per_seq].  Returns (k, v).
+    """
+    torch = _torch()
+    where = "attn_cache_read_fp4"
+    B = cu_seqlens_k.shape[0] - 1
+    num_pages, page_size, Hkv, d = _check_cache_fp4(where, k_codes, v_codes, k_scales, v_scales)
+    _check_table(where, block_table, B)
+    _expect(where, cu_seqlens_k, "cu_seqlens_k", torch.int32, (B + 1,))
+    if starts is not None:
+        _expect(where, starts, "starts", torch.int32, (B,))
+    if dtype is None:
+        dtype = k.dtype if k is not None else v.dtype if v is not None else torch.bfloat16
+    total = int(total)
+    with _allocating(stream, k_codes.device):
+        if k is None:
+            k = torch.empty((total, Hkv, d), device=k_codes.device, dtype=dtype)
+        if v is None:
+            v = torch.empty((total, Hkv, d), device=k_codes.device, dtype=dtype)
+    _expect(where, k, "k", dtype, (total, Hkv, d))
+    _expect(where, v, "v", dtype, (total, Hkv, d))
+    index, (*p, kp, vp) = _pointers(
+        where, ("k_codes", "v_codes", "k_scales", "v_scales", "block_table", "cu_seqlens_k", "starts",
+                "k", "v"),
+        (k_codes, v_codes, k_scales, v_scales, block_table, cu_seqlens_k, starts, k, v))
+    with _device(index):
+        st = lib.attn_cache_read_fp4(*p, num_pages, page_size, block_table.shape[1], kp, vp, total, B,
+                                     Hkv, d, _dtype_code(k), _stream_handle(stream, k.device))
+    _check(st, where)
+    return k, v
+
+
+def _check_pages(where, block_table, seqlens, lengths, name, extra, free_pages, n_free):
+    """The (B, max_pages, num_pages) of page lists, their tensors checked."""
+    torch = _torch()
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise AttnError(-1, f"{where}: block_table must be int32 [B, max_pages] and free_pages int32 "
+                            "[num_pages]")
+    B, width = block_table.shape
+    _expect(where, block_table, "block_table", torch.int32, (B, width))
+    _expect(where, seqlens, "seqlens", torch.int32, (B,))
+    _expect(where, lengths, name, torch.int32, (B + extra,))
+    _expect(where, free_pages, "free_pages", torch.int32, free_pages.shape)
+    _expect(where, n_free, "n_free", torch.int32, (1,))
+    return B, width, free_pages.shape[0]
+
+
+def attn_pages_extend(block_table, seqlens, cu_seqlens_q, free_pages, n_free, page_size: int,
+                      total: int, slots=None, stream=None):
+    """Pages for sequences that grow, taken from a free list on the GPU.
+
+    block_table int32 CUDA [B, max_pages_per_seq] and seqlens int32 CUDA [B] are updated in place for
+    the new tokens, packed rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 (int32 CUDA [B+1]) of sequence
+    b; free_pages int32 CUDA [num_pages] is a stack whose first n_free (int32 CUDA [1], updated)
+    entries are free.  Returns slots int32 [total]: each row's place page * page_size + offset in the
+    pool, -1 for rows of no sequence.  A call that the list cannot meet changes nothing, gives slots
+    of -1 and is reported by attn_poll_status.
+    """
+    torch = _torch()
+    where = "attn_pages_extend"
+    B, width, num_pages = _check_pages(where, block_table, seqlens, cu_seqlens_q, "cu_seqlens_q", 1,
+                                       free_pages, n_free)
+    total = int(total)
+    if slots is not None:
+        _expect(where, slots, "slots", torch.int32, (total,))
+    elif total < 0:
+        raise AttnError(-1, f"{where}: total {total}")
+    with _allocating(stream, block_table.device):
+        if slots is None:
+            slots = torch.empty(total, device=block_table.device, dtype=torch.int32)
+    index, p = _pointers(
+        where, ("block_table", "seqlens", "cu_seqlens_q", "free_pages", "n_free", "slots"),
+        (block_table, seqlens, cu_seqlens_q, free_pages, n_free, slots))
+    with _device(index):
+        st = lib.attn_pages_extend(*p, num_pages, int(page_size), width, total, B,
+                                   _stream_handle(stream, block_table.device))
+    _check(st, where)
+    return slots
+
+
+def attn_pages_trim(block_table, seqlens, keep, free_pages, n_free, page_size: int,
+                    stream=None) -> None:
+    """Cuts sequences to their first keep[b] tokens (int32 CUDA [B]; 0: the sequence ends) and puts
+    the pages that they no longer use on top of the free list; the others as attn_pages_extend, all
+    updated in place.  The entries of pages given back become -1.
+    """
+    where = "attn_pages_trim"
+    B, width, num_pages = _check_pages(where, block_table, seqlens, keep, "keep", 0, free_pages, n_free)
+    index, p = _pointers(where, ("block_table", "seqlens", "keep", "free_pages", "n_free"),
+                         (block_table, seqlens, keep, free_pages, n_free))
+    with _device(index):
+        st = lib.attn_pages_trim(*p, num_pages, int(page_size), width, B,
+                                 _stream_handle(stream, block_table.device))
+    _check(st, where)
 
 
 def attn_decode_workspace_bytes(B: int, Hq: int, max_seqlen_k: int, split_size: int, d: int) -> int:

@@ -595,6 +595,105 @@ int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_page
   return launch_attn_decode_fp8(a, c, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Checks shared by the entry points that write and read the 4-bit cache.
+static int check_cache_fp4(const CacheFp4& c, int total, int Hkv, int d, attn_dtype_t dtype) {
+  if (Hkv <= 0 || total < 0) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  const int pages_ok = check_pages(c.num_pages, c.page_size, c.max_pages, 0);
+  if (pages_ok != ATTN_OK) return pages_ok;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (total == 0) return ATTN_OK;
+  if (!c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales || c.num_pages == 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(c.k_codes) || !aligned16(c.v_codes) || !aligned16(c.k_scales) || !aligned16(c.v_scales))
+    return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+static CacheFp4 cache_fp4(const void* k_codes, const void* v_codes, const void* k_scales,
+                          const void* v_scales, const int32_t* block_table, int num_pages, int page_size,
+                          int max_pages) {
+  auto bytes = [](const void* p) { return static_cast<uint8_t*>(const_cast<void*>(p)); };
+  return {bytes(k_codes), bytes(v_codes), bytes(k_scales), bytes(v_scales), block_table,
+          num_pages,      page_size,      max_pages};
+}
+
+int attn_cache_write_fp4(const void* k, const void* v, void* k_codes, void* v_codes, void* k_scales,
+                         void* v_scales, const int32_t* slots, int num_pages, int page_size, int total,
+                         int Hkv, int d, attn_dtype_t dtype, attn_stream_t stream) {
+  const CacheFp4 c = cache_fp4(k_codes, v_codes, k_scales, v_scales, nullptr, num_pages, page_size, 0);
+  const int ok = check_cache_fp4(c, total, Hkv, d, dtype);
+  if (ok != ATTN_OK) return ok;
+  if (total == 0) return ATTN_OK;
+  if (!k || !v || !slots) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(slots)) return ATTN_ERR_MISALIGNED;
+  const int dev_ok = check_device(k);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  return launch_cache_write_fp4(c, k, v, slots, total, Hkv, d, dtype == ATTN_BF16,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_read_fp4(const void* k_codes, const void* v_codes, const void* k_scales,
+                        const void* v_scales, const int32_t* block_table, const int32_t* cu_seqlens_k,
+                        const int32_t* starts, int num_pages, int page_size, int max_pages_per_seq,
+                        void* k, void* v, int total, int B, int Hkv, int d, attn_dtype_t dtype,
+                        attn_stream_t stream) {
+  const CacheFp4 c = cache_fp4(k_codes, v_codes, k_scales, v_scales, block_table, num_pages, page_size,
+                               max_pages_per_seq);
+  if (B < 0) return ATTN_ERR_INVALID_ARG;
+  const int ok = check_cache_fp4(c, total, Hkv, d, dtype);
+  if (ok != ATTN_OK) return ok;
+  if (B == 0 || total == 0) return ATTN_OK;
+  if (!k || !v || !block_table || !cu_seqlens_k || max_pages_per_seq == 0) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(block_table) || !aligned4(cu_seqlens_k) ||
+      !aligned4(starts))
+    return ATTN_ERR_MISALIGNED;
+  const int dev_ok = check_device(k);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  return launch_cache_read_fp4(c, k, v, cu_seqlens_k, starts, total, B, Hkv, d, dtype == ATTN_BF16,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Checks shared by the page-list entry points, then the launch.
+static int pages_common(const PagesArgs& a, bool extend, attn_stream_t stream) {
+  if (a.B < 0 || a.total < 0) return ATTN_ERR_INVALID_ARG;
+  const int pages_ok = check_pages(a.num_pages, a.page_size, a.max_pages, 0);
+  if (pages_ok != ATTN_OK) return pages_ok;
+  if (static_cast<int64_t>(a.max_pages) * a.page_size > kMaxPagedTokens) return ATTN_ERR_UNSUPPORTED;
+  if (a.B == 0 && a.total == 0) return ATTN_OK;
+  if (extend && a.total > 0 && !a.slots) return ATTN_ERR_INVALID_ARG;
+  if (a.B > 0 && (!a.block_table || !a.seqlens || !a.lengths || !a.free_pages || !a.n_free ||
+                  a.num_pages == 0 || a.max_pages == 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(a.slots) || !aligned4(a.block_table) || !aligned4(a.seqlens) || !aligned4(a.lengths) ||
+      !aligned4(a.free_pages) || !aligned4(a.n_free))
+    return ATTN_ERR_MISALIGNED;
+  const int dev_ok = check_device(a.B > 0 ? a.block_table : a.slots);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.B == 0)  // rows of no sequence
+    return cudaMemsetAsync(a.slots, 0xff, static_cast<size_t>(a.total) * 4, st) == cudaSuccess
+               ? ATTN_OK
+               : ATTN_ERR_LAUNCH;
+  return extend ? launch_pages_extend(a, st) : launch_pages_trim(a, st);
+}
+
+int attn_pages_extend(int32_t* block_table, int32_t* seqlens, const int32_t* cu_seqlens_q,
+                      const int32_t* free_pages, int32_t* n_free, int32_t* slots, int num_pages,
+                      int page_size, int max_pages_per_seq, int total, int B, attn_stream_t stream) {
+  return pages_common({block_table, seqlens, cu_seqlens_q, const_cast<int32_t*>(free_pages), n_free, slots,
+                       num_pages, page_size, max_pages_per_seq, total, B},
+                      true, stream);
+}
+
+int attn_pages_trim(int32_t* block_table, int32_t* seqlens, const int32_t* keep, int32_t* free_pages,
+                    int32_t* n_free, int num_pages, int page_size, int max_pages_per_seq, int B,
+                    attn_stream_t stream) {
+  return pages_common({block_table, seqlens, keep, free_pages, n_free, nullptr, num_pages, page_size,
+                       max_pages_per_seq, 0, B},
+                      false, stream);
+}
+
 size_t attn_decode_static_scratch_bytes(void) { return size_t(32) << 20; }
 
 int attn_poll_status(attn_stream_t stream) {
@@ -624,6 +723,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_TIMEOUT: return "a bounded wait inside a kernel timed out";
     case ATTN_ERR_DEVICE: return "no usable sm_103 device";
     case ATTN_ERR_BAD_LENGTHS: return "a sequence length exceeds max_seqlen_k or kv_capacity";
+    case ATTN_ERR_NO_PAGES: return "the free list holds too few pages";
     default: return "unknown status";
   }
 }

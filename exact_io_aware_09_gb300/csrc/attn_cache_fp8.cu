@@ -18,15 +18,11 @@
 // streams the run's rows, d / 16 lanes per row with 32 bytes of 16-bit values and 16 bytes of codes each.
 // Packed rows are consecutive, and so are cache rows inside a page, so every access of a warp is whole
 // lines but for the scales.
-#include "internal.h"
-#include "ptx.cuh"
+#include "attn_cache.cuh"
 
 namespace attn {
 
 namespace {
-
-constexpr int kCacheThreads = 256;
-constexpr int kMaxRun = 64;  // tokens of a block
 
 struct CacheParams {
   const uint16_t* k;  // [total, Hkv, d] (written by the reader)
@@ -53,34 +49,6 @@ __device__ __forceinline__ float pow2i(int e) {  // 2^e for -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Magnitudes of a 16-bit pair, and the larger of two pairs (a NaN stays one).
-template <bool BF16>
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (BF16)
-    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
-  else
-    asm("{\n\t.reg .b32 t;\n\tabs.f16x2 t, %2;\n\tmax.NaN.f16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4 w, float* v) {
-  const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (BF16) {
-      v[2 * i] = __uint_as_float(h[i] << 16);
-      v[2 * i + 1] = __uint_as_float(h[i] & 0xffff0000u);
-    } else {
-      asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
-          "cvt.f32.f16 %1, b;\n\t}"
-          : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
-          : "r"(h[i]));
-    }
-  }
-}
-
 // Two values -> a 16-bit pair, nearest even, saturating at the largest finite value (NaN stays).
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2_sat(float lo, float hi) {
@@ -105,19 +73,6 @@ __device__ __forceinline__ void codes4(uint32_t w, float* v) {
   asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
       : "=f"(v[2]), "=f"(v[3])
       : "r"(hi));
-}
-
-// The sequence that owns packed row i (cu[b] <= i < cu[b + 1]); i lies in [cu[0], cu[B]).
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int i) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] <= i)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  return lo;
 }
 
 // The (page, slot) of each token of the block's run as one pool row (page * page_size + slot), or
@@ -297,9 +252,7 @@ static int cache_params(CacheParams& p, const CacheFp8& c, const void* k, const 
   while ((1 << p.page_log2) < c.page_size) ++p.page_log2;
   p.status = device_status_ptr();
   if (!p.status) return -5;
-  // short runs while there are few tokens, so that they spread over the SMs
-  const int want = total / (152 * 8);
-  p.run = want < 1 ? 1 : want > kMaxRun ? kMaxRun : want;
+  p.run = cache_run(total);
   return 0;
 }
 

@@ -204,6 +204,33 @@ int launch_cache_read_fp8(const CacheFp8& c, void* k, void* v, const int32_t* cu
 int launch_attn_decode_fp8(const DecodeArgs& a, const CacheFp8& c, cudaStream_t stream);
 size_t decode_fp8_workspace_bytes(int B, int Hq, int max_seqlen, int split, int d);
 int decode_fp8_split(int B, int Hkv, int max_seqlen);
+// A 4-bit paged cache (fp4.cuh): codes [num_pages, Hkv, page_size, d / 2] and scale bytes
+// [num_pages, Hkv, page_size, d / 16].
+struct CacheFp4 {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  const int32_t* block_table;
+  int num_pages, page_size, max_pages;
+};
+int launch_cache_write_fp4(const CacheFp4& c, const void* k, const void* v, const int32_t* slots, int total,
+                           int Hkv, int d, bool bf16, cudaStream_t stream);
+int launch_cache_read_fp4(const CacheFp4& c, void* k, void* v, const int32_t* cu_k, const int32_t* starts,
+                          int total, int B, int Hkv, int d, bool bf16, cudaStream_t stream);
+// Page lists (attn_pages.cu): lengths is cu_seqlens_q of an extension, the kept lengths of a trim, which
+// has no slots.
+struct PagesArgs {
+  int32_t* block_table;
+  int32_t* seqlens;
+  const int32_t* lengths;
+  int32_t* free_pages;
+  int32_t* n_free;
+  int32_t* slots;
+  int num_pages, page_size, max_pages, total, B;
+};
+int launch_pages_extend(const PagesArgs& a, cudaStream_t stream);
+int launch_pages_trim(const PagesArgs& a, cudaStream_t stream);
 int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream);
 // Whether a call has few enough rows for attn_paged_few.cu, how it splits there, and its launch.
 bool paged_few_rows(const PagedArgs& a);

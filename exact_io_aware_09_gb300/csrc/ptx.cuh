@@ -12,6 +12,7 @@ namespace attn {
 // ------------------------------------------------------------------------------------------
 constexpr int kStatusTimeout = -6;     // == ATTN_ERR_TIMEOUT
 constexpr int kStatusBadLengths = -8;  // == ATTN_ERR_BAD_LENGTHS
+constexpr int kStatusNoPages = -9;     // == ATTN_ERR_NO_PAGES
 
 // A wait that has not completed after this long is treated as a hang.  No wait on the
 // path legitimately lasts more than a few microseconds.

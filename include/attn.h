@@ -56,8 +56,10 @@ typedef enum {
     ATTN_ERR_LAUNCH = -5,      /* the CUDA runtime refused a launch or a tensor map            */
     ATTN_ERR_TIMEOUT = -6,     /* a bounded wait inside a kernel expired (device status word)  */
     ATTN_ERR_DEVICE = -7,      /* no usable sm_103 device, or a device-side argument check     */
-    ATTN_ERR_BAD_LENGTHS = -8  /* device-side: a sequence is longer than max_seqlen_k or runs
+    ATTN_ERR_BAD_LENGTHS = -8, /* device-side: a sequence is longer than max_seqlen_k or runs
                                   past kv_capacity (its rows of o and lse are not written)     */
+    ATTN_ERR_NO_PAGES = -9     /* device-side: attn_pages_extend found too few free pages (it
+                                  changed nothing)                                             */
 } attn_status_t;
 
 /*
@@ -450,6 +452,93 @@ int attn_decode_paged_fp8(const void *q, const void *k_pages, const void *v_page
                           float *lse, int B, int Hq, int Hkv, int d, int split_size, float scale,
                           attn_dtype_t dtype, void *workspace, size_t workspace_bytes,
                           attn_stream_t stream);
+
+/*
+ * attn_cache_write_fp4 -- new tokens into a paged KV cache held in 4 bits.
+ *
+ *   k, v          [total, Hkv, d] device, contiguous, `dtype`: the new tokens, packed
+ *   k_codes, v_codes    [num_pages, Hkv, page_size, d / 2] device: E2M1 codes, channel 2c in the low
+ *                 four bits of byte c, channel 2c + 1 in the high ones
+ *   k_scales, v_scales  [num_pages, Hkv, page_size, d / 16] device: a scale byte for every 16 channels
+ *   slots         [total] int32 device: where each token goes, page * page_size + offset in the page, as
+ *                 attn_pages_extend gives it; -1: nowhere
+ * Note the order: a head's rows of a page lie side by side (the 16- and 8-bit pools have the heads of a
+ * token side by side).  A scale byte is an unsigned 8-bit number of five exponent and three mantissa
+ * bits: fp16's bits shifted right by seven.  The scale of 16 channels is max |x| / 6 rounded to that type,
+ * nearest even, at least 2^-17 where max |x| > 0 and at most 10240; 0 where it is 0.  The codes are
+ * x / scale rounded to E2M1, nearest even, at most 6 in magnitude (0 for a zero of either sign): values
+ * past 61440 saturate there.  Sixteen channels of which one is not finite are stored with the scale byte 255 and read back as NaN.  Only the
+ * new tokens' rows are written.  A slot outside [0, num_pages * page_size) other than -1 is reported as
+ * ATTN_ERR_BAD_LENGTHS by attn_poll_status and not written.  Two tokens must not share a slot.  d in
+ * {64, 128}; page_size a power of two from 16 to 65536.  Returns ATTN_OK or a negative attn_status_t.
+ */
+int attn_cache_write_fp4(const void *k, const void *v, void *k_codes, void *v_codes, void *k_scales,
+                         void *v_scales, const int32_t *slots, int num_pages, int page_size, int total,
+                         int Hkv, int d, attn_dtype_t dtype, attn_stream_t stream);
+
+/*
+ * attn_cache_read_fp4 -- tokens of each sequence of a 4-bit cache as the packed 16-bit cache
+ * attn_decode_splitkv takes.
+ *
+ *   cu_seqlens_k  [B + 1] int32 device: sequence b's tokens go to the rows cu[b] .. cu[b+1]-1 of k, v
+ *   starts        [B] int32 device, or null: the first of them (null: token 0)
+ *   k, v          [total, Hkv, d] out, `dtype`: code times scale, exact in both types
+ *   block_table, num_pages, page_size, max_pages_per_seq   as attn_decode_paged; the cache as
+ *                 attn_cache_write_fp4
+ * Rows outside cu_seqlens_k[0] .. cu_seqlens_k[B]-1 are left as they were.  Positions outside the table
+ * and block-table entries outside the pool are reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status, and
+ * their rows not written.
+ */
+int attn_cache_read_fp4(const void *k_codes, const void *v_codes, const void *k_scales,
+                        const void *v_scales, const int32_t *block_table, const int32_t *cu_seqlens_k,
+                        const int32_t *starts, int num_pages, int page_size, int max_pages_per_seq,
+                        void *k, void *v, int total, int B, int Hkv, int d, attn_dtype_t dtype,
+                        attn_stream_t stream);
+
+/*
+ * attn_pages_extend -- pages for sequences that grow: takes them from a free list, enters them into the
+ * block table and gives the slots of the new tokens.  All of it on the device, so that a captured step
+ * can do it again and again.
+ *
+ *   block_table   [B, max_pages_per_seq] int32 device, in and out: as attn_decode_paged reads it; the
+ *                 entries of new pages are written, all others left as they were
+ *   seqlens       [B] int32 device, in and out: cached tokens L_b, which grow by n_b
+ *   cu_seqlens_q  [B + 1] int32 device, non-decreasing: the packed rows of the new tokens; n_b =
+ *                 cu_seqlens_q[b+1] - cu_seqlens_q[b] >= 0 of them, at positions L_b .. L_b + n_b - 1
+ *   free_pages    [num_pages] int32 device: a stack, of which the first n_free entries are pages that no
+ *                 sequence holds
+ *   n_free        [1] int32 device, in and out
+ *   slots         [total] int32 device out: page * page_size + (position % page_size) of each packed
+ *                 row's token; -1 for rows outside cu_seqlens_q[0] .. cu_seqlens_q[B]-1
+ *   num_pages     pages of the pool and entries of free_pages; page_size a power of two from 16 to
+ *                 65536, num_pages * page_size <= 2^31 - 1
+ * A sequence takes ceil((L_b + n_b) / page_size) - ceil(L_b / page_size) pages.  Numbered over the
+ * sequences in their order, the k-th new page is free_pages[n_free - 1 - k]; free_pages itself is not
+ * written.  A call that the list cannot meet changes nothing but slots, all -1, and is reported as
+ * ATTN_ERR_NO_PAGES by attn_poll_status; so is one with lengths that are negative, decrease, pass
+ * `total` or pass the table's reach, or with n_free outside [0, num_pages], as ATTN_ERR_BAD_LENGTHS.  A
+ * list or table entry outside the pool gives its tokens the slot -1 and is reported the same way.
+ * Calls on the same lists must not overlap.  Returns ATTN_OK or a negative attn_status_t.
+ */
+int attn_pages_extend(int32_t *block_table, int32_t *seqlens, const int32_t *cu_seqlens_q,
+                      const int32_t *free_pages, int32_t *n_free, int32_t *slots, int num_pages,
+                      int page_size, int max_pages_per_seq, int total, int B, attn_stream_t stream);
+
+/*
+ * attn_pages_trim -- cuts sequences short (drafted tokens that were not accepted, or, with 0 tokens
+ * kept, sequences that end) and puts the pages that they no longer use back on the free list.
+ *
+ *   keep          [B] int32 device: tokens to keep, 0 <= keep[b] <= seqlens[b] (its length: no change)
+ *   the others    as attn_pages_extend; seqlens becomes keep, the entries of pages given back become
+ *                 -1 and the pages go on top of the stack, so that the trim that follows an extension
+ *                 and takes back all its tokens restores the stack.
+ * Pages belong to one sequence: one that two table rows name must not be given back.  A call with a
+ * length outside those bounds or past the table's reach, or whose pages do not fit on the stack, changes
+ * nothing and is reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status.
+ */
+int attn_pages_trim(int32_t *block_table, int32_t *seqlens, const int32_t *keep,
+                    int32_t *free_pages, int32_t *n_free, int num_pages, int page_size,
+                    int max_pages_per_seq, int B, attn_stream_t stream);
 
 /* attn_decode_static_scratch_bytes -- size of the scratch attn_decode_splitkv_static uses. */
 size_t attn_decode_static_scratch_bytes(void);
