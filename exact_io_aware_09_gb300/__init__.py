@@ -24,6 +24,8 @@ __all__ = [
     "attn_decode_paged_fp8", "attn_decode_paged_fp8_workspace_bytes",
     "attn_pages_extend", "attn_pages_trim",
     "attn_cache_write_fp4", "attn_cache_read_fp4",
+    "attn_fwd_paged_fp4", "attn_fwd_paged_fp4_workspace_bytes",
+    "attn_decode_paged_fp4", "attn_decode_paged_fp4_workspace_bytes",
     "attn_bwd", "attn_bwd_workspace_bytes",
     "attn_decode_splitkv", "attn_decode_workspace_bytes", "attn_decode_paged",
     "attn_decode_splitkv_static", "attn_decode_static_scratch_bytes",
@@ -86,6 +88,14 @@ lib.attn_cache_write_fp4.argtypes = [_P] * 7 + [_I] * 6 + [_P]
 lib.attn_cache_write_fp4.restype = _I
 lib.attn_cache_read_fp4.argtypes = [_P] * 7 + [_I] * 3 + [_P, _P] + [_I] * 5 + [_P]
 lib.attn_cache_read_fp4.restype = _I
+lib.attn_fwd_paged_fp4_workspace_bytes.argtypes = [_I] * 9
+lib.attn_fwd_paged_fp4_workspace_bytes.restype = _SZ
+lib.attn_fwd_paged_fp4.argtypes = [_P] * 8 + [_I] * 6 + [_P, _P] + [_I] * 6 + [_F, _I, _P, _SZ, _P]
+lib.attn_fwd_paged_fp4.restype = _I
+lib.attn_decode_paged_fp4_workspace_bytes.argtypes = [_I] * 5
+lib.attn_decode_paged_fp4_workspace_bytes.restype = _SZ
+lib.attn_decode_paged_fp4.argtypes = [_P] * 7 + [_I] * 4 + [_P, _P] + [_I] * 4 + [_F, _I, _P, _SZ, _P]
+lib.attn_decode_paged_fp4.restype = _I
 lib.attn_pages_extend.argtypes = [_P] * 6 + [_I] * 5 + [_P]
 lib.attn_pages_extend.restype = _I
 lib.attn_pages_trim.argtypes = [_P] * 5 + [_I] * 4 + [_P]
@@ -777,6 +787,106 @@ def attn_cache_read_fp4(k_codes, v_codes, k_scales, v_scales, block_table, cu_se
     return k, v
 
 
+def attn_fwd_paged_fp4_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, window=-1,
+                                       sinks=0) -> int:
+    return int(lib.attn_fwd_paged_fp4_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k,
+                                                      window, sinks, d))
+
+
+def attn_fwd_paged_fp4(q, k_codes, v_codes, k_scales, v_scales, block_table, cu_seqlens_q, seqlens_k,
+                       max_seqlen_q: int, max_seqlen_k: int, window: int = -1, sinks: int = 0, o=None,
+                       lse=None, scale: float | None = None, workspace=None, stream=None):
+    """A chunk of new tokens of each sequence over its 4-bit paged cache, causal; the new tokens'
+    keys and values are the cache's last rows already (attn_cache_write_fp4).
+
+    q [total_q,Hq,d] packed new tokens; the cache as attn_cache_write_fp4 takes it; the others and the
+    return value as attn_fwd_paged.
+    """
+    torch = _torch()
+    where = "attn_fwd_paged_fp4"
+    total_q, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = _check_cache_fp4(where, k_codes, v_codes, k_scales, v_scales)
+    if dk != d:
+        raise AttnError(-1, f"{where}: the cache disagrees with q")
+    B = seqlens_k.shape[0]
+    _expect(where, seqlens_k, "seqlens_k", torch.int32, (B,))
+    _expect(where, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    _check_table(where, block_table, B)
+    if o is not None:
+        _expect(where, o, "o", q.dtype, q.shape)
+    if lse is not None:
+        _expect(where, lse, "lse", torch.float32, (total_q, Hq))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _allocating(stream, q.device):
+        o = torch.empty_like(q) if o is None else o
+        if lse is None:
+            lse = torch.empty((total_q, Hq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            need = attn_fwd_paged_fp4_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k,
+                                                      d, window, sinks)
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+    index, (*p, op, lp, ws) = _pointers(
+        where, ("q", "k_codes", "v_codes", "k_scales", "v_scales", "block_table", "cu_seqlens_q",
+                "seqlens_k", "o", "lse", "workspace"),
+        (q, k_codes, v_codes, k_scales, v_scales, block_table, cu_seqlens_q, seqlens_k, o, lse,
+         workspace))
+    with _device(index):
+        st = lib.attn_fwd_paged_fp4(*p, num_pages, page_size, block_table.shape[1], total_q,
+                                    int(max_seqlen_q), int(max_seqlen_k), op, lp, B, Hq, Hkv, d,
+                                    int(window), int(sinks), float(scale), _dtype_code(q), ws,
+                                    0 if workspace is None else workspace.nbytes,
+                                    _stream_handle(stream, q.device))
+    _check(st, where)
+    return o, lse
+
+
+def attn_decode_paged_fp4_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d) -> int:
+    return int(lib.attn_decode_paged_fp4_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d))
+
+
+def attn_decode_paged_fp4(q, k_codes, v_codes, k_scales, v_scales, block_table, seqlens_k,
+                          max_seqlen_k: int, o=None, lse=None, scale: float | None = None,
+                          workspace=None, stream=None):
+    """One split-KV decode step over a 4-bit paged cache (written by attn_cache_write_fp4).
+
+    q [B,Hq,d]; the cache as attn_cache_write_fp4 takes it; block_table int32 CUDA
+    [B, max_pages_per_seq]; seqlens_k int32 CUDA [B].  Returns (o [B,Hq,d], lse [B,Hq] fp32).
+    """
+    torch = _torch()
+    where = "attn_decode_paged_fp4"
+    B, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = _check_cache_fp4(where, k_codes, v_codes, k_scales, v_scales)
+    if dk != d:
+        raise AttnError(-1, f"{where}: the cache disagrees with q")
+    _expect(where, seqlens_k, "seqlens_k", torch.int32, (B,))
+    _check_table(where, block_table, B)
+    if o is not None:
+        _expect(where, o, "o", q.dtype, q.shape)
+    if lse is not None:
+        _expect(where, lse, "lse", torch.float32, (B, Hq))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _allocating(stream, q.device):
+        o = torch.empty_like(q) if o is None else o
+        if lse is None:
+            lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            need = attn_decode_paged_fp4_workspace_bytes(B, Hq, Hkv, max_seqlen_k, d)
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+    index, (*p, op, lp, ws) = _pointers(
+        where, ("q", "k_codes", "v_codes", "k_scales", "v_scales", "block_table", "seqlens_k", "o",
+                "lse", "workspace"),
+        (q, k_codes, v_codes, k_scales, v_scales, block_table, seqlens_k, o, lse, workspace))
+    with _device(index):
+        st = lib.attn_decode_paged_fp4(*p, num_pages, page_size, block_table.shape[1],
+                                       int(max_seqlen_k), op, lp, B, Hq, Hkv, d, float(scale),
+                                       _dtype_code(q), ws, 0 if workspace is None else workspace.nbytes,
+                                       _stream_handle(stream, q.device))
+    _check(st, where)
+    return o, lse
+
+
 def _check_pages(where, block_table, seqlens, lengths, name, extra, free_pages, n_free):
     """The (B, max_pages, num_pages) of page lists, their tensors checked."""
     torch = _torch()
@@ -798,8 +908,8 @@ def attn_pages_extend(block_table, seqlens, cu_seqlens_q, free_pages, n_free, pa
 
     block_table int32 CUDA [B, max_pages_per_seq] and seqlens int32 CUDA [B] are updated in place for
     the new tokens, packed rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 (int32 CUDA [B+1]) of sequence
-    b; free_pages int32 CUDA [num_pages] is a stack whose first n_free (int32 CUDA [1], updated)
-    entries are free.  Returns slots int32 [total]: each row's place page * page_size + offset in the
+    b; free_pages int32 CUDA [num_pages], an entry for every page of the pool, is a stack whose first
+    n_free (int32 CUDA [1], updated) entries are free.  Returns slots int32 [total]: each row's place page * page_size + offset in the
     pool, -1 for rows of no sequence.  A call that the list cannot meet changes nothing, gives slots
     of -1 and is reported by attn_poll_status.
     """

@@ -118,6 +118,21 @@ bool make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_4d_u8(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t strides[3],
+                     const uint32_t box[4]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || dims[0] == 0 || dims[1] == 0 || dims[2] == 0 || dims[3] == 0) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), d, st, bx, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box[0] == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 int* device_status_ptr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -652,6 +667,76 @@ int attn_cache_read_fp4(const void* k_codes, const void* v_codes, const void* k_
   if (dev_ok != ATTN_OK) return dev_ok;
   return launch_cache_read_fp4(c, k, v, cu_seqlens_k, starts, total, B, Hkv, d, dtype == ATTN_BF16,
                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t attn_fwd_paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_seqlen_q,
+                                          int max_seqlen_k, int window, int sinks, int d) {
+  return paged_fp4_workspace_bytes(total_q, B, Hq, Hkv, max_seqlen_q, max_seqlen_k,
+                                   window < max_seqlen_k ? window : max_seqlen_k,
+                                   sinks < max_seqlen_k ? sinks : max_seqlen_k, d);
+}
+
+// The two attention entry points of the 4-bit cache: their checks and the launch.
+static int paged_fp4_common(const PagedArgs& a, const CacheFp4& c, attn_dtype_t dtype, size_t workspace_bytes,
+                            attn_stream_t stream) {
+  if (a.B < 0 || a.Hq <= 0 || a.Hkv <= 0 || a.Hq % a.Hkv != 0 || a.total_q < 0 || a.max_q < 0 || a.max_k < 0 ||
+      (a.cu_q && a.max_k < a.max_q))
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(a.scale) || !(a.scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+  const int pages_ok = check_pages(c.num_pages, c.page_size, c.max_pages, a.max_k);
+  if (pages_ok != ATTN_OK) return pages_ok;
+  if (a.d != 64 && a.d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (a.Hq / a.Hkv > (a.cu_q ? 128 : 16) || a.B > kMaxDecodeBatch || a.Hkv > 65535)
+    return ATTN_ERR_UNSUPPORTED;
+  if (a.B == 0 || a.total_q == 0 || a.max_q == 0) return ATTN_OK;
+  if (!a.q || !a.o || !a.lse || !c.block_table || !a.seqlens) return ATTN_ERR_INVALID_ARG;
+  if (a.max_k > 0 && (c.num_pages == 0 || !c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(a.q) || !aligned16(a.o) || !aligned16(c.k_codes) || !aligned16(c.v_codes) ||
+      !aligned16(c.k_scales) || !aligned16(c.v_scales) || !aligned16(a.workspace) || !aligned4(a.lse) ||
+      !aligned4(c.block_table) || !aligned4(a.cu_q) || !aligned4(a.seqlens))
+    return ATTN_ERR_MISALIGNED;
+  const size_t need =
+      paged_fp4_workspace_bytes(a.total_q, a.B, a.Hq, a.Hkv, a.max_q, a.max_k, a.window, a.sinks, a.d);
+  if (need > 0 && (!a.workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+  const int dev_ok = check_device(a.q);
+  if (dev_ok != ATTN_OK) return dev_ok;
+  return launch_attn_paged_fp4(a, c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_fwd_paged_fp4(const void* q, const void* k_codes, const void* v_codes, const void* k_scales,
+                       const void* v_scales, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                       const int32_t* seqlens_k, int num_pages, int page_size, int max_pages_per_seq,
+                       int total_q, int max_seqlen_q, int max_seqlen_k, void* o, float* lse, int B, int Hq,
+                       int Hkv, int d, int window, int sinks, float scale, attn_dtype_t dtype, void* workspace,
+                       size_t workspace_bytes, attn_stream_t stream) {
+  if (window < -1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  if (!cu_seqlens_q) return ATTN_ERR_INVALID_ARG;  // (null stands for the decode step below)
+  const CacheFp4 c = cache_fp4(k_codes, v_codes, k_scales, v_scales, block_table, num_pages, page_size,
+                               max_pages_per_seq);
+  const PagedArgs a{q, nullptr, nullptr, block_table, cu_seqlens_q, seqlens_k, num_pages, page_size,
+                    max_pages_per_seq, total_q, max_seqlen_q, max_seqlen_k, o, lse, B, Hq, Hkv, d,
+                    window < max_seqlen_k ? window : max_seqlen_k,
+                    sinks < max_seqlen_k ? sinks : max_seqlen_k, scale, dtype == ATTN_BF16, workspace};
+  return paged_fp4_common(a, c, dtype, workspace_bytes, stream);
+}
+
+size_t attn_decode_paged_fp4_workspace_bytes(int B, int Hq, int Hkv, int max_seqlen_k, int d) {
+  return paged_fp4_workspace_bytes(B, B, Hq, Hkv, 1, max_seqlen_k, -1, 0, d);
+}
+
+int attn_decode_paged_fp4(const void* q, const void* k_codes, const void* v_codes, const void* k_scales,
+                          const void* v_scales, const int32_t* block_table, const int32_t* seqlens_k,
+                          int num_pages, int page_size, int max_pages_per_seq, int max_seqlen_k, void* o,
+                          float* lse, int B, int Hq, int Hkv, int d, float scale, attn_dtype_t dtype,
+                          void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  const CacheFp4 c = cache_fp4(k_codes, v_codes, k_scales, v_scales, block_table, num_pages, page_size,
+                               max_pages_per_seq);
+  const PagedArgs a{q, nullptr, nullptr, block_table, nullptr, seqlens_k, num_pages, page_size,
+                    max_pages_per_seq, B, 1, max_seqlen_k, o, lse, B, Hq, Hkv, d, -1, 0, scale,
+                    dtype == ATTN_BF16, workspace};
+  return paged_fp4_common(a, c, dtype, workspace_bytes, stream);
 }
 
 // Checks shared by the page-list entry points, then the launch.

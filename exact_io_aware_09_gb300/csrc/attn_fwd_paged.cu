@@ -14,57 +14,11 @@
 // 1,320-1,480, box by box (on the prefill kernel, one block an SM: 1,750 and 1,400, its producers' 16 copies
 // a tile being as long as the tile); over 12k-16k 1,260-1,280; 64 sequences of 3-8 tokens over 1k-32k 736 us (6.5 TB/s).
 // Calls of at most 16 rows per key/value head go to attn_paged_few.cu.
-#include "attn_fwd_two.cuh"
-#include "attn_rows.cuh"
+#include "attn_paged.cuh"
 
 namespace attn {
 
 namespace {
-
-constexpr int kSms = 152;  // SMs of a GB300, two blocks each
-constexpr int kMaxSplits = 128;
-// Measured, us: a 64-key step and a block's start and end with two blocks on an SM, with one alone; the
-// merge's launch, and its bytes (written and read) per us.
-constexpr double kStepTwo = 0.88, kItemTwo = 4.0, kStepOne = 0.6, kItemOne = 3.5;
-constexpr double kMerge = 4.0, kMergeBytes = 5e6;
-
-struct PagedSplit {
-  int tile_tokens, n_qtiles, n_splits, split_steps;
-};
-
-// How a call's work is cut.  An item is one query tile of one key/value head of a sequence; its 64-key
-// steps are cut into the number of splits that is estimated to finish first: rounds of blocks over the
-// SMs, two on each, a last round of few blocks running one on an SM, and the merge.  (The lengths are
-// the caller's bounds: what the sequences really hold is on the device.)
-PagedSplit paged_split(int B, int Hq, int Hkv, int max_q, int max_k, int window, int sinks, int d) {
-  PagedSplit s;
-  s.tile_tokens = kWM / (Hq / Hkv);
-  s.n_qtiles = (max_q + s.tile_tokens - 1) / s.tile_tokens;
-  long long steps = (static_cast<long long>(max_k) + kWN - 1) / kWN;
-  if (window >= 0) {
-    const long long near = (static_cast<long long>(window) + s.tile_tokens) / kWN + 2 +
-                           (static_cast<long long>(sinks) + kWN - 1) / kWN;
-    if (near < steps) steps = near;
-  }
-  const long long items = static_cast<long long>(B) * Hkv * s.n_qtiles;
-  const double part_bytes = 2.0 * 4.0 * d * B * static_cast<double>(max_q) * Hq;
-  s.n_splits = 1;
-  s.split_steps = static_cast<int>(steps);
-  double best = -1.0;
-  for (int n = 1; n <= kMaxSplits && n <= steps; ++n) {
-    const long long per = (steps + n - 1) / n, blocks = items * n;
-    const double two = per * kStepTwo + kItemTwo, one = per * kStepOne + kItemOne;
-    const long long left = blocks % (2 * kSms);
-    double cost = static_cast<double>(blocks / (2 * kSms)) * two + (left == 0 ? 0.0 : left <= kSms ? one : two);
-    if (n > 1) cost += kMerge + n * part_bytes / kMergeBytes;
-    if (best < 0 || cost < best) {
-      best = cost;
-      s.split_steps = static_cast<int>(per);
-      s.n_splits = static_cast<int>((steps + per - 1) / per);
-    }
-  }
-  return s;
-}
 
 size_t parts_o_bytes(size_t parts, int d) {
   return (parts * d * 4 + 255) & ~static_cast<size_t>(255);
@@ -91,6 +45,10 @@ size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int
     n_splits = paged_split(B, Hq, Hkv, max_q, max_k, window, sinks, d).n_splits;
     if (n_splits == 1) return 0;
   }
+  return paged_parts_bytes(total_q, Hq, n_splits, d);
+}
+
+size_t paged_parts_bytes(int total_q, int Hq, int n_splits, int d) {
   const size_t parts = static_cast<size_t>(total_q) * Hq * n_splits;
   return parts_o_bytes(parts, d) + parts * 8;
 }
@@ -114,8 +72,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int lane = threadIdx.x & 31;
   const size_t row = static_cast<size_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
-  const size_t tok = row / Hq;
-  if (static_cast<long long>(tok) < cu_q[0] || static_cast<long long>(tok) >= cu_q[B]) return;
+  if (cu_q) {  // (null: one token of each sequence)
+    const long long tok = static_cast<long long>(row / Hq);
+    if (tok < cu_q[0] || tok >= cu_q[B]) return;
+  }
   const float2* ml = reinterpret_cast<const float2*>(ws_ml) + row * n_splits;
   float m = -INFINITY;
   for (int s = lane; s < n_splits; s += 32) m = fmaxf(m, ml[s].x);
@@ -181,72 +141,12 @@ int launch_paged_merge(const PagedArgs& a, int n_splits, cudaStream_t stream) {
                 : launch_merge_variant<128, false>(a, n_splits, stream);
 }
 
-template <int D, bool BF16>
-static int launch_paged_variant(const PagedArgs& a, cudaStream_t stream) {
-  using L = WinLayout<D>;
-  const PagedSplit sp = paged_split(a.B, a.Hq, a.Hkv, a.max_q, a.max_k, a.window, a.sinks, D);
-  const int G = a.Hq / a.Hkv;
-  const uint64_t row = static_cast<uint64_t>(D) * 2;
-  const uint64_t tokens = static_cast<uint64_t>(a.num_pages) * a.page_size;
-  const uint32_t box = static_cast<uint32_t>(a.page_size < kWN ? a.page_size : kWN);
-  CUtensorMap tq, tk, tv, to;
-  if (!make_tmap_3d(&tq, a.q, BF16, D, a.Hq, a.total_q, row, row * a.Hq, 64, G, sp.tile_tokens) ||
-      !make_tmap_3d(&to, a.o, BF16, D, a.Hq, a.total_q, row, row * a.Hq, 64, G, sp.tile_tokens) ||
-      !make_tmap_3d(&tk, a.k_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box) ||
-      !make_tmap_3d(&tv, a.v_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box))
-    return -5;
-  PagedParams p = {};
-  p.o = a.o;
-  p.lse = a.lse;
-  p.status = device_status_ptr();
-  if (!p.status) return -5;
-  p.Hq = a.Hq;
-  p.Hkv = a.Hkv;
-  p.n_qtiles = sp.n_qtiles;
-  p.G = G;
-  p.window = a.window;
-  p.sinks = a.sinks;
-  const uint64_t planes = static_cast<uint64_t>(a.B) * a.Hkv;
-  if (planes > 0x7fffffffull) return -2;
-  p.BH = static_cast<int>(planes);
-  {
-    // planes whose cache fills about half of L2 walk their query tiles together
-    uint64_t group = (64ull << 20) / (2ull * a.max_k * D * 2);
-    if (group < 1) group = 1;
-    if (group > planes) group = planes;
-    p.head_group = static_cast<int>(group);
-  }
-  p.sl2 = a.scale * 1.4426950408889634f;
-  p.block_table = a.block_table;
-  p.cu_q = a.cu_q;
-  p.seqlens = a.seqlens;
-  while ((1 << p.page_log2) < a.page_size) ++p.page_log2;
-  p.max_pages = a.max_pages;
-  p.num_pages = a.num_pages;
-  p.total_q = a.total_q;
-  p.max_q = a.max_q;
-  p.max_k = a.max_k;
-  p.tile_tokens = sp.tile_tokens;
-  p.n_splits = sp.n_splits;
-  p.split_steps = sp.split_steps;
-  if (sp.n_splits > 1) paged_parts(a, D, sp.n_splits, p.ws_o, p.ws_ml);
-  auto kern = sp.n_qtiles == 1 ? attn_fwd_two_kernel<D, BF16, true, true> : attn_fwd_two_kernel<D, BF16, true>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
-      cudaSuccess)
-    return -5;
-  const uint64_t blocks = planes * sp.n_qtiles * sp.n_splits;
-  if (blocks > 0x7fffffffull) return -2;
-  kern<<<static_cast<unsigned>(blocks), two_threads(true), L::kBytes, stream>>>(tq, tk, tv, to, p);
-  if (cudaGetLastError() != cudaSuccess) return -5;
-  return sp.n_splits == 1 ? 0 : launch_paged_merge(a, sp.n_splits, stream);
-}
-
 int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
   if (paged_few_rows(a)) return launch_attn_paged_few(a, stream);
   if (a.d == 64)
-    return a.bf16 ? launch_paged_variant<64, true>(a, stream) : launch_paged_variant<64, false>(a, stream);
+    return a.bf16 ? launch_paged_variant<64, true, false>(a, nullptr, stream) : launch_paged_variant<64, false, false>(a, nullptr, stream);
   if (a.d == 128)
-    return a.bf16 ? launch_paged_variant<128, true>(a, stream) : launch_paged_variant<128, false>(a, stream);
+    return a.bf16 ? launch_paged_variant<128, true, false>(a, nullptr, stream) : launch_paged_variant<128, false, false>(a, nullptr, stream);
   return -2;
 }
 

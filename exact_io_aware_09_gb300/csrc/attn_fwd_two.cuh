@@ -30,6 +30,8 @@
 // slower: a persistent grid of two blocks an SM (321 us when this kernel took 282), the same with
 // 128-key tiles (319); three blocks an SM at d=64 (27 us against 25).
 #pragma once
+#include "attn_rows.cuh"
+#include "fp4.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -272,19 +274,146 @@ __device__ __forceinline__ void two_write_part(const PagedItem& it, const PagedP
   }
 }
 
-template <bool PAGED>
+// A chunk over a 4-bit cache (fp4.cuh): codes [page, head, token, d / 2], scale bytes [.., d / 16].
+struct Paged4Params : PagedParams {
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+};
+
+template <bool PAGED, bool FP4>
 struct TwoOf {
   using Params = WinParams;
   using Item = WinItem;
 };
 template <>
-struct TwoOf<true> {
+struct TwoOf<true, false> {
   using Params = PagedParams;
   using Item = PagedItem;
+};
+template <>
+struct TwoOf<true, true> {
+  using Params = Paged4Params;
+  using Item = PagedItem;
+};
+
+// The weights of the 4-bit variant: the largest is 2^7 to 2^15, so that fp16's subnormals lose at most
+// 2^-32 of it.
+constexpr float kTwoTop = 7.0f;
+
+// A producer warp's part of the 4-bit variant: the codes of a step from memory to registers a step ahead,
+// and as f16 values to the operand's place.  In pass i the lanes take 16 bytes of codes each: kKeys keys'
+// rows side by side.
+template <int D, bool STREAM>
+struct Codes4 {
+  static constexpr int kLanes = D / 32;         // lanes of a row
+  static constexpr int kKeys = 32 / kLanes;     // keys of a pass
+  static constexpr int kPasses = kWN / kKeys;
+  uint4 codes[kPasses];
+  uint32_t scale[kPasses];  // two bytes
+
+  // Pass i of step j; row: the pool row of this lane's page of the step (page_row); last: the last position
+  // of the tile.  Tokens that no row of the tile sees become zeros, whatever they hold.
+  __device__ __forceinline__ void load(int i, const uint8_t* c, const uint8_t* s, const Paged4Params& p,
+                                       const PagedItem& it, int last, int j, int row, int box_log2, int lane) {
+    const int key = i * kKeys + lane / kLanes, part = lane % kLanes;
+    const int at = __shfl_sync(0xffffffffu, row, key >> box_log2);
+    const int t = j * kWN + key;
+    const bool seen = t <= last && (p.window < 0 || t >= it.pos0 - p.window || t < p.sinks);
+    codes[i] = make_uint4(0, 0, 0, 0);
+    scale[i] = 0;
+    if (at >= 0 && seen) {
+      const size_t r = ((static_cast<size_t>(at >> p.page_log2) * p.Hkv + it.kv_plane) << p.page_log2) +
+                       (at & ((1 << p.page_log2) - 1)) + (key & ((1 << box_log2) - 1));
+      const uint4* src = reinterpret_cast<const uint4*>(c + r * (D / 2)) + part;
+      const uint16_t* by = reinterpret_cast<const uint16_t*>(s + r * (D / 16)) + part;
+      codes[i] = STREAM ? __ldcs(src) : __ldg(src);
+      scale[i] = STREAM ? __ldcs(by) : __ldg(by);
+    }
+  }
+
+  // Pass i's values to the step's operand: [64 channels][key][128 bytes], 128-byte swizzle.
+  __device__ __forceinline__ void store(int i, uint8_t* dst, int lane) const {
+    const int key = i * kKeys + lane / kLanes, part = lane % kLanes;
+    const uint32_t lo = fp4_scale_pair(scale[i] & 0xffu), hi = fp4_scale_pair(scale[i] >> 8);
+    // at d = 128 the lanes of the upper 64 channels take their chunks in another order: else two lanes of
+    // eight meet in a bank
+    const bool turn = D == 128 && (part & 2);
+    const uint32_t w[4] = {turn ? codes[i].z : codes[i].x, turn ? codes[i].w : codes[i].y,
+                           turn ? codes[i].x : codes[i].z, turn ? codes[i].y : codes[i].w};
+    uint8_t* base = dst + (part >> 1) * kWSubKV;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t v[4];
+      fp4_values8(w[q], (q >= 2) != turn ? hi : lo, v);
+      *reinterpret_cast<uint4*>(base + sw128(key, (part & 1) * 4 + (turn ? q ^ 2 : q))) =
+          make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
 };
 
 // Threads of a block: softmax, producer, two issuers; the paged variant has a producer for V.
 constexpr int two_threads(bool paged) { return paged ? 256 : 224; }
+
+// The two producers' loop in the 4-bit variant: each step's codes come into registers while the step before
+// is converted.  entry: this lane's block-table entry of the first step.
+template <int D, bool STREAM>
+__device__ __forceinline__ void two_convert(const uint8_t* codes, const uint8_t* scales,
+                                            const Paged4Params& p, const PagedItem& it, int entry,
+                                            uint8_t* ring, uint32_t step_bytes, int slots, uint32_t full,
+                                            uint32_t empty, volatile int* abort_flag, bool report) {
+  using X = Codes4<D, STREAM>;
+  X x;
+  const int lane = threadIdx.x & 31, box_log2 = min(p.page_log2, 6);
+  const int last = it.pos0 + it.rows / p.G - 1;
+  int j = it.key_step(0);
+  int row = page_row(p, it, j, lane, entry, report);
+  if (it.n > 1) entry = page_entry(p, it, it.key_step(1), lane);
+#pragma unroll
+  for (int i = 0; i < X::kPasses; ++i) x.load(i, codes, scales, p, it, last, j, row, box_log2, lane);
+  for (int t = 0; t < it.n; ++t) {
+    const int s = t % slots;
+    const bool more = t + 1 < it.n;
+    if (more) {
+      j = it.key_step(t + 1);
+      row = page_row(p, it, j, lane, entry, report);
+      if (t + 2 < it.n) entry = page_entry(p, it, it.key_step(t + 2), lane);
+    }
+    bool ok = true;
+    if (lane == 0 && t >= slots) ok = wait_bounded(empty + 8u * s, ((t / slots) - 1) & 1, abort_flag, p.status);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+#pragma unroll
+    for (int i = 0; i < X::kPasses; ++i) {
+      x.store(i, ring + s * step_bytes, lane);
+      if (more) x.load(i, codes, scales, p, it, last, j, row, box_log2, lane);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + 8u * s);
+  }
+}
+
+// Row r of the query tile, bf16, as f16 times 2^-e in its place; returns 2^e (q_biased_exp).
+template <int D>
+__device__ __forceinline__ float two_turn_q(uint8_t* q, int r) {
+  float mx = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 w = *reinterpret_cast<const uint4*>(q + (c >> 3) * kWSubQ + sw128(r, c & 7));
+    mx = fmaxf(mx, fmaxf(fmaxf(pair_amax(w.x), pair_amax(w.y)), fmaxf(pair_amax(w.z), pair_amax(w.w))));
+  }
+  const int e = q_biased_exp(mx);
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * kWSubQ + sw128(r, c & 7));
+    const uint4 w = *at;
+    *at = make_uint4(q_pair<true>(w.x, inv), q_pair<true>(w.y, inv), q_pair<true>(w.z, inv),
+                     q_pair<true>(w.w, inv));
+  }
+  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
 
 __device__ __forceinline__ bool win_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                          int* status) {
@@ -295,15 +424,20 @@ __device__ __forceinline__ bool win_wait(uint32_t bar, uint32_t parity, volatile
 // STREAM (paged): a cache that only one query tile reads is streamed through L2.  64 x 3-8 tokens over
 // 1k-32k (Hq=64 Hkv=8 d=128) 747 -> 736 us, 16 tokens over 32k 42.5 -> 39.2; an instantiation of its own,
 // since a choice at every copy costs long chunks 2.5%.
-template <int D, bool BF16, bool PAGED, bool STREAM = false>
+// FP4 (paged): a 4-bit cache.  Both producer warps turn its codes into f16 operands, the softmax warps a bf16
+// query into f16 times a power of two a row; P is f16, of weights up to 2^15.
+template <int D, bool BF16, bool PAGED, bool STREAM = false, bool FP4 = false>
 __global__ void __launch_bounds__(two_threads(PAGED), 2)
     attn_fwd_two_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_o,
-                        const typename TwoOf<PAGED>::Params p) {
+                        const typename TwoOf<PAGED, FP4>::Params p) {
   using L = WinLayout<D>;
   constexpr int KS = L::kKS, VS = L::kVS, NS = L::kNS;
+  constexpr bool kBfOps = BF16 && !FP4;            // operands of the products
+  constexpr bool kTurnQ = BF16 && FP4;             // Q becomes f16 in place
+  constexpr float kTop = FP4 ? kTwoTop : 0.0f;     // weights are 2^(x - m + kTop)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -327,7 +461,7 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  const typename TwoOf<PAGED>::Item it = two_item(static_cast<int>(blockIdx.x), p);
+  const typename TwoOf<PAGED, FP4>::Item it = two_item(static_cast<int>(blockIdx.x), p);
   const int n = it.n;
   [[maybe_unused]] auto load_k = [&](int t) {
     mbar_arrive_expect_tx(K_FULL(t % KS), L::kStep);
@@ -365,7 +499,7 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     }
     mbar_init(bar_drain, 1);
     mbar_init(bar_drain_s, 1);
-    if constexpr (PAGED) mbar_init(bar_ragged, 1);
+    if constexpr (PAGED) mbar_init(bar_ragged, FP4 ? kWM : 1);  // (4 bits: Q in f16)
     *abort_flag = 0;
     fence_barrier_init();
     if constexpr (!PAGED) {
@@ -414,32 +548,38 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
           for (int sub = 0; sub < D / 64; ++sub)
             tma_load_3d(base + sub * kWSubQ, &tm_q, bar_q, sub * 64, it.kv_plane * p.G, it.tok0);
         }
-        [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
-        int issued = 0;
-        for (int t = 0; t < n; ++t) {
-          const int s = t % KS;
-          const int row = page_row(p, it, it.key_step(t), lane, entry, true);
-          if (t + 1 < n) entry = page_entry(p, it, it.key_step(t + 1), lane);
-          bool ok = true;
-          if (lane == 0 && t >= KS)
-            ok = wait_bounded(K_EMPTY(s), ((t / KS) - 1) & 1, abort_flag, p.status);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-          const uint32_t n_loads = __popc(__ballot_sync(0xffffffffu, row >= 0));
-          if (lane == 0) mbar_arrive_expect_tx(K_FULL(s), n_loads * box.rows * D * 2);
-          __syncwarp();
-          if (row >= 0) {
-#pragma unroll
-            for (int sub = 0; sub < D / 64; ++sub)
-              load_page<STREAM>(base + L::kK + s * L::kStep + sub * kWSubKV + lane * box.rows * 128, &tm_k,
-                        K_FULL(s), sub * 64, it.kv_plane, row, policy);
+        if constexpr (FP4) {
+          two_convert<D, STREAM>(p.k_codes, p.k_scales, p, it, entry, gbase + L::kK, L::kStep, KS, K_FULL(0),
+                                 K_EMPTY(0), abort_flag, true);
+          if (lane == 0) wait_bounded(bar_q, 0, nullptr, p.status, kWDrainNs);
+        } else {
+          [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
+          int issued = 0;
+          for (int t = 0; t < n; ++t) {
+            const int s = t % KS;
+            const int row = page_row(p, it, it.key_step(t), lane, entry, true);
+            if (t + 1 < n) entry = page_entry(p, it, it.key_step(t + 1), lane);
+            bool ok = true;
+            if (lane == 0 && t >= KS)
+              ok = wait_bounded(K_EMPTY(s), ((t / KS) - 1) & 1, abort_flag, p.status);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            const uint32_t n_loads = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(K_FULL(s), n_loads * box.rows * D * 2);
+            __syncwarp();
+            if (row >= 0) {
+  #pragma unroll
+              for (int sub = 0; sub < D / 64; ++sub)
+                load_page<STREAM>(base + L::kK + s * L::kStep + sub * kWSubKV + lane * box.rows * 128, &tm_k,
+                          K_FULL(s), sub * 64, it.kv_plane, row, policy);
+            }
+            issued = t + 1;
           }
-          issued = t + 1;
-        }
-        // Every asynchronous write into this block's shared memory lands before it may exit.
-        if (lane == 0) {
-          wait_bounded(bar_q, 0, nullptr, p.status, kWDrainNs);
-          for (int t = (issued > KS ? issued - KS : 0); t < issued; ++t)
-            wait_bounded(K_FULL(t % KS), (t / KS) & 1, nullptr, p.status, kWDrainNs);
+          // Every asynchronous write into this block's shared memory lands before it may exit.
+          if (lane == 0) {
+            wait_bounded(bar_q, 0, nullptr, p.status, kWDrainNs);
+            for (int t = (issued > KS ? issued - KS : 0); t < issued; ++t)
+              wait_bounded(K_FULL(t % KS), (t / KS) & 1, nullptr, p.status, kWDrainNs);
+          }
         }
       }
     } else if (lane == 0 && n > 0) {
@@ -464,9 +604,9 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
   } else if (warp == 5) {
     // ----------------------------------------------------------------- tcgen05 issuer of S
     if (lane == 0 && n > 0) {
-      constexpr uint32_t idesc_qk = make_idesc_f16(BF16, kWM, kWN, false);
+      constexpr uint32_t idesc_qk = make_idesc_f16(kBfOps, kWM, kWN, false);
       const uint64_t q_desc = make_sdesc_sw128(base, 16, 1024);
-      if (wait_bounded(bar_q, 0, abort_flag, p.status)) {
+      if (wait_bounded(kTurnQ ? bar_ragged : bar_q, 0, abort_flag, p.status)) {
         for (int t = 0; t < n; ++t) {  // S_t into buffer t % NS, once S_{t-NS} has been read
           const int s = t % KS, b = t % NS;
           if (!wait_bounded(K_FULL(s), (t / KS) & 1, abort_flag, p.status)) break;
@@ -490,62 +630,67 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     // ----------------------------------------------------------------- V producer (paged)
     if constexpr (PAGED) {
       if (n > 0) {
-        const PageBox box(p.page_log2);
-        int issued = 0;
-        [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
-        uint32_t ragged = 0;  // ragged steps so far
-        for (int t = 0; t < n; ++t) {
-          const int s = t % VS, j = it.key_step(t);
-          const int row = page_row(p, it, j, lane, entry, false);
-          if (t + 1 < n) entry = page_entry(p, it, it.key_step(t + 1), lane);
-          bool ok = true;
-          if (lane == 0 && t >= VS)
-            ok = wait_bounded(V_EMPTY(s), ((t / VS) - 1) & 1, abort_flag, p.status);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-          // The step that holds the sequence's end: its rows past the end hold other sequences' or
-          // unwritten tokens, or were not loaded at all.  P is zero there, but 0 * V has to stay 0:
-          // the rows are cleared once the loads have landed, and only then is the step handed on.  The
-          // same for pages that could not be loaded.
-          const uint32_t loaded = __ballot_sync(0xffffffffu, row >= 0);
-          const uint32_t bytes = __popc(loaded) * box.rows * D * 2;
-          const int valid = it.len - j * kWN;  // rows of the step that hold tokens
-          const bool clear = valid < kWN || bytes < L::kStep;
-          const uint32_t bar = clear ? bar_ragged : V_FULL(s);
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-          __syncwarp();
-          if (row >= 0) {
-#pragma unroll
-            for (int sub = 0; sub < D / 64; ++sub)
-              load_page<STREAM>(base + L::kV + s * L::kStep + sub * kWSubKV + lane * box.rows * 128, &tm_v, bar,
-                        sub * 64, it.kv_plane, row, policy);
-          }
-          if (clear) {
-            if (!win_wait(bar, ragged & 1, abort_flag, p.status)) break;
-            ++ragged;
-            for (int i = lane; i < kWN * (D / 8); i += 32) {
-              const int rr = i / (D / 8), c = i % (D / 8);
-              if (rr >= valid || !((loaded >> (rr >> box.log2)) & 1u))
-                *reinterpret_cast<uint4*>(gbase + L::kV + s * L::kStep + (c >> 3) * kWSubKV + rr * 128 +
-                                          (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
+        if constexpr (FP4) {
+          two_convert<D, STREAM>(p.v_codes, p.v_scales, p, it, entry, gbase + L::kV, L::kStep, VS, V_FULL(0),
+                                 V_EMPTY(0), abort_flag, false);
+        } else {
+          const PageBox box(p.page_log2);
+          int issued = 0;
+          [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
+          uint32_t ragged = 0;  // ragged steps so far
+          for (int t = 0; t < n; ++t) {
+            const int s = t % VS, j = it.key_step(t);
+            const int row = page_row(p, it, j, lane, entry, false);
+            if (t + 1 < n) entry = page_entry(p, it, it.key_step(t + 1), lane);
+            bool ok = true;
+            if (lane == 0 && t >= VS)
+              ok = wait_bounded(V_EMPTY(s), ((t / VS) - 1) & 1, abort_flag, p.status);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            // The step that holds the sequence's end: its rows past the end hold other sequences' or
+            // unwritten tokens, or were not loaded at all.  P is zero there, but 0 * V has to stay 0:
+            // the rows are cleared once the loads have landed, and only then is the step handed on.  The
+            // same for pages that could not be loaded.
+            const uint32_t loaded = __ballot_sync(0xffffffffu, row >= 0);
+            const uint32_t bytes = __popc(loaded) * box.rows * D * 2;
+            const int valid = it.len - j * kWN;  // rows of the step that hold tokens
+            const bool clear = valid < kWN || bytes < L::kStep;
+            const uint32_t bar = clear ? bar_ragged : V_FULL(s);
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
             __syncwarp();
-            if (lane == 0) mbar_arrive(V_FULL(s));
+            if (row >= 0) {
+  #pragma unroll
+              for (int sub = 0; sub < D / 64; ++sub)
+                load_page<STREAM>(base + L::kV + s * L::kStep + sub * kWSubKV + lane * box.rows * 128, &tm_v, bar,
+                          sub * 64, it.kv_plane, row, policy);
+            }
+            if (clear) {
+              if (!win_wait(bar, ragged & 1, abort_flag, p.status)) break;
+              ++ragged;
+              for (int i = lane; i < kWN * (D / 8); i += 32) {
+                const int rr = i / (D / 8), c = i % (D / 8);
+                if (rr >= valid || !((loaded >> (rr >> box.log2)) & 1u))
+                  *reinterpret_cast<uint4*>(gbase + L::kV + s * L::kStep + (c >> 3) * kWSubKV + rr * 128 +
+                                            (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(V_FULL(s));
+            }
+            issued = t + 1;
           }
-          issued = t + 1;
+          // loads that nothing waited for land before the block may exit (an aborted ragged step's wait
+          // has already taken its limit)
+          if (lane == 0)
+            for (int t = (issued > VS ? issued - VS : 0); t < issued; ++t)
+              wait_bounded(V_FULL(t % VS), (t / VS) & 1, nullptr, p.status, kWDrainNs);
         }
-        // loads that nothing waited for land before the block may exit (an aborted ragged step's wait
-        // has already taken its limit)
-        if (lane == 0)
-          for (int t = (issued > VS ? issued - VS : 0); t < issued; ++t)
-            wait_bounded(V_FULL(t % VS), (t / VS) & 1, nullptr, p.status, kWDrainNs);
       }
     }
     __syncwarp();
   } else if (warp == 6) {
     // ----------------------------------------------------------------- tcgen05 issuer of O += P V
     if (lane == 0 && n > 0) {
-      constexpr uint32_t idesc_pv = make_idesc_f16(BF16, kWM, D, true);
+      constexpr uint32_t idesc_pv = make_idesc_f16(kBfOps, kWM, D, true);
       for (int t = 0; t < n; ++t) {
         const int s = t % VS, b = t & 1;
         if (!wait_bounded(V_FULL(s), (t / VS) & 1, abort_flag, p.status)) break;
@@ -568,14 +713,26 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     // ----------------------------------------------------------------- softmax + epilogue
     const int r = warp * 32 + lane;
     const uint32_t row_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const float sl2 = p.sl2;
+    [[maybe_unused]] float sl2_row = p.sl2;
+    bool ok = true;
+    if constexpr (kTurnQ) {
+      if (n > 0) {
+        ok = win_wait(bar_q, 0, abort_flag, p.status);
+        if (ok) {
+          sl2_row *= two_turn_q<D>(gbase, r);
+          fence_proxy_async_smem();
+          mbar_arrive(bar_ragged);
+        }
+      }
+    }
+    const float sl2 = kTurnQ ? sl2_row : p.sl2;
     const bool store = r < it.rows;
     const int pos = two_position(it, p, r);  // this row's position, and the last key it may see
     const int last = min(pos, two_keys(it, p) - 1);
     const size_t row_index = store ? two_row(it, p, r) : 0;  // of o and lse
     float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int t = 0; t < n; ++t) {
+    [[maybe_unused]] float m_raw = -INFINITY;
+    for (int t = 0; ok && t < n; ++t) {
       const int j = it.key_step(t);
       const int b = t & 1;
       if (!win_wait(S_FULL(t % NS), (t / NS) & 1, abort_flag, p.status)) {
@@ -619,14 +776,37 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
       const float tile_max = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]),
                                    fmaxf(mx[6], mx[7]));
       // the maximum moves when it rises by more than 2^8 (and at the first finite one)
-      const float m_new = fmaxf(m, tile_max * sl2);
-      float alpha = 1.0f;
-      if (m_new - m > kWRescale) {
-        alpha = ex2(m - m_new);
-        m = m_new;
-        l *= alpha;
+      float alpha = 1.0f, neg_mu;
+      if constexpr (FP4) {
+        // The maximum is kept as a product Q K, unscaled.  Where it is 2^24 or more in log2 units, its
+        // rounding in the fused step below (s sl2 - m) is more than the weights' range allows, and the
+        // difference is taken before the scaling.
+        const float r_new = fmaxf(m_raw, tile_max);
+        if ((r_new - m_raw) * sl2 > kWRescale) {
+          alpha = ex2((m_raw - r_new) * sl2);
+          m_raw = r_new;
+          m = m_raw * sl2;
+          l *= alpha;
+        }
+        neg_mu = (m == -INFINITY) ? 0.0f : kTop - m;
+        const bool far = m != -INFINITY && fabsf(m) >= 16777216.0f;
+        if (__any_sync(0xffffffffu, far)) {
+          const float ref = far ? m_raw : 0.0f;
+          if (far) neg_mu = kTop;
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sr[g][c] = __float_as_uint(__uint_as_float(sr[g][c]) - ref);
+        }
+      } else {
+        const float m_new = fmaxf(m, tile_max * sl2);
+        if (m_new - m > kWRescale) {
+          alpha = ex2(m - m_new);
+          m = m_new;
+          l *= alpha;
+        }
+        neg_mu = (m == -INFINITY) ? 0.0f : -m;
       }
-      const float neg_mu = (m == -INFINITY) ? 0.0f : -m;
       uint32_t pk[32];
       float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -646,7 +826,7 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
           const float p0 = __uint_as_float(sr[g][c]), p1 = __uint_as_float(sr[g][c + 1]);
           const int k2 = c & 6;
           add2(ps[k2], ps[k2 + 1], p0, p1);
-          pk[(g * 32 + c) >> 1] = pack2<BF16>(p0, p1);
+          pk[(g * 32 + c) >> 1] = pack2<kBfOps>(p0, p1);
         }
       l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
       if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
@@ -724,10 +904,10 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
           }
         }
         if (store && !whole)
-          two_write_ml(it, p, row_index, m, l);
+          two_write_ml(it, p, row_index, m - kTop, l);
         else if (store)
           p.lse[row_index] = (l == 0.0f) ? -INFINITY
-                                         : ((m == -INFINITY ? 0.0f : m) + lg2(l)) * 0.69314718055994531f;
+                                         : ((m == -INFINITY ? 0.0f : m - kTop) + lg2(l)) * 0.69314718055994531f;
       }
       fence_proxy_async_smem();
       named_bar_sync(1, kWM);

@@ -1,0 +1,560 @@
+// New tokens of each sequence over a paged cache held in 4 bits (fp4.cuh; attn_cache_fp4.cu writes it): at
+// most 16 (token, query head) rows per key/value head, so a decode step, or a few tokens of a small group.
+//
+// Keys and values are code * scale, exact in fp16, so both products run on the warp-level f16 tiles with
+// nothing rounded but the weights: x_j = scale log2(e) (q . k_j), w_j = 2^(x_j - m + 7) rounded to fp16,
+// o = sum_j w_j v_j / sum_j w_j.  m is at most 8 below the largest x_j so far (it follows a score that
+// exceeds it by 8: most steps find none, and need no maximum over the warp), so that w_j <= 2^15 fits fp16
+// and half a step of a weight below fp16's normal numbers is 2^-32 of the largest.  A bf16 query is scaled
+// by a power of two to at most 2 in magnitude before its conversion to f16.
+//
+// The split kernel is that of a few rows over the 16-bit cache (attn_paged_few.cu) with the codes' channel
+// orders: thread (g, c) = (lane / 4, lane % 4) takes channels D/4 c .. of its keys for the scores, so that a
+// 16-byte load holds its operands of several steps, and channels D/8 g .. of its values, so that their
+// scale is one byte a token.  Values meet the second product as pairs of tokens: the low four bits of two
+// tokens' bytes side by side in one, and the high ones, which convert as pairs.  The pool's order (a
+// head's rows of a page side by side) makes a page's rows one contiguous copy.  Scale bytes come straight to
+// registers two stages ahead and reach their lanes through a few bytes of shared memory of the warp's own.
+// A token that no row sees gets a value scale of zero, which makes its values zeros whatever they hold.
+#include "attn_decode.cuh"
+#include "attn_rows.cuh"
+#include "fp4.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kFew4Rows = 16;
+constexpr int kFew4Stages = 6;                  // of the ring
+constexpr int kFew4MaxStages = 2048 / kDecTok;  // of a split (row_split_tokens)
+constexpr float kRise = 8.0f, kTop = 7.0f;
+
+struct Few4Params {
+  const uint16_t* q;  // [total_q, Hq, D]
+  const int32_t* block_table;
+  const int32_t* cu_q;  // null: sequence b's one token is row b
+  const int32_t* seqlens;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  int* status;
+  int page_log2, max_pages, num_pages, total_q, max_q, max_k;
+  int Hq, Hkv, G, window, sinks, split_stages;
+  float sl2;
+  float* ws_o;  // partial states, or null with a cluster
+  float* ws_ml;
+  uint16_t* out;
+  float* lse;
+  int n_splits, cluster;
+};
+
+template <int D, int NT>
+struct Few4Layout {
+  static constexpr int kMaxR = NT * 8;
+  static constexpr uint32_t kTensor = kDecTok * D / 2;  // codes of K or V of one stage
+  static constexpr uint32_t kStage = 2 * kTensor;
+  static constexpr uint32_t kRing = kFew4Stages * kStage;
+  static constexpr uint32_t kRed = kDecWarps * kMaxR * (D + 2) * 4;  // reuses the ring
+  static constexpr uint32_t kFin = kRed;
+  static_assert(kFin + kMaxR * (D + 2) * 4 <= kRing, "merge scratch must fit in the ring");
+  static constexpr uint32_t kScale = kRing;  // [warp][K's 16 tokens, V's][D / 16]
+  static constexpr uint32_t kBar = kScale + kDecWarps * 32 * (D / 16);
+  static constexpr uint32_t kMisc = kBar + 2 * kFew4Stages * 8;
+  static constexpr uint32_t kPages = kMisc + 16;  // the split's pages, box by box, or -1
+  static constexpr uint32_t kBytes = kPages + kFew4MaxStages * 4 * 4 + 1024;
+};
+
+// Blocks that share an SM, by registers.
+constexpr int few4_blocks_per_sm(int d, int nt) { return nt == 1 ? 4 : d == 64 ? 3 : 2; }
+
+// Byte offset of 16-byte chunk `chunk` of a stage's row: D/2-byte rows in the swizzle of that width
+// (address bits 4-5 exclusive-ored with bits 7-8, at d = 64 bit 4 with bit 7).
+template <int D>
+__device__ __forceinline__ uint32_t code4_off(int row, int chunk) {
+  const uint32_t a = static_cast<uint32_t>(row) * (D / 2) + static_cast<uint32_t>(chunk) * 16;
+  return a ^ ((a >> 3) & (D == 128 ? 0x30u : 0x10u));
+}
+
+}  // namespace
+
+// A warp's query rows and state and its work on sixteen tokens; o and l count in units of 2^(m - kTop).
+template <int D, bool BF16, int NT>
+struct Few4Warp : RowState<D, NT, false> {
+  static constexpr int kB = D / kFp4Block;  // scale bytes of a row
+  uint32_t qf[NT][D / 16][2];
+  float f[NT][2];  // factors of the rows' products
+
+  // row(r): query row r < rows
+  template <typename F>
+  __device__ __forceinline__ void init(F row, int rows, float sl2, int lane) {
+    RowState<D, NT, false>::init();
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint16_t* q = row(n * 8 + g < rows ? n * 8 + g : 0) + c * (D / 4);
+      float mx = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        // channels D/4 c + 4 ks .. + 3: the first pair at the step's k = 2c, 2c + 1, the second at
+        // k = 2c + 8, 2c + 9
+        const uint2 a = n * 8 + g < rows ? *reinterpret_cast<const uint2*>(q + ks * 4) : make_uint2(0, 0);
+        qf[n][ks][0] = a.x;
+        qf[n][ks][1] = a.y;
+        if constexpr (BF16) mx = fmaxf(mx, fmaxf(pair_amax(a.x), pair_amax(a.y)));
+      }
+      float mine = sl2;
+      if constexpr (BF16) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = q_biased_exp(mx);
+        const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        mine *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          qf[n][ks][0] = q_pair<BF16>(qf[n][ks][0], inv);
+          qf[n][ks][1] = q_pair<BF16>(qf[n][ks][1], inv);
+        }
+      }
+      f[n][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
+      f[n][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+    }
+  }
+
+  // Stage rows w0 .. w0 + 15, whose scale bytes are sc[0 .. 15] (keys) and sc[16 .. 31] (values).
+  // see(n, k, r): whether row 2c + r of tile n sees key g + 8k; asked only where `edge`.
+  template <typename F>
+  __device__ __forceinline__ void tokens(const uint8_t* kbuf, const uint8_t* vbuf, const uint8_t* sc, int w0,
+                                         bool edge, F see, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    float acc[NT][4] = {};
+    constexpr int kW = D / 32;  // words of a thread's keys' channels: eight codes each
+    uint32_t wa[kW], wb[kW];
+    if constexpr (D == 128) {
+      *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(kbuf + code4_off<D>(w0 + g, c));
+      *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(kbuf + code4_off<D>(w0 + g + 8, c));
+    } else {
+      *reinterpret_cast<uint2*>(wa) =
+          *reinterpret_cast<const uint2*>(kbuf + code4_off<D>(w0 + g, c >> 1) + (c & 1) * 8);
+      *reinterpret_cast<uint2*>(wb) =
+          *reinterpret_cast<const uint2*>(kbuf + code4_off<D>(w0 + g + 8, c >> 1) + (c & 1) * 8);
+    }
+    uint32_t sa[kB / 4], sb[kB / 4];  // f16 pairs of this thread's blocks of keys g and g + 8
+#pragma unroll
+    for (int i = 0; i < kB / 4; ++i) {
+      sa[i] = fp4_scale_pair(sc[g * kB + c * (kB / 4) + i]);
+      sb[i] = fp4_scale_pair(sc[(g + 8) * kB + c * (kB / 4) + i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      uint32_t a[4], b[4];
+      fp4_values8(wa[i], sa[i / 2], a);
+      fp4_values8(wb[i], sb[i / 2], b);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t ab[4] = {a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma_m16n8k16<false>(acc[n], ab, qf[n][2 * i + h][0], qf[n][2 * i + h][1]);
+      }
+    }
+    float x[NT][2][2];
+    bool rise = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) x[n][k][r] = acc[n][2 * k + r] * f[n][r];
+    if (edge) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (!see(n, k, r)) x[n][k][r] = -INFINITY;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        rise = rise || fmaxf(x[n][0][r], x[n][1][r]) > this->m[n][r] + kRise;
+    if (__any_sync(0xffffffffu, rise)) raise(x);
+    // Token pairs are taken in the order that keeps the values' loads free of bank conflicts: a thread
+    // whose `swap` is set has its pairs the other way round, of the weights too.
+    const int swap = D == 128 ? c & 1 : c >> 1;
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float w[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float shift = this->m[n][r] == -INFINITY ? 0.0f : kTop - this->m[n][r];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          w[k][r] = ex2(x[n][k][r] + shift);
+          this->l[n][r] += w[k][r];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t t = transpose_8x8(pack2<false>(w[k][0], w[k][1]));
+        pb[n][k] = __byte_perm(t, t, swap ? 0x1032 : 0x3210);
+      }
+    }
+    constexpr int kV = D / 64;  // words of a thread's channels of one token
+    uint32_t v[4][kV], sv[2];
+    uint32_t by[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tok = (r >> 1) * 8 + 2 * c + ((r & 1) ^ swap);
+      const uint8_t* src = vbuf + code4_off<D>(w0 + tok, D == 128 ? g >> 1 : g >> 2);
+      if constexpr (D == 128)
+        *reinterpret_cast<uint2*>(v[r]) = *reinterpret_cast<const uint2*>(src + (g & 1) * 8);
+      else
+        v[r][0] = *reinterpret_cast<const uint32_t*>(src + (g & 3) * 4);
+      by[r] = sc[(16 + tok) * kB + (D == 128 ? g : g >> 1)];
+    }
+    sv[0] = fp4_scale_pair(by[0], by[1]);
+    sv[1] = fp4_scale_pair(by[2], by[3]);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      // byte t: the codes of channel 2t of two tokens (even), of channel 2t + 1 (odd)
+      constexpr uint32_t kLow = 0x0f0f0f0fu;
+      uint32_t ev[2][4], od[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t u0 = v[2 * h][i], u1 = v[2 * h + 1][i];
+        fp4_values8((u0 & kLow) | ((u1 << 4) & ~kLow), sv[h], ev[h]);
+        fp4_values8(((u0 >> 4) & kLow) | (u1 & ~kLow), sv[h], od[h]);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t av[4] = {ev[0][t], od[0][t], ev[1][t], od[1][t]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_m16n8k16<false>(this->o[n][i * 4 + t], av, pb[n][0], pb[n][1]);
+      }
+    }
+  }
+
+  // Raises m to the largest x where that exceeds it by more than 2^kRise.
+  __device__ __forceinline__ void raise(const float (&x)[NT][2][2]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float a[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(x[n][0][r], x[n][1][r]);
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        float& m = this->m[n][r];
+        a[r] = 1.0f;
+        if (mx > m + kRise) {
+          a[r] = (m == -INFINITY) ? 0.f : ex2(m - mx);
+          m = mx;
+        }
+        this->l[n][r] *= a[r];
+      }
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        this->o[n][t][0] *= a[0];
+        this->o[n][t][1] *= a[1];
+        this->o[n][t][2] *= a[0];
+        this->o[n][t][3] *= a[1];
+      }
+    }
+  }
+
+  // The state to the merge scratch, m such that l counts in units of 2^m.
+  __device__ __forceinline__ void store(float* rw, int rows, int lane) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) this->m[n][r] -= kTop;
+    RowState<D, NT, false>::store(
+        rw, rows, lane, [&](int t, int i) { return (lane >> 2) * (D / 8) + 2 * t + i; },
+        [](int, int, float x) { return x; });
+  }
+};
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(kDecThreads, few4_blocks_per_sm(D, NT))
+    attn_paged_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_k,
+                              const __grid_constant__ CUtensorMap tm_v, const Few4Params p) {
+  using L = Few4Layout<D, NT>;
+  using Warp = Few4Warp<D, BF16, NT>;
+  const int split = blockIdx.x;
+  const int hk = blockIdx.y;
+  const int b = blockIdx.z;
+  if (threadIdx.x == 0) griddep_launch_dependents();  // the merge may be scheduled (it waits)
+  const int c0 = p.cu_q ? p.cu_q[b] : b, n = p.cu_q ? p.cu_q[b + 1] - c0 : 1;
+  const int len = p.seqlens[b];
+  if (c0 < 0 || n < 0 || n > p.max_q || n > p.total_q - c0 || len < (p.cu_q ? n : 0) || len > p.max_k ||
+      ((len - 1) >> p.page_log2) >= p.max_pages) {
+    if (split == 0 && hk == 0 && threadIdx.x == 0) latch_status(p.status, kStatusBadLengths);
+    return;
+  }
+  if (n == 0) return;
+  const int rows = n * p.G;
+  const int pos0 = len - n;  // (-1: an empty cache, whose row sees no key)
+  // 64-key stages of the visible keys: `sink_st` of them from key 0, then from stage w_begin on
+  const int w_begin = p.window < 0 ? 0 : max(pos0 - p.window, 0) / kDecTok;
+  const int sink_st = p.window < 0 ? 0 : min((min(p.sinks, len) + kDecTok - 1) / kDecTok, w_begin);
+  const int all = sink_st + (len + kDecTok - 1) / kDecTok - w_begin;
+  const int i0 = split * p.split_stages;
+  const int n_stages = min(max(all - i0, 0), p.split_stages);
+  auto stage_token = [&](int st) {
+    const int i = i0 + st;
+    return (i < sink_st ? i : w_begin + i - sink_st) * kDecTok;
+  };
+  auto out_row = [&](int row) {
+    const int t = row / p.G;
+    return static_cast<size_t>(c0 + t) * p.Hq + hk * p.G + (row - t * p.G);
+  };
+  if (n_stages == 0 && !p.cluster) {
+    // no key of its own: the merge gives it no weight
+    if (static_cast<int>(threadIdx.x) < rows)
+      reinterpret_cast<float2*>(p.ws_ml)[out_row(threadIdx.x) * p.n_splits + split] =
+          make_float2(-INFINITY, 0.0f);
+    return;
+  }
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + L::kBar;
+#define FULL(s) (bars + 8u * (s))
+#define EMPTY(s) (bars + 8u * (kFew4Stages + (s)))
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFew4Stages; ++s) {
+      mbar_init(FULL(s), 1);
+      mbar_init(EMPTY(s), kDecWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  // pages of the split, as boxes of a page's rows (64 of them where it has more)
+  const int box_log2 = min(p.page_log2, 6), box = 1 << box_log2, pg_log2 = 6 - box_log2;
+  int* pages = reinterpret_cast<int*>(gbase + L::kPages);  // [stage][box of it]
+  for (int i = threadIdx.x; i < n_stages << pg_log2; i += kDecThreads) {
+    const int t = stage_token(i >> pg_log2) + (i & ((1 << pg_log2) - 1)) * box;
+    int page = -1;
+    if (t < len) {
+      page = p.block_table[static_cast<size_t>(b) * p.max_pages + (t >> p.page_log2)];
+      if (page < 0 || page >= p.num_pages) {
+        latch_status(p.status, kStatusBadLengths);
+        page = -1;
+      }
+    }
+    pages[i] = page;
+  }
+  __syncthreads();
+
+  const int page_mask = (1 << p.page_log2) - 1;
+  if (warp == kDecWarps) {
+    // ------------------------------------------------------------------ TMA producer
+    const uint64_t stream_policy = l2_policy_evict_first();
+    const uint32_t box_bytes = static_cast<uint32_t>(box) * (D / 2);
+    int issued = 0;
+    for (int st = 0; st < n_stages; ++st) {
+      const int s = st % kFew4Stages;
+      bool ok = true;
+      if (lane == 0 && st >= kFew4Stages)
+        ok = wait_bounded(EMPTY(s), ((st / kFew4Stages) - 1) & 1, abort_flag, p.status);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      const uint32_t kbuf = base + s * L::kStage + lane * box_bytes;
+      const int page = lane < (1 << pg_log2) ? pages[(st << pg_log2) + lane] : -1;
+      const uint32_t n_loads = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(FULL(s), n_loads * 2 * box_bytes);
+      __syncwarp();
+      if (page >= 0) {
+        const int at = (stage_token(st) + lane * box) & page_mask;
+        tma_load_4d_hint(kbuf, &tm_k, FULL(s), 0, at, hk, page, stream_policy);
+        tma_load_4d_hint(kbuf + L::kTensor, &tm_v, FULL(s), 0, at, hk, page, stream_policy);
+      }
+      issued = st + 1;
+    }
+    if (lane == 0)
+      for (int st = (issued > kFew4Stages ? issued - kFew4Stages : 0); st < issued; ++st)
+        wait_bounded(FULL(st % kFew4Stages), (st / kFew4Stages) & 1, nullptr, p.status, 100000000ull);
+    return;  // the producer takes no part in the reduction below
+  }
+
+  // -------------------------------------------------------------------- compute warps
+  const int g = lane >> 2, c = lane & 3;
+  Warp ws;
+  ws.init([&](int row) { return p.q + out_row(row) * D; }, rows, p.sl2, lane);
+  const int last = pos0 + n - 1;                     // position of the last new token
+  const int first = p.window < 0 ? 0 : pos0 - p.window;  // first key of the first one's window
+  // Scale bytes of stage st: lane i < 16 has those of key i of this warp's sixteen, lane 16 + i of value
+  // i (zeros where no row sees it).  The sixteen lie in one page.
+  auto scales_at = [&](int st) -> uint2 {
+    uint2 r = make_uint2(0, 0);
+    if (st >= n_stages) return r;
+    const int t = stage_token(st) + warp * 16, mine = t + (lane & 15);
+    const int page = t < len ? pages[(st << pg_log2) + ((warp * 16) >> box_log2)] : -1;
+    if (page < 0 || mine >= len || (mine < first && mine >= p.sinks)) return r;
+    const uint8_t* src = (lane < 16 ? p.k_scales : p.v_scales) +
+                         ((((static_cast<size_t>(page) * p.Hkv + hk) << p.page_log2) + (mine & page_mask)) *
+                          Warp::kB);
+    if constexpr (D == 128)
+      r = __ldcs(reinterpret_cast<const uint2*>(src));
+    else
+      r.x = __ldcs(reinterpret_cast<const uint32_t*>(src));
+    return r;
+  };
+  uint8_t* sc = gbase + L::kScale + warp * 32 * Warp::kB;
+  uint2 sc0 = scales_at(0), sc1 = scales_at(1);
+  bool ok = true;
+  for (int st = 0; st < n_stages; ++st) {
+    const int s = st % kFew4Stages;
+    if constexpr (D == 128)
+      reinterpret_cast<uint2*>(sc)[lane] = sc0;
+    else
+      reinterpret_cast<uint32_t*>(sc)[lane] = sc0.x;
+    sc0 = sc1;
+    sc1 = scales_at(st + 2);
+    __syncwarp();
+    if (!dec_warp_wait(FULL(s), (st / kFew4Stages) & 1, abort_flag, p.status)) {
+      ok = false;
+      break;
+    }
+    const uint8_t* kbuf = gbase + s * L::kStage;
+    const int key0 = stage_token(st) + warp * 16;  // first key of this warp
+    if (key0 <= last) {
+      const bool edge = key0 + 15 > pos0 || (p.window >= 0 && key0 < last - p.window);
+      ws.tokens(kbuf, kbuf + L::kTensor, sc, warp * 16, edge,
+                [&](int u, int k, int r) {
+                  const int key = key0 + g + 8 * k;
+                  const int pos = pos0 + min((u * 8 + 2 * c + r) / p.G, n - 1);
+                  return key <= pos && (p.window < 0 || pos - key <= p.window || key < p.sinks);
+                },
+                lane);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(EMPTY(s));
+  }
+
+  // ---------------------------------------------------- merge the four warps' states
+  ws.finish();
+  named_bar_sync(1, kDecWarps * 32);  // every warp is done with the ring
+  ok = ok && (*abort_flag == 0);
+  float* red = reinterpret_cast<float*>(gbase);  // [warp][row][D + 2]
+  if (ok) ws.store(red + warp * L::kMaxR * (D + 2), rows, lane);
+  named_bar_sync(1, kDecWarps * 32);
+  const RowsOut w{p.ws_o, p.ws_ml, p.out, p.lse, p.n_splits, split, p.cluster != 0};
+  merge_rows<D, BF16, kDecWarps, L::kMaxR, false>(red, reinterpret_cast<float*>(gbase + L::kFin), rows, ok,
+                                                  n_stages > 0, w, out_row);
+#undef FULL
+#undef EMPTY
+}
+
+static bool few_rows(int max_q, int G) { return static_cast<long long>(max_q) * G <= kFew4Rows; }
+
+// Splits of a call with few rows, and 64-key stages of each.
+static void few_split(int B, int Hkv, int G, int max_q, int max_k, int window, int sinks, int d,
+                      int& n_splits, int& stages) {
+  long long tokens = max_k;
+  if (window >= 0) {
+    // the window's keys with those of the stages its ends lie in, and the sinks' stages
+    const long long near = static_cast<long long>(window) + max_q + 2 * kDecTok +
+                           (static_cast<long long>(sinks) + kDecTok - 1) / kDecTok * kDecTok;
+    if (near < tokens) tokens = near;
+  }
+  const int slots = 152 * few4_blocks_per_sm(d, max_q * G <= 8 ? 1 : 2);
+  const int per = row_split_tokens(static_cast<long long>(B) * Hkv, tokens, slots);
+  stages = per / kDecTok;
+  const long long all = (tokens + kDecTok - 1) / kDecTok;
+  n_splits = all > 0 ? static_cast<int>((all + stages - 1) / stages) : 1;
+}
+
+template <int D, bool BF16, int NT>
+static int launch_few4(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream) {
+  using L = Few4Layout<D, NT>;
+  // {bytes of a row, token of a page, head, page}
+  const uint64_t row = D / 2, head = row * c.page_size;
+  const uint64_t dims[4] = {row, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(a.Hkv),
+                            static_cast<uint64_t>(c.num_pages)};
+  const uint64_t strides[3] = {row, head, head * a.Hkv};
+  const uint32_t box[4] = {D / 2, static_cast<uint32_t>(c.page_size < kDecTok ? c.page_size : kDecTok), 1, 1};
+  CUtensorMap tk = {}, tv = {};
+  if (c.num_pages > 0 &&
+      (!make_tmap_4d_u8(&tk, c.k_codes, dims, strides, box) || !make_tmap_4d_u8(&tv, c.v_codes, dims, strides, box)))
+    return -5;
+  Few4Params p = {};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.block_table = c.block_table;
+  p.cu_q = a.cu_q;
+  p.seqlens = a.seqlens;
+  p.k_scales = c.k_scales;
+  p.v_scales = c.v_scales;
+  p.status = device_status_ptr();
+  if (!p.status) return -5;
+  while ((1 << p.page_log2) < c.page_size) ++p.page_log2;
+  p.max_pages = c.max_pages;
+  p.num_pages = c.num_pages;
+  p.total_q = a.total_q;
+  p.max_q = a.max_q;
+  p.max_k = a.max_k;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = a.Hq / a.Hkv;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.sl2 = a.scale * 1.4426950408889634f;
+  p.out = static_cast<uint16_t*>(a.o);
+  p.lse = a.lse;
+  few_split(a.B, a.Hkv, p.G, a.max_q, a.max_k, a.window, a.sinks, D, p.n_splits,
+            p.split_stages);
+  p.cluster = p.n_splits <= kMaxCluster;
+  if (!p.cluster) paged_parts(a, D, p.n_splits, p.ws_o, p.ws_ml);
+  auto kern = attn_paged_fp4_few_kernel<D, BF16, NT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess)
+    return -5;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n_splits, a.Hkv, a.B);
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.n_splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, tk, tv, p) != cudaSuccess) return -5;
+  return p.cluster ? 0 : launch_paged_merge(a, p.n_splits, stream);
+}
+
+template <int D, bool BF16>
+static int launch_variant(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream) {
+  const int G = a.Hq / a.Hkv;
+  if (few_rows(a.max_q, G))
+    return a.max_q * G <= 8 ? launch_few4<D, BF16, 1>(a, c, stream) : launch_few4<D, BF16, 2>(a, c, stream);
+  return launch_attn_fp4_chunk(a, c, stream);
+}
+
+int launch_attn_paged_fp4(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream) {
+  if (a.d == 64)
+    return a.bf16 ? launch_variant<64, true>(a, c, stream) : launch_variant<64, false>(a, c, stream);
+  return a.bf16 ? launch_variant<128, true>(a, c, stream) : launch_variant<128, false>(a, c, stream);
+}
+
+size_t paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
+                                 int sinks, int d) {
+  if (total_q <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_q <= 0 || max_k <= 0 || d <= 0) return 0;
+  const int G = Hq / Hkv;
+  int n_splits, stages;
+  if (!few_rows(max_q, G)) {
+    n_splits = G <= 128 ? fp4_chunk_splits(B, Hq, Hkv, max_q, max_k, window, sinks, d) : 1;
+    return n_splits == 1 ? 0 : paged_parts_bytes(total_q, Hq, n_splits, d);
+  }
+  few_split(B, Hkv, G, max_q, max_k, window, sinks, d, n_splits, stages);
+  return n_splits <= kMaxCluster ? 0 : paged_parts_bytes(total_q, Hq, n_splits, d);
+}
+
+}  // namespace attn

@@ -25,6 +25,25 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return y;
 }
 
+// The query row (16-bit) as f16 pairs times 2^-e, and 2^e: e = 0 for f16, for bf16 such that the
+// largest magnitude lies in [1, 2) (0 where the row is zero or not finite).
+template <bool BF16>
+__device__ __forceinline__ uint32_t q_pair(uint32_t w, float inv) {
+  if constexpr (!BF16) return w;
+  return pack2<false>(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xffff0000u) * inv);
+}
+
+__device__ __forceinline__ float pair_amax(uint32_t w) {  // of a bf16 pair
+  return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u)));
+}
+
+// Biased exponent of a bf16 query row's scale: that of its largest magnitude, kept where 2^-e is a
+// normal number too.
+__device__ __forceinline__ int q_biased_exp(float amax) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23);
+  return e == 255 || amax == 0.0f ? 127 : e < 1 ? 1 : e > 253 ? 253 : e;
+}
+
 template <int D, int NT, bool BF16_MMA>
 struct RowState {
   float m[NT][2], l[NT][2];  // running maximum (log2 units); partial sum over this thread's keys

@@ -25,6 +25,10 @@ bool make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t
                      uint64_t dim2, uint64_t stride1, uint64_t stride2, uint32_t box0,
                      uint32_t box1, uint32_t box2);
 
+// A 4-D descriptor over bytes whose box rows are 32 or 64 bytes, in the swizzle of that width.
+bool make_tmap_4d_u8(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t strides[3],
+                     const uint32_t box[4]);
+
 // Device address of the status word of the current device (nullptr on failure).
 int* device_status_ptr();
 
@@ -218,6 +222,14 @@ int launch_cache_write_fp4(const CacheFp4& c, const void* k, const void* v, cons
                            int Hkv, int d, bool bf16, cudaStream_t stream);
 int launch_cache_read_fp4(const CacheFp4& c, void* k, void* v, const int32_t* cu_k, const int32_t* starts,
                           int total, int B, int Hkv, int d, bool bf16, cudaStream_t stream);
+// Attention over a 4-bit cache (attn_paged_fp4.cu); a.k_pages and v_pages are not used, a.cu_q == null: one
+// token of each sequence, which may have none in the cache.
+int launch_attn_paged_fp4(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream);
+// ... with more than 16 rows per key/value head (attn_paged_fp4_chunk.cu), and its key splits.
+int launch_attn_fp4_chunk(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream);
+int fp4_chunk_splits(int B, int Hq, int Hkv, int max_q, int max_k, int window, int sinks, int d);
+size_t paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
+                                 int sinks, int d);
 // Page lists (attn_pages.cu): lengths is cu_seqlens_q of an extension, the kept lengths of a trim, which
 // has no slots.
 struct PagesArgs {
@@ -237,7 +249,9 @@ bool paged_few_rows(const PagedArgs& a);
 void paged_few_split(int B, int Hkv, int max_q, int max_k, int window, int sinks, int d,
                      int& n_splits, int& stages);
 int launch_attn_paged_few(const PagedArgs& a, cudaStream_t stream);
-// The partial states of n_splits splits in the call's workspace, and their merge into o and lse.
+// The partial states of n_splits splits in the call's workspace: their bytes, their places, and their merge
+// into o and lse.
+size_t paged_parts_bytes(int total_q, int Hq, int n_splits, int d);
 void paged_parts(const PagedArgs& a, int d, int n_splits, float*& ws_o, float*& ws_ml);
 int launch_paged_merge(const PagedArgs& a, int n_splits, cudaStream_t stream);
 size_t paged_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,

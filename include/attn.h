@@ -496,6 +496,47 @@ int attn_cache_read_fp4(const void *k_codes, const void *v_codes, const void *k_
                         attn_stream_t stream);
 
 /*
+ * attn_fwd_paged_fp4_workspace_bytes -- bytes of the workspace attn_fwd_paged_fp4 needs: partial states of
+ * the key splits a call is cut into; 0 when the call's splits are merged without one (the workspace may
+ * then be null) and for invalid arguments.
+ */
+size_t attn_fwd_paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_seqlen_q,
+                                          int max_seqlen_k, int window, int sinks, int d);
+
+/*
+ * attn_fwd_paged_fp4 -- attn_fwd_paged over a 4-bit cache: a chunk of new tokens of each sequence (chunked
+ * prefill, draft verification, or one token each), causal, optionally under a sliding window with sinks.
+ * The new tokens' keys and values are in the cache already, as attn_cache_write_fp4 stores them.
+ *
+ *   k_codes, v_codes, k_scales, v_scales   the cache, as attn_cache_write_fp4 (scale bytes it writes)
+ *   the others    as attn_fwd_paged; the workspace is that of attn_fwd_paged_fp4_workspace_bytes
+ * Keys and values are code times scale, exact in fp16, and both products are made in fp16 with fp32 sums;
+ * a bf16 query is scaled by a power of two per row and rounded to fp16, which loses at most 2^-25 of the
+ * row's largest magnitude.  The weights p_j are rounded to fp16: o is off by at most
+ * 2^-11 sum_j p_j |v_j| and, from what fp16's subnormals lose, 2^-32 max_j(p_j) sum_j |v_j|.
+ * A value that is NaN and that some new token of its sequence sees may reach all of them.
+ */
+int attn_fwd_paged_fp4(const void *q, const void *k_codes, const void *v_codes, const void *k_scales,
+                       const void *v_scales, const int32_t *block_table, const int32_t *cu_seqlens_q,
+                       const int32_t *seqlens_k, int num_pages, int page_size, int max_pages_per_seq,
+                       int total_q, int max_seqlen_q, int max_seqlen_k, void *o, float *lse, int B,
+                       int Hq, int Hkv, int d, int window, int sinks, float scale, attn_dtype_t dtype,
+                       void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * attn_decode_paged_fp4_workspace_bytes, attn_decode_paged_fp4 -- attn_decode_paged over a 4-bit cache:
+ * one new token of each sequence, q [B, Hq, d].  The cache and the roundings as attn_fwd_paged_fp4;
+ * the others as attn_decode_paged, Hq / Hkv <= 16, the number of splits the library's choice.
+ */
+size_t attn_decode_paged_fp4_workspace_bytes(int B, int Hq, int Hkv, int max_seqlen_k, int d);
+int attn_decode_paged_fp4(const void *q, const void *k_codes, const void *v_codes,
+                          const void *k_scales, const void *v_scales, const int32_t *block_table,
+                          const int32_t *seqlens_k, int num_pages, int page_size,
+                          int max_pages_per_seq, int max_seqlen_k, void *o, float *lse, int B, int Hq,
+                          int Hkv, int d, float scale, attn_dtype_t dtype, void *workspace,
+                          size_t workspace_bytes, attn_stream_t stream);
+
+/*
  * attn_pages_extend -- pages for sequences that grow: takes them from a free list, enters them into the
  * block table and gives the slots of the new tokens.  All of it on the device, so that a captured step
  * can do it again and again.
@@ -505,8 +546,8 @@ int attn_cache_read_fp4(const void *k_codes, const void *v_codes, const void *k_
  *   seqlens       [B] int32 device, in and out: cached tokens L_b, which grow by n_b
  *   cu_seqlens_q  [B + 1] int32 device, non-decreasing: the packed rows of the new tokens; n_b =
  *                 cu_seqlens_q[b+1] - cu_seqlens_q[b] >= 0 of them, at positions L_b .. L_b + n_b - 1
- *   free_pages    [num_pages] int32 device: a stack, of which the first n_free entries are pages that no
- *                 sequence holds
+ *   free_pages    [num_pages] int32 device, an entry for every page of the pool: a stack, of which the
+ *                 first n_free are pages that no sequence holds
  *   n_free        [1] int32 device, in and out
  *   slots         [total] int32 device out: page * page_size + (position % page_size) of each packed
  *                 row's token; -1 for rows outside cu_seqlens_q[0] .. cu_seqlens_q[B]-1
