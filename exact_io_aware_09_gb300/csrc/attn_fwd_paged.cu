@@ -144,9 +144,9 @@ int launch_paged_merge(const PagedArgs& a, int n_splits, cudaStream_t stream) {
 int launch_attn_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
   if (paged_few_rows(a)) return launch_attn_paged_few(a, stream);
   if (a.d == 64)
-    return a.bf16 ? launch_paged_variant<64, true, false>(a, nullptr, stream) : launch_paged_variant<64, false, false>(a, nullptr, stream);
+    return a.bf16 ? launch_paged_variant<64, true, kKvRows>(a, nullptr, 0, stream) : launch_paged_variant<64, false, kKvRows>(a, nullptr, 0, stream);
   if (a.d == 128)
-    return a.bf16 ? launch_paged_variant<128, true, false>(a, nullptr, stream) : launch_paged_variant<128, false, false>(a, nullptr, stream);
+    return a.bf16 ? launch_paged_variant<128, true, kKvRows>(a, nullptr, 0, stream) : launch_paged_variant<128, false, kKvRows>(a, nullptr, 0, stream);
   return -2;
 }
 

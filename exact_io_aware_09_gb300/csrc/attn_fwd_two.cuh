@@ -54,7 +54,7 @@ struct WinParams {
   float sl2;
 };
 
-template <int D>
+template <int D, bool CODES = false>
 struct WinLayout {
   static constexpr int kKS = D == 128 ? 2 : 3, kVS = D == 128 ? 2 : 3;  // ring slots
   static constexpr int kNS = D == 128 ? 1 : 2;                          // S buffers
@@ -64,10 +64,15 @@ struct WinLayout {
   static constexpr uint32_t kStep = kWN * D * 2;
   static constexpr uint32_t kK = kQBytes;
   static constexpr uint32_t kV = kK + kKS * kStep;
-  static constexpr uint32_t kBar = kV + kVS * kStep;
+  // codes and scale bytes of K or of V of a step
+  static constexpr int kRawK = CODES ? 2 : 0, kRaw = CODES ? 3 : 0;  // slots of K, and with the one of V
+  static constexpr uint32_t kRawCodes = kWN * D / 2, kRawBytes = kRawCodes + kWN * D / 16;
+  static constexpr uint32_t kRawAt = kV + kVS * kStep;
+  static constexpr uint32_t kBar = kRawAt + kRaw * kRawBytes;
   // q_full, k_full, k_empty, v_full, v_empty, s_full[2], p_ready[2], pv_done[2], drain, s_free[2],
-  // drain of the S issuer, a ragged V step's loads (paged)
-  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 11;
+  // drain of the S issuer, a ragged V step's loads (paged), Q in f16 (4-bit cache)
+  // and raw_full, raw_empty (codes)
+  static constexpr uint32_t kNumBars = 1 + 2 * kKS + 2 * kVS + 12 + 2 * kRaw;
   static constexpr uint32_t kMisc = kBar + kNumBars * 8;
   static constexpr uint32_t kBytes = kMisc + 16 + 1024;  // + alignment
   static_assert(2 * (kBytes + 1024) <= 233472, "two blocks on an SM");
@@ -124,6 +129,18 @@ struct PagedParams {
   int n_splits, split_steps;   // 64-key steps of one split (n_splits == 1: the whole item)
   float* ws_o;                 // [total_q * Hq, n_splits, D] normalised partial outputs
   float* ws_ml;                // [total_q * Hq, n_splits, 2] (m in log2 units, l)
+};
+
+// Where the paged variants' keys and values come from: 16-bit pages, a 4-bit cache's codes
+// ([page, head, token, d / 2], scale bytes [.., d / 16]; fp4.cuh), or its f16 copy [B, copy_rows, Hkv, d].
+enum { kKvRows = 0, kKvCodes = 1, kKvCopy = 2 };
+
+struct Paged4Params : PagedParams {
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  int copy_rows;
 };
 
 // One work item: a query tile of one (sequence, key/value head), or one split of its keys.  The tile's
@@ -227,6 +244,11 @@ __device__ __forceinline__ int page_row(const PagedParams& p, const PagedItem& i
   return (entry << p.page_log2) + (t & ((1 << p.page_log2) - 1));
 }
 
+// The row of the f16 copy that step j starts at, for lane 0 (one box brings the step).
+__device__ __forceinline__ int copy_row(const Paged4Params& p, const PagedItem& it, int j, int lane) {
+  return lane == 0 ? it.b * p.copy_rows + j * kWN : -1;
+}
+
 // Position of row r of an item's tile, keys of its sequence, and its row of o and lse.
 __device__ __forceinline__ int two_position(const WinItem& it, const WinParams& p, int r) {
   return it.qt * kWM + r + p.N_kv - p.N_q;
@@ -274,119 +296,157 @@ __device__ __forceinline__ void two_write_part(const PagedItem& it, const PagedP
   }
 }
 
-// A chunk over a 4-bit cache (fp4.cuh): codes [page, head, token, d / 2], scale bytes [.., d / 16].
-struct Paged4Params : PagedParams {
-  const uint8_t* k_codes;
-  const uint8_t* v_codes;
-  const uint8_t* k_scales;
-  const uint8_t* v_scales;
-};
-
-template <bool PAGED, bool FP4>
+template <bool PAGED, int KV>
 struct TwoOf {
+  using Params = Paged4Params;
+  using Item = PagedItem;
+};
+template <>
+struct TwoOf<false, kKvRows> {
   using Params = WinParams;
   using Item = WinItem;
 };
 template <>
-struct TwoOf<true, false> {
+struct TwoOf<true, kKvRows> {
   using Params = PagedParams;
   using Item = PagedItem;
 };
-template <>
-struct TwoOf<true, true> {
-  using Params = Paged4Params;
-  using Item = PagedItem;
-};
 
-// The weights of the 4-bit variant: the largest is 2^7 to 2^15, so that fp16's subnormals lose at most
+// The weights of the 4-bit variants: the largest is 2^7 to 2^15, so that fp16's subnormals lose at most
 // 2^-32 of it.
 constexpr float kTwoTop = 7.0f;
 
-// A producer warp's part of the 4-bit variant: the codes of a step from memory to registers a step ahead,
-// and as f16 values to the operand's place.  In pass i the lanes take 16 bytes of codes each: kKeys keys'
-// rows side by side.
+// Threads of a block: softmax, producer, two issuers; the paged variant has a producer for V, or of codes and
+// four warps that convert them.
+constexpr int two_threads(bool paged, int kv = kKvRows) {
+  return !paged ? 224 : kv == kKvCodes ? 384 : 256;
+}
+// ... over codes its registers are shared out anew: 384 threads at 80, which the converting warpgroup keeps
+constexpr uint32_t kRegsTwoSoftmax = 120, kRegsTwoIssue = 40, kRegsTwoConvert = 80;
+static_assert(kRegsTwoSoftmax + kRegsTwoIssue + kRegsTwoConvert <= 3 * 80, "registers of the launch");
+
+// The raw slot of step t's K (v = 0) or V, and which of the slot's uses that is.  K and V have slots of their
+// own: copies need not land in the order they were issued in, and a warp that skipped a use of a slot could
+// take the one before it for its own.
+template <int D>
+__device__ __forceinline__ int raw_slot(int t, int v) {
+  return v ? WinLayout<D, true>::kRawK : t % WinLayout<D, true>::kRawK;
+}
+template <int D>
+__device__ __forceinline__ int raw_use(int t, int v) {
+  return v ? t : t / WinLayout<D, true>::kRawK;
+}
+
+// The producer warp of the codes: each step's of K, then of V, page by page into the raw slots.
 template <int D, bool STREAM>
-struct Codes4 {
-  static constexpr int kLanes = D / 32;         // lanes of a row
-  static constexpr int kKeys = 32 / kLanes;     // keys of a pass
-  static constexpr int kPasses = kWN / kKeys;
-  uint4 codes[kPasses];
-  uint32_t scale[kPasses];  // two bytes
-
-  // Pass i of step j; row: the pool row of this lane's page of the step (page_row); last: the last position
-  // of the tile.  Tokens that no row of the tile sees become zeros, whatever they hold.
-  __device__ __forceinline__ void load(int i, const uint8_t* c, const uint8_t* s, const Paged4Params& p,
-                                       const PagedItem& it, int last, int j, int row, int box_log2, int lane) {
-    const int key = i * kKeys + lane / kLanes, part = lane % kLanes;
-    const int at = __shfl_sync(0xffffffffu, row, key >> box_log2);
-    const int t = j * kWN + key;
-    const bool seen = t <= last && (p.window < 0 || t >= it.pos0 - p.window || t < p.sinks);
-    codes[i] = make_uint4(0, 0, 0, 0);
-    scale[i] = 0;
-    if (at >= 0 && seen) {
-      const size_t r = ((static_cast<size_t>(at >> p.page_log2) * p.Hkv + it.kv_plane) << p.page_log2) +
-                       (at & ((1 << p.page_log2) - 1)) + (key & ((1 << box_log2) - 1));
-      const uint4* src = reinterpret_cast<const uint4*>(c + r * (D / 2)) + part;
-      const uint16_t* by = reinterpret_cast<const uint16_t*>(s + r * (D / 16)) + part;
-      codes[i] = STREAM ? __ldcs(src) : __ldg(src);
-      scale[i] = STREAM ? __ldcs(by) : __ldg(by);
-    }
-  }
-
-  // Pass i's values to the step's operand: [64 channels][key][128 bytes], 128-byte swizzle.
-  __device__ __forceinline__ void store(int i, uint8_t* dst, int lane) const {
-    const int key = i * kKeys + lane / kLanes, part = lane % kLanes;
-    const uint32_t lo = fp4_scale_pair(scale[i] & 0xffu), hi = fp4_scale_pair(scale[i] >> 8);
-    // at d = 128 the lanes of the upper 64 channels take their chunks in another order: else two lanes of
-    // eight meet in a bank
-    const bool turn = D == 128 && (part & 2);
-    const uint32_t w[4] = {turn ? codes[i].z : codes[i].x, turn ? codes[i].w : codes[i].y,
-                           turn ? codes[i].x : codes[i].z, turn ? codes[i].y : codes[i].w};
-    uint8_t* base = dst + (part >> 1) * kWSubKV;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t v[4];
-      fp4_values8(w[q], (q >= 2) != turn ? hi : lo, v);
-      *reinterpret_cast<uint4*>(base + sw128(key, (part & 1) * 4 + (turn ? q ^ 2 : q))) =
-          make_uint4(v[0], v[1], v[2], v[3]);
-    }
-  }
-};
-
-// Threads of a block: softmax, producer, two issuers; the paged variant has a producer for V.
-constexpr int two_threads(bool paged) { return paged ? 256 : 224; }
-
-// The two producers' loop in the 4-bit variant: each step's codes come into registers while the step before
-// is converted.  entry: this lane's block-table entry of the first step.
-template <int D, bool STREAM>
-__device__ __forceinline__ void two_convert(const uint8_t* codes, const uint8_t* scales,
-                                            const Paged4Params& p, const PagedItem& it, int entry,
-                                            uint8_t* ring, uint32_t step_bytes, int slots, uint32_t full,
-                                            uint32_t empty, volatile int* abort_flag, bool report) {
-  using X = Codes4<D, STREAM>;
-  X x;
-  const int lane = threadIdx.x & 31, box_log2 = min(p.page_log2, 6);
-  const int last = it.pos0 + it.rows / p.G - 1;
-  int j = it.key_step(0);
-  int row = page_row(p, it, j, lane, entry, report);
-  if (it.n > 1) entry = page_entry(p, it, it.key_step(1), lane);
-#pragma unroll
-  for (int i = 0; i < X::kPasses; ++i) x.load(i, codes, scales, p, it, last, j, row, box_log2, lane);
+__device__ __forceinline__ void two_load_codes(const Paged4Params& p, const PagedItem& it, int entry,
+                                               uint32_t raw, uint32_t full, uint32_t empty,
+                                               volatile int* abort_flag) {
+  using L = WinLayout<D, true>;
+  const int lane = threadIdx.x & 31;
+  const PageBox box(p.page_log2);
+  [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
+  int issued[2] = {0, 0};
   for (int t = 0; t < it.n; ++t) {
-    const int s = t % slots;
-    const bool more = t + 1 < it.n;
-    if (more) {
-      j = it.key_step(t + 1);
-      row = page_row(p, it, j, lane, entry, report);
-      if (t + 2 < it.n) entry = page_entry(p, it, it.key_step(t + 2), lane);
-    }
+    const int row = page_row(p, it, it.key_step(t), lane, entry, true);
+    if (t + 1 < it.n) entry = page_entry(p, it, it.key_step(t + 1), lane);
+    const size_t at = ((static_cast<size_t>(row >> p.page_log2) * p.Hkv + it.kv_plane) << p.page_log2) +
+                      (row & ((1 << p.page_log2) - 1));
+    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * box.rows * (D / 2 + D / 16);
     bool ok = true;
-    if (lane == 0 && t >= slots) ok = wait_bounded(empty + 8u * s, ((t / slots) - 1) & 1, abort_flag, p.status);
-    if (!__shfl_sync(0xffffffffu, ok, 0)) break;
 #pragma unroll
-    for (int i = 0; i < X::kPasses; ++i) {
-      x.store(i, ring + s * step_bytes, lane);
-      if (more) x.load(i, codes, scales, p, it, last, j, row, box_log2, lane);
+    for (int v = 0; v < 2 && ok; ++v) {
+      const int s = raw_slot<D>(t, v), use = raw_use<D>(t, v);
+      if (lane == 0) {
+        if (use > 0) ok = wait_bounded(empty + 8u * s, (use - 1) & 1, abort_flag, p.status);
+        if (ok) mbar_arrive_expect_tx(full + 8u * s, bytes);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (row >= 0) {
+        const uint32_t dst = raw + s * L::kRawBytes + lane * box.rows * (D / 2);
+        const uint32_t dst_s = raw + s * L::kRawBytes + L::kRawCodes + lane * box.rows * (D / 16);
+        const uint8_t* src = (v ? p.v_codes : p.k_codes) + at * (D / 2);
+        const uint8_t* src_s = (v ? p.v_scales : p.k_scales) + at * (D / 16);
+        if constexpr (STREAM) {
+          bulk_load_hint(dst, src, box.rows * (D / 2), full + 8u * s, policy);
+          bulk_load_hint(dst_s, src_s, box.rows * (D / 16), full + 8u * s, policy);
+        } else {
+          bulk_load(dst, src, box.rows * (D / 2), full + 8u * s);
+          bulk_load(dst_s, src_s, box.rows * (D / 16), full + 8u * s);
+        }
+      }
+      issued[v] = t + 1;
+    }
+    if (!ok) break;
+  }
+  // every copy lands before the block may exit
+  if (lane == 0)
+    for (int v = 0; v < 2; ++v)
+      for (int t = max(issued[v] - (v ? 1 : L::kRawK), 0); t < issued[v]; ++t)
+        wait_bounded(full + 8u * raw_slot<D>(t, v), raw_use<D>(t, v) & 1, nullptr, p.status, kWDrainNs);
+}
+
+// A converting warp: the keys from key0 on (half of a step's) of K (v = 0) or V (v = 1), from the raw slots as
+// f16 values to the operand's place, [64 channels][key][128 bytes] in the 128-byte swizzle.  In a pass the
+// lanes take 16 bytes of codes each, kKeys keys' rows side by side.  Tokens that no row of the tile sees
+// become zeros, whatever they hold.
+constexpr int kConvWarps = 4;
+template <int D>
+__device__ __forceinline__ void two_convert(const Paged4Params& p, const PagedItem& it, int v, int key0,
+                                            const uint8_t* raw, uint32_t raw_full, uint32_t raw_empty,
+                                            uint8_t* ring, int slots, uint32_t full, uint32_t empty,
+                                            volatile int* abort_flag) {
+  using L = WinLayout<D, true>;
+  constexpr int kLanes = D / 32, kKeys = 32 / kLanes, kPasses = kWN / 2 / kKeys;
+  const int lane = threadIdx.x & 31, part = lane % kLanes, key = key0 + lane / kLanes;
+  const int last = it.pos0 + it.rows / p.G - 1, first = p.window < 0 ? 0 : it.pos0 - p.window;
+  // at d = 128 the lanes of the upper 64 channels take their chunks in another order: else two lanes of
+  // eight meet in a bank
+  const bool turn = D == 128 && (part & 2);
+  uint32_t to[4];  // (a pass is a multiple of eight keys: the swizzle is the same in each)
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    to[q] = (part >> 1) * kWSubKV + sw128(key, (part & 1) * 4 + (turn ? q ^ 2 : q));
+  for (int t = 0; t < it.n; ++t) {
+    const int rs = raw_slot<D>(t, v), s = t % slots;
+    if (!__all_sync(0xffffffffu,
+                    wait_bounded(raw_full + 8u * rs, raw_use<D>(t, v) & 1, abort_flag, p.status)))
+      break;
+    const uint8_t* src = raw + rs * L::kRawBytes;
+    uint4 codes[kPasses];
+    uint32_t scale[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      codes[i] = *reinterpret_cast<const uint4*>(src + (key + i * kKeys) * (D / 2) + part * 16);
+      scale[i] = *reinterpret_cast<const uint16_t*>(src + L::kRawCodes + (key + i * kKeys) * (D / 16) + part * 2);
+    }
+    const int t0 = it.key_step(t) * kWN;
+    if (t0 + kWN - 1 > last || t0 < first) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int k = t0 + key + i * kKeys;
+        if (k > last || (k < first && k >= p.sinks)) scale[i] = 0;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(raw_empty + 8u * rs);
+    if (t >= slots &&
+        !__all_sync(0xffffffffu, wait_bounded(empty + 8u * s, ((t / slots) - 1) & 1, abort_flag, p.status)))
+      break;
+    uint8_t* dst = ring + s * L::kStep;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t sa = fp4_scale_pair(turn ? scale[i] >> 8 : scale[i] & 0xffu);
+      const uint32_t sb = fp4_scale_pair(turn ? scale[i] & 0xffu : scale[i] >> 8);
+      const uint32_t w[4] = {turn ? codes[i].z : codes[i].x, turn ? codes[i].w : codes[i].y,
+                             turn ? codes[i].x : codes[i].z, turn ? codes[i].y : codes[i].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t x[4];
+        fp4_values8(w[q], q < 2 ? sa : sb, x);
+        *reinterpret_cast<uint4*>(dst + to[q] + i * kKeys * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -424,17 +484,18 @@ __device__ __forceinline__ bool win_wait(uint32_t bar, uint32_t parity, volatile
 // STREAM (paged): a cache that only one query tile reads is streamed through L2.  64 x 3-8 tokens over
 // 1k-32k (Hq=64 Hkv=8 d=128) 747 -> 736 us, 16 tokens over 32k 42.5 -> 39.2; an instantiation of its own,
 // since a choice at every copy costs long chunks 2.5%.
-// FP4 (paged): a 4-bit cache.  Both producer warps turn its codes into f16 operands, the softmax warps a bf16
-// query into f16 times a power of two a row; P is f16, of weights up to 2^15.
-template <int D, bool BF16, bool PAGED, bool STREAM = false, bool FP4 = false>
-__global__ void __launch_bounds__(two_threads(PAGED), 2)
+// KV (paged): where keys and values come from.  Over a 4-bit cache both products are f16: the softmax warps turn
+// a bf16 query into f16 times a power of two a row, and P is f16, of weights up to 2^15.
+template <int D, bool BF16, bool PAGED, bool STREAM = false, int KV = kKvRows>
+__global__ void __launch_bounds__(two_threads(PAGED, KV), 2)
     attn_fwd_two_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_o,
-                        const typename TwoOf<PAGED, FP4>::Params p) {
-  using L = WinLayout<D>;
+                        const typename TwoOf<PAGED, KV>::Params p) {
+  using L = WinLayout<D, KV == kKvCodes>;
   constexpr int KS = L::kKS, VS = L::kVS, NS = L::kNS;
+  constexpr bool FP4 = KV != kKvRows, CODES = KV == kKvCodes;
   constexpr bool kBfOps = BF16 && !FP4;            // operands of the products
   constexpr bool kTurnQ = BF16 && FP4;             // Q becomes f16 in place
   constexpr float kTop = FP4 ? kTwoTop : 0.0f;     // weights are 2^(x - m + kTop)
@@ -456,12 +517,15 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
 #define S_FREE(b) (bar_b + 8u * (7 + (b)))
   const uint32_t bar_drain_s = bar_b + 8u * 9;
   [[maybe_unused]] const uint32_t bar_ragged = bar_b + 8u * 10;
+  [[maybe_unused]] const uint32_t bar_turned = bar_b + 8u * 11;
+#define RAW_FULL(s) (bar_b + 8u * (12 + (s)))
+#define RAW_EMPTY(s) (bar_b + 8u * (12 + L::kRaw + (s)))
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  const typename TwoOf<PAGED, FP4>::Item it = two_item(static_cast<int>(blockIdx.x), p);
+  const typename TwoOf<PAGED, KV>::Item it = two_item(static_cast<int>(blockIdx.x), p);
   const int n = it.n;
   [[maybe_unused]] auto load_k = [&](int t) {
     mbar_arrive_expect_tx(K_FULL(t % KS), L::kStep);
@@ -484,11 +548,11 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     prefetch_tmap(&tm_v);
     mbar_init(bar_q, 1);
     for (int s = 0; s < KS; ++s) {
-      mbar_init(K_FULL(s), 1);
+      mbar_init(K_FULL(s), CODES ? kConvWarps / 2 : 1);
       mbar_init(K_EMPTY(s), 1);
     }
     for (int s = 0; s < VS; ++s) {
-      mbar_init(V_FULL(s), 1);
+      mbar_init(V_FULL(s), CODES ? kConvWarps / 2 : 1);
       mbar_init(V_EMPTY(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -499,7 +563,12 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     }
     mbar_init(bar_drain, 1);
     mbar_init(bar_drain_s, 1);
-    if constexpr (PAGED) mbar_init(bar_ragged, FP4 ? kWM : 1);  // (4 bits: Q in f16)
+    if constexpr (PAGED) mbar_init(bar_ragged, 1);
+    if constexpr (kTurnQ) mbar_init(bar_turned, kWM);
+    for (int u = 0; u < L::kRaw; ++u) {
+      mbar_init(RAW_FULL(u), 1);
+      mbar_init(RAW_EMPTY(u), kConvWarps / 2);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     if constexpr (!PAGED) {
@@ -516,8 +585,8 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
   }
   // paged: this lane's block-table entry of the next step
   [[maybe_unused]] int entry = -1;
-  if constexpr (PAGED) {
-    if ((warp == 4 || warp == 7) && n > 0) entry = page_entry(p, it, it.key_step(0), lane);
+  if constexpr (PAGED && KV != kKvCopy) {
+    if ((CODES ? warp == 7 : warp == 4 || warp == 7) && n > 0) entry = page_entry(p, it, it.key_step(0), lane);
   }
   if (warp == 5) {
     tmem_alloc(smem_u32(tmem_slot), kWTmemCols);
@@ -527,12 +596,24 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-
+  if (CODES && warp >= 8) {
+    // ----------------------------------------------------------------- codes to operands
+    if constexpr (CODES) {
+      if (n > 0) {
+        const int v = (warp - 8) >> 1;  // two warps for K, two for V
+        two_convert<D>(p, it, v, (warp & 1) * (kWN / 2), gbase + L::kRawAt, RAW_FULL(0), RAW_EMPTY(0),
+                       gbase + (v ? L::kV : L::kK), v ? VS : KS, v ? V_FULL(0) : K_FULL(0),
+                       v ? V_EMPTY(0) : K_EMPTY(0), abort_flag);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+  if constexpr (CODES) setmaxnreg_dec<kRegsTwoIssue>();
   if (warp == 4) {
     // ------------------------------------------------- TMA producer (paged: of Q and K)
     if constexpr (PAGED) {
       if (n > 0) {
-        const PageBox box(p.page_log2);
+        const PageBox box(KV == kKvCopy ? 6 : p.page_log2);
         // Rows of the query tile that no token fills stay zero.
         const int rows_filled = p.tile_tokens * p.G;
         for (int i = lane; i < (kWM - rows_filled) * (D / 8); i += 32) {
@@ -548,17 +629,20 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
           for (int sub = 0; sub < D / 64; ++sub)
             tma_load_3d(base + sub * kWSubQ, &tm_q, bar_q, sub * 64, it.kv_plane * p.G, it.tok0);
         }
-        if constexpr (FP4) {
-          two_convert<D, STREAM>(p.k_codes, p.k_scales, p, it, entry, gbase + L::kK, L::kStep, KS, K_FULL(0),
-                                 K_EMPTY(0), abort_flag, true);
+        if constexpr (CODES) {  // (only Q is the producer's)
           if (lane == 0) wait_bounded(bar_q, 0, nullptr, p.status, kWDrainNs);
         } else {
           [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
           int issued = 0;
           for (int t = 0; t < n; ++t) {
             const int s = t % KS;
-            const int row = page_row(p, it, it.key_step(t), lane, entry, true);
-            if (t + 1 < n) entry = page_entry(p, it, it.key_step(t + 1), lane);
+            int row;
+            if constexpr (KV == kKvCopy) {
+              row = copy_row(p, it, it.key_step(t), lane);
+            } else {
+              row = page_row(p, it, it.key_step(t), lane, entry, true);
+              if (t + 1 < n) entry = page_entry(p, it, it.key_step(t + 1), lane);
+            }
             bool ok = true;
             if (lane == 0 && t >= KS)
               ok = wait_bounded(K_EMPTY(s), ((t / KS) - 1) & 1, abort_flag, p.status);
@@ -606,7 +690,7 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     if (lane == 0 && n > 0) {
       constexpr uint32_t idesc_qk = make_idesc_f16(kBfOps, kWM, kWN, false);
       const uint64_t q_desc = make_sdesc_sw128(base, 16, 1024);
-      if (wait_bounded(kTurnQ ? bar_ragged : bar_q, 0, abort_flag, p.status)) {
+      if (wait_bounded(kTurnQ ? bar_turned : bar_q, 0, abort_flag, p.status)) {
         for (int t = 0; t < n; ++t) {  // S_t into buffer t % NS, once S_{t-NS} has been read
           const int s = t % KS, b = t % NS;
           if (!wait_bounded(K_FULL(s), (t / KS) & 1, abort_flag, p.status)) break;
@@ -627,63 +711,66 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     }
     __syncwarp();
   } else if (PAGED && warp == 7) {
-    // ----------------------------------------------------------------- V producer (paged)
-    if constexpr (PAGED) {
+    // ----------------------------------------------------------------- V producer (paged), or of codes
+    if constexpr (CODES) {
+      if (n > 0)
+        two_load_codes<D, STREAM>(p, it, entry, base + L::kRawAt, RAW_FULL(0), RAW_EMPTY(0), abort_flag);
+    } else if constexpr (PAGED) {
       if (n > 0) {
-        if constexpr (FP4) {
-          two_convert<D, STREAM>(p.v_codes, p.v_scales, p, it, entry, gbase + L::kV, L::kStep, VS, V_FULL(0),
-                                 V_EMPTY(0), abort_flag, false);
-        } else {
-          const PageBox box(p.page_log2);
-          int issued = 0;
-          [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
-          uint32_t ragged = 0;  // ragged steps so far
-          for (int t = 0; t < n; ++t) {
-            const int s = t % VS, j = it.key_step(t);
-            const int row = page_row(p, it, j, lane, entry, false);
+        const PageBox box(KV == kKvCopy ? 6 : p.page_log2);
+        int issued = 0;
+        [[maybe_unused]] const uint64_t policy = STREAM ? l2_policy_evict_first() : 0;
+        uint32_t ragged = 0;  // ragged steps so far
+        for (int t = 0; t < n; ++t) {
+          const int s = t % VS, j = it.key_step(t);
+          int row;
+          if constexpr (KV == kKvCopy) {
+            row = copy_row(p, it, j, lane);
+          } else {
+            row = page_row(p, it, j, lane, entry, false);
             if (t + 1 < n) entry = page_entry(p, it, it.key_step(t + 1), lane);
-            bool ok = true;
-            if (lane == 0 && t >= VS)
-              ok = wait_bounded(V_EMPTY(s), ((t / VS) - 1) & 1, abort_flag, p.status);
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-            // The step that holds the sequence's end: its rows past the end hold other sequences' or
-            // unwritten tokens, or were not loaded at all.  P is zero there, but 0 * V has to stay 0:
-            // the rows are cleared once the loads have landed, and only then is the step handed on.  The
-            // same for pages that could not be loaded.
-            const uint32_t loaded = __ballot_sync(0xffffffffu, row >= 0);
-            const uint32_t bytes = __popc(loaded) * box.rows * D * 2;
-            const int valid = it.len - j * kWN;  // rows of the step that hold tokens
-            const bool clear = valid < kWN || bytes < L::kStep;
-            const uint32_t bar = clear ? bar_ragged : V_FULL(s);
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-            __syncwarp();
-            if (row >= 0) {
-  #pragma unroll
-              for (int sub = 0; sub < D / 64; ++sub)
-                load_page<STREAM>(base + L::kV + s * L::kStep + sub * kWSubKV + lane * box.rows * 128, &tm_v, bar,
-                          sub * 64, it.kv_plane, row, policy);
-            }
-            if (clear) {
-              if (!win_wait(bar, ragged & 1, abort_flag, p.status)) break;
-              ++ragged;
-              for (int i = lane; i < kWN * (D / 8); i += 32) {
-                const int rr = i / (D / 8), c = i % (D / 8);
-                if (rr >= valid || !((loaded >> (rr >> box.log2)) & 1u))
-                  *reinterpret_cast<uint4*>(gbase + L::kV + s * L::kStep + (c >> 3) * kWSubKV + rr * 128 +
-                                            (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(V_FULL(s));
-            }
-            issued = t + 1;
           }
-          // loads that nothing waited for land before the block may exit (an aborted ragged step's wait
-          // has already taken its limit)
-          if (lane == 0)
-            for (int t = (issued > VS ? issued - VS : 0); t < issued; ++t)
-              wait_bounded(V_FULL(t % VS), (t / VS) & 1, nullptr, p.status, kWDrainNs);
+          bool ok = true;
+          if (lane == 0 && t >= VS)
+            ok = wait_bounded(V_EMPTY(s), ((t / VS) - 1) & 1, abort_flag, p.status);
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          // The step that holds the sequence's end: its rows past the end hold other sequences' or
+          // unwritten tokens, or were not loaded at all.  P is zero there, but 0 * V has to stay 0:
+          // the rows are cleared once the loads have landed, and only then is the step handed on.  The
+          // same for pages that could not be loaded.
+          const uint32_t loaded = __ballot_sync(0xffffffffu, row >= 0);
+          const uint32_t bytes = __popc(loaded) * box.rows * D * 2;
+          const int valid = it.len - j * kWN;  // rows of the step that hold tokens
+          const bool clear = valid < kWN || bytes < L::kStep;
+          const uint32_t bar = clear ? bar_ragged : V_FULL(s);
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (row >= 0) {
+#pragma unroll
+            for (int sub = 0; sub < D / 64; ++sub)
+              load_page<STREAM>(base + L::kV + s * L::kStep + sub * kWSubKV + lane * box.rows * 128, &tm_v, bar,
+                        sub * 64, it.kv_plane, row, policy);
+          }
+          if (clear) {
+            if (!win_wait(bar, ragged & 1, abort_flag, p.status)) break;
+            ++ragged;
+            for (int i = lane; i < kWN * (D / 8); i += 32) {
+              const int rr = i / (D / 8), c = i % (D / 8);
+              if (rr >= valid || !((loaded >> (rr >> box.log2)) & 1u))
+                *reinterpret_cast<uint4*>(gbase + L::kV + s * L::kStep + (c >> 3) * kWSubKV + rr * 128 +
+                                          (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(V_FULL(s));
+          }
+          issued = t + 1;
         }
+        // loads that nothing waited for land before the block may exit (an aborted ragged step's wait
+        // has already taken its limit)
+        if (lane == 0)
+          for (int t = (issued > VS ? issued - VS : 0); t < issued; ++t)
+            wait_bounded(V_FULL(t % VS), (t / VS) & 1, nullptr, p.status, kWDrainNs);
       }
     }
     __syncwarp();
@@ -709,8 +796,10 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
       wait_bounded(bar_drain, 0, nullptr, p.status, kWDrainNs);
     }
     __syncwarp();
+  }
   } else {
     // ----------------------------------------------------------------- softmax + epilogue
+    if constexpr (CODES) setmaxnreg_inc<kRegsTwoSoftmax>();
     const int r = warp * 32 + lane;
     const uint32_t row_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     [[maybe_unused]] float sl2_row = p.sl2;
@@ -721,7 +810,7 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
         if (ok) {
           sl2_row *= two_turn_q<D>(gbase, r);
           fence_proxy_async_smem();
-          mbar_arrive(bar_ragged);
+          mbar_arrive(bar_turned);
         }
       }
     }
@@ -732,6 +821,20 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
     const size_t row_index = store ? two_row(it, p, r) : 0;  // of o and lse
     float m = -INFINITY, l = 0.0f;
     [[maybe_unused]] float m_raw = -INFINITY;
+    if constexpr (CODES) {
+      if (warp * 32 >= it.rows) {
+        // none of this warp's rows exists (a few tokens fill part of a tile): whatever P holds there only
+        // reaches its own rows, which are not stored
+        for (int t = 0; ok && t < n; ++t) {
+          ok = win_wait(S_FULL(t % NS), (t / NS) & 1, abort_flag, p.status);
+          if (ok) {
+            mbar_arrive(S_FREE(t % NS));
+            mbar_arrive(P_READY(t & 1));
+          }
+        }
+        ok = false;  // and nothing to write
+      }
+    }
     for (int t = 0; ok && t < n; ++t) {
       const int j = it.key_step(t);
       const int b = t & 1;
@@ -932,6 +1035,8 @@ __global__ void __launch_bounds__(two_threads(PAGED), 2)
 #undef P_READY
 #undef PV_DONE
 #undef S_FREE
+#undef RAW_FULL
+#undef RAW_EMPTY
   tc_fence_before();
   __syncthreads();
   if (warp == 5) {

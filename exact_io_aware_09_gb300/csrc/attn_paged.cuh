@@ -50,24 +50,27 @@ inline PagedSplit paged_split(int B, int Hq, int Hkv, int max_q, int max_k, int 
   return s;
 }
 
-// The chunk over a 16-bit cache, or (FP4) over the 4-bit cache c.
-template <int D, bool BF16, bool FP4>
-static int launch_paged_variant(const PagedArgs& a, const CacheFp4* c, cudaStream_t stream) {
-  using L = WinLayout<D>;
+// The chunk over a 16-bit cache (kKvRows), over a 4-bit cache's codes c (kKvCodes) or over its f16 copy
+// (kKvCopy: a.k_pages and v_pages [B, copy_rows, Hkv, d]).
+template <int D, bool BF16, int KV>
+static int launch_paged_variant(const PagedArgs& a, const CacheFp4* c, int copy_rows, cudaStream_t stream) {
+  using L = WinLayout<D, KV == kKvCodes>;
   const PagedSplit sp = paged_split(a.B, a.Hq, a.Hkv, a.max_q, a.max_k, a.window, a.sinks, D);
   const int G = a.Hq / a.Hkv;
   const uint64_t row = static_cast<uint64_t>(D) * 2;
-  const uint64_t tokens = static_cast<uint64_t>(a.num_pages) * a.page_size;
-  const uint32_t box = static_cast<uint32_t>(a.page_size < kWN ? a.page_size : kWN);
+  const bool copy = KV == kKvCopy;
+  const uint64_t tokens = copy ? static_cast<uint64_t>(a.B) * copy_rows
+                               : static_cast<uint64_t>(a.num_pages) * a.page_size;
+  const uint32_t box = static_cast<uint32_t>(a.page_size < kWN && !copy ? a.page_size : kWN);
   CUtensorMap tq, tk = {}, tv = {}, to;
   if (!make_tmap_3d(&tq, a.q, BF16, D, a.Hq, a.total_q, row, row * a.Hq, 64, G, sp.tile_tokens) ||
       !make_tmap_3d(&to, a.o, BF16, D, a.Hq, a.total_q, row, row * a.Hq, 64, G, sp.tile_tokens))
     return -5;
-  if (!FP4 &&
-      (!make_tmap_3d(&tk, a.k_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box) ||
-       !make_tmap_3d(&tv, a.v_pages, BF16, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box)))
+  if (KV != kKvCodes &&
+      (!make_tmap_3d(&tk, a.k_pages, BF16 && !copy, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box) ||
+       !make_tmap_3d(&tv, a.v_pages, BF16 && !copy, D, a.Hkv, tokens, row, row * a.Hkv, 64, 1, box)))
     return -5;
-  typename TwoOf<true, FP4>::Params p = {};
+  typename TwoOf<true, KV>::Params p = {};
   p.o = a.o;
   p.lse = a.lse;
   p.status = device_status_ptr();
@@ -83,7 +86,7 @@ static int launch_paged_variant(const PagedArgs& a, const CacheFp4* c, cudaStrea
   p.BH = static_cast<int>(planes);
   {
     // planes whose cache fills about half of L2 walk their query tiles together
-    uint64_t group = (64ull << 20) / (2ull * a.max_k * (FP4 ? D / 2 + D / 16 : D * 2));
+    uint64_t group = (64ull << 20) / (2ull * a.max_k * (KV == kKvCodes ? D / 2 + D / 16 : D * 2));
     if (group < 1) group = 1;
     if (group > planes) group = planes;
     p.head_group = static_cast<int>(group);
@@ -102,20 +105,23 @@ static int launch_paged_variant(const PagedArgs& a, const CacheFp4* c, cudaStrea
   p.n_splits = sp.n_splits;
   p.split_steps = sp.split_steps;
   if (sp.n_splits > 1) paged_parts(a, D, sp.n_splits, p.ws_o, p.ws_ml);
-  if constexpr (FP4) {
+  if constexpr (KV == kKvCodes) {
     p.k_codes = c->k_codes;
     p.v_codes = c->v_codes;
     p.k_scales = c->k_scales;
     p.v_scales = c->v_scales;
   }
-  auto kern = sp.n_qtiles == 1 ? attn_fwd_two_kernel<D, BF16, true, true, FP4>
-                               : attn_fwd_two_kernel<D, BF16, true, false, FP4>;
+  if constexpr (KV == kKvCopy) p.copy_rows = copy_rows;
+  auto kern = attn_fwd_two_kernel<D, BF16, true, false, KV>;
+  if constexpr (KV != kKvCopy) {
+    if (sp.n_qtiles == 1) kern = attn_fwd_two_kernel<D, BF16, true, true, KV>;
+  }
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
       cudaSuccess)
     return -5;
   const uint64_t blocks = planes * sp.n_qtiles * sp.n_splits;
   if (blocks > 0x7fffffffull) return -2;
-  kern<<<static_cast<unsigned>(blocks), two_threads(true), L::kBytes, stream>>>(tq, tk, tv, to, p);
+  kern<<<static_cast<unsigned>(blocks), two_threads(true, KV), L::kBytes, stream>>>(tq, tk, tv, to, p);
   if (cudaGetLastError() != cudaSuccess) return -5;
   return sp.n_splits == 1 ? 0 : launch_paged_merge(a, sp.n_splits, stream);
 }

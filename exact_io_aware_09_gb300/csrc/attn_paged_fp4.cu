@@ -548,11 +548,9 @@ size_t paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q,
                                  int sinks, int d) {
   if (total_q <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || max_q <= 0 || max_k <= 0 || d <= 0) return 0;
   const int G = Hq / Hkv;
+  if (!few_rows(max_q, G))
+    return G <= 128 ? fp4_chunk_workspace_bytes(total_q, B, Hq, Hkv, max_q, max_k, window, sinks, d) : 0;
   int n_splits, stages;
-  if (!few_rows(max_q, G)) {
-    n_splits = G <= 128 ? fp4_chunk_splits(B, Hq, Hkv, max_q, max_k, window, sinks, d) : 1;
-    return n_splits == 1 ? 0 : paged_parts_bytes(total_q, Hq, n_splits, d);
-  }
   few_split(B, Hkv, G, max_q, max_k, window, sinks, d, n_splits, stages);
   return n_splits <= kMaxCluster ? 0 : paged_parts_bytes(total_q, Hq, n_splits, d);
 }

@@ -225,9 +225,10 @@ int launch_cache_read_fp4(const CacheFp4& c, void* k, void* v, const int32_t* cu
 // Attention over a 4-bit cache (attn_paged_fp4.cu); a.k_pages and v_pages are not used, a.cu_q == null: one
 // token of each sequence, which may have none in the cache.
 int launch_attn_paged_fp4(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream);
-// ... with more than 16 rows per key/value head (attn_paged_fp4_chunk.cu), and its key splits.
+// ... with more than 16 rows per key/value head (attn_paged_fp4_chunk.cu), and its workspace.
 int launch_attn_fp4_chunk(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream);
-int fp4_chunk_splits(int B, int Hq, int Hkv, int max_q, int max_k, int window, int sinks, int d);
+size_t fp4_chunk_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
+                                 int sinks, int d);
 size_t paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, int max_q, int max_k, int window,
                                  int sinks, int d);
 // Page lists (attn_pages.cu): lengths is cu_seqlens_q of an extension, the kept lengths of a trim, which
