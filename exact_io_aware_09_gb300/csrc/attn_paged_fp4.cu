@@ -13,8 +13,7 @@
 // 16-byte load holds its operands of several steps, and channels D/8 g .. of its values, so that their
 // scale is one byte a token.  Values meet the second product as pairs of tokens: the low four bits of two
 // tokens' bytes side by side in one, and the high ones, which convert as pairs.  The pool's order (a
-// head's rows of a page side by side) makes a page's rows one contiguous copy.  Scale bytes come straight to
-// registers two stages ahead and reach their lanes through a few bytes of shared memory of the warp's own.
+// head's rows of a page side by side) makes a page's codes one contiguous copy, and its scale bytes another.
 // A token that no row sees gets a value scale of zero, which makes its values zeros whatever they hold.
 #include "attn_decode.cuh"
 #include "attn_rows.cuh"
@@ -25,9 +24,11 @@ namespace attn {
 namespace {
 
 constexpr int kFew4Rows = 16;
-constexpr int kFew4Stages = 6;                  // of the ring
-constexpr int kFew4MaxStages = 2048 / kDecTok;  // of a split (row_split_tokens)
-constexpr float kRise = 8.0f, kTop = 7.0f;
+constexpr int kFew4Tok = 128;                    // tokens of a stage, 32 of each compute warp
+constexpr int kFew4Groups = kFew4Tok / 16 / kDecWarps;
+constexpr int kFew4Stages = 4;                   // of the ring
+constexpr int kFew4MaxStages = 2048 / kFew4Tok;  // of a split (row_split_tokens)
+constexpr float kRise = 8.0f, kTop = 7.0f, kNone = 3.0e38f;
 
 struct Few4Params {
   const uint16_t* q;  // [total_q, Hq, D]
@@ -50,21 +51,55 @@ struct Few4Params {
 template <int D, int NT>
 struct Few4Layout {
   static constexpr int kMaxR = NT * 8;
-  static constexpr uint32_t kTensor = kDecTok * D / 2;  // codes of K or V of one stage
-  static constexpr uint32_t kStage = 2 * kTensor;
+  static constexpr uint32_t kTensor = kFew4Tok * D / 2;   // codes of K or V of one stage
+  static constexpr uint32_t kScales = kFew4Tok * D / 16;  // and scale bytes
+  static constexpr uint32_t kStage = 2 * (kTensor + kScales);
   static constexpr uint32_t kRing = kFew4Stages * kStage;
   static constexpr uint32_t kRed = kDecWarps * kMaxR * (D + 2) * 4;  // reuses the ring
   static constexpr uint32_t kFin = kRed;
   static_assert(kFin + kMaxR * (D + 2) * 4 <= kRing, "merge scratch must fit in the ring");
-  static constexpr uint32_t kScale = kRing;  // [warp][K's 16 tokens, V's][D / 16]
-  static constexpr uint32_t kBar = kScale + kDecWarps * 32 * (D / 16);
+  static constexpr uint32_t kBar = (kRing + 7) / 8 * 8;
   static constexpr uint32_t kMisc = kBar + 2 * kFew4Stages * 8;
   static constexpr uint32_t kPages = kMisc + 16;  // the split's pages, box by box, or -1
-  static constexpr uint32_t kBytes = kPages + kFew4MaxStages * 4 * 4 + 1024;
+  static constexpr uint32_t kBytes = kPages + kFew4MaxStages * (kFew4Tok / 16) * 4 + 1024;
 };
 
 // Blocks that share an SM, by registers.
-constexpr int few4_blocks_per_sm(int d, int nt) { return nt == 1 ? 4 : d == 64 ? 3 : 2; }
+constexpr int few4_blocks_per_sm(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) : d == 64 ? 3 : 2; }
+
+template <typename T>
+__device__ __forceinline__ T lds(uint32_t addr);
+template <>
+__device__ __forceinline__ uint32_t lds<uint32_t>(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+template <>
+__device__ __forceinline__ uint2 lds<uint2>(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+template <>
+__device__ __forceinline__ uint4 lds<uint4>(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+// One byte and two, zero extended.
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 
 // Byte offset of 16-byte chunk `chunk` of a stage's row: D/2-byte rows in the swizzle of that width
 // (address bits 4-5 exclusive-ored with bits 7-8, at d = 64 bit 4 with bit 7).
@@ -76,12 +111,15 @@ __device__ __forceinline__ uint32_t code4_off(int row, int chunk) {
 
 }  // namespace
 
-// A warp's query rows and state and its work on sixteen tokens; o and l count in units of 2^(m - kTop).
+// A warp's query rows and state and its work on sixteen tokens; o and l count in units of 2^(m - kTop), and
+// a score's weight is 2^(x + shift), shift = kTop - m (kNone before the first key: any score is above it, and
+// one of -inf has no weight).
 template <int D, bool BF16, int NT>
 struct Few4Warp : RowState<D, NT, false> {
   static constexpr int kB = D / kFp4Block;  // scale bytes of a row
   uint32_t qf[NT][D / 16][2];
   float f[NT][2];  // factors of the rows' products
+  float shift[NT][2];
 
   // row(r): query row r < rows
   template <typename F>
@@ -116,134 +154,168 @@ struct Few4Warp : RowState<D, NT, false> {
       }
       f[n][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
       f[n][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+      shift[n][0] = shift[n][1] = kNone;
     }
   }
 
-  // Stage rows w0 .. w0 + 15, whose scale bytes are sc[0 .. 15] (keys) and sc[16 .. 31] (values).
-  // see(n, k, r): whether row 2c + r of tile n sees key g + 8k; asked only where `edge`.
-  template <typename F>
-  __device__ __forceinline__ void tokens(const uint8_t* kbuf, const uint8_t* vbuf, const uint8_t* sc, int w0,
-                                         bool edge, F see, int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    float acc[NT][4] = {};
-    constexpr int kW = D / 32;  // words of a thread's keys' channels: eight codes each
-    uint32_t wa[kW], wb[kW];
-    if constexpr (D == 128) {
-      *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(kbuf + code4_off<D>(w0 + g, c));
-      *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(kbuf + code4_off<D>(w0 + g + 8, c));
-    } else {
-      *reinterpret_cast<uint2*>(wa) =
-          *reinterpret_cast<const uint2*>(kbuf + code4_off<D>(w0 + g, c >> 1) + (c & 1) * 8);
-      *reinterpret_cast<uint2*>(wb) =
-          *reinterpret_cast<const uint2*>(kbuf + code4_off<D>(w0 + g + 8, c >> 1) + (c & 1) * 8);
+  // Places of this thread's operands in a stage, from the warp's first token: key g and, eight rows on, key
+  // g + 8; value tokens 2c and 2c + 1 in the thread's order and those eight rows on (the swizzles do not
+  // change over eight rows); their scale bytes.
+  uint32_t k_at, v_at[2], ks_at, vs_at[2];
+
+  __device__ __forceinline__ void places(int warp, int lane) {
+    using L = Few4Layout<D, NT>;
+    const int g = lane >> 2, c = lane & 3, w0 = warp * 16 * kFew4Groups;
+    k_at = D == 128 ? code4_off<D>(w0 + g, c) : code4_off<D>(w0 + g, c >> 1) + (c & 1) * 8;
+    ks_at = 2 * L::kTensor + (w0 + g) * kB + c * (kB / 4);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = w0 + 2 * c + (r ^ swap(c));
+      v_at[r] = L::kTensor + code4_off<D>(row, D == 128 ? g >> 1 : g >> 2) + (D == 128 ? (g & 1) * 8 : (g & 3) * 4);
+      vs_at[r] = 2 * L::kTensor + L::kScales + row * kB + (D == 128 ? g : g >> 1);
     }
-    uint32_t sa[kB / 4], sb[kB / 4];  // f16 pairs of this thread's blocks of keys g and g + 8
+  }
+  // Token pairs are taken in the order that keeps the values' loads free of bank conflicts: a thread whose
+  // `swap` is set has its pairs the other way round, of the weights too.
+  static __device__ __forceinline__ int swap(int c) { return D == 128 ? c & 1 : c >> 1; }
+
+  // The warp's tokens of the stage at shared address `stage`, in groups of sixteen.  Where `edge`:
+  // see(i, n, k, r), whether row 2c + r of tile n sees key g + 8k of group i, and some(t), whether any row
+  // sees the warp's token t.
+  template <typename F, typename S>
+  __device__ __forceinline__ void tokens(uint32_t stage, bool edge, F see, S some, int lane) {
+    constexpr uint32_t kRow8 = 8 * D / 2, kS8 = 8 * kB;  // eight rows of codes, of scale bytes
+    const int c = lane & 3;
+    float x[kFew4Groups][NT][2][2];
 #pragma unroll
-    for (int i = 0; i < kB / 4; ++i) {
-      sa[i] = fp4_scale_pair(sc[g * kB + c * (kB / 4) + i]);
-      sb[i] = fp4_scale_pair(sc[(g + 8) * kB + c * (kB / 4) + i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      uint32_t a[4], b[4];
-      fp4_values8(wa[i], sa[i / 2], a);
-      fp4_values8(wb[i], sb[i / 2], b);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t ab[4] = {a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma_m16n8k16<false>(acc[n], ab, qf[n][2 * i + h][0], qf[n][2 * i + h][1]);
+    for (int gr = 0; gr < kFew4Groups; ++gr) {
+      float acc[NT][4] = {};
+      constexpr int kW = D / 32;  // words of a thread's keys' channels: eight codes each
+      uint32_t wa[kW], wb[kW], sa[kB / 4], sb[kB / 4];
+      const uint32_t at = stage + k_at + 2 * gr * kRow8, s_at = stage + ks_at + 2 * gr * kS8;
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint4*>(wa) = lds<uint4>(at);
+        *reinterpret_cast<uint4*>(wb) = lds<uint4>(at + kRow8);
+        const uint32_t a = lds16(s_at), b = lds16(s_at + kS8);
+        sa[0] = fp4_scale_pair(a & 0xffu);
+        sa[1] = fp4_scale_pair(a >> 8);
+        sb[0] = fp4_scale_pair(b & 0xffu);
+        sb[1] = fp4_scale_pair(b >> 8);
+      } else {
+        *reinterpret_cast<uint2*>(wa) = lds<uint2>(at);
+        *reinterpret_cast<uint2*>(wb) = lds<uint2>(at + kRow8);
+        sa[0] = fp4_scale_pair(lds8(s_at));
+        sb[0] = fp4_scale_pair(lds8(s_at + kS8));
       }
-    }
-    float x[NT][2][2];
-    bool rise = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < kW; ++i) {
+        uint32_t a[4], b[4];
+        fp4_values8(wa[i], sa[i / 2], a);
+        fp4_values8(wb[i], sb[i / 2], b);
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t ab[4] = {a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1]};
 #pragma unroll
-        for (int r = 0; r < 2; ++r) x[n][k][r] = acc[n][2 * k + r] * f[n][r];
-    if (edge) {
+          for (int n = 0; n < NT; ++n)
+            mma_m16n8k16<false>(acc[n], ab, qf[n][2 * i + h][0], qf[n][2 * i + h][1]);
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            if (!see(n, k, r)) x[n][k][r] = -INFINITY;
+          for (int r = 0; r < 2; ++r) x[gr][n][k][r] = acc[n][2 * k + r] * f[n][r];
     }
+    if (edge) {
+#pragma unroll
+      for (int gr = 0; gr < kFew4Groups; ++gr)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (!see(gr, n, k, r)) x[gr][n][k][r] = -INFINITY;
+    }
+    bool rise = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        rise = rise || fmaxf(x[n][0][r], x[n][1][r]) > this->m[n][r] + kRise;
-    if (__any_sync(0xffffffffu, rise)) raise(x);
-    // Token pairs are taken in the order that keeps the values' loads free of bank conflicts: a thread
-    // whose `swap` is set has its pairs the other way round, of the weights too.
-    const int swap = D == 128 ? c & 1 : c >> 1;
-    uint32_t pb[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float w[2][2];
-#pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float shift = this->m[n][r] == -INFINITY ? 0.0f : kTop - this->m[n][r];
+        float top = fmaxf(x[0][n][0][r], x[0][n][1][r]);
+#pragma unroll
+        for (int gr = 1; gr < kFew4Groups; ++gr) top = max3f(top, x[gr][n][0][r], x[gr][n][1][r]);
+        rise = rise || top + shift[n][r] > kRise + kTop;
+      }
+    if (__any_sync(0xffffffffu, rise)) raise(x);
+#pragma unroll
+    for (int gr = 0; gr < kFew4Groups; ++gr) {
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float w[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            w[k][r] = ex2(x[gr][n][k][r] + shift[n][r]);
+            this->l[n][r] += w[k][r];
+          }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          w[k][r] = ex2(x[n][k][r] + shift);
-          this->l[n][r] += w[k][r];
+          const uint32_t t = transpose_8x8(pack2<false>(w[k][0], w[k][1]));
+          pb[n][k] = __byte_perm(t, t, swap(c) ? 0x1032 : 0x3210);
         }
       }
+      constexpr int kV = D / 64;  // words of a thread's channels of one token
+      uint32_t v[4][kV], by[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t t = transpose_8x8(pack2<false>(w[k][0], w[k][1]));
-        pb[n][k] = __byte_perm(t, t, swap ? 0x1032 : 0x3210);
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t at = stage + v_at[r & 1] + (2 * gr + (r >> 1)) * kRow8;
+        if constexpr (D == 128)
+          *reinterpret_cast<uint2*>(v[r]) = lds<uint2>(at);
+        else
+          v[r][0] = lds<uint32_t>(at);
+        by[r] = lds8(stage + vs_at[r & 1] + (2 * gr + (r >> 1)) * kS8);
       }
-    }
-    constexpr int kV = D / 64;  // words of a thread's channels of one token
-    uint32_t v[4][kV], sv[2];
-    uint32_t by[4];
+      if (edge) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int tok = (r >> 1) * 8 + 2 * c + ((r & 1) ^ swap);
-      const uint8_t* src = vbuf + code4_off<D>(w0 + tok, D == 128 ? g >> 1 : g >> 2);
-      if constexpr (D == 128)
-        *reinterpret_cast<uint2*>(v[r]) = *reinterpret_cast<const uint2*>(src + (g & 1) * 8);
-      else
-        v[r][0] = *reinterpret_cast<const uint32_t*>(src + (g & 3) * 4);
-      by[r] = sc[(16 + tok) * kB + (D == 128 ? g : g >> 1)];
-    }
-    sv[0] = fp4_scale_pair(by[0], by[1]);
-    sv[1] = fp4_scale_pair(by[2], by[3]);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      // byte t: the codes of channel 2t of two tokens (even), of channel 2t + 1 (odd)
-      constexpr uint32_t kLow = 0x0f0f0f0fu;
-      uint32_t ev[2][4], od[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t u0 = v[2 * h][i], u1 = v[2 * h + 1][i];
-        fp4_values8((u0 & kLow) | ((u1 << 4) & ~kLow), sv[h], ev[h]);
-        fp4_values8(((u0 >> 4) & kLow) | (u1 & ~kLow), sv[h], od[h]);
+        for (int r = 0; r < 4; ++r)
+          if (!some(gr * 16 + (r >> 1) * 8 + 2 * c + ((r & 1) ^ swap(c)))) by[r] = 0;
       }
+      const uint32_t sv[2] = {fp4_scale_pair(by[0], by[1]), fp4_scale_pair(by[2], by[3])};
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t av[4] = {ev[0][t], od[0][t], ev[1][t], od[1][t]};
+      for (int i = 0; i < kV; ++i) {
+        // byte t: the codes of channel 2t of two tokens (even), of channel 2t + 1 (odd)
+        constexpr uint32_t kLow = 0x0f0f0f0fu;
+        uint32_t ev[2][4], od[2][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_m16n8k16<false>(this->o[n][i * 4 + t], av, pb[n][0], pb[n][1]);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t u0 = v[2 * h][i], u1 = v[2 * h + 1][i];
+          fp4_values8((u0 & kLow) | ((u1 << 4) & ~kLow), sv[h], ev[h]);
+          fp4_values8(((u0 >> 4) & kLow) | (u1 & ~kLow), sv[h], od[h]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t av[4] = {ev[0][t], od[0][t], ev[1][t], od[1][t]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_m16n8k16<false>(this->o[n][i * 4 + t], av, pb[n][0], pb[n][1]);
+        }
       }
     }
   }
 
   // Raises m to the largest x where that exceeds it by more than 2^kRise.
-  __device__ __forceinline__ void raise(const float (&x)[NT][2][2]) {
+  __device__ __forceinline__ void raise(const float (&x)[kFew4Groups][NT][2][2]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float a[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(x[n][0][r], x[n][1][r]);
+        float mx = fmaxf(x[0][n][0][r], x[0][n][1][r]);
+#pragma unroll
+        for (int gr = 1; gr < kFew4Groups; ++gr) mx = max3f(mx, x[gr][n][0][r], x[gr][n][1][r]);
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
         float& m = this->m[n][r];
@@ -252,6 +324,7 @@ struct Few4Warp : RowState<D, NT, false> {
           a[r] = (m == -INFINITY) ? 0.f : ex2(m - mx);
           m = mx;
         }
+        shift[n][r] = (m == -INFINITY) ? kNone : kTop - m;
         this->l[n][r] *= a[r];
       }
 #pragma unroll
@@ -296,15 +369,15 @@ __global__ void __launch_bounds__(kDecThreads, few4_blocks_per_sm(D, NT))
   if (n == 0) return;
   const int rows = n * p.G;
   const int pos0 = len - n;  // (-1: an empty cache, whose row sees no key)
-  // 64-key stages of the visible keys: `sink_st` of them from key 0, then from stage w_begin on
-  const int w_begin = p.window < 0 ? 0 : max(pos0 - p.window, 0) / kDecTok;
-  const int sink_st = p.window < 0 ? 0 : min((min(p.sinks, len) + kDecTok - 1) / kDecTok, w_begin);
-  const int all = sink_st + (len + kDecTok - 1) / kDecTok - w_begin;
+  // stages of the visible keys: `sink_st` of them from key 0, then from stage w_begin on
+  const int w_begin = p.window < 0 ? 0 : max(pos0 - p.window, 0) / kFew4Tok;
+  const int sink_st = p.window < 0 ? 0 : min((min(p.sinks, len) + kFew4Tok - 1) / kFew4Tok, w_begin);
+  const int all = sink_st + (len + kFew4Tok - 1) / kFew4Tok - w_begin;
   const int i0 = split * p.split_stages;
   const int n_stages = min(max(all - i0, 0), p.split_stages);
   auto stage_token = [&](int st) {
     const int i = i0 + st;
-    return (i < sink_st ? i : w_begin + i - sink_st) * kDecTok;
+    return (i < sink_st ? i : w_begin + i - sink_st) * kFew4Tok;
   };
   auto out_row = [&](int row) {
     const int t = row / p.G;
@@ -336,8 +409,10 @@ __global__ void __launch_bounds__(kDecThreads, few4_blocks_per_sm(D, NT))
     *abort_flag = 0;
     fence_barrier_init();
   }
-  // pages of the split, as boxes of a page's rows (64 of them where it has more)
-  const int box_log2 = min(p.page_log2, 6), box = 1 << box_log2, pg_log2 = 6 - box_log2;
+  // pages of the split, as boxes of a page's rows (a stage's where it has more)
+  constexpr int kTokLog2 = 7;
+  static_assert(1 << kTokLog2 == kFew4Tok, "tokens of a stage");
+  const int box_log2 = min(p.page_log2, kTokLog2), box = 1 << box_log2, pg_log2 = kTokLog2 - box_log2;
   int* pages = reinterpret_cast<int*>(gbase + L::kPages);  // [stage][box of it]
   for (int i = threadIdx.x; i < n_stages << pg_log2; i += kDecThreads) {
     const int t = stage_token(i >> pg_log2) + (i & ((1 << pg_log2) - 1)) * box;
@@ -357,7 +432,7 @@ __global__ void __launch_bounds__(kDecThreads, few4_blocks_per_sm(D, NT))
   if (warp == kDecWarps) {
     // ------------------------------------------------------------------ TMA producer
     const uint64_t stream_policy = l2_policy_evict_first();
-    const uint32_t box_bytes = static_cast<uint32_t>(box) * (D / 2);
+    const uint32_t box_bytes = static_cast<uint32_t>(box) * (D / 2), box_scales = box * Warp::kB;
     int issued = 0;
     for (int st = 0; st < n_stages; ++st) {
       const int s = st % kFew4Stages;
@@ -366,14 +441,18 @@ __global__ void __launch_bounds__(kDecThreads, few4_blocks_per_sm(D, NT))
         ok = wait_bounded(EMPTY(s), ((st / kFew4Stages) - 1) & 1, abort_flag, p.status);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       const uint32_t kbuf = base + s * L::kStage + lane * box_bytes;
+      const uint32_t ks = base + s * L::kStage + 2 * L::kTensor + lane * box_scales;
       const int page = lane < (1 << pg_log2) ? pages[(st << pg_log2) + lane] : -1;
       const uint32_t n_loads = __popc(__ballot_sync(0xffffffffu, page >= 0));
-      if (lane == 0) mbar_arrive_expect_tx(FULL(s), n_loads * 2 * box_bytes);
+      if (lane == 0) mbar_arrive_expect_tx(FULL(s), n_loads * 2 * (box_bytes + box_scales));
       __syncwarp();
       if (page >= 0) {
         const int at = (stage_token(st) + lane * box) & page_mask;
         tma_load_4d_hint(kbuf, &tm_k, FULL(s), 0, at, hk, page, stream_policy);
         tma_load_4d_hint(kbuf + L::kTensor, &tm_v, FULL(s), 0, at, hk, page, stream_policy);
+        const size_t row = ((static_cast<size_t>(page) * p.Hkv + hk) << p.page_log2) + at;
+        bulk_load_hint(ks, p.k_scales + row * Warp::kB, box_scales, FULL(s), stream_policy);
+        bulk_load_hint(ks + L::kScales, p.v_scales + row * Warp::kB, box_scales, FULL(s), stream_policy);
       }
       issued = st + 1;
     }
@@ -387,55 +466,34 @@ __global__ void __launch_bounds__(kDecThreads, few4_blocks_per_sm(D, NT))
   const int g = lane >> 2, c = lane & 3;
   Warp ws;
   ws.init([&](int row) { return p.q + out_row(row) * D; }, rows, p.sl2, lane);
+  ws.places(warp, lane);
   const int last = pos0 + n - 1;                     // position of the last new token
   const int first = p.window < 0 ? 0 : pos0 - p.window;  // first key of the first one's window
-  // Scale bytes of stage st: lane i < 16 has those of key i of this warp's sixteen, lane 16 + i of value
-  // i (zeros where no row sees it).  The sixteen lie in one page.
-  auto scales_at = [&](int st) -> uint2 {
-    uint2 r = make_uint2(0, 0);
-    if (st >= n_stages) return r;
-    const int t = stage_token(st) + warp * 16, mine = t + (lane & 15);
-    const int page = t < len ? pages[(st << pg_log2) + ((warp * 16) >> box_log2)] : -1;
-    if (page < 0 || mine >= len || (mine < first && mine >= p.sinks)) return r;
-    const uint8_t* src = (lane < 16 ? p.k_scales : p.v_scales) +
-                         ((((static_cast<size_t>(page) * p.Hkv + hk) << p.page_log2) + (mine & page_mask)) *
-                          Warp::kB);
-    if constexpr (D == 128)
-      r = __ldcs(reinterpret_cast<const uint2*>(src));
-    else
-      r.x = __ldcs(reinterpret_cast<const uint32_t*>(src));
-    return r;
-  };
-  uint8_t* sc = gbase + L::kScale + warp * 32 * Warp::kB;
-  uint2 sc0 = scales_at(0), sc1 = scales_at(1);
   bool ok = true;
+  int s = 0, parity = 0;
   for (int st = 0; st < n_stages; ++st) {
-    const int s = st % kFew4Stages;
-    if constexpr (D == 128)
-      reinterpret_cast<uint2*>(sc)[lane] = sc0;
-    else
-      reinterpret_cast<uint32_t*>(sc)[lane] = sc0.x;
-    sc0 = sc1;
-    sc1 = scales_at(st + 2);
-    __syncwarp();
-    if (!dec_warp_wait(FULL(s), (st / kFew4Stages) & 1, abort_flag, p.status)) {
+    if (!dec_warp_wait(FULL(s), parity, abort_flag, p.status)) {
       ok = false;
       break;
     }
-    const uint8_t* kbuf = gbase + s * L::kStage;
-    const int key0 = stage_token(st) + warp * 16;  // first key of this warp
+    const int key0 = stage_token(st) + warp * 16 * kFew4Groups;  // first key of this warp
     if (key0 <= last) {
-      const bool edge = key0 + 15 > pos0 || (p.window >= 0 && key0 < last - p.window);
-      ws.tokens(kbuf, kbuf + L::kTensor, sc, warp * 16, edge,
-                [&](int u, int k, int r) {
-                  const int key = key0 + g + 8 * k;
-                  const int pos = pos0 + min((u * 8 + 2 * c + r) / p.G, n - 1);
-                  return key <= pos && (p.window < 0 || pos - key <= p.window || key < p.sinks);
-                },
-                lane);
+      const bool edge = key0 + 16 * kFew4Groups - 1 > pos0 || (p.window >= 0 && key0 < last - p.window);
+      ws.tokens(
+          base + s * L::kStage, edge,
+          [&](int i, int u, int k, int r) {
+            const int key = key0 + 16 * i + g + 8 * k;
+            const int pos = pos0 + min((u * 8 + 2 * c + r) / p.G, n - 1);
+            return key <= pos && (p.window < 0 || pos - key <= p.window || key < p.sinks);
+          },
+          [&](int t) { return key0 + t <= last && (key0 + t >= first || key0 + t < p.sinks); }, lane);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(EMPTY(s));
+    if (++s == kFew4Stages) {
+      s = 0;
+      parity ^= 1;
+    }
   }
 
   // ---------------------------------------------------- merge the four warps' states
@@ -460,14 +518,14 @@ static void few_split(int B, int Hkv, int G, int max_q, int max_k, int window, i
   long long tokens = max_k;
   if (window >= 0) {
     // the window's keys with those of the stages its ends lie in, and the sinks' stages
-    const long long near = static_cast<long long>(window) + max_q + 2 * kDecTok +
-                           (static_cast<long long>(sinks) + kDecTok - 1) / kDecTok * kDecTok;
+    const long long near = static_cast<long long>(window) + max_q + 2 * kFew4Tok +
+                           (static_cast<long long>(sinks) + kFew4Tok - 1) / kFew4Tok * kFew4Tok;
     if (near < tokens) tokens = near;
   }
   const int slots = 152 * few4_blocks_per_sm(d, max_q * G <= 8 ? 1 : 2);
   const int per = row_split_tokens(static_cast<long long>(B) * Hkv, tokens, slots);
-  stages = per / kDecTok;
-  const long long all = (tokens + kDecTok - 1) / kDecTok;
+  stages = (per + kFew4Tok - 1) / kFew4Tok;
+  const long long all = (tokens + kFew4Tok - 1) / kFew4Tok;
   n_splits = all > 0 ? static_cast<int>((all + stages - 1) / stages) : 1;
 }
 
@@ -479,7 +537,7 @@ static int launch_few4(const PagedArgs& a, const CacheFp4& c, cudaStream_t strea
   const uint64_t dims[4] = {row, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(a.Hkv),
                             static_cast<uint64_t>(c.num_pages)};
   const uint64_t strides[3] = {row, head, head * a.Hkv};
-  const uint32_t box[4] = {D / 2, static_cast<uint32_t>(c.page_size < kDecTok ? c.page_size : kDecTok), 1, 1};
+  const uint32_t box[4] = {D / 2, static_cast<uint32_t>(c.page_size < kFew4Tok ? c.page_size : kFew4Tok), 1, 1};
   CUtensorMap tk = {}, tv = {};
   if (c.num_pages > 0 &&
       (!make_tmap_4d_u8(&tk, c.k_codes, dims, strides, box) || !make_tmap_4d_u8(&tv, c.v_codes, dims, strides, box)))

@@ -37,8 +37,10 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 
 // A scale byte as an f16 pair of twice the same, and two as a pair.
-__device__ __forceinline__ uint32_t fp4_scale_pair(uint32_t s) { return (s | (s << 16)) << 7; }
-__device__ __forceinline__ uint32_t fp4_scale_pair(uint32_t lo, uint32_t hi) { return (lo | (hi << 16)) << 7; }
+__device__ __forceinline__ uint32_t fp4_scale_pair(uint32_t s) { return s * 0x00800080u; }
+__device__ __forceinline__ uint32_t fp4_scale_pair(uint32_t lo, uint32_t hi) {
+  return lo * 0x80u + hi * 0x800000u;
+}
 
 // A scale byte's value (not the NaN's).
 __device__ __forceinline__ float fp4_scale(uint32_t s) {
