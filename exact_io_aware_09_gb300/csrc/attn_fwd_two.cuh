@@ -56,7 +56,8 @@ struct WinParams {
 
 template <int D, bool CODES = false>
 struct WinLayout {
-  static constexpr int kKS = D == 128 ? 2 : 3, kVS = D == 128 ? 2 : 3;  // ring slots
+  static constexpr int kKS = D == 128 ? 2 : 3;  // ring slots
+  static constexpr int kVS = D == 128 ? (CODES ? 1 : 2) : 3;
   static constexpr int kNS = D == 128 ? 1 : 2;                          // S buffers
   static constexpr uint32_t kColO = kWColS + kNS * kWN;
   static_assert(kColO + D <= kWTmemCols, "tensor memory");
@@ -64,8 +65,8 @@ struct WinLayout {
   static constexpr uint32_t kStep = kWN * D * 2;
   static constexpr uint32_t kK = kQBytes;
   static constexpr uint32_t kV = kK + kKS * kStep;
-  // codes and scale bytes of K or of V of a step
-  static constexpr int kRawK = CODES ? 2 : 0, kRaw = CODES ? 3 : 0;  // slots of K, and with the one of V
+  // codes and scale bytes of a step, in slots of K and of V
+  static constexpr int kRawKV = CODES ? 3 : 0, kRaw = 2 * kRawKV;
   static constexpr uint32_t kRawCodes = kWN * D / 2, kRawBytes = kRawCodes + kWN * D / 16;
   static constexpr uint32_t kRawAt = kV + kVS * kStep;
   static constexpr uint32_t kBar = kRawAt + kRaw * kRawBytes;
@@ -330,11 +331,11 @@ static_assert(kRegsTwoSoftmax + kRegsTwoIssue + kRegsTwoConvert <= 3 * 80, "regi
 // take the one before it for its own.
 template <int D>
 __device__ __forceinline__ int raw_slot(int t, int v) {
-  return v ? WinLayout<D, true>::kRawK : t % WinLayout<D, true>::kRawK;
+  return v * WinLayout<D, true>::kRawKV + t % WinLayout<D, true>::kRawKV;
 }
 template <int D>
-__device__ __forceinline__ int raw_use(int t, int v) {
-  return v ? t : t / WinLayout<D, true>::kRawK;
+__device__ __forceinline__ int raw_use(int t) {
+  return t / WinLayout<D, true>::kRawKV;
 }
 
 // The producer warp of the codes: each step's of K, then of V, page by page into the raw slots.
@@ -356,7 +357,7 @@ __device__ __forceinline__ void two_load_codes(const Paged4Params& p, const Page
     bool ok = true;
 #pragma unroll
     for (int v = 0; v < 2 && ok; ++v) {
-      const int s = raw_slot<D>(t, v), use = raw_use<D>(t, v);
+      const int s = raw_slot<D>(t, v), use = raw_use<D>(t);
       if (lane == 0) {
         if (use > 0) ok = wait_bounded(empty + 8u * s, (use - 1) & 1, abort_flag, p.status);
         if (ok) mbar_arrive_expect_tx(full + 8u * s, bytes);
@@ -383,8 +384,8 @@ __device__ __forceinline__ void two_load_codes(const Paged4Params& p, const Page
   // every copy lands before the block may exit
   if (lane == 0)
     for (int v = 0; v < 2; ++v)
-      for (int t = max(issued[v] - (v ? 1 : L::kRawK), 0); t < issued[v]; ++t)
-        wait_bounded(full + 8u * raw_slot<D>(t, v), raw_use<D>(t, v) & 1, nullptr, p.status, kWDrainNs);
+      for (int t = max(issued[v] - L::kRawKV, 0); t < issued[v]; ++t)
+        wait_bounded(full + 8u * raw_slot<D>(t, v), raw_use<D>(t) & 1, nullptr, p.status, kWDrainNs);
 }
 
 // A converting warp: the keys from key0 on (half of a step's) of K (v = 0) or V (v = 1), from the raw slots as
@@ -411,7 +412,7 @@ __device__ __forceinline__ void two_convert(const Paged4Params& p, const PagedIt
   for (int t = 0; t < it.n; ++t) {
     const int rs = raw_slot<D>(t, v), s = t % slots;
     if (!__all_sync(0xffffffffu,
-                    wait_bounded(raw_full + 8u * rs, raw_use<D>(t, v) & 1, abort_flag, p.status)))
+                    wait_bounded(raw_full + 8u * rs, raw_use<D>(t) & 1, abort_flag, p.status)))
       break;
     const uint8_t* src = raw + rs * L::kRawBytes;
     uint4 codes[kPasses];
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(two_threads(PAGED, KV), 2)
       }
     } else if (lane == 0 && n > 0) {
       int issued_k = min(KS, n), issued_v = min(VS, n);
-      static_assert(KS == VS, "one loop for both rings");
+      static_assert(KS == VS || CODES, "one loop for both rings");
       for (int t = KS; t < n; ++t) {
         if (!wait_bounded(K_EMPTY(t % KS), ((t / KS) - 1) & 1, abort_flag, p.status)) break;
         load_k(t);

@@ -26,7 +26,7 @@ namespace {
 constexpr int kFew4Rows = 16;
 constexpr int kFew4Tok = 128;                    // tokens of a stage, 32 of each compute warp
 constexpr int kFew4Groups = kFew4Tok / 16 / kDecWarps;
-constexpr int kFew4Stages = 4;                   // of the ring
+constexpr int kFew4Stages = 3;                   // of the ring
 constexpr int kFew4MaxStages = 2048 / kFew4Tok;  // of a split (row_split_tokens)
 constexpr float kRise = 8.0f, kTop = 7.0f, kNone = 3.0e38f;
 
@@ -65,7 +65,7 @@ struct Few4Layout {
 };
 
 // Blocks that share an SM, by registers.
-constexpr int few4_blocks_per_sm(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) : d == 64 ? 3 : 2; }
+constexpr int few4_blocks_per_sm(int d, int nt) { return nt == 1 ? 4 : d == 64 ? 3 : 2; }
 
 template <typename T>
 __device__ __forceinline__ T lds(uint32_t addr);
