@@ -13,6 +13,11 @@
 // cluster's barrier) are they changed.  A call that cannot be met changes nothing.  Then the blocks share
 // the tokens (or the pages that go back), each finding its sequence by a search of the offsets in shared
 // memory.  Bound by latency: launch, two dependent reads and the barrier.
+//
+// Whole prompts' slots are more than a cluster's eight SMs write quickly (1.2 M tokens of 256 prompts: 40 us).
+// From kPgManyRows rows on a first launch over all SMs writes the slots and the new entries, which nothing
+// else reads, and a second of one block comes to the same verdict from what the first left unchanged, and
+// changes the lengths and the list's.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -23,6 +28,10 @@ namespace {
 constexpr int kPgThreads = 1024;
 constexpr int kPgChunk = 2048;  // sequences whose offsets are in shared memory at a time
 constexpr int kPgBlocks = 8;    // of a cluster
+constexpr int kPgManyRows = 1 << 16, kPgManyBlocks = 152;
+
+// What a launch does: everything (one cluster), the slots and entries, or the lengths and the list's.
+enum { kPgAll, kPgSlots, kPgLengths };
 
 struct PagesParams {
   int32_t* block_table;    // [B, max_pages]
@@ -125,10 +134,60 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
   return lo;
 }
 
-template <bool EXTEND>
+// The page of token t of the chunk's sequence u: one it has, or its new one, which goes into the table with
+// its first token; -1 for an entry outside the pool, which is reported.
+__device__ __forceinline__ int page_of_token(const PagesParams& p, const PagesShared& s, int b0, int u, int t,
+                                             int base, int top) {
+  const int j = t >> p.page_log2, have = pages_of(s.len[u], p.page_log2);
+  int32_t* entry = p.block_table + static_cast<size_t>(b0 + u) * p.max_pages + j;
+  const int page = j < have ? *entry : p.free_pages[top - (base + s.off[u] + j - have)];
+  if (j >= have && (t & ((1 << p.page_log2) - 1)) == 0) *entry = page;
+  if (page >= 0 && page < p.num_pages) return page;
+  latch_status(p.status, kStatusBadLengths);
+  return -1;
+}
+
+// Slots of the chunk's n sequences; `top`: the list's place of page 0, `base` the number of the chunk's first
+// page.  A thread takes sixteen rows where there are many: they are mostly one sequence's, and lie in two
+// pages at most.
+__device__ __forceinline__ void give_slots(const PagesParams& p, const PagesShared& s, int b0, int n, int base,
+                                           int top, int tid, int step) {
+  const int page_mask = (1 << p.page_log2) - 1;
+  const int lo = s.start[0], hi = s.start[n];
+  const int per = hi - lo <= step ? 1 : 16;
+  if (lo >= hi) return;
+  for (int g = lo / per + tid; g <= (hi - 1) / per; g += step) {
+    const int i0 = max(g * per, lo), i1 = hi - g * per < per ? hi : g * per + per;
+    int u = last_at_most(s.start, n, i0);
+    if (per == 16 && i1 - i0 == 16 && s.start[u + 1] >= i1) {
+      const int t = s.len[u] + (i0 - s.start[u]), cut = page_mask + 1 - (t & page_mask);
+      const int a = page_of_token(p, s, b0, u, t, base, top);
+      const int b = cut < 16 ? page_of_token(p, s, b0, u, t + cut, base, top) : -1;
+      const int at_a = (a << p.page_log2) + (t & page_mask), at_b = (b << p.page_log2) - cut;
+      int slot[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) slot[e] = e < cut ? (a < 0 ? -1 : at_a + e) : b < 0 ? -1 : at_b + e;
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<int4*>(p.slots + i0 + e) = make_int4(slot[e], slot[e + 1], slot[e + 2], slot[e + 3]);
+      continue;
+    }
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      while (i >= s.start[u + 1]) ++u;
+      const int t = s.len[u] + (i - s.start[u]);
+      const int page = page_of_token(p, s, b0, u, t, base, top);
+      p.slots[i] = page < 0 ? -1 : (page << p.page_log2) + (t & page_mask);
+    }
+  }
+}
+
+template <bool EXTEND, int WHAT>
 __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParams p) {
   __shared__ PagesShared s;
-  const int rank = blockIdx.x, step = gridDim.x * kPgThreads;  // the grid is one cluster
+  if (WHAT == kPgSlots) griddep_launch_dependents();
+  if (WHAT == kPgLengths) griddep_wait();
+  const int rank = blockIdx.x, step = gridDim.x * kPgThreads;  // (kPgAll: the grid is one cluster)
   const int tid = rank * kPgThreads + threadIdx.x;
   if (threadIdx.x == 0) s.bad = 0;
   const int n_free = *p.n_free;
@@ -145,15 +204,14 @@ __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParam
   cluster_sync();  // every block has read the lengths and the list's, which change from here on
   if (refuse != 0) {
     if (tid == 0) latch_status(p.status, refuse);
-    if (EXTEND)
+    if (EXTEND && WHAT != kPgLengths)
       for (int i = tid; i < p.total; i += step) p.slots[i] = -1;
     return;
   }
-  if (EXTEND) {  // rows of no sequence
+  if (EXTEND && WHAT != kPgLengths) {  // rows of no sequence
     for (int i = tid; i < row0; i += step) p.slots[i] = -1;
     for (int i = row1 + tid; i < p.total; i += step) p.slots[i] = -1;
   }
-  const int page_mask = (1 << p.page_log2) - 1;
   // the list's place of page 0
   const int top = EXTEND ? n_free - 1 : n_free + static_cast<int>(all) - 1;
   int base = 0;
@@ -164,38 +222,7 @@ __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParam
       cluster_sync();  // every block has this chunk's lengths
     }
     if (EXTEND) {
-      // four packed rows a thread, which search once and share their pages' entries
-      const int lo = s.start[0], hi = s.start[n];
-      for (int g = (lo >> 2) + tid; g < (hi + 3) >> 2; g += step) {
-        int slot[4];
-        int u = last_at_most(s.start, n, max(g * 4, lo)), page = -1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = g * 4 + e;
-          if (i < lo || i >= hi) continue;
-          const int was = u;
-          while (i >= s.start[u + 1]) ++u;
-          const int t = s.len[u] + (i - s.start[u]), in_page = t & page_mask;
-          if (page < 0 || u != was || in_page == 0) {
-            const int j = t >> p.page_log2, have = pages_of(s.len[u], p.page_log2);
-            int32_t* entry = p.block_table + static_cast<size_t>(b0 + u) * p.max_pages + j;
-            page = j < have ? *entry : p.free_pages[top - (base + s.off[u] + j - have)];
-            if (j >= have && in_page == 0) *entry = page;  // (by the page's first token)
-            if (page < 0 || page >= p.num_pages) {
-              latch_status(p.status, kStatusBadLengths);
-              page = -1;
-            }
-          }
-          slot[e] = page < 0 ? -1 : (page << p.page_log2) + in_page;
-        }
-        if (g * 4 >= lo && g * 4 + 4 <= hi) {
-          *reinterpret_cast<int4*>(p.slots + g * 4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (g * 4 + e >= lo && g * 4 + e < hi) p.slots[g * 4 + e] = slot[e];
-        }
-      }
+      if (WHAT != kPgLengths) give_slots(p, s, b0, n, base, top, tid, step);
     } else {
       for (int x = tid; x < s.off[n]; x += step) {
         const int u = last_at_most(s.off, n, x);
@@ -204,12 +231,12 @@ __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParam
         *entry = -1;
       }
     }
-    if (rank == 0)
+    if (WHAT != kPgSlots && rank == 0)
       for (int u = threadIdx.x; u < n; u += kPgThreads)
         p.seqlens[b0 + u] = EXTEND ? s.len[u] + (s.start[u + 1] - s.start[u]) : p.lengths[b0 + u];
     base += s.off[n];
   }
-  if (tid == 0) *p.n_free = EXTEND ? n_free - static_cast<int>(all) : n_free + static_cast<int>(all);
+  if (WHAT != kPgSlots && tid == 0) *p.n_free = EXTEND ? n_free - static_cast<int>(all) : n_free + static_cast<int>(all);
 }
 
 }  // namespace
@@ -220,21 +247,30 @@ static int launch_pages(const PagesArgs& a, cudaStream_t stream) {
                    device_status_ptr(), a.num_pages, 0, a.max_pages, a.total, a.B};
   if (!p.status) return -5;
   while ((1 << p.page_log2) < a.page_size) ++p.page_log2;
-  // one block where it has a few rows a thread at most
-  const long long rows = EXTEND ? a.total : static_cast<long long>(a.B) * a.max_pages;
-  const int blocks = rows > 4 * kPgThreads ? kPgBlocks : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kPgThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  if (EXTEND && a.total >= kPgManyRows) {
+    cfg.gridDim = dim3(kPgManyBlocks);
+    if (cudaLaunchKernelEx(&cfg, attn_pages_kernel<true, kPgSlots>, p) != cudaSuccess) return -5;
+    cfg.gridDim = dim3(1);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_pages_kernel<true, kPgLengths>, p) == cudaSuccess ? 0 : -5;
+  }
+  // one block where it has a few rows a thread at most
+  const long long rows = EXTEND ? a.total : static_cast<long long>(a.B) * a.max_pages;
+  const int blocks = rows > 4 * kPgThreads ? kPgBlocks : 1;
+  cfg.gridDim = dim3(blocks);
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = blocks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_pages_kernel<EXTEND>, p) == cudaSuccess ? 0 : -5;
+  return cudaLaunchKernelEx(&cfg, attn_pages_kernel<EXTEND, kPgAll>, p) == cudaSuccess ? 0 : -5;
 }
 
 int launch_pages_extend(const PagesArgs& a, cudaStream_t stream) { return launch_pages<true>(a, stream); }

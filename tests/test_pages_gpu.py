@@ -82,6 +82,35 @@ def test_growing_and_shrinking(attn, B, page, steps, most):
     assert attn.attn_poll_status() == 0
 
 
+@pytest.mark.parametrize("B,most,pages", [(3, 70000, 9000), (40, 4000, 6000), (2500, 60, 12000), (40, 4000, 20)])
+def test_many_rows(attn, B, most, pages):
+    """Whole prompts, whose slots take a launch of their own; the last list is too short for them."""
+    rng = np.random.default_rng(B)
+    a, d = both(attn, B, pages, 16, most // 16 + 3, seed=2)
+    first = rng.integers(0, 20, size=B)
+    if pages > 20:
+        a.extend(first.tolist())
+        d.extend(first)
+    n = rng.integers(most // 2, most, size=B)
+    total = int(n.sum())
+    assert total >= 1 << 16
+    before = d.state()
+    want = a.extend(n.tolist())
+    got = d.extend(n, total=total + 9, first=5).cpu().numpy()
+    if want is None:
+        assert attn.attn_poll_status() == -9 and (got == -1).all()
+        assert all(np.array_equal(x, y) for x, y in zip(before, d.state()))
+        return
+    assert got[:5].tolist() == [-1] * 5 and got[5 + total:].tolist() == [-1] * 4
+    assert np.array_equal(got[5:5 + total], want)
+    d.same_as(a)
+    keep = np.where(rng.random(B) < 0.5, first, 0)
+    a.trim(keep.tolist())
+    d.trim(keep)
+    d.same_as(a)
+    assert attn.attn_poll_status() == 0
+
+
 def test_trim_undoes_an_extension(attn):
     rng = np.random.default_rng(3)
     _, d = both(attn, 40, 700, 16, 30, seed=9)
