@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_fp4_kernel(const Cac
   const int rows = n * p.Hkv;
   const int lane = threadIdx.x % kLanes;
   const bool is_v = blockIdx.y != 0;
-  uint16_t* dst0 = (is_v ? p.v : p.k) + static_cast<size_t>(i0) * p.Hkv * D + lane * kFp4Block;
+  uint16_t* dst0 = (is_v ? p.v : p.k) + static_cast<size_t>(i0) * p.Hkv * D;
   const uint8_t* codes = is_v ? p.c.v_codes : p.c.k_codes;
   const uint8_t* scales = is_v ? p.c.v_scales : p.c.k_scales;
   for (int r = threadIdx.x; r < n; r += kCacheThreads) {
@@ -172,16 +172,21 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_fp4_kernel(const Cac
     const int at = slot[rr.tok];
     if (at < 0) continue;
     const size_t row = pool_row(at, rr.h, p.Hkv, p.page_log2);
-    const uint2 w = *reinterpret_cast<const uint2*>(codes + row * (D / 2) + lane * 8);
-    const uint32_t s = fp4_scale_pair(scales[row * kLanes + lane]);
-    uint32_t lo[4], hi[4];
-    fp4_values8(w.x, s, lo);
-    fp4_values8(w.y, s, hi);
+    // eight values of each half of the row, so that a row's threads store side by side
     uint4* dst = reinterpret_cast<uint4*>(dst0 + (static_cast<size_t>(rr.tok) * p.Hkv + rr.h) * D);
-    dst[0] = make_uint4(f16x2_out<BF16>(lo[0]), f16x2_out<BF16>(lo[1]), f16x2_out<BF16>(lo[2]),
-                        f16x2_out<BF16>(lo[3]));
-    dst[1] = make_uint4(f16x2_out<BF16>(hi[0]), f16x2_out<BF16>(hi[1]), f16x2_out<BF16>(hi[2]),
-                        f16x2_out<BF16>(hi[3]));
+    uint32_t w[2], s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = __ldcs(reinterpret_cast<const uint32_t*>(codes + row * (D / 2)) + lane + i * kLanes);
+      s[i] = __ldcs(scales + row * kLanes + (lane + i * kLanes) / 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t v[4];
+      fp4_values8(w[i], fp4_scale_pair(s[i]), v);
+      __stcs(dst + lane + i * kLanes, make_uint4(f16x2_out<BF16>(v[0]), f16x2_out<BF16>(v[1]),
+                                                 f16x2_out<BF16>(v[2]), f16x2_out<BF16>(v[3])));
+    }
   }
 }
 

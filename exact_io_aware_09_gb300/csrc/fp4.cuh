@@ -72,7 +72,10 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float* v) {
 // The scale byte of a block whose largest magnitude is amax (finite): amax / 6 rounded to E5M3, nearest
 // even; at least the smallest one where amax is not zero, at most kFp4MaxScale.
 __device__ __forceinline__ uint32_t fp4_scale_byte(float amax) {
-  const float t = __fdiv_rn(amax, 6.0f);
+  // amax is a 16-bit number.  Half way between two scales (amax = 6 m, m of five bits) the product with the
+  // rounded 1/6, 2^-25 too large, rounds to m itself: half of fp32's step there is more.  Elsewhere amax / 6 is
+  // 2^-12 or more away from half way.
+  const float t = amax * (1.0f / 6.0f);
   uint32_t b;
   if (t >= 6.103515625e-05f) {  // 2^-14, the smallest normal number
     const uint32_t u = __float_as_uint(t);
