@@ -7,7 +7,7 @@ namespace attn {
 
 constexpr int kPagedSms = 152;  // SMs of a GB300, two blocks each
 constexpr int kPagedMaxSplits = 128;
-// Measured, us: a 64-key step and a block's start and end with two blocks on an SM, with one alone; the
+// Measured over the 16-bit cache, us: a 64-key step and a block's start and end with two blocks on an SM, with one alone; the
 // merge's launch, and its bytes (written and read) per us.
 constexpr double kStepTwo = 0.88, kItemTwo = 4.0, kStepOne = 0.6, kItemOne = 3.5;
 constexpr double kMerge = 4.0, kMergeBytes = 5e6;

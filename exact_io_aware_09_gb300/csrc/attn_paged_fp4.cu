@@ -15,6 +15,17 @@
 // tokens' bytes side by side in one, and the high ones, which convert as pairs.  The pool's order (a
 // head's rows of a page side by side) makes a page's codes one contiguous copy, and its scale bytes another.
 // A token that no row sees gets a value scale of zero, which makes its values zeros whatever they hold.
+//
+// A stage is 128 tokens, 32 of each warp: its barriers, mask and maximum check cost as much as a third of the
+// work on sixteen tokens.  Three stages and 96 registers let four blocks share an SM.
+//
+// Bound by instructions: 128 of the 350 a warp takes for sixteen tokens at d = 128 convert a pair of codes and
+// scale it, at half an instruction a cycle and scheduler.  64 sequences of 16k tokens (Hq=64 Hkv=8 d=128,
+// 1.21 GB): 250 us (4.8 TB/s) in 64-token pages, 299 in 16-token ones (four copies a page and stage);
+// of 1k-32k tokens 283 with the merge, the 8-bit cache 394; d = 64: 167 us.  Measured at the first shape: 64-token
+// stages 307, one of 128 tokens more with three blocks an SM 281; scale bytes straight to registers, as the 8-bit
+// decode has them, 329; a ring for every warp without a producer, five blocks an SM, 278; two chains of products
+// for the scores 262; splits of 1,024 tokens 297.
 #include "attn_decode.cuh"
 #include "attn_rows.cuh"
 #include "fp4.cuh"
