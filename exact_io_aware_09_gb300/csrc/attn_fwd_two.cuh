@@ -828,10 +828,11 @@ __global__ void __launch_bounds__(two_threads(PAGED, KV), 2)
         // reaches its own rows, which are not stored
         for (int t = 0; ok && t < n; ++t) {
           ok = win_wait(S_FULL(t % NS), (t / NS) & 1, abort_flag, p.status);
-          if (ok) {
-            mbar_arrive(S_FREE(t % NS));
-            mbar_arrive(P_READY(t & 1));
-          }
+          if (ok) mbar_arrive(S_FREE(t % NS));
+          // with two S buffers S_{t+2} may be there before the other warps have handed over P_t: an arrival
+          // for P_{t+2} would count for P_t
+          if (ok && t > 1) ok = win_wait(PV_DONE(t & 1), ((t - 2) >> 1) & 1, abort_flag, p.status);
+          if (ok) mbar_arrive(P_READY(t & 1));
         }
         ok = false;  // and nothing to write
       }

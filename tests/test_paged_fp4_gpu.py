@@ -240,6 +240,22 @@ def test_long_caches_are_split(attn, d, dtype, Hq, Hkv, n):
     compare(o, lse, rows, extra, dtype, f"split {n}")
 
 
+@pytest.mark.parametrize("d,dtype,n", [(64, "bf16", 3), (64, "f16", 8), (64, "f16", 5), (128, "bf16", 4)])
+def test_part_of_a_tile_over_many_steps(attn, d, dtype, n):
+    """24 to 64 rows of 128: the warps without rows pass the barriers on over hundreds of steps, in many
+    blocks at a time; two calls give the same bits."""
+    import torch
+
+    lengths = [6000, 5111] * 12
+    cache = Cache(lengths, 2, d, 32, 13)
+    news = [n] * len(lengths)
+    a = attend(attn, cache, news, 16, 2, d, dtype)
+    b = attend(attn, cache, news, 16, 2, d, dtype)
+    assert attn.attn_poll_status() == 0
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+    compare(a[0], a[1], *a[2], dtype, f"part of a tile {d} {n}")
+
+
 @pytest.mark.parametrize("q_scale,k_scale,v_scale", [(30.0, 30.0, 1.0), (1.0, 1.0, 3000.0), (1e-3, 1e-3, 1.0)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_chunk_magnitudes(attn, dtype, q_scale, k_scale, v_scale):
