@@ -7,14 +7,14 @@
 //
 //   few query tiles a chunk: four more warps of each block convert its codes into shared memory, so that
 //     the cache is read as it is: 1.4 us a 64-key step at two blocks an SM, against 0.9 over 16 bits.  32
-//     sequences of 16k tokens, 4 or 16 new ones each (Hq=64 Hkv=8 d=128 bf16): 296 and 303 us, as long as
-//     over the 16-bit cache (310, its bytes); 64 of 3-8 tokens over 1k-32k 693 us (736).  Without the
+//     sequences of 16k tokens, 4 or 16 new ones each (Hq=64 Hkv=8 d=128 bf16): 287 and 302 us, as long as
+//     over the 16-bit cache (310, its bytes); 64 of 3-8 tokens over 1k-32k 688 us (736).  Without the
 //     conversions' arithmetic it takes as long, without the exponentials too: what counts is the chain of a
 //     step through copies, converting warps, both products and the softmax, at 96 KB of shared-memory traffic
 //     a step.  Asking for the codes in L2 2 to 8 steps ahead: 338-347 us.
 //   many: every tile would convert the same codes again.  They are converted once, into an f16 copy in the
 //     workspace that the kernel reads as it reads a 16-bit cache.  2 x 2,048 tokens over 12k-16k in 16-token
-//     pages: 1,284 us with the copy's 27 (1,390 TFLOP/s), by codes 2,000.
+//     pages: 1,213-1,284 us with the copy's 27 (1,390-1,480 TFLOP/s), by codes 2,000.
 #include "attn_paged.cuh"
 
 namespace attn {
@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(kCopyThreads) attn_fp4_copy_kernel(const CopyP
     const size_t row = ((static_cast<size_t>(pg) * p.Hkv + h) << p.page_log2) + (t & ((1 << p.page_log2) - 1));
     w[i] = __ldcs(reinterpret_cast<const uint2*>(codes + row * (D / 2)) + lane);
     s[i] = __ldcs(scales + row * kLanes + lane);
+    // a token that no new one sees becomes zeros, whatever it holds
+    if (p.window >= 0 && t < len - n - p.window && t >= p.sinks) s[i] = 0;
   }
 #pragma unroll
   for (int i = 0; i < kUnits / kCopyThreads; ++i) {

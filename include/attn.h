@@ -514,7 +514,8 @@ size_t attn_fwd_paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, i
  * a bf16 query is scaled by a power of two per row and rounded to fp16, which loses at most 2^-25 of the
  * row's largest magnitude.  The weights p_j are rounded to fp16: o is off by at most
  * 2^-11 sum_j p_j |v_j| and, from what fp16's subnormals lose, 2^-32 max_j(p_j) sum_j |v_j|.
- * A value that is NaN and that some new token of its sequence sees may reach all of them.
+ * A value that is NaN and that some new token of its sequence sees may reach all of them; what no new token
+ * sees reaches none.  B and Hkv <= 65535.
  */
 int attn_fwd_paged_fp4(const void *q, const void *k_codes, const void *v_codes, const void *k_scales,
                        const void *v_scales, const int32_t *block_table, const int32_t *cu_seqlens_q,

@@ -283,7 +283,8 @@ def test_far_apart_query_elements(attn):
         compare(o, lse, rows, extra, "bf16", "far apart")
 
 
-@pytest.mark.parametrize("Hq,news", [(2, [4, 1]), (8, [40, 1])])
+# few rows, codes converted by the kernel, and an f16 copy (eight query tiles and more)
+@pytest.mark.parametrize("Hq,news", [(2, [4, 1]), (8, [40, 1]), (32, [41, 7])])
 def test_nan_in_unseen_places(attn, Hq, news):
     """Places behind a sequence's end are NaN in every test here; keys before every window too."""
     import torch
