@@ -39,7 +39,7 @@ constexpr int kFew4Tok = 128;                    // tokens of a stage, 32 of eac
 constexpr int kFew4Groups = kFew4Tok / 16 / kDecWarps;
 constexpr int kFew4Stages = 3;                   // of the ring
 constexpr int kFew4MaxStages = 2048 / kFew4Tok;  // of a split (row_split_tokens)
-constexpr float kRise = 8.0f, kTop = 7.0f, kNone = 3.0e38f;
+constexpr float kRise = 8.0f, kTop = 7.0f, kNone = 3.402823466e38f;
 
 struct Few4Params {
   const uint16_t* q;  // [total_q, Hq, D]
@@ -317,7 +317,9 @@ struct Few4Warp : RowState<D, NT, false> {
     }
   }
 
-  // Raises m to the largest x where that exceeds it by more than 2^kRise.
+  // Raises m to the largest x where that exceeds it by more than kRise: where its weight would pass
+  // 2^(kRise + kTop), by the sum that makes the weight (of an m past 2^24 shift is rounded, and x - m > kRise
+  // may say otherwise).  After it no weight passes 2^(kTop + 1).
   __device__ __forceinline__ void raise(const float (&x)[kFew4Groups][NT][2][2]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -331,11 +333,11 @@ struct Few4Warp : RowState<D, NT, false> {
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
         float& m = this->m[n][r];
         a[r] = 1.0f;
-        if (mx > m + kRise) {
-          a[r] = (m == -INFINITY) ? 0.f : ex2(m - mx);
+        if (mx + shift[n][r] > kRise + kTop) {
+          a[r] = ex2((kTop - mx) - shift[n][r]);  // (0 at the first key)
           m = mx;
+          shift[n][r] = kTop - mx;
         }
-        shift[n][r] = (m == -INFINITY) ? kNone : kTop - m;
         this->l[n][r] *= a[r];
       }
 #pragma unroll

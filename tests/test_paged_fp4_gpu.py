@@ -497,3 +497,59 @@ def test_a_pool_past_32_bit_offsets(attn):
     o, lse, (rows, extra) = attend(attn, small, [70, 30], 16, Hkv, d, "bf16")
     assert attn.attn_poll_status() == 0
     compare(o, lse, rows, extra, "bf16", "far pages, chunk")
+
+
+# products of whole numbers in log2 units, far from zero: `lo` above base at tokens 0 .. 63, `hi` at tokens 64 and
+# 128, base elsewhere.  The references lie 8 (or fp32's step there) below `hi`
+FAR_SCORES = [(2.0 ** 24, 16, 24), (2.0 ** 24, 16, 26), (2.0 ** 25, 8, 16), (2.0 ** 27, 16, 32), (-2.0 ** 24, 4, 12),
+              (2.0 ** 23, 3, 11), (-2.0 ** 25, 16, 24)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("B,Hq,n", [(640, 1, 1), (640, 8, 2)])
+@pytest.mark.parametrize("base,lo,hi", FAR_SCORES)
+def test_scores_far_from_zero(attn, base, lo, hi, B, Hq, n, dtype):
+    """Scores of 10^7 and more whose differences are small: a reference of the weights that fp32 rounds must
+    not carry a weight past fp16.  (B: as many sequences, all of the same pages, as leave a sequence in one
+    split.)  Scores are exact, weights powers of two; o is rounded once, its weights half a step at most."""
+    import torch
+
+    L, d, page = 300, 64, 64
+    x = np.zeros(L)
+    x[:64], x[[64, 128]] = lo, hi
+    n_pages = -(-L // page)
+    kc = np.zeros((n_pages, 1, page, d // 2), dtype=np.uint8)
+    ks = np.zeros((n_pages, 1, page, d // 16), dtype=np.uint8)
+    at = lambda s: np.searchsorted(paged4.E5M3, s)
+    pg, sl = np.arange(L) // page, np.arange(L) % page
+    kc[pg, 0, sl, 0] = 6 + 8 * (base < 0)                       # channel 0: 4 times its scale
+    ks[pg, 0, sl, 0] = at(abs(base) / 131072)                   # (and 32768 in the query)
+    kc[pg, 0, sl, 8] = np.where(x > 0, 6, 0)                    # channel 16
+    ks[pg, 0, sl, 1] = at(x / 4)
+    v = np.random.default_rng(3).standard_normal((L, 1, d))
+    codes, scales, val = paged4.quantise(v)
+    vc, vs = kc.copy(), ks.copy()
+    vc[pg, :, sl], vs[pg, :, sl] = codes, scales
+    q = torch.zeros((B * n, Hq, d), dtype=syn.torch_dtype(dtype), device="cuda")
+    q[..., 0], q[..., 16] = 32768.0, 1.0
+    cache = [torch.from_numpy(a).cuda() for a in (kc, vc, ks, vs)]
+    table = i32(np.tile(np.arange(n_pages), (B, 1)))
+    scale = float(np.float32(np.log(2.0)))                      # (times log2 e in fp32: 1)
+    assert np.float32(scale) * np.float32(1.4426950408889634) == 1.0
+    if n == 1:
+        o, lse = attn.attn_decode_paged_fp4(q, *cache, table, i32([L] * B), L, scale=scale)
+    else:
+        o, lse = attn.attn_fwd_paged_fp4(q, *cache, table, i32(np.arange(B + 1) * n), i32([L] * B), n, L,
+                                         scale=scale)
+    assert attn.attn_poll_status() == 0
+    w = np.exp2(x - hi)[None] * (np.arange(L)[None] <= np.arange(L - n, L)[:, None])
+    l = w.sum(1, keepdims=True)
+    want, size = (w @ val[:, 0]) / l, (w @ np.abs(val[:, 0])) / l
+    lim = (2.0 ** -11 + 2.0 ** -17) * size + 2.0 ** -32 * np.abs(val[:, 0]).sum(0)
+    lim = (lim + EPS[dtype] / 2 * (np.abs(want) + lim) + 2.0 ** -25)[None, :, None]
+    got = o.double().cpu().numpy().reshape(B, n, Hq, d)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want[None, :, None]) <= lim).all()
+    ref = (base + hi + np.log2(l[:, 0])) * np.log(2.0)
+    got = lse.double().cpu().numpy().reshape(B, n, Hq)
+    assert (np.abs(got - ref[None, :, None]) <= 2.0 ** -22 * np.abs(ref)[None, :, None]).all()
