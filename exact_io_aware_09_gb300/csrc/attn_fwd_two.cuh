@@ -883,9 +883,10 @@ __global__ void __launch_bounds__(two_threads(PAGED, KV), 2)
       // the maximum moves when it rises by more than 2^8 (and at the first finite one)
       float alpha = 1.0f, neg_mu;
       if constexpr (FP4) {
-        // The maximum is kept as a product Q K, unscaled.  Where it is 2^24 or more in log2 units, its
+        // The maximum is kept as a product Q K, unscaled.  Where it is 2^23 or more in log2 units, its
         // rounding in the fused step below (s sl2 - m) is more than the weights' range allows, and the
-        // difference is taken before the scaling.
+        // difference is taken before the scaling.  Below, m is rounded by 1/4 at most and kTop - m by 1/2:
+        // no weight passes 2^(8 + kTop + 3/4), 55,109.
         const float r_new = fmaxf(m_raw, tile_max);
         if ((r_new - m_raw) * sl2 > kWRescale) {
           alpha = ex2((m_raw - r_new) * sl2);
@@ -894,7 +895,7 @@ __global__ void __launch_bounds__(two_threads(PAGED, KV), 2)
           l *= alpha;
         }
         neg_mu = (m == -INFINITY) ? 0.0f : kTop - m;
-        const bool far = m != -INFINITY && fabsf(m) >= 16777216.0f;
+        const bool far = m != -INFINITY && fabsf(m) >= 8388608.0f;
         if (__any_sync(0xffffffffu, far)) {
           const float ref = far ? m_raw : 0.0f;
           if (far) neg_mu = kTop;

@@ -506,7 +506,7 @@ FAR_SCORES = [(2.0 ** 24, 16, 24), (2.0 ** 24, 16, 26), (2.0 ** 25, 8, 16), (2.0
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("B,Hq,n", [(640, 1, 1), (640, 8, 2)])
+@pytest.mark.parametrize("B,Hq,n", [(640, 1, 1), (640, 8, 2), (1, 8, 40), (1, 32, 41)])
 @pytest.mark.parametrize("base,lo,hi", FAR_SCORES)
 def test_scores_far_from_zero(attn, base, lo, hi, B, Hq, n, dtype):
     """Scores of 10^7 and more whose differences are small: a reference of the weights that fp32 rounds must
