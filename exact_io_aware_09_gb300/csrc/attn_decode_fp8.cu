@@ -49,8 +49,9 @@ struct DecFp8Params : DecParams {
   float* lse;
 };
 
-// m and the weights' reference r rise when a key exceeds them by more than 2^kRise; a key at r weighs 2^kTop.
-constexpr float kRise = 8.0f, kTop = 7.0f;
+// m and the weights' reference r rise when a key exceeds them by more than kRise; a key at r weighs 2^kTop, one
+// at y 2^(y + shift), shift = kTop - r (kNone before the first value row that is not zero: any y is above it).
+constexpr float kRise = 8.0f, kTop = 7.0f, kNone = 3.402823466e38f;
 
 template <int D>
 struct Fp8Layout {
@@ -106,12 +107,12 @@ __device__ __forceinline__ void load_v_words(const uint8_t* vbuf, int row, int g
 }  // namespace
 
 // A warp's query rows and state (attn_rows.cuh) and its work on sixteen tokens.  The state's m and l are
-// those of the scores, its o counts in units of 2^(ref - kTop).
+// those of the scores, its o counts in units of 2^-shift.
 template <int D, bool BF16, int NT>
 struct Fp8Warp : RowState<D, NT, false> {
   uint32_t qf[NT][D / 16][2];
-  float f[NT][2];    // factors of the rows' products
-  float ref[NT][2];  // the weights' reference; -inf before the first value row that is not zero
+  float f[NT][2];  // factors of the rows' products
+  float shift[NT][2];
 
   // q: the group's query rows, G of them
   __device__ __forceinline__ void init(const uint16_t* q, int G, float sl2, int lane) {
@@ -119,7 +120,7 @@ struct Fp8Warp : RowState<D, NT, false> {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      ref[n][0] = ref[n][1] = -INFINITY;
+      shift[n][0] = shift[n][1] = kNone;
       const int row = n * 8 + g;
       float mx = 0.0f;
 #pragma unroll
@@ -184,7 +185,7 @@ struct Fp8Warp : RowState<D, NT, false> {
         for (int r = 0; r < 2; ++r) {
           x[n][k][r] = in ? sc[n][2 * k + r] * (f[n][r] * kj) : -INFINITY;
           y[n][k][r] = x[n][k][r] + bj;
-          rise = rise || x[n][k][r] > this->m[n][r] + kRise || y[n][k][r] > ref[n][r] + kRise;
+          rise = rise || x[n][k][r] > this->m[n][r] + kRise || y[n][k][r] + shift[n][r] > kRise + kTop;
         }
     }
     if (__any_sync(0xffffffffu, rise)) raise(x, y, vbuf, w0, lane);
@@ -195,11 +196,10 @@ struct Fp8Warp : RowState<D, NT, false> {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float mu = (this->m[n][r] == -INFINITY) ? 0.f : this->m[n][r];
-        const float shift = (ref[n][r] == -INFINITY) ? 0.f : kTop - ref[n][r];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           this->l[n][r] += ex2(x[n][k][r] - mu);
-          w[k][r] = ex2(y[n][k][r] + shift);
+          w[k][r] = ex2(y[n][k][r] + shift[n][r]);
         }
       }
 #pragma unroll
@@ -225,8 +225,10 @@ struct Fp8Warp : RowState<D, NT, false> {
       }
   }
 
-  // Takes value rows of zeros out of y, and raises m to the largest x, the references to the largest y left,
-  // where those exceed them by more than 2^kRise.  Lane i looks at half a row's codes.
+  // Takes value rows of zeros out of y, and raises m to the largest x, the reference to the largest y left,
+  // where those exceed them by more than kRise: for the reference by the sum that makes the weight (of one
+  // past 2^24 shift is rounded, and y - r > kRise may say otherwise), so that no weight passes 2^(kRise + kTop).
+  // Lane i looks at half a row's codes.
   __device__ __forceinline__ void raise(const float (&x)[NT][2][2], float (&y)[NT][2][2], const uint8_t* vbuf,
                                         int w0, int lane) {
     uint32_t any = 0;
@@ -257,9 +259,9 @@ struct Fp8Warp : RowState<D, NT, false> {
           m = mx;
         }
         a[r] = 1.0f;
-        if (my > ref[n][r] + kRise) {
-          a[r] = (ref[n][r] == -INFINITY) ? 0.f : ex2(ref[n][r] - my);
-          ref[n][r] = my;
+        if (my + shift[n][r] > kRise + kTop) {
+          a[r] = ex2((kTop - my) - shift[n][r]);  // (0 at the first value row)
+          shift[n][r] = kTop - my;
         }
       }
 #pragma unroll
@@ -272,7 +274,7 @@ struct Fp8Warp : RowState<D, NT, false> {
     }
   }
 
-  // The state to the merge scratch, its rows divided by their sums: o 2^(ref - kTop - m) / l, the power
+  // The state to the merge scratch, its rows divided by their sums: o 2^(-shift - m) / l, the power
   // of two in two halves, so that it leaves fp32's range only where the result does.
   __device__ __forceinline__ void store(float* rw, int rows, int lane) const {
     float h[NT][2], hl[NT][2];
@@ -280,8 +282,8 @@ struct Fp8Warp : RowState<D, NT, false> {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const bool none = ref[n][r] == -INFINITY;  // no key, or no value row that is not zero
-        h[n][r] = none ? 1.0f : ex2(0.5f * (ref[n][r] - kTop - this->m[n][r]));
+        const bool none = shift[n][r] == kNone;  // no key, or no value row that is not zero
+        h[n][r] = none ? 1.0f : ex2(0.5f * (-shift[n][r] - this->m[n][r]));
         hl[n][r] = this->l[n][r] == 0.f ? 0.f : h[n][r] / this->l[n][r];
       }
     RowState<D, NT, false>::store(

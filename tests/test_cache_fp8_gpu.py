@@ -546,3 +546,51 @@ def test_decode_keeps_what_is_not_finite(attn, split):
     bad[1, :4] = True
     assert torch.equal(torch.isnan(o), bad)
     assert torch.equal(torch.isnan(lse), bad.all(-1))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq", [1, 16])
+@pytest.mark.parametrize("base,lo,hi", [(2.0 ** 24, 16, 24), (2.0 ** 24, 16, 26), (2.0 ** 25, 8, 16), (2.0 ** 27, 16, 32),
+                                        (-2.0 ** 24, 4, 12), (2.0 ** 23, 3, 11), (-2.0 ** 25, 16, 24)])
+def test_decode_of_scores_far_from_zero(attn, base, lo, hi, Hq, dtype):
+    """Scores of 10^7 and more whose differences are small, in whole log2 units and exact: base + lo at tokens
+    0 .. 15, base + hi at token 64, which the same warp takes a stage later, base elsewhere.  A reference of
+    the weights that fp32 rounds must not carry a weight past fp16.  Weights are powers of two: o is off by
+    its rounding and half a step of each weight at most."""
+    import torch
+
+    B, L, d, page = 700, 200, 64, 64     # (as many sequences as leave each in one split; all of the same pages)
+    x = np.zeros(L)
+    x[:16], x[64] = lo, hi
+    k = np.zeros((L, 1, d), dtype=np.float32)
+    k[:, 0, 0], k[:, 0, 1] = base / 32768, x
+    v = np.random.default_rng(3).standard_normal((L, 1, d)).astype(np.float32)
+    v[..., 5] = 300.0                                           # a value scale of 1: no exponent to add to a score
+    bits = [syn.round_bits(a, "f16") for a in (k, v)]
+    ks, kv = chunk.quantise(k.astype(np.float64))
+    assert np.array_equal(ks[..., None] * kv, k.astype(np.float64)), "the keys have to be exact"
+    vs, vv = chunk.quantise(bits_to_double(bits[1], "f16"))
+    assert (vs == 1.0).all()
+    val = vv[:, 0]
+    n_pages = -(-L // page)
+    cache = pool(n_pages, page, 1, d)
+    i32 = lambda a: torch.as_tensor(np.asarray(a, dtype=np.int32), device="cuda")
+    row = np.arange(n_pages)[None]
+    attn.attn_cache_write_fp8(*(syn.bits_to_tensor(b, "f16", "cuda") for b in bits), *cache, i32(row), i32([0, L]),
+                              i32([L]))
+    q = torch.zeros((B, Hq, d), dtype=syn.torch_dtype(dtype), device="cuda")
+    q[..., 0], q[..., 1] = 32768.0, 1.0
+    scale = float(np.float32(np.log(2.0)))                      # (times log2 e in fp32: 1)
+    o, lse = attn.attn_decode_paged_fp8(q, *cache, i32(np.tile(row, (B, 1))), i32([L] * B), L, scale=scale)
+    assert attn.attn_poll_status() == 0
+    w = np.exp2(x - hi)
+    want, size = (w @ val) / w.sum(), (w @ np.abs(val)) / w.sum()
+    # (half a step of a weight below fp16's normal numbers is 2^-32 of the largest)
+    lim = (2.0 ** -11 + 2.0 ** -17) * size + 2.0 ** -32 * np.abs(val).sum(0)
+    eps = 2.0 ** -11 if dtype == "f16" else 2.0 ** -8
+    lim = lim + eps * (np.abs(want) + lim) + 2.0 ** -25
+    got = o.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= lim).all()
+    ref = (base + hi + np.log2(w.sum())) * np.log(2.0)
+    assert (np.abs(lse.double().cpu().numpy() - ref) <= 2.0 ** -22 * abs(ref)).all()
