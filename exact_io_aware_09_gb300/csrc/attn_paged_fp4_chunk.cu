@@ -43,14 +43,16 @@ struct CopyParams {
   const int32_t* seqlens;
   uint16_t* k;  // [B, copy_rows, Hkv, d]
   uint16_t* v;
-  int page_log2, Hkv, max_q, max_k, total_q, rows, window, sinks;
+  int* status;
+  int page_log2, Hkv, max_q, max_k, rows, window, sinks;
 };
 
 constexpr int kCopyThreads = 256;
 
 // One 64-key step of a sequence, K (y even) or V of one head.  A thread takes blocks of sixteen codes; those of
 // four (d = 64: eight) consecutive tokens lie side by side in the pool.  Steps that no new token sees, and
-// sequences whose lengths are refused (the attention kernel reports them), stay as they were.
+// sequences whose lengths are refused (the attention kernel reports them), stay as they were.  The attention
+// kernel does not look at the table: entries outside the pool are reported here, and their tokens zeros.
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) attn_fp4_copy_kernel(const CopyParams p) {
   constexpr int kLanes = D / kFp4Block, kUnits = kWN * kLanes;
@@ -69,10 +71,15 @@ __global__ void __launch_bounds__(kCopyThreads) attn_fp4_copy_kernel(const CopyP
 #pragma unroll
   for (int i = 0; i < kUnits / kCopyThreads; ++i) {
     const int u = threadIdx.x + i * kCopyThreads, t = t0 + u / kLanes, lane = u % kLanes;
-    int pg = -1;
-    if (t < len) pg = p.c.block_table[static_cast<size_t>(b) * p.c.max_pages + (t >> p.page_log2)];
-    if (pg < 0 || pg >= p.c.num_pages) {
+    if (t >= len) {
       s[i] = 0x100;  // nothing to copy
+      continue;
+    }
+    const int pg = p.c.block_table[static_cast<size_t>(b) * p.c.max_pages + (t >> p.page_log2)];
+    if (pg < 0 || pg >= p.c.num_pages) {
+      latch_status(p.status, kStatusBadLengths);
+      w[i] = make_uint2(0, 0);
+      s[i] = 0;
       continue;
     }
     const size_t row = ((static_cast<size_t>(pg) * p.Hkv + h) << p.page_log2) + (t & ((1 << p.page_log2) - 1));
@@ -110,7 +117,8 @@ int launch_copy(const PagedArgs& a, const CacheFp4& c, cudaStream_t stream) {
   p.Hkv = a.Hkv;
   p.max_q = a.max_q;
   p.max_k = a.max_k;
-  p.total_q = a.total_q;
+  p.status = device_status_ptr();
+  if (!p.status) return -5;
   p.window = a.window;
   p.sinks = a.sinks;
   attn_fp4_copy_kernel<D><<<dim3(p.rows / kWN, 2 * a.Hkv, a.B), kCopyThreads, 0, stream>>>(p);

@@ -553,3 +553,43 @@ def test_scores_far_from_zero(attn, base, lo, hi, B, Hq, n, dtype):
     ref = (base + hi + np.log2(l[:, 0])) * np.log(2.0)
     got = lse.double().cpu().numpy().reshape(B, n, Hq)
     assert (np.abs(got - ref[None, :, None]) <= 2.0 ** -22 * np.abs(ref)[None, :, None]).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "f16"), (128, "bf16")])
+def test_bad_pages_of_a_long_chunk(attn, d, dtype):
+    """Over the f16 copy of the cache: a table entry outside the pool is reported, its tokens count as zeros
+    whatever the workspace held, and the other sequences' rows are right.  Entries of pages before the tiles
+    that a window reaches are not looked at."""
+    import torch
+
+    Hq, n, lengths = 32, 41, [400, 300, 500]
+    cache = Cache(lengths, 1, d, 16, 6)
+    need = attn.attn_fwd_paged_fp4_workspace_bytes(3 * n, 3, Hq, 1, n, max(lengths), d)
+    assert need >= 3 * 448 * d * 4, "the call takes a copy"
+    run = lambda **kw: attend(attn, cache, [n] * 3, Hq, 1, d, dtype, workspace=torch.full(
+        (attn.attn_fwd_paged_fp4_workspace_bytes(3 * n, 3, Hq, 1, n, max(lengths), d, **kw),), 0xFF,
+        dtype=torch.uint8, device="cuda"), **kw)
+    o, lse, (rows, extra) = run()
+    assert attn.attn_poll_status() == 0
+    compare(o, lse, rows, extra, dtype, "all pages good")
+    for bad, at in ((2, 3), (0, 24), (1, 18)):
+        was = int(cache.table[bad, at])
+        keep = np.ones(3 * n, dtype=bool)
+        keep[bad * n:(bad + 1) * n] = False
+        for wrong in (-1, cache.dev[0].shape[0], 2147483647, -2147483648):
+            cache.table[bad, at] = wrong
+            o, lse, _ = run()
+            assert attn.attn_poll_status() == -8
+            compare(o[keep], lse[keep], chunk.Rows(*(x[keep] for x in rows)), extra[keep], dtype, "the others")
+            assert o.isfinite().all() and lse.isfinite().all()
+        cache.table[bad, at] = was
+    # a window of 30 keys with 5 sinks reads the tiles of 128 keys that hold either
+    o, lse, (rows, extra) = run(window=30, sinks=5)
+    assert attn.attn_poll_status() == 0
+    for b, L in enumerate(lengths):
+        first = (L - n - 30) // 128 * 128 // 16
+        cache.table[b, 128 // 16:first] = -1
+    o2, lse2, _ = run(window=30, sinks=5)
+    assert attn.attn_poll_status() == 0
+    compare(o2, lse2, rows, extra, dtype, "entries before the window")
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
