@@ -78,10 +78,15 @@ def row_tolerance(rows, eps_p, eps_o, tiny_p, extra_score=0.0):
     terms of 2^-24 each would be 2^-17 if all went the same way; the tensor cores add in blocks),
     plus extra_score.  A score off by t moves every p_j and l by a factor within e^(2t).  Weights:
     half a step, eps_p / 2 relative or tiny_p / 2 absolute; relative to the running maximum, which
-    the largest weight is at least.  o: half a step.  exp2, sums and the division: 2^-17 together."""
+    the largest weight is at least.  o: half a step.  exp2, sums and the division: 2^-17 together.
+
+    Where the scores' error says nothing about the weights (e^(2t) past float64) the bound is infinite,
+    of values that have no weight at all too."""
     t = 2.0 ** -20 * rows.score + extra_score
-    rel = np.expm1(2.0 * t)[..., None] + 0.5 * eps_p + 2.0 ** -17
-    el = rel * rows.pv + 0.5 * tiny_p * rows.top[..., None] * rows.v
+    with np.errstate(over="ignore", invalid="ignore"):
+        rel = np.expm1(2.0 * t)[..., None] + 0.5 * eps_p + 2.0 ** -17
+        moved = np.where(np.isposinf(rel), np.inf, rel * rows.pv)
+    el = moved + 0.5 * tiny_p * rows.top[..., None] * rows.v
     el = el + 0.5 * eps_o * (np.abs(rows.o) + el) + 2.0 ** -25  # half an fp16 subnormal step
     lse = 2.0 * t + 2.0 ** -18 + 2.0 ** -21 * np.abs(np.where(np.isfinite(rows.lse), rows.lse, 0.0))
     return el, lse
@@ -97,8 +102,9 @@ def check(o, lse, rows, tol, what=""):
     for name, got, ref, lim in (("o", o[live], rows.o[live], tol[0][live]),
                                 ("lse", lse[live], rows.lse[live], tol[1][live])):
         assert np.all(np.isfinite(got)), f"{what}: non-finite {name}"
+        assert not np.any(np.isnan(lim)), f"{what}: a tolerance of {name} that is not a number"
         r = np.abs(got - ref) / lim
-        if r.size and r.max() > 1.0:
+        if not np.all(r <= 1.0):
             at = np.unravel_index(int(np.argmax(r)), r.shape)
             raise AssertionError(f"{what}: {name} at {tuple(map(int, at))} of the live rows: "
                                  f"{got[at]!r} for {ref[at]!r}, {r[at]:.2f} times the tolerance "

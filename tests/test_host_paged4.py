@@ -246,3 +246,35 @@ def test_plain_forms_agree_with_the_oracle():
     assert np.array_equal(codes.numpy(), want[0]) and np.array_equal(scales.numpy(), want[1])
     assert np.array_equal(m._join4(codes, scales).double().numpy(), want[2])
     assert torch.equal(m._rounded64(x), torch.from_numpy(want[2]))
+
+
+def test_rows_without_a_bound_hide_no_other():
+    """A row of huge scores, whose bound is infinite, leaves the other rows checked, and a bound that is not a
+    number is refused."""
+    from oracle import chunk
+
+    rng = np.random.default_rng(5)
+    q, k, v = (rng.standard_normal((n, 16)) for n in (4, 50, 50))
+    q[2] *= 2.0 ** 80
+    rows = chunk.attend(q, k, v, np.arange(46, 50), 0.25)
+    tol = chunk.row_tolerance(rows, 2.0 ** -10, 2.0 ** -7, 2.0 ** -31)
+    assert not np.isnan(tol[0]).any() and np.isinf(tol[0][2]).all() and np.isfinite(np.delete(tol[0], 2, 0)).all()
+    chunk.check(rows.o, rows.lse, rows, tol)
+    for row in (0, 1, 3):
+        wrong = rows.o.copy()
+        wrong[row, 3] += 0.1
+        with pytest.raises(AssertionError, match="times the tolerance"):
+            chunk.check(wrong, rows.lse, rows, tol)
+    bad = tol[0].copy()
+    bad[1, 1] = np.nan
+    with pytest.raises(AssertionError, match="not a number"):
+        chunk.check(rows.o, rows.lse, rows, (bad, tol[1]))
+
+
+def test_an_infinite_bound_of_no_weight():
+    """Infinity times a sum that is zero is no bound: it stays infinite."""
+    from oracle import chunk
+
+    rows = chunk.Rows(np.zeros((1, 2)), np.zeros(1), np.array([[0.0, 1.0]]), np.ones((1, 2)),
+                      np.array([1e30]), np.ones(1))
+    assert np.isposinf(chunk.row_tolerance(rows, 2.0 ** -10, 2.0 ** -7, 2.0 ** -31)[0]).all()

@@ -593,3 +593,39 @@ def test_bad_pages_of_a_long_chunk(attn, d, dtype):
     assert attn.attn_poll_status() == 0
     compare(o2, lse2, rows, extra, dtype, "entries before the window")
     assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+
+
+def test_far_apart_query_rows(attn):
+    """bf16 queries whose elements span more than fp16's range and rows of zeros, by a tolerance that is a
+    number everywhere; rows of huge numbers, whose scores are so far apart that one value is the answer."""
+    rng = np.random.default_rng(11)
+    for news, Hq in (([3, 1], 4), ([60, 31], 4), ([33, 7], 32)):
+        total = sum(news)
+        q = rng.standard_normal((total, Hq, 64)) * 2.0 ** rng.integers(-60, 4, size=(total, Hq, 64))
+        q[0, 0] = 0.0
+        huge = [(t, h) for t, h in ((1, 1), (total - 1, 2), (2, Hq - 1))]
+        for t, h in huge:
+            q[t, h] *= 2.0 ** 80
+        q = syn.round_bits(q.astype(np.float32), "bf16")
+        lengths = [90, 300]
+        cache = Cache(lengths, 1, 64, 16, 2, k_scale=2.0 ** -3)
+        o, lse, (rows, extra) = attend(attn, cache, news, Hq, 1, 64, "bf16", q=q)
+        assert attn.attn_poll_status() == 0
+        qd, cu = bits_to_double(q, "bf16"), syn.cu_seqlens(news)
+        ordinary = np.ones((total, Hq), dtype=bool)
+        for t, h in huge:
+            ordinary[t, h] = False
+            b = int(np.searchsorted(cu, t, side="right")) - 1
+            seen = lengths[b] - news[b] + (t - cu[b]) + 1
+            s = 0.125 * (cache.seqs[0][b][:seen, 0] @ qd[t, h])
+            top, second = np.sort(s)[::-1][:2]
+            off = 2.0 ** -20 * rows.score[t, h] + 2.0 ** -25 * extra[t, h]
+            assert top - second > 2 * off + 100.0, "the largest score is not certain"
+            assert np.array_equal(o[t, h].double().cpu().numpy(), cache.seqs[1][b][int(np.argmax(s)), 0])
+            assert abs(float(lse[t, h]) - top) <= off + 2.0 ** -22 * abs(top)
+        pick = chunk.Rows(*(x[ordinary] for x in rows))
+        tol = chunk.row_tolerance(pick, 2.0 ** -10, EPS["bf16"], 2.0 ** -31, 2.0 ** -25 * extra[ordinary])
+        assert all(np.isfinite(t).all() for t in tol)
+        for got, want, lim in ((o, pick.o, tol[0]), (lse, pick.lse, tol[1])):
+            got = got.double().cpu().numpy()[ordinary]
+            assert (np.abs(got - want) <= lim).all()
