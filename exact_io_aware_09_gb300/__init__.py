@@ -939,7 +939,8 @@ def attn_pages_trim(block_table, seqlens, keep, free_pages, n_free, page_size: i
                     stream=None) -> None:
     """Cuts sequences to their first keep[b] tokens (int32 CUDA [B]; 0: the sequence ends) and puts
     the pages that they no longer use on top of the free list; the others as attn_pages_extend, all
-    updated in place.  The entries of pages given back become -1.
+    updated in place.  The entries of pages given back become -1; one outside the pool goes on the list as
+    it is and is reported by attn_poll_status.
     """
     where = "attn_pages_trim"
     B, width, num_pages = _check_pages(where, block_table, seqlens, keep, "keep", 0, free_pages, n_free)

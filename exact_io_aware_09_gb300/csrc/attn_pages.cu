@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParam
       for (int x = tid; x < s.off[n]; x += step) {
         const int u = last_at_most(s.off, n, x);
         int32_t* entry = p.block_table + static_cast<size_t>(b0 + u) * p.max_pages + s.start[u] + (x - s.off[u]);
-        p.free_pages[top - (base + x)] = *entry;
+        const int page = *entry;  // (as it is, so that the numbering holds; one outside the pool is reported)
+        if (page < 0 || page >= p.num_pages) latch_status(p.status, kStatusBadLengths);
+        p.free_pages[top - (base + x)] = page;
         *entry = -1;
       }
     }

@@ -576,7 +576,10 @@ int attn_pages_extend(int32_t *block_table, int32_t *seqlens, const int32_t *cu_
  *                 and takes back all its tokens restores the stack.
  * Pages belong to one sequence: one that two table rows name must not be given back.  A call with a
  * length outside those bounds or past the table's reach, or whose pages do not fit on the stack, changes
- * nothing and is reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status.
+ * nothing and is reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status.  A table entry outside the pool is
+ * reported the same way and goes on the stack as it is: the caller has to take it off before an extension
+ * reaches it (which gives its tokens the slot -1 and reports it again).  So pages that the caller took out of
+ * a table row itself, behind a window say, have to be entered again or kept from the trim.
  */
 int attn_pages_trim(int32_t *block_table, int32_t *seqlens, const int32_t *keep,
                     int32_t *free_pages, int32_t *n_free, int num_pages, int page_size,

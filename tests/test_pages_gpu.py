@@ -257,3 +257,31 @@ def test_another_stream(attn):
     side.synchronize()
     assert slots.cpu().tolist() == a.extend(n.tolist())
     assert attn.attn_poll_status(side) == 0
+
+
+@pytest.mark.parametrize("B,most", [(3, 60), (70, 1500)])   # one block, a cluster of eight
+def test_trim_of_entries_outside_the_pool(attn, B, most):
+    """They are reported, go onto the list as they are, and come off it again as an extension reports them."""
+    rng = np.random.default_rng(B)
+    for wrong in (-1, B * 100, 2147483647, -2147483648):
+        a, d = both(attn, B, B * 100, 16, 100, seed=5)
+        n = rng.integers(most // 2, most, size=B)
+        a.extend(n.tolist())
+        d.extend(n)
+        first = n // 3
+        at = len(a.table[1]) - 1                 # the last page of sequence 1
+        a.table[1][at] = wrong
+        d.table[1, at] = wrong
+        d.trim(n)                                # nothing goes back: the entry is not looked at
+        assert attn.attn_poll_status() == 0
+        a.trim(first.tolist())
+        d.trim(first)
+        assert attn.attn_poll_status() == -8
+        d.same_as(a)
+        assert wrong in a.free
+        slots = d.extend(n - first).cpu().numpy()
+        assert attn.attn_poll_status() == -8
+        want = np.array(a.extend((n - first).tolist()))
+        bad = np.concatenate([np.isin(np.repeat(a.table[b], 16)[first[b]:n[b]], [wrong]) for b in range(B)])
+        assert bad.any() and (slots[bad] == -1).all() and np.array_equal(slots[~bad], want[~bad])
+        d.same_as(a)
