@@ -744,7 +744,8 @@ static int pages_common(const PagesArgs& a, bool extend, attn_stream_t stream) {
   if (a.B < 0 || a.total < 0) return ATTN_ERR_INVALID_ARG;
   const int pages_ok = check_pages(a.num_pages, a.page_size, a.max_pages, 0);
   if (pages_ok != ATTN_OK) return pages_ok;
-  if (static_cast<int64_t>(a.max_pages) * a.page_size > kMaxPagedTokens) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(a.max_pages) * a.page_size > kMaxPagedTokens || a.B > kMaxPagedTokens)
+    return ATTN_ERR_UNSUPPORTED;
   if (a.B == 0 && a.total == 0) return ATTN_OK;
   if (extend && a.total > 0 && !a.slots) return ATTN_ERR_INVALID_ARG;
   if (a.B > 0 && (!a.block_table || !a.seqlens || !a.lengths || !a.free_pages || !a.n_free ||

@@ -149,15 +149,15 @@ __device__ __forceinline__ int page_of_token(const PagesParams& p, const PagesSh
 
 // Slots of the chunk's n sequences; `top`: the list's place of page 0, `base` the number of the chunk's first
 // page.  A thread takes sixteen rows where there are many: they are mostly one sequence's, and lie in two
-// pages at most.
+// pages at most.  (Rows go to 2^31 - 1: what steps past the last is unsigned.)
 __device__ __forceinline__ void give_slots(const PagesParams& p, const PagesShared& s, int b0, int n, int base,
-                                           int top, int tid, int step) {
+                                           int top, unsigned tid, unsigned step) {
   const int page_mask = (1 << p.page_log2) - 1;
-  const int lo = s.start[0], hi = s.start[n];
-  const int per = hi - lo <= step ? 1 : 16;
+  const unsigned lo = s.start[0], hi = s.start[n];
+  const unsigned per = hi - lo <= step ? 1 : 16;
   if (lo >= hi) return;
-  for (int g = lo / per + tid; g <= (hi - 1) / per; g += step) {
-    const int i0 = max(g * per, lo), i1 = hi - g * per < per ? hi : g * per + per;
+  for (unsigned g = lo / per + tid; g <= (hi - 1) / per; g += step) {
+    const int i0 = max(g * per, lo), i1 = min(g * per + per, hi);
     int u = last_at_most(s.start, n, i0);
     if (per == 16 && i1 - i0 == 16 && s.start[u + 1] >= i1) {
       const int t = s.len[u] + (i0 - s.start[u]), cut = page_mask + 1 - (t & page_mask);
@@ -187,8 +187,9 @@ __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParam
   __shared__ PagesShared s;
   if (WHAT == kPgSlots) griddep_launch_dependents();
   if (WHAT == kPgLengths) griddep_wait();
-  const int rank = blockIdx.x, step = gridDim.x * kPgThreads;  // (kPgAll: the grid is one cluster)
-  const int tid = rank * kPgThreads + threadIdx.x;
+  const int rank = blockIdx.x;
+  const unsigned step = gridDim.x * kPgThreads;  // (kPgAll: the grid is one cluster)
+  const unsigned tid = rank * kPgThreads + threadIdx.x;
   if (threadIdx.x == 0) s.bad = 0;
   const int n_free = *p.n_free;
   const int row0 = EXTEND ? p.lengths[0] : 0, row1 = EXTEND ? p.lengths[p.B] : 0;
@@ -205,12 +206,12 @@ __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParam
   if (refuse != 0) {
     if (tid == 0) latch_status(p.status, refuse);
     if (EXTEND && WHAT != kPgLengths)
-      for (int i = tid; i < p.total; i += step) p.slots[i] = -1;
+      for (unsigned i = tid; i < static_cast<unsigned>(p.total); i += step) p.slots[i] = -1;
     return;
   }
   if (EXTEND && WHAT != kPgLengths) {  // rows of no sequence
-    for (int i = tid; i < row0; i += step) p.slots[i] = -1;
-    for (int i = row1 + tid; i < p.total; i += step) p.slots[i] = -1;
+    for (unsigned i = tid; i < static_cast<unsigned>(row0); i += step) p.slots[i] = -1;
+    for (unsigned i = row1 + tid; i < static_cast<unsigned>(p.total); i += step) p.slots[i] = -1;
   }
   // the list's place of page 0
   const int top = EXTEND ? n_free - 1 : n_free + static_cast<int>(all) - 1;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kPgThreads) attn_pages_kernel(const PagesParam
     if (EXTEND) {
       if (WHAT != kPgLengths) give_slots(p, s, b0, n, base, top, tid, step);
     } else {
-      for (int x = tid; x < s.off[n]; x += step) {
+      for (int x = tid; x < s.off[n]; x += step) {  // (at most 2^27 pages)
         const int u = last_at_most(s.off, n, x);
         int32_t* entry = p.block_table + static_cast<size_t>(b0 + u) * p.max_pages + s.start[u] + (x - s.off[u]);
         const int page = *entry;  // (as it is, so that the numbering holds; one outside the pool is reported)

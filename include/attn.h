@@ -553,7 +553,7 @@ int attn_decode_paged_fp4(const void *q, const void *k_codes, const void *v_code
  *   slots         [total] int32 device out: page * page_size + (position % page_size) of each packed
  *                 row's token; -1 for rows outside cu_seqlens_q[0] .. cu_seqlens_q[B]-1
  *   num_pages     pages of the pool and entries of free_pages; page_size a power of two from 16 to
- *                 65536, num_pages * page_size <= 2^31 - 1
+ *                 65536, num_pages * page_size <= 2^31 - 1, max_pages_per_seq * page_size and B <= 2^30
  * A sequence takes ceil((L_b + n_b) / page_size) - ceil(L_b / page_size) pages.  Numbered over the
  * sequences in their order, the k-th new page is free_pages[n_free - 1 - k]; free_pages itself is not
  * written.  A call that the list cannot meet changes nothing but slots, all -1, and is reported as

@@ -278,3 +278,10 @@ def test_an_infinite_bound_of_no_weight():
     rows = chunk.Rows(np.zeros((1, 2)), np.zeros(1), np.array([[0.0, 1.0]]), np.ones((1, 2)),
                       np.array([1e30]), np.ones(1))
     assert np.isposinf(chunk.row_tolerance(rows, 2.0 ** -10, 2.0 ** -7, 2.0 ** -31)[0]).all()
+
+
+def test_pages_of_too_many_sequences(attn):
+    """Sequences are numbered by 32 bits with room for a pass of the kernel behind the last."""
+    for B in ((1 << 30) + 1, (1 << 31) - 1):
+        assert attn.lib.attn_pages_extend(*[FAKE] * 6, 8, 16, 4, 9, B, NUL) == -2
+        assert attn.lib.attn_pages_trim(*[FAKE] * 5, 8, 16, 4, B, NUL) == -2

@@ -285,3 +285,21 @@ def test_trim_of_entries_outside_the_pool(attn, B, most):
         bad = np.concatenate([np.isin(np.repeat(a.table[b], 16)[first[b]:n[b]], [wrong]) for b in range(B)])
         assert bad.any() and (slots[bad] == -1).all() and np.array_equal(slots[~bad], want[~bad])
         d.same_as(a)
+
+
+@pytest.mark.parametrize("n,pages", [(5, 120), (400_000, 120), (400_000, 3)])
+def test_the_most_rows(attn, n, pages):
+    """2^31 - 1 packed rows, a sequence's tokens the last of them (the last list is too short)."""
+    import torch
+
+    T, page = (1 << 31) - 1, 4096
+    a, d = both(attn, 1, pages, page, 130, seed=3)
+    slots = torch.zeros(T, dtype=torch.int32, device="cuda")
+    got = attn.attn_pages_extend(d.table, d.len, d.i32([T - n, T]), d.free, d.n_free, page, T, slots=slots)
+    assert got is slots
+    want = a.extend([n])
+    assert attn.attn_poll_status() == (-9 if want is None else 0)
+    assert bool((slots[:T - n] == -1).all())
+    tail = slots[T - n:].cpu().numpy()
+    assert np.array_equal(tail, np.full(n, -1) if want is None else want)
+    d.same_as(a)
