@@ -34,7 +34,8 @@ size_t copy_bytes(int B, int Hkv, int max_k, int d) {  // of K and V
 }
 
 bool takes_copy(int B, int Hkv, int max_k, int d, int n_qtiles) {
-  return n_qtiles >= kCopyTiles && Hkv <= 32767 && copy_bytes(B, Hkv, max_k, d) <= kCopyBytes;
+  // (one sequence's bytes fit 64 bits whatever the bounds, all sequences' need not)
+  return n_qtiles >= kCopyTiles && Hkv <= 32767 && copy_bytes(1, Hkv, max_k, d) <= kCopyBytes / B;
 }
 
 struct CopyParams {

@@ -285,3 +285,15 @@ def test_pages_of_too_many_sequences(attn):
     for B in ((1 << 30) + 1, (1 << 31) - 1):
         assert attn.lib.attn_pages_extend(*[FAKE] * 6, 8, 16, 4, 9, B, NUL) == -2
         assert attn.lib.attn_pages_trim(*[FAKE] * 5, 8, 16, 4, B, NUL) == -2
+
+
+@pytest.mark.parametrize("B,Hkv,max_k", [(43940, 31337, 52331392), (56806, 32749, 38733568), (36513, 20011, 98619648),
+                                         (32768, 2048, 1 << 30)])
+def test_no_copy_whose_size_passes_64_bits(attn, B, Hkv, max_k):
+    """A chunk of eight query tiles whose f16 copy would be more bytes than 2^64, and little more: it goes by
+    the codes, with the workspace of the 16-bit cache's call (none)."""
+    rows = -(-max_k // 64) * 64
+    assert B * Hkv * rows * 64 * 4 >= 1 << 64 and B * Hkv * rows * 64 * 4 % (1 << 64) <= 1 << 30
+    args = (1024, B, Hkv, Hkv, 1024, max_k, 64)
+    assert attn.attn_fwd_paged_workspace_bytes(*args) == 0
+    assert attn.attn_fwd_paged_fp4_workspace_bytes(*args) == 0
