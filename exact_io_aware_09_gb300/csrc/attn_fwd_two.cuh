@@ -22,7 +22,8 @@
 // Roles: warps 0-3 softmax and epilogue; warp 4 TMA producer (paged: of Q and K, page by page, a page's
 // copy issued by its own lane, the block-table entries read a step ahead); warp 5 tcgen05 issuer of S
 // (it owns the tensor memory), warp 6 of P V (one thread for both: 268 us against 260); paged: warp 7
-// producer of V.  Every wait on a barrier is bounded.
+// producer of V.  Over 4-bit codes warp 4 loads Q alone, warp 7 the codes and scale bytes of K and V, and
+// warps 8-11 convert them (two K, two V).  Every wait on a barrier is bounded.
 //
 // Bound by the tensor pipe's 64-wide products and a step's chain at two blocks an SM.  B=1 Hq=64 Hkv=8
 // N=8192 d=128 bf16, W=1024, 4 sinks: 250 us (1,030 TFLOP/s of visible products; tensor pipe 52% busy,
@@ -545,8 +546,10 @@ __global__ void __launch_bounds__(two_threads(PAGED, KV), 2)
 
   if (warp == 4 && lane == 0) {
     prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
+    if constexpr (!CODES) {  // (codes come by plain bulk copies: there are no maps of K and V)
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
     mbar_init(bar_q, 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(K_FULL(s), CODES ? kConvWarps / 2 : 1);
