@@ -14,7 +14,8 @@
 // head's.  The writer takes its tokens' places as a slot map; a thread takes one block, the threads of a
 // warp the blocks of one head's consecutive tokens, which are neighbours in the pool too.
 //
-// Bound by memory, of which the writer takes 5.5 TB/s and the reader 5.6-6.4 (a copy 6.8): 77k tokens (Hkv=8
+// Bound by memory, of which the writer takes 5.5 TB/s and the reader 5.6-6.4 (a copy 6.8); the writer issues in
+// four of five cycles beside it.  77k tokens (Hkv=8
 // d=128) into 16-token pages 74 us and back out 72, 440k out of 32-token pages 357 us; 64 sequences' single
 // tokens are launch and latency.  The reader's threads take eight values of each half of a row, so that their
 // 16-byte stores lie side by side (sixteen together: 79 us; with streaming stores 75 -> 72); the same in the

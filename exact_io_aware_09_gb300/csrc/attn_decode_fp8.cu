@@ -6,7 +6,7 @@
 // p_j = 2^(x_j - m), o = sum_j p_j 2^b_j vc_j / sum_j p_j.  m and the row sum are those of the scores
 // alone.  The weights of the second product take the values' scales into their exponent, y_j = x_j + b_j,
 // and have a reference of their own: w_j = 2^(y_j - r + 7), r at most 8 below the largest y_j so far, so
-// that w_j <= 2^15 fits a 16-bit number and o is off by at most half a step of each w_j (2^-12 of it) and,
+// that w_j <= 2^15 fits a 16-bit number and o is off by at most half a step of each w_j (2^-11 of it) and,
 // where w_j is below fp16's normal numbers, by 2^-32 of the largest p_j 2^b_j for each code.  A value row
 // of zeros adds nothing to o whatever its scale (the writer's is 1, often far above the other rows'), so
 // it takes no part in r: sixteen tokens that would raise r look at their codes first.  m, too, only

@@ -19,8 +19,10 @@
 // A stage is 128 tokens, 32 of each warp: its barriers, mask and maximum check cost as much as a third of the
 // work on sixteen tokens.  Three stages and 96 registers let four blocks share an SM.
 //
-// Bound by instructions: 128 of the 350 a warp takes for sixteen tokens at d = 128 convert a pair of codes and
-// scale it, at half an instruction a cycle and scheduler.  64 sequences of 16k tokens (Hq=64 Hkv=8 d=128,
+// Bound by latency: half an instruction a cycle and scheduler with 4.5 warps to choose from and no pipe above 45%;
+// what a warp waits for most are its own results, through conversion, scale and product (fixed latency), then
+// the pipes.  128 of the 350 instructions it takes for sixteen tokens at d = 128 convert a pair of codes and scale
+// it.  64 sequences of 16k tokens (Hq=64 Hkv=8 d=128,
 // 1.21 GB): 250 us (4.8 TB/s) in 64-token pages, 299 in 16-token ones (four copies a page and stage);
 // of 1k-32k tokens 283 with the merge, the 8-bit cache 394; d = 64: 167 us.  Measured at the first shape: 64-token
 // stages 307, one of 128 tokens more with three blocks an SM 281; scale bytes straight to registers, as the 8-bit
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kDecThreads, few4_blocks_per_sm(D, NT))
 
 static bool few_rows(int max_q, int G) { return static_cast<long long>(max_q) * G <= kFew4Rows; }
 
-// Splits of a call with few rows, and 64-key stages of each.
+// Splits of a call with few rows, and 128-token stages of each.
 static void few_split(int B, int Hkv, int G, int max_q, int max_k, int window, int sinks, int d,
                       int& n_splits, int& stages) {
   long long tokens = max_k;

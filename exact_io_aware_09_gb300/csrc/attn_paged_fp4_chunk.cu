@@ -14,7 +14,7 @@
 //     a step.  Asking for the codes in L2 2 to 8 steps ahead: 338-347 us.
 //   many: every tile would convert the same codes again.  They are converted once, into an f16 copy in the
 //     workspace that the kernel reads as it reads a 16-bit cache.  2 x 2,048 tokens over 12k-16k in 16-token
-//     pages: 1,213-1,284 us with the copy's 27 (1,390-1,480 TFLOP/s), by codes 2,000.
+//     pages: 1,290-1,320 us with the copy's 27 (1,360-1,390 TFLOP/s), by codes 2,000.
 #include "attn_paged.cuh"
 
 namespace attn {

@@ -8,7 +8,7 @@
 // numbering, so that it undoes an extension exactly.  Which page a token gets depends on the numbers
 // alone, not on the order in which threads run.
 //
-// One launch.  Every block of a cluster adds up the needs of all sequences by itself (a few loads a
+// One launch, but for whole prompts.  Every block of a cluster adds up the needs of all sequences by itself (a few loads a
 // thread), so that all of them come to the same verdict; only when the last has read the lengths (the
 // cluster's barrier) are they changed.  A call that cannot be met changes nothing.  Then the blocks share
 // the tokens (or the pages that go back), each finding its sequence by a search of the offsets in shared

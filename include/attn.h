@@ -442,8 +442,9 @@ size_t attn_decode_paged_fp8_workspace_bytes(int B, int Hq, int Hkv, int max_seq
  * products take the codes as they are (exact in fp16); a bf16 query is scaled by a power of two
  * per row and rounded to fp16; sums and the softmax statistics are fp32, so a value's magnitude times
  * the sequence's tokens has to stay within fp32's range.  The weights p_j take the value rows' scales
- * 2^b_j and are rounded to fp16: o is off by at most 2^-12 sum_j p_j |v_j| and, from what fp16's
+ * 2^b_j and are rounded to fp16, which moves o by at most 2^-11 sum_j p_j |v_j| and, from what fp16's
  * subnormals lose, 2^-32 max_j(p_j 2^b_j) sum_j |code_j|, the maximum over value rows that are not zero.
+ * Beside that stand o's own rounding to its type and what fp32 loses in scores, exponentials and sums.
  */
 int attn_decode_paged_fp8(const void *q, const void *k_pages, const void *v_pages,
                           const float *k_scales, const float *v_scales,
@@ -512,8 +513,9 @@ size_t attn_fwd_paged_fp4_workspace_bytes(int total_q, int B, int Hq, int Hkv, i
  *   the others    as attn_fwd_paged; the workspace is that of attn_fwd_paged_fp4_workspace_bytes
  * Keys and values are code times scale, exact in fp16, and both products are made in fp16 with fp32 sums;
  * a bf16 query is scaled by a power of two per row and rounded to fp16, which loses at most 2^-25 of the
- * row's largest magnitude.  The weights p_j are rounded to fp16: o is off by at most
- * 2^-11 sum_j p_j |v_j| and, from what fp16's subnormals lose, 2^-32 max_j(p_j) sum_j |v_j|.
+ * row's largest magnitude.  The weights p_j are rounded to fp16, which moves o by at most
+ * 2^-11 sum_j p_j |v_j| and, from what fp16's subnormals lose, 2^-32 max_j(p_j) sum_j |v_j|.  Beside that
+ * stand o's own rounding to its type and what fp32 loses in scores, exponentials and sums.
  * A value that is NaN and that some new token of its sequence sees may reach all of them; what no new token
  * sees reaches none.  B and Hkv <= 65535.
  */
@@ -591,7 +593,8 @@ size_t attn_decode_static_scratch_bytes(void);
 /*
  * attn_poll_status -- synchronise `stream`, then read and clear the status word of the
  * current device.  Returns ATTN_OK, the first device-side error latched since the last poll
- * (ATTN_ERR_TIMEOUT, ATTN_ERR_BAD_LENGTHS), or ATTN_ERR_LAUNCH if the synchronisation failed.
+ * (ATTN_ERR_TIMEOUT, ATTN_ERR_BAD_LENGTHS, ATTN_ERR_NO_PAGES), or ATTN_ERR_LAUNCH if the synchronisation
+ * failed.
  */
 int attn_poll_status(attn_stream_t stream);
 
