@@ -909,9 +909,9 @@ def attn_pages_extend(block_table, seqlens, cu_seqlens_q, free_pages, n_free, pa
     block_table int32 CUDA [B, max_pages_per_seq] and seqlens int32 CUDA [B] are updated in place for
     the new tokens, packed rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 (int32 CUDA [B+1]) of sequence
     b; free_pages int32 CUDA [num_pages], an entry for every page of the pool, is a stack whose first
-    n_free (int32 CUDA [1], updated) entries are free.  Returns slots int32 [total]: each row's place page * page_size + offset in the
-    pool, -1 for rows of no sequence.  A call that the list cannot meet changes nothing, gives slots
-    of -1 and is reported by attn_poll_status.
+    n_free (int32 CUDA [1], updated) entries are free.  Returns slots int32 [total]: each row's place
+    page * page_size + offset in the pool, -1 for rows of no sequence.  A call that the list cannot
+    meet changes nothing, gives slots of -1 and is reported by attn_poll_status.
     """
     torch = _torch()
     where = "attn_pages_extend"

@@ -8,9 +8,9 @@
 // numbering, so that it undoes an extension exactly.  Which page a token gets depends on the numbers
 // alone, not on the order in which threads run.
 //
-// One launch, but for whole prompts.  Every block of a cluster adds up the needs of all sequences by itself (a few loads a
-// thread), so that all of them come to the same verdict; only when the last has read the lengths (the
-// cluster's barrier) are they changed.  A call that cannot be met changes nothing.  Then the blocks share
+// One launch, but for whole prompts.  Every block of a cluster adds up the needs of all sequences by itself
+// (a few loads a thread), so that all of them come to the same verdict; only when the last has read the
+// lengths (the cluster's barrier) are they changed.  A call that cannot be met changes nothing.  Then the blocks share
 // the tokens (or the pages that go back), each finding its sequence by a search of the offsets in shared
 // memory.  Bound by latency: launch, two dependent reads and the barrier.
 //

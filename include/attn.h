@@ -468,9 +468,10 @@ int attn_decode_paged_fp8(const void *q, const void *k_pages, const void *v_page
  * bits: fp16's bits shifted right by seven.  The scale of 16 channels is max |x| / 6 rounded to that type,
  * nearest even, at least 2^-17 where max |x| > 0 and at most 10240; 0 where it is 0.  The codes are
  * x / scale rounded to E2M1, nearest even, at most 6 in magnitude (0 for a zero of either sign): values
- * past 61440 saturate there.  Sixteen channels of which one is not finite are stored with the scale byte 255 and read back as NaN.  Only the
- * new tokens' rows are written.  A slot outside [0, num_pages * page_size) other than -1 is reported as
- * ATTN_ERR_BAD_LENGTHS by attn_poll_status and not written.  Two tokens must not share a slot.  d in
+ * past 61440 saturate there.  Sixteen channels of which one is not finite are stored with the scale byte
+ * 255 and read back as NaN.  Only the new tokens' rows are written.  A slot outside
+ * [0, num_pages * page_size) other than -1 is reported as ATTN_ERR_BAD_LENGTHS by attn_poll_status and not
+ * written.  Two tokens must not share a slot.  d in
  * {64, 128}; page_size a power of two from 16 to 65536.  Returns ATTN_OK or a negative attn_status_t.
  */
 int attn_cache_write_fp4(const void *k, const void *v, void *k_codes, void *v_codes, void *k_scales,
